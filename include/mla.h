@@ -273,6 +273,143 @@ mla_status mla_query_from_hidden(const mla_config* cfg, int d_q, const void* h, 
                                  void* q_pe, void* workspace, size_t workspace_bytes,
                                  void* stream);
 
+/* ---- a prefix shared by a batch -------------------------------------------------------
+ * Requests that open with the same tokens (a system prompt, few-shot examples) can attend to
+ * them together: the prefix is expanded once from its cached latents into per-head keys and
+ * values (huny.dev §2-1: k^C = c W^UK, v^C = c W^UV), each step attends to those for every
+ * request of the batch at once, and the result is joined with mla_decode's over the request's
+ * own tokens. Per key, head and query this multiplies d_n + d_r + d_v elements instead of
+ * the absorbed form's 2 d_c + d_r, and the prefix is read once per step instead of once per
+ * request. A step is
+ *   mla_prefix_attend(..)        -> u_prefix, lse_prefix   (the shared tokens)
+ *   mla_decode(..)               -> out_latent, lse        (each request's own tokens)
+ *   mla_output_proj_prefix(..)   -> out
+ * Positions: the prefix's tokens were appended at positions 0..prefix_len - 1. A request's
+ * own tokens are appended to its own pages, numbered from 0 (append and decode rotate by
+ * that number; scores depend on differences of positions alone, so the decode over own
+ * tokens needs no offset), and mla_prefix_attend rotates the query of token t at
+ * prefix_len + seq_lens[b] - q_len + t, where seq_lens counts own tokens only, as given to
+ * mla_decode. Every prefix key is visible to every query token. Several prefixes in one
+ * batch: one mla_prefix_attend per prefix, on the rows of its requests. */
+
+/* Expand the prefix's cached rows, once per prefix (and weights):
+ *   keys[i][l] = c_l W_UK[:, i*d_n : (i+1)*d_n],  values[i][l] = c_l W_UV[:, i*d_v : (i+1)*d_v],
+ *   k_pe[l] = the rotated key of row l as cached (fp8: the values of the codes).
+ *   W_UK, W_UV as given to mla_absorb_weights; cache, num_pages as in mla_append_cache;
+ *   prefix_pages [ceil(prefix_len / P)] int32 (device): the prefix's pages;
+ *   keys [H][prefix_len][d_n], values [H][prefix_len][d_v], k_pe [prefix_len][d_r]: outputs,
+ *   act dtype, fp32 sums. From a block-scaled fp8 cache the tensor-core form rounds code *
+ *   scale to bf16 before the product. prefix_len == 0 is a no-op; above 4194304 it is
+ *   MLA_ERR_UNSUPPORTED. A page id out of range gives rows of zeros and MLA_ERR_DEVICE_GUARD
+ *   in *dev_status (optional, may be NULL; OR-ed in, never cleared by the call). */
+mla_status mla_prefix_expand(const mla_config* cfg, const void* W_UK, const void* W_UV,
+                             const void* cache, int num_pages, const int32_t* prefix_pages,
+                             int prefix_len, void* keys, void* values, void* k_pe,
+                             int32_t* dev_status, void* stream);
+
+/* Bytes of workspace mla_prefix_attend needs for this batch on the current device (may be 0). */
+mla_status mla_prefix_attend_workspace_size(const mla_config* cfg, int batch, int q_len,
+                                            int prefix_len, size_t* bytes);
+
+/* Attention of every request's query tokens to an expanded prefix; for each head i
+ *   s_l = softmax_scale * (q_nope[b][t][i] . keys[i][l] + RoPE(q_pe[b][t][i], p) . k_pe[l]),
+ *   p = prefix_len + seq_lens[b] - q_len + t,
+ *   u[b][t][i] = sum_l softmax(s)_l values[i][l],  lse[b][t][i] = ln sum_l exp(s_l).
+ *   q_nope [batch][q_len][H][d_n], q_pe [batch][q_len][H][d_r] as given to mla_decode (not
+ *   rotated); keys, values, k_pe from mla_prefix_expand; seq_lens [batch] int32 (device): each
+ *   request's own cached tokens including this step's q_len; u [batch][q_len][H][d_v] (act
+ *   dtype), lse [batch][q_len][H] (fp32) outputs.
+ * The softmax's weights are rounded to the act dtype for the product with the values; scores,
+ * maxima, sums and the rotated query are held in fp32 precision (bf16: the rotated query as
+ * the sum of two bf16 terms), so lse is an fp32 result.
+ * seq_lens[b] == 0 marks an empty request (u = 0, lse = -inf), as does prefix_len == 0 for
+ * every request; 0 < seq_lens[b] < q_len is a guard error (same outputs). workspace: 256-byte
+ * aligned device buffer of mla_prefix_attend_workspace_size bytes (NULL if that is 0), any
+ * contents; calls that share one must be ordered on the GPU. dev_status as above. */
+mla_status mla_prefix_attend(const mla_config* cfg, const void* q_nope, const void* q_pe,
+                             const void* keys, const void* values, const void* k_pe, int prefix_len,
+                             const int32_t* seq_lens, int batch, int q_len, void* u, float* lse,
+                             void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                             void* stream);
+
+/* Bytes of workspace mla_output_proj_prefix needs for `rows` rows. */
+mla_status mla_output_proj_prefix_workspace_size(const mla_config* cfg, int rows, size_t* bytes);
+
+/* mla_output_proj_unfolded of the attention over both key sets, own tokens and prefix:
+ *   a = exp(lse) / (exp(lse) + exp(lse_prefix)) per row and head (both -inf: no keys at all,
+ *       u = 0),
+ *   u[r][i] = a out_latent[r][i] W_i^UV + (1 - a) u_prefix[r][i]   (rounded to the act dtype)
+ *   out[r]  = sum_i u[r][i] W_i^O
+ *   out_latent [rows][H*d_c] and lse [rows][H] from mla_decode, u_prefix [rows][H*d_v] and
+ *   lse_prefix [rows][H] from mla_prefix_attend; the rest as mla_output_proj_unfolded. A part
+ *   whose weight is 0 is not read into the sum, whatever it holds. */
+mla_status mla_output_proj_prefix(const mla_config* cfg, const void* out_latent, const float* lse,
+                                  const void* u_prefix, const float* lse_prefix, const void* W_UV,
+                                  const void* W_O, int rows, void* out, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
+/* ---- eviction by accumulated attention weight ------------------------------------------
+ * mla_key_weights adds up how much attention each cached token receives; mla_evict_cache keeps
+ * the tokens that received most and closes the gaps, so that the request goes on with a
+ * shorter cache: mla_append_cache and mla_decode then take the new lengths (and pages). */
+
+/* The query as mla_decode forms it, for mla_key_weights:
+ *   q_lat[b][t][i] = [ q_nope[b][t][i] W_UK_abs[i] ; RoPE(q_pe[b][t][i], p) ],
+ *   p = seq_lens[b] - q_len + t; arguments as in mla_decode, q_lat [batch][q_len][H][d_c + d_r]
+ *   (act dtype, fp32 sums). Rows of a request with seq_lens[b] < q_len are not defined. */
+mla_status mla_absorb_query(const mla_config* cfg, const void* q_nope, const void* q_pe,
+                            const void* W_UK_abs, const int32_t* seq_lens, int batch, int q_len,
+                            void* q_lat, void* stream);
+
+/* Accumulate the attention weight of every cached token over heads and query tokens:
+ *   mass_j = sum over t, i of exp(softmax_scale * q_lat[b][t][i] . cache_row_j - lse[b][t][i])
+ *     (fp8: cache_row_j as the values of its codes), over the t that see j, i.e. with
+ *     j <= seq_lens[b] - q_len + t;
+ *   weights[b][j] = decay * weights[b][j] + mass_j   for tokens cached before this step
+ *   weights[b][j] = mass_j                           for its q_len new tokens, or decay == 0
+ * for j < seq_lens[b]; entries behind are left as they are. With lse from mla_decode on the
+ * same step, mass sums to H * q_len over a request's tokens; with the LSE of a larger key set (a
+ * shared prefix joined in) it is the own tokens' share of it.
+ *   q_lat [batch][q_len][H][d_c + d_r] (act dtype; mla_absorb_query), lse [batch][q_len][H]
+ *   (fp32); cache, block_table, seq_lens, batch, q_len as in mla_decode; decay in [0, 1];
+ *   weights [batch][max_pages * P] fp32 (device), updated in place: no initial contents needed
+ *   for tokens that were never cached before.
+ * Sums are fp32, in a fixed order (the same bits every time). seq_lens[b] == 0: nothing is
+ * written. Requests with a bad length and tokens on a bad page are left out, with
+ * MLA_ERR_DEVICE_GUARD in *dev_status (optional, OR-ed in). */
+mla_status mla_key_weights(const mla_config* cfg, const void* q_lat, const float* lse,
+                           const void* cache, int num_pages, const int32_t* block_table,
+                           int max_pages, const int32_t* seq_lens, int batch, int q_len, float decay,
+                           float* weights, int32_t* dev_status, void* stream);
+
+/* Cut every request's cache down to at most `budget` tokens. A request with
+ * seq_lens[b] <= budget keeps all; otherwise its first `sinks` tokens, its last `recent` ones
+ * and, of those between, the budget - sinks - recent with the largest weights (equal weights:
+ * the lowest index first; NaN below every number). In ascending order they become tokens
+ * 0, 1, .. of the request: row kept[i] of the old pages is written as row i of the new
+ * pages, in the cache's own encoding. rotate != 0 turns its rotary key by (i - kept[i])
+ * theta_k (fp32, rounded to the cache's type; e4m3 saturates), so that row i carries the
+ * rotation of position i that mla_append_cache writes and mla_decode assumes; rotate == 0
+ * copies rows as they are. Rows with i == kept[i] are copied bit for bit.
+ *   weights [batch][max_pages * P] fp32; seq_lens [batch]; block_table [batch][max_pages];
+ *   new_block_table [batch][new_max_pages] int32: the same array as block_table (in place:
+ *     nothing moves for requests within the budget; no page may belong to two requests), or
+ *     an array whose pages are none that block_table names;
+ *   new_weights [batch][new_max_pages * P] fp32, optional (NULL): the kept tokens' weights in
+ *     their new order (entries behind are left as they are); may be `weights` itself if
+ *     new_max_pages == max_pages, otherwise they must not overlap;
+ *   kept [batch][budget] int32: the kept tokens' old indices, ascending, then -1;
+ *   new_seq_lens [batch] int32: min(seq_lens[b], budget); may be seq_lens itself.
+ * A request with seq_lens[b] outside [0, max_pages * P], or more kept tokens than
+ * new_max_pages * P, is left alone (kept all -1, new length the old one), and a row whose old
+ * or new page is out of range is not moved: MLA_ERR_DEVICE_GUARD in *dev_status (optional,
+ * OR-ed in). MLA_ERR_UNSUPPORTED: max_pages * P above 393216. No workspace. */
+mla_status mla_evict_cache(const mla_config* cfg, const float* weights, const int32_t* seq_lens,
+                           const int32_t* block_table, int max_pages, int batch, int budget,
+                           int sinks, int recent, int rotate, void* cache, int num_pages,
+                           const int32_t* new_block_table, int new_max_pages, float* new_weights,
+                           int32_t* kept, int32_t* new_seq_lens, int32_t* dev_status, void* stream);
+
 /* Wait for `stream`, then read the device status word at `status_word` (a decode
  * workspace or an append dev_status) into *code (an mla_status value, MLA_OK if clean)
  * and reset it to 0. */
@@ -285,7 +422,7 @@ const char* mla_status_string(mla_status status);
 const char* mla_last_error(void);
 
 /* Library ABI version (major * 100 + minor). 1.02: mla_append_cache needs no workspace
- * (its size is 0). */
+ * (its size is 0). 1.03: the shared-prefix and eviction calls. */
 int mla_version(void);
 
 /* Number of CUDA kernels the library has launched in this process so far (all

@@ -83,6 +83,15 @@ _SIGNATURES = {
     "mla_cache_row_bytes": (_I, [_CFG, ctypes.POINTER(_SZ)]),
     "mla_query_workspace_size": (_I, [_CFG, _I, _I, ctypes.POINTER(_SZ)]),
     "mla_query_from_hidden": (_I, [_CFG, _I, _P, _P, _P, _P, _I, _P, _P, _P, _SZ, _P]),
+    "mla_prefix_expand": (_I, [_CFG, _P, _P, _P, _I, _P, _I, _P, _P, _P, _P, _P]),
+    "mla_prefix_attend_workspace_size": (_I, [_CFG, _I, _I, _I, ctypes.POINTER(_SZ)]),
+    "mla_prefix_attend": (_I, [_CFG, _P, _P, _P, _P, _P, _I, _P, _I, _I, _P, _P, _P, _SZ, _P, _P]),
+    "mla_output_proj_prefix_workspace_size": (_I, [_CFG, _I, ctypes.POINTER(_SZ)]),
+    "mla_output_proj_prefix": (_I, [_CFG, _P, _P, _P, _P, _P, _P, _I, _P, _P, _SZ, _P]),
+    "mla_absorb_query": (_I, [_CFG, _P, _P, _P, _P, _I, _I, _P, _P]),
+    "mla_key_weights": (_I, [_CFG, _P, _P, _P, _I, _P, _I, _P, _I, _I, ctypes.c_float, _P, _P, _P]),
+    "mla_evict_cache": (_I, [_CFG, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _I, _P, _I, _P, _P, _P,
+                             _P, _P]),
     "mla_read_device_status": (_I, [_P, _P, ctypes.POINTER(_I)]),
     "mla_status_string": (ctypes.c_char_p, [_I]),
     "mla_last_error": (ctypes.c_char_p, []),
@@ -393,6 +402,127 @@ def mla_query_from_hidden(cfg, d_q, h, W_DQ, W_UQ, W_QR, q_nope, q_pe, workspace
         _ptr(q_nope, "q_nope", a, T * H * cfg.d_nope), _ptr(q_pe, "q_pe", a, T * H * cfg.d_rope),
         _ptr(workspace, "workspace", (_torch().uint8,)), workspace.numel(), _stream(stream)),
         "mla_query_from_hidden")
+
+
+def mla_prefix_expand(cfg, W_UK, W_UV, cache, prefix_pages, prefix_len, keys, values, k_pe,
+                      dev_status=None, stream=None):
+    """keys [H][L][d_n], values [H][L][d_v], k_pe [L][d_r] of the first L = prefix_len tokens on
+    prefix_pages (int32, at least ceil(L / page_size) entries)."""
+    a = (_act_dtype(cfg),)
+    H, d_c, d_n, d_v, L = cfg.num_heads, cfg.d_latent, cfg.d_nope, cfg.d_v, int(prefix_len)
+    num_pages = cache.numel() // (cfg.page_size * _cache_row_elems(cfg))
+    if prefix_pages.numel() * cfg.page_size < L:
+        raise ValueError(f"prefix_pages has {prefix_pages.numel()} pages, too few for {L} tokens")
+    _check(lib().mla_prefix_expand(
+        ctypes.byref(cfg), _ptr(W_UK, "W_UK", a, d_c * H * d_n), _ptr(W_UV, "W_UV", a, d_c * H * d_v),
+        _ptr(cache, "cache", _cache_dtypes(cfg), num_pages * cfg.page_size * _cache_row_elems(cfg)), num_pages,
+        _ptr(prefix_pages, "prefix_pages", _i32(0)), L, _ptr(keys, "keys", a, H * L * d_n),
+        _ptr(values, "values", a, H * L * d_v), _ptr(k_pe, "k_pe", a, L * cfg.d_rope),
+        _ptr(dev_status, "dev_status", _i32(0), allow_none=True), _stream(stream)), "mla_prefix_expand")
+
+
+def mla_prefix_attend_workspace_size(cfg, batch, q_len, prefix_len) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().mla_prefix_attend_workspace_size(ctypes.byref(cfg), int(batch), int(q_len),
+                                                  int(prefix_len), ctypes.byref(n)),
+           "mla_prefix_attend_workspace_size")
+    return int(n.value)
+
+
+def mla_prefix_attend(cfg, q_nope, q_pe, keys, values, k_pe, seq_lens, u, lse, workspace=None,
+                      dev_status=None, stream=None):
+    """q_nope [B][q_len][H][d_n]; the prefix length is k_pe's. workspace: uint8 device tensor of
+    mla_prefix_attend_workspace_size bytes (None if 0)."""
+    a = (_act_dtype(cfg),)
+    t = _torch()
+    batch, q_len = q_nope.shape[0], q_nope.shape[1]
+    H, d_n, d_r, d_v = cfg.num_heads, cfg.d_nope, cfg.d_rope, cfg.d_v
+    L = k_pe.numel() // d_r
+    _check(lib().mla_prefix_attend(
+        ctypes.byref(cfg), _ptr(q_nope, "q_nope", a, batch * q_len * H * d_n),
+        _ptr(q_pe, "q_pe", a, batch * q_len * H * d_r), _ptr(keys, "keys", a, H * L * d_n),
+        _ptr(values, "values", a, H * L * d_v), _ptr(k_pe, "k_pe", a, L * d_r), L,
+        _ptr(seq_lens, "seq_lens", _i32(0), batch), batch, q_len,
+        _ptr(u, "u", a, batch * q_len * H * d_v), _ptr(lse, "lse", (t.float32,), batch * q_len * H),
+        _ptr(workspace, "workspace", (t.uint8,), allow_none=True),
+        0 if workspace is None else workspace.numel(),
+        _ptr(dev_status, "dev_status", _i32(0), allow_none=True), _stream(stream)), "mla_prefix_attend")
+
+
+def mla_output_proj_prefix_workspace_size(cfg, rows) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().mla_output_proj_prefix_workspace_size(ctypes.byref(cfg), int(rows), ctypes.byref(n)),
+           "mla_output_proj_prefix_workspace_size")
+    return int(n.value)
+
+
+def mla_output_proj_prefix(cfg, out_latent, lse, u_prefix, lse_prefix, W_UV, W_O, out, workspace,
+                           stream=None):
+    a = (_act_dtype(cfg),)
+    t = _torch()
+    H, d_c, d_v, d = cfg.num_heads, cfg.d_latent, cfg.d_v, cfg.d_model
+    rows = out_latent.numel() // (H * d_c)
+    _check(lib().mla_output_proj_prefix(
+        ctypes.byref(cfg), _ptr(out_latent, "out_latent", a, rows * H * d_c),
+        _ptr(lse, "lse", (t.float32,), rows * H), _ptr(u_prefix, "u_prefix", a, rows * H * d_v),
+        _ptr(lse_prefix, "lse_prefix", (t.float32,), rows * H), _ptr(W_UV, "W_UV", a, d_c * H * d_v),
+        _ptr(W_O, "W_O", a, H * d_v * d), rows, _ptr(out, "out", a, rows * d),
+        _ptr(workspace, "workspace", (t.uint8,)), workspace.numel(), _stream(stream)),
+        "mla_output_proj_prefix")
+
+
+def mla_absorb_query(cfg, q_nope, q_pe, W_UK_abs, seq_lens, q_lat, stream=None):
+    """q_lat [B][q_len][H][d_c + d_r] from q_nope, q_pe [B][q_len][H][..] (mla_decode's query)."""
+    a = (_act_dtype(cfg),)
+    batch, q_len = q_nope.shape[0], q_nope.shape[1]
+    H, d_c, d_r, d_n = cfg.num_heads, cfg.d_latent, cfg.d_rope, cfg.d_nope
+    _check(lib().mla_absorb_query(
+        ctypes.byref(cfg), _ptr(q_nope, "q_nope", a, batch * q_len * H * d_n),
+        _ptr(q_pe, "q_pe", a, batch * q_len * H * d_r), _ptr(W_UK_abs, "W_UK_abs", a, H * d_n * d_c),
+        _ptr(seq_lens, "seq_lens", _i32(0), batch), batch, q_len,
+        _ptr(q_lat, "q_lat", a, batch * q_len * H * (d_c + d_r)), _stream(stream)), "mla_absorb_query")
+
+
+def mla_key_weights(cfg, q_lat, lse, cache, block_table, seq_lens, weights, decay=1.0, dev_status=None,
+                    stream=None):
+    """q_lat [B][q_len][H][d_c + d_r]; weights [B][max_pages * page_size] fp32, updated in place."""
+    a = (_act_dtype(cfg),)
+    t = _torch()
+    batch, q_len = q_lat.shape[0], q_lat.shape[1]
+    max_pages = block_table.shape[1]
+    num_pages = cache.numel() // (cfg.page_size * _cache_row_elems(cfg))
+    _check(lib().mla_key_weights(
+        ctypes.byref(cfg), _ptr(q_lat, "q_lat", a, batch * q_len * cfg.num_heads * (cfg.d_latent + cfg.d_rope)),
+        _ptr(lse, "lse", (t.float32,), batch * q_len * cfg.num_heads),
+        _ptr(cache, "cache", _cache_dtypes(cfg), num_pages * cfg.page_size * _cache_row_elems(cfg)), num_pages,
+        _ptr(block_table, "block_table", _i32(0), batch * max_pages), max_pages,
+        _ptr(seq_lens, "seq_lens", _i32(0), batch), batch, q_len, float(decay),
+        _ptr(weights, "weights", (t.float32,), batch * max_pages * cfg.page_size),
+        _ptr(dev_status, "dev_status", _i32(0), allow_none=True), _stream(stream)), "mla_key_weights")
+
+
+def mla_evict_cache(cfg, weights, seq_lens, block_table, cache, budget, kept, new_seq_lens,
+                    new_block_table=None, new_weights=None, sinks=0, recent=0, rotate=True,
+                    dev_status=None, stream=None):
+    """Cuts every request to at most `budget` tokens; new_block_table None: in place. kept
+    [B][budget] and new_seq_lens [B] int32 are outputs; new_weights (optional) gets the kept
+    tokens' weights, new_seq_lens may be seq_lens."""
+    t = _torch()
+    batch, max_pages = block_table.shape
+    if new_block_table is None:
+        new_block_table = block_table
+    new_max = new_block_table.shape[1]
+    num_pages = cache.numel() // (cfg.page_size * _cache_row_elems(cfg))
+    _check(lib().mla_evict_cache(
+        ctypes.byref(cfg), _ptr(weights, "weights", (t.float32,), batch * max_pages * cfg.page_size),
+        _ptr(seq_lens, "seq_lens", _i32(0), batch), _ptr(block_table, "block_table", _i32(0), batch * max_pages),
+        max_pages, batch, int(budget), int(sinks), int(recent), 1 if rotate else 0,
+        _ptr(cache, "cache", _cache_dtypes(cfg), num_pages * cfg.page_size * _cache_row_elems(cfg)), num_pages,
+        _ptr(new_block_table, "new_block_table", _i32(0), batch * new_max), new_max,
+        _ptr(new_weights, "new_weights", (t.float32,), batch * new_max * cfg.page_size, allow_none=True),
+        _ptr(kept, "kept", _i32(0), batch * max(int(budget), 0)),
+        _ptr(new_seq_lens, "new_seq_lens", _i32(0), batch),
+        _ptr(dev_status, "dev_status", _i32(0), allow_none=True), _stream(stream)), "mla_evict_cache")
 
 
 def mla_read_device_status(status_word, stream=None) -> int:

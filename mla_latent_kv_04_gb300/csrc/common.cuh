@@ -34,6 +34,27 @@ __device__ __forceinline__ void rope_sincos(const RopeTable& rt, int k, int pos,
   __sincosf((float)a, s, c);
 }
 
+// The same frequencies as binary fractions of a turn, turns[k] = theta^(-2k/d_r) / (2 pi) in
+// units of 2^-64 turn: the product with an integer position wraps to the angle modulo one
+// turn by itself, exactly up to |position| 2^-65 turns, in integer arithmetic (the double
+// reduction above costs three fp64 operations per angle, which this GPU runs at a 64th of
+// the fp32 rate: kernels that turn many rows are then bound by it).
+struct TurnTable {
+  unsigned long long turns[kMaxRopePairs];
+  int pairs;
+};
+
+// Sine and cosine of position pos, pair k. kExact: sincosf (fp32 activations); otherwise the
+// hardware approximation, absolute error about 2^-21 on [-pi, pi].
+template <bool kExact>
+__device__ __forceinline__ void turn_sincos(const TurnTable& tt, int k, long long pos, float* s,
+                                            float* c) {
+  const int phase = (int)(((unsigned long long)pos * tt.turns[k]) >> 32);   // 2^-32 turn, signed
+  const float a = (float)phase * 1.4629180792671596e-9f;                    // 2 pi / 2^32
+  if (kExact) sincosf(a, s, c);
+  else __sincosf(a, s, c);
+}
+
 // ---- element conversion -------------------------------------------------------------
 template <typename T> __device__ __forceinline__ float to_f32(T v);
 template <> __device__ __forceinline__ float to_f32<float>(float v) { return v; }
@@ -74,6 +95,23 @@ __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
+}
+
+// Softmax weights of two disjoint key sets from their natural-log LSEs (-inf: no keys; both
+// -inf: both weights 0).
+__device__ __forceinline__ void merge_weights(float lse_a, float lse_b, float* a, float* b) {
+  const float m = fmaxf(lse_a, lse_b);
+  if (m == -INFINITY) {
+    *a = *b = 0.f;
+    return;
+  }
+  const float ea = expf(lse_a - m), eb = expf(lse_b - m), inv = 1.f / (ea + eb);
+  *a = ea * inv;
+  *b = eb * inv;
+}
+// a x + b y, a part of weight 0 left out (its value may be undefined)
+__device__ __forceinline__ float merge_parts(float a, float x, float b, float y) {
+  return (a != 0.f ? a * x : 0.f) + (b != 0.f ? b * y : 0.f);
 }
 
 __device__ __forceinline__ void flag_status(int32_t* status, int code) {

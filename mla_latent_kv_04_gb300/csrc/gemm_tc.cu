@@ -388,6 +388,22 @@ struct EpiU {                 // bf16 u[n][z * dv + m]: head z's latent output o
   }
 };
 
+// u[n][z * dv + m] = a v + b u_prefix[n][z * dv + m]: head z's lifted output of row n joined
+// with that of a shared prefix, the softmax weights (a, b) of the two parts from their LSEs.
+struct EpiUMerge {
+  bf16* u;
+  const bf16* u_prefix;
+  const float* lse;           // [rows][heads]
+  const float* lse_prefix;
+  long long ld;
+  int dv, heads;
+  __device__ __forceinline__ void operator()(int z, int m, int n, float v) const {
+    float a, b;
+    merge_weights(lse[(long long)n * heads + z], lse_prefix[(long long)n * heads + z], &a, &b);
+    const long long i = (long long)n * ld + (long long)z * dv + m;
+    u[i] = __float2bfloat16_rn(merge_parts(a, v, b, __bfloat162float(u_prefix[i])));
+  }
+};
 
 struct EpiStore {             // bf16 out[z][n][m] (leading dims ld_n, ld_z): the W^UV W^O fold
   bf16* out;
@@ -762,8 +778,9 @@ cudaError_t launch_two_proj_tc(const void* x, const void* W_a, const void* W_b, 
 }
 
 // u[r][h][0:d_v] = o_lat[r][h][:] . W_UV[:, h d_v : (h + 1) d_v]  (per head, bf16 out).
+// With `join`, joined with the shared prefix's part (EpiUMerge).
 cudaError_t launch_lift_tc(const void* o_lat, const void* W_UV, int rows, int H, int d_c, int d_v,
-                           void* u, int32_t* status, cudaStream_t s) {
+                           void* u, int32_t* status, cudaStream_t s, const PrefixJoin* join) {
   using namespace gemm;
   if (rows <= 0) return cudaSuccess;
   CUtensorMap A, Bm[4];
@@ -785,6 +802,10 @@ cudaError_t launch_lift_tc(const void* o_lat, const void* W_UV, int rows, int H,
   // (typically the decode's combine, which writes o_lat) ahead of reading any input
   gp.pdl = 1;
   gp.wait_first = 1;
+  if (join)
+    return dispatch(A, Bm[0], Bm[1], Bm[2], Bm[3], gp,
+                    EpiUMerge{reinterpret_cast<bf16*>(u), reinterpret_cast<const bf16*>(join->u_prefix),
+                              join->lse, join->lse_prefix, (long long)H * d_v, d_v, H}, s);
   return dispatch(A, Bm[0], Bm[1], Bm[2], Bm[3], gp,
                   EpiU{reinterpret_cast<bf16*>(u), (long long)H * d_v, d_v}, s);
 }
@@ -838,10 +859,11 @@ cudaError_t launch_query_absorb_tc(const void* q_nope, const void* W_UK_abs, int
   // with the planner as an extra block this is the decode's first kernel and the planner
   // clears the status word; otherwise the prep kernel before it did
   gp.reset_status = 0;
-  // with the planner it is also launched with programmatic serialization, waiting for the
-  // kernel before it (whatever the caller ran) ahead of every read of an input
+  // with the planner, or as a call of its own (the rotation without the planner), it is also
+  // launched with programmatic serialization, waiting for the kernel before it (whatever the
+  // caller ran) ahead of every read of an input
   gp.pdl = 1;
-  gp.wait_first = plan ? 1 : 0;
+  gp.wait_first = plan || rope ? 1 : 0;
   gp.plan_block = plan ? 1 : 0;
   if (plan) gp.plan = *plan;
   gp.rope_blocks = rope ? rope->groups * rope->hblocks : 0;

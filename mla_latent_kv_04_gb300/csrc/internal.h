@@ -155,16 +155,95 @@ cudaError_t launch_q_rope(mla_dtype act, const void* q_pe, const int32_t* seq_le
                           int q_len, int H, int d_c, int d_r, const RopeTable& rt, float q_scale,
                           int planar, void* q_lat, cudaStream_t s);
 
+// The attention output of a shared prefix, to be joined with that of a request's own tokens.
+struct PrefixJoin {
+  const void* u_prefix;       // [rows][H][d_v] act dtype
+  const float* lse;           // [rows][H] of the own tokens
+  const float* lse_prefix;    // [rows][H] of the prefix
+};
+
 // u[r][h][:] = o_lat[r][h][:] . W_i^UV (the latent output lifted to the value width):
-// tensor-core GEMM for bf16 (d_c and d_v multiples of 64), SIMT GEMM otherwise.
+// tensor-core GEMM for bf16 (d_c and d_v multiples of 64), SIMT GEMM otherwise. join: u is
+// the two parts' sum under their softmax weights.
 cudaError_t launch_lift_tc(const void* o_lat, const void* W_UV, int rows, int H, int d_c, int d_v,
-                           void* u, int32_t* status, cudaStream_t s);
+                           void* u, int32_t* status, cudaStream_t s, const PrefixJoin* join = nullptr);
 cudaError_t launch_lift_simt(mla_dtype act, const void* o_lat, const void* W_UV, int rows, int H,
-                             int d_c, int d_v, void* u, cudaStream_t s);
+                             int d_c, int d_v, void* u, cudaStream_t s,
+                             const PrefixJoin* join = nullptr);
 
 // out = o_lat . W_comb; `acc` is an fp32 [rows][N] accumulator in the caller's workspace.
 cudaError_t launch_output_proj_simt_ws(mla_dtype act, const void* o_lat, const void* W_comb,
                                        int rows, int K, int N, void* out, float* acc,
                                        cudaStream_t s);
+
+// ---- shared prefix and cache eviction ----------------------------------------------------
+// Every guard of these calls is OR-ed into `status` (a caller's word, may be null).
+
+// Per-head keys and values of a prefix: keys [H][L][d_n], values [H][L][d_v], k_pe [L][d_r].
+struct PrefixExpandParams {
+  const void* W_UK;           // [d_c][H * d_n]
+  const void* W_UV;           // [d_c][H * d_v]
+  const void* cache;
+  const int32_t* table;       // the prefix's pages
+  int num_pages, L, H, d_c, d_r, d_n, d_v, P;
+  long long row_bytes;
+  float cache_scale;          // of a per-tensor fp8 cache, else 1
+  void* keys;
+  void* values;
+  void* k_pe;
+  int32_t* status;
+};
+cudaError_t launch_prefix_expand_simt(mla_dtype act, mla_dtype cache, const PrefixExpandParams& p,
+                                      cudaStream_t s);
+
+struct PrefixAttendParams {
+  const void* q_nope;         // [rows][H][d_n], row b * q_len + t
+  const void* q_pe;           // [rows][H][d_r], not rotated
+  const void* keys;
+  const void* values;
+  const void* k_pe;
+  const int32_t* seq_lens;    // [rows / q_len]
+  void* u;                    // [rows][H][d_v]
+  float* lse;                 // [rows][H]
+  int rows, q_len, H, L, d_n, d_r, d_v;
+  float scale_log2;           // softmax scale * log2(e)
+  TurnTable tt;
+  int32_t* status;
+};
+cudaError_t launch_prefix_attend_simt(mla_dtype act, const PrefixAttendParams& p, cudaStream_t s);
+
+struct KeyWeightParams {
+  const void* q_lat;          // [batch * q_len][H][D]
+  const float* lse;           // [batch * q_len][H], natural log
+  const void* cache;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  int max_pages, num_pages, batch, q_len, H, d_c, D, P;
+  long long row_bytes;
+  float scale_log2;           // softmax scale * log2(e) (* the scale of a per-tensor fp8 cache)
+  float decay;
+  float* weights;             // [batch][max_pages * P]
+  int32_t* status;
+};
+cudaError_t launch_key_weights_simt(mla_dtype act, mla_dtype cache, const KeyWeightParams& p,
+                                    cudaStream_t s);
+
+struct EvictParams {
+  const float* weights;       // [batch][max_pages * P]
+  const int32_t* seq_lens;
+  const int32_t* block_table;
+  const int32_t* new_block_table;
+  int max_pages, new_max_pages, num_pages, batch, budget, sinks, recent, rotate, P, d_c, d_r;
+  long long row_bytes;
+  void* cache;
+  float* new_weights;         // [batch][new_max_pages * P] or null
+  int32_t* kept;              // [batch][budget]
+  int32_t* new_seq_lens;
+  TurnTable tt;
+  int32_t* status;
+};
+// Weights of one request that the selection holds on chip: a cluster of 8 CTAs, 48 K each.
+constexpr long long kEvictMaxKeys = 8LL * 48 * 1024;
+cudaError_t launch_evict(mla_dtype cache, const EvictParams& p, cudaStream_t s);
 
 }  // namespace mla

@@ -10,6 +10,7 @@
 #include <stdio.h>
 
 #include "internal.h"
+#include "page_elem.cuh"
 #include "prologue.cuh"
 #include "sm100_ptx.cuh"
 
@@ -94,6 +95,27 @@ struct StoreEpi {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       if (col0 + j < N) C[(long long)z * sC + (long long)row * ldc + col0 + j] = from_f32<TC>(v[j]);
+  }
+};
+
+// Head z's lifted output joined with that of a shared prefix under the two parts' softmax
+// weights, into C[row * ldc + z * dv + col].
+template <typename TC>
+struct JoinEpi {
+  TC* C;
+  const TC* u_prefix;
+  const float* lse;
+  const float* lse_prefix;
+  int heads, dv;
+  __device__ void operator()(int z, int row, int col0, const float* v, int N) const {
+    float a, b;
+    merge_weights(lse[(long long)row * heads + z], lse_prefix[(long long)row * heads + z], &a, &b);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (col0 + j >= N) break;
+      const long long i = ((long long)row * heads + z) * dv + col0 + j;
+      C[i] = from_f32<TC>(merge_parts(a, v[j], b, to_f32(u_prefix[i])));
+    }
   }
 };
 
@@ -305,73 +327,6 @@ __global__ void __launch_bounds__(256) prep_kernel(PlanParams pp, const T* __res
 // One CTA = one worker x 8 heads (one warp per head). Per page: the page rows are
 // copied into shared memory with an odd word stride (conflict-free row-parallel reads);
 // lanes own tokens for the scores and latent dims for the output accumulation.
-template <typename CT> struct PageElem;
-template <> struct PageElem<float> {
-  __device__ __forceinline__ static float get(const uint32_t* row, int k, int) {
-    return __uint_as_float(row[k]);
-  }
-  __device__ __forceinline__ static float dot(const uint32_t* row, const float* q, int D, int) {
-    float acc = 0.f;
-    for (int w = 0; w < D; ++w) acc = fmaf(q[w], __uint_as_float(row[w]), acc);
-    return acc;
-  }
-};
-template <> struct PageElem<bf16> {
-  __device__ __forceinline__ static float get(const uint32_t* row, int k, int) {
-    const uint32_t w = row[k >> 1];
-    return __uint_as_float((k & 1) ? (w & 0xFFFF0000u) : (w << 16));
-  }
-  __device__ __forceinline__ static float dot(const uint32_t* row, const float* q, int D, int) {
-    float acc = 0.f;
-    for (int w = 0; w < D / 2; ++w) {
-      const uint32_t v = row[w];
-      acc = fmaf(q[2 * w], __uint_as_float(v << 16), acc);
-      acc = fmaf(q[2 * w + 1], __uint_as_float(v & 0xFFFF0000u), acc);
-    }
-    return acc;
-  }
-};
-template <> struct PageElem<uint8_t> {
-  __device__ __forceinline__ static float get(const uint32_t* row, int k, int) {
-    return fp8_to_f32((uint8_t)(row[k >> 2] >> (8 * (k & 3))));
-  }
-  __device__ __forceinline__ static float dot(const uint32_t* row, const float* q, int D, int) {
-    float acc = 0.f;
-    for (int w = 0; w < D / 4; ++w) {
-      const uint32_t v = row[w];
-#pragma unroll
-      for (int b = 0; b < 4; ++b) acc = fmaf(q[4 * w + b], fp8_to_f32((uint8_t)(v >> (8 * b))), acc);
-    }
-    return acc;
-  }
-};
-// Block-scaled fp8 rows: d_c e4m3 codes, d_c / 128 fp32 scales, d_r bf16 (k_pe).
-struct E4m3B128 {};
-template <> struct PageElem<E4m3B128> {
-  __device__ __forceinline__ static float get(const uint32_t* row, int k, int d_c) {
-    return fp8_to_f32((uint8_t)(row[k >> 2] >> (8 * (k & 3)))) * __uint_as_float(row[(d_c >> 2) + (k >> 7)]);
-  }
-  __device__ __forceinline__ static float dot(const uint32_t* row, const float* q, int D, int d_c) {
-    float acc = 0.f;
-    for (int blk = 0; blk < d_c / 128; ++blk) {
-      float part = 0.f;
-      for (int w = 32 * blk; w < 32 * blk + 32; ++w) {
-        const uint32_t v = row[w];
-#pragma unroll
-        for (int b = 0; b < 4; ++b) part = fmaf(q[4 * w + b], fp8_to_f32((uint8_t)(v >> (8 * b))), part);
-      }
-      acc = fmaf(part, __uint_as_float(row[(d_c >> 2) + blk]), acc);
-    }
-    const uint32_t* kr = row + (d_c >> 2) + (d_c >> 7);
-    for (int w = 0; w < (D - d_c) / 2; ++w) {
-      const uint32_t v = kr[w];
-      acc = fmaf(q[d_c + 2 * w], __uint_as_float(v << 16), acc);
-      acc = fmaf(q[d_c + 2 * w + 1], __uint_as_float(v & 0xFFFF0000u), acc);
-    }
-    return acc;
-  }
-};
-
 constexpr int SIMT_HEADS = 8;
 
 template <typename QT, typename CT, int VPL>
@@ -882,7 +837,14 @@ static cudaError_t output_proj_t(const void* o_lat, const void* W_comb, int rows
 // u[r][h][0:d_v] = o_lat[r][h][:] . W_UV[:, h d_v : (h + 1) d_v], one batch entry per head.
 template <typename T>
 static cudaError_t lift_t(const void* o_lat, const void* W_UV, int rows, int H, int d_c, int d_v,
-                          void* u, cudaStream_t s) {
+                          void* u, cudaStream_t s, const PrefixJoin* join) {
+  if (join) {
+    JoinEpi<T> epi{reinterpret_cast<T*>(u), reinterpret_cast<const T*>(join->u_prefix), join->lse,
+                   join->lse_prefix, H, d_v};
+    return simt_gemm(reinterpret_cast<const T*>(o_lat), (long long)H * d_c, (long long)d_c,
+                     reinterpret_cast<const T*>(W_UV), (long long)H * d_v, (long long)d_v, rows, d_v,
+                     d_c, H, 1, epi, s);
+  }
   StoreEpi<T> epi{reinterpret_cast<T*>(u), (long long)H * d_v, (long long)d_v};
   return simt_gemm(reinterpret_cast<const T*>(o_lat), (long long)H * d_c, (long long)d_c,
                    reinterpret_cast<const T*>(W_UV), (long long)H * d_v, (long long)d_v, rows, d_v,
@@ -890,10 +852,10 @@ static cudaError_t lift_t(const void* o_lat, const void* W_UV, int rows, int H, 
 }
 
 cudaError_t launch_lift_simt(mla_dtype act, const void* o_lat, const void* W_UV, int rows, int H,
-                             int d_c, int d_v, void* u, cudaStream_t s) {
+                             int d_c, int d_v, void* u, cudaStream_t s, const PrefixJoin* join) {
   if (rows <= 0) return cudaSuccess;
-  if (act == MLA_F32) return lift_t<float>(o_lat, W_UV, rows, H, d_c, d_v, u, s);
-  return lift_t<bf16>(o_lat, W_UV, rows, H, d_c, d_v, u, s);
+  if (act == MLA_F32) return lift_t<float>(o_lat, W_UV, rows, H, d_c, d_v, u, s, join);
+  return lift_t<bf16>(o_lat, W_UV, rows, H, d_c, d_v, u, s, join);
 }
 
 cudaError_t launch_output_proj_simt_ws(mla_dtype act, const void* o_lat, const void* W_comb,

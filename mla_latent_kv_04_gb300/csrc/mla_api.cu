@@ -105,6 +105,19 @@ RopeTable rope_table(const mla_config* c) {
   return rt;
 }
 
+// The frequencies as fractions of a turn in units of 2^-64 (TurnTable), from the same doubles.
+TurnTable turn_table(const mla_config* c) {
+  TurnTable tt;
+  memset(&tt, 0, sizeof(tt));
+  const RopeTable rt = rope_table(c);
+  tt.pairs = rt.pairs;
+  for (int k = 0; k < rt.pairs; ++k) {
+    const double turns = rt.inv_freq[k] * 0.15915494309189533576888376337251;   // 1 / (2 pi)
+    tt.turns[k] = (unsigned long long)ldexp(turns - floor(turns), 64);
+  }
+  return tt;
+}
+
 int default_workers(const mla_config* c, const mla_decode_opts* o, bool tc) {
   if (o && o->num_workers > 0) return o->num_workers;
   const int sms = device_sm_count();
@@ -151,7 +164,7 @@ void set_last_error(const std::string& what) { g_last_error = what; }
 
 extern "C" {
 
-int mla_version(void) { return 102; }
+int mla_version(void) { return 103; }
 
 uint64_t mla_kernel_launches(void) { return (uint64_t)mla::g_launches.load(); }
 
@@ -479,17 +492,14 @@ mla_status mla_output_proj_unfolded_workspace_size(const mla_config* cfg, int ro
   return MLA_OK;
 }
 
-mla_status mla_output_proj_unfolded(const mla_config* cfg, const void* out_latent, const void* W_UV,
-                                    const void* W_O, int rows, void* out, void* workspace,
-                                    size_t workspace_bytes, void* stream) {
-  mla_status st = check_config(cfg);
-  if (st != MLA_OK) return st;
-  if (rows < 0) return invalid("rows must be >= 0");
-  if (rows == 0) return MLA_OK;
+static mla_status output_proj_unfolded(const mla_config* cfg, const void* out_latent, const void* W_UV,
+                                       const void* W_O, int rows, void* out, void* workspace,
+                                       size_t workspace_bytes, void* stream, const PrefixJoin* join,
+                                       const char* name) {
   if (!out_latent || !W_UV || !W_O || !out) return invalid("null pointer");
   const size_t acc_bytes = unfolded_acc_bytes(cfg, rows);
   if (!workspace || workspace_bytes < acc_bytes + 256 + unfolded_u_bytes(cfg, rows)) {
-    g_last_error = "workspace smaller than mla_output_proj_unfolded_workspace_size";
+    g_last_error = std::string("workspace smaller than ") + name + "_workspace_size";
     return MLA_ERR_WORKSPACE;
   }
   if (((uintptr_t)workspace & 255) != 0) return invalid("workspace must be 256-byte aligned");
@@ -500,14 +510,43 @@ mla_status mla_output_proj_unfolded(const mla_config* cfg, const void* out_laten
   const int H = cfg->num_heads, d_c = cfg->d_latent, d_v = cfg->d_v, d = cfg->d_model;
   cudaError_t e;
   if (cfg->act_dtype == MLA_BF16 && d_c % 64 == 0 && d_v % 64 == 0) {
-    e = launch_lift_tc(out_latent, W_UV, rows, H, d_c, d_v, u, status, s);
+    e = launch_lift_tc(out_latent, W_UV, rows, H, d_c, d_v, u, status, s, join);
     if (e == cudaSuccess) e = launch_output_proj_tc(u, W_O, rows, H * d_v, d, out, status, s);
   } else {
-    e = launch_lift_simt(cfg->act_dtype, out_latent, W_UV, rows, H, d_c, d_v, u, s);
+    e = launch_lift_simt(cfg->act_dtype, out_latent, W_UV, rows, H, d_c, d_v, u, s, join);
     if (e == cudaSuccess)
       e = launch_output_proj_simt_ws(cfg->act_dtype, u, W_O, rows, H * d_v, d, out, acc, s);
   }
-  return e == cudaSuccess ? MLA_OK : cuda_fail(e, "mla_output_proj_unfolded");
+  return e == cudaSuccess ? MLA_OK : cuda_fail(e, name);
+}
+
+mla_status mla_output_proj_unfolded(const mla_config* cfg, const void* out_latent, const void* W_UV,
+                                    const void* W_O, int rows, void* out, void* workspace,
+                                    size_t workspace_bytes, void* stream) {
+  mla_status st = check_config(cfg);
+  if (st != MLA_OK) return st;
+  if (rows < 0) return invalid("rows must be >= 0");
+  if (rows == 0) return MLA_OK;
+  return output_proj_unfolded(cfg, out_latent, W_UV, W_O, rows, out, workspace, workspace_bytes,
+                              stream, nullptr, "mla_output_proj_unfolded");
+}
+
+mla_status mla_output_proj_prefix_workspace_size(const mla_config* cfg, int rows, size_t* bytes) {
+  return mla_output_proj_unfolded_workspace_size(cfg, rows, bytes);
+}
+
+mla_status mla_output_proj_prefix(const mla_config* cfg, const void* out_latent, const float* lse,
+                                  const void* u_prefix, const float* lse_prefix, const void* W_UV,
+                                  const void* W_O, int rows, void* out, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
+  mla_status st = check_config(cfg);
+  if (st != MLA_OK) return st;
+  if (rows < 0) return invalid("rows must be >= 0");
+  if (rows == 0) return MLA_OK;
+  if (!lse || !u_prefix || !lse_prefix) return invalid("null pointer");
+  const PrefixJoin join{u_prefix, lse, lse_prefix};
+  return output_proj_unfolded(cfg, out_latent, W_UV, W_O, rows, out, workspace, workspace_bytes,
+                              stream, &join, "mla_output_proj_prefix");
 }
 
 // Query side: three GEMMs through fp32 accumulators, one accumulator region reused in stream
@@ -567,6 +606,224 @@ mla_status mla_query_from_hidden(const mla_config* cfg, int d_q, const void* h, 
       e = launch_output_proj_simt_ws(cfg->act_dtype, c_q, W_UQ, T, d_q, n_nope, q_nope, acc, s);
   }
   return e == cudaSuccess ? MLA_OK : cuda_fail(e, "mla_query_from_hidden");
+}
+
+// ------------------------------------------------------------------ shared prefix, eviction
+
+mla_status mla_absorb_query(const mla_config* cfg, const void* q_nope, const void* q_pe,
+                            const void* W_UK_abs, const int32_t* seq_lens, int batch, int q_len,
+                            void* q_lat, void* stream) {
+  mla_status st = check_decode_shape(cfg, batch, q_len);
+  if (st != MLA_OK) return st;
+  if (!q_nope || !q_pe || !W_UK_abs || !seq_lens || !q_lat) return invalid("null pointer");
+  const RopeTable rt = rope_table(cfg);
+  const int D = cfg->d_latent + cfg->d_rope;
+  cudaError_t e;
+  if (cfg->act_dtype == MLA_BF16) {
+    RopeJob rj;
+    rj.q_pe = reinterpret_cast<const bf16*>(q_pe);
+    rj.seq_lens = seq_lens;
+    rj.q_lat = reinterpret_cast<bf16*>(q_lat);
+    rj.groups = batch * q_len;
+    rj.q_len = q_len;
+    rj.H = cfg->num_heads;
+    rj.d_c = cfg->d_latent;
+    rj.d_r = cfg->d_rope;
+    rj.planar = 0;
+    rj.hblocks = (cfg->num_heads + 31) / 32;
+    rj.f16 = 0;
+    rj.qs = 1.f;
+    rj.rt = rt;
+    e = launch_query_absorb_tc(q_nope, W_UK_abs, batch * q_len, cfg->num_heads, cfg->d_nope,
+                               cfg->d_latent, D, 1.f, 0, 0, q_lat, nullptr, nullptr, &rj,
+                               (cudaStream_t)stream);
+  } else {
+    e = launch_query_prologue(cfg->act_dtype, q_nope, q_pe, W_UK_abs, seq_lens, batch, q_len,
+                              cfg->num_heads, cfg->d_nope, cfg->d_latent, cfg->d_rope, rt, q_lat,
+                              (cudaStream_t)stream);
+  }
+  return e == cudaSuccess ? MLA_OK : cuda_fail(e, "mla_absorb_query");
+}
+
+static float code_scale_of(const mla_config* c) {
+  return c->cache_dtype == MLA_FP8_E4M3 ? c->cache_scale : 1.f;
+}
+
+static mla_status check_prefix(const mla_config* cfg, int prefix_len) {
+  mla_status st = check_config(cfg);
+  if (st != MLA_OK) return st;
+  if (prefix_len < 0) return invalid("prefix_len must be >= 0");
+  if (prefix_len > (1 << 22)) return unsupported("prefix_len above 4194304");
+  return MLA_OK;
+}
+
+mla_status mla_prefix_expand(const mla_config* cfg, const void* W_UK, const void* W_UV,
+                             const void* cache, int num_pages, const int32_t* prefix_pages,
+                             int prefix_len, void* keys, void* values, void* k_pe,
+                             int32_t* dev_status, void* stream) {
+  mla_status st = check_prefix(cfg, prefix_len);
+  if (st != MLA_OK) return st;
+  if (num_pages <= 0) return invalid("num_pages must be positive");
+  if (prefix_len == 0) return MLA_OK;
+  if (!W_UK || !W_UV || !cache || !prefix_pages || !keys || !values || !k_pe)
+    return invalid("null pointer");
+  PrefixExpandParams p;
+  p.W_UK = W_UK;
+  p.W_UV = W_UV;
+  p.cache = cache;
+  p.table = prefix_pages;
+  p.num_pages = num_pages;
+  p.L = prefix_len;
+  p.H = cfg->num_heads;
+  p.d_c = cfg->d_latent;
+  p.d_r = cfg->d_rope;
+  p.d_n = cfg->d_nope;
+  p.d_v = cfg->d_v;
+  p.P = cfg->page_size;
+  p.row_bytes = (long long)cache_row_bytes(cfg);
+  p.cache_scale = code_scale_of(cfg);
+  p.keys = keys;
+  p.values = values;
+  p.k_pe = k_pe;
+  p.status = dev_status;
+  cudaError_t e = launch_prefix_expand_simt(cfg->act_dtype, cfg->cache_dtype, p, (cudaStream_t)stream);
+  return e == cudaSuccess ? MLA_OK : cuda_fail(e, "mla_prefix_expand");
+}
+
+mla_status mla_prefix_attend_workspace_size(const mla_config* cfg, int batch, int q_len,
+                                            int prefix_len, size_t* bytes) {
+  mla_status st = check_decode_shape(cfg, batch, q_len);
+  if (st == MLA_OK) st = check_prefix(cfg, prefix_len);
+  if (st != MLA_OK) return st;
+  if (!bytes) return invalid("bytes is NULL");
+  *bytes = 0;
+  return MLA_OK;
+}
+
+mla_status mla_prefix_attend(const mla_config* cfg, const void* q_nope, const void* q_pe,
+                             const void* keys, const void* values, const void* k_pe, int prefix_len,
+                             const int32_t* seq_lens, int batch, int q_len, void* u, float* lse,
+                             void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                             void* stream) {
+  size_t need = 0;
+  mla_status st = mla_prefix_attend_workspace_size(cfg, batch, q_len, prefix_len, &need);
+  if (st != MLA_OK) return st;
+  if (!q_nope || !q_pe || !seq_lens || !u || !lse || (prefix_len > 0 && (!keys || !values || !k_pe)))
+    return invalid("null pointer");
+  if (need > 0 && (!workspace || workspace_bytes < need)) {
+    g_last_error = "workspace smaller than mla_prefix_attend_workspace_size";
+    return MLA_ERR_WORKSPACE;
+  }
+  if (need > 0 && ((uintptr_t)workspace & 255) != 0)
+    return invalid("workspace must be 256-byte aligned");
+  PrefixAttendParams p;
+  p.q_nope = q_nope;
+  p.q_pe = q_pe;
+  p.keys = keys;
+  p.values = values;
+  p.k_pe = k_pe;
+  p.seq_lens = seq_lens;
+  p.u = u;
+  p.lse = lse;
+  p.rows = batch * q_len;
+  p.q_len = q_len;
+  p.H = cfg->num_heads;
+  p.L = prefix_len;
+  p.d_n = cfg->d_nope;
+  p.d_r = cfg->d_rope;
+  p.d_v = cfg->d_v;
+  p.scale_log2 = softmax_scale_of(cfg) * kLog2e;
+  p.tt = turn_table(cfg);
+  p.status = dev_status;
+  cudaError_t e = launch_prefix_attend_simt(cfg->act_dtype, p, (cudaStream_t)stream);
+  return e == cudaSuccess ? MLA_OK : cuda_fail(e, "mla_prefix_attend");
+}
+
+mla_status mla_key_weights(const mla_config* cfg, const void* q_lat, const float* lse,
+                           const void* cache, int num_pages, const int32_t* block_table,
+                           int max_pages, const int32_t* seq_lens, int batch, int q_len, float decay,
+                           float* weights, int32_t* dev_status, void* stream) {
+  mla_status st = check_decode_shape(cfg, batch, q_len);
+  if (st != MLA_OK) return st;
+  if (!q_lat || !lse || !cache || !block_table || !seq_lens || !weights) return invalid("null pointer");
+  if (num_pages <= 0 || max_pages <= 0) return invalid("num_pages and max_pages must be positive");
+  if (!(decay >= 0.f && decay <= 1.f)) return invalid("decay must be in [0, 1]");
+  if ((long long)batch * max_pages > 0x7FFFFFFFLL) return unsupported("batch * max_pages above 2^31 - 1");
+  if ((long long)max_pages * cfg->page_size > 0x7FFFFFFFLL)
+    return unsupported("max_pages * page_size above 2^31 - 1");
+  KeyWeightParams p;
+  p.q_lat = q_lat;
+  p.lse = lse;
+  p.cache = cache;
+  p.block_table = block_table;
+  p.seq_lens = seq_lens;
+  p.max_pages = max_pages;
+  p.num_pages = num_pages;
+  p.batch = batch;
+  p.q_len = q_len;
+  p.H = cfg->num_heads;
+  p.d_c = cfg->d_latent;
+  p.D = cfg->d_latent + cfg->d_rope;
+  p.P = cfg->page_size;
+  p.row_bytes = (long long)cache_row_bytes(cfg);
+  p.scale_log2 = softmax_scale_of(cfg) * code_scale_of(cfg) * kLog2e;
+  p.decay = decay;
+  p.weights = weights;
+  p.status = dev_status;
+  cudaError_t e = launch_key_weights_simt(cfg->act_dtype, cfg->cache_dtype, p, (cudaStream_t)stream);
+  return e == cudaSuccess ? MLA_OK : cuda_fail(e, "mla_key_weights");
+}
+
+mla_status mla_evict_cache(const mla_config* cfg, const float* weights, const int32_t* seq_lens,
+                           const int32_t* block_table, int max_pages, int batch, int budget,
+                           int sinks, int recent, int rotate, void* cache, int num_pages,
+                           const int32_t* new_block_table, int new_max_pages, float* new_weights,
+                           int32_t* kept, int32_t* new_seq_lens, int32_t* dev_status, void* stream) {
+  mla_status st = check_config(cfg);
+  if (st != MLA_OK) return st;
+  if (batch <= 0 || batch > 32768) return invalid("batch must be in [1, 32768]");
+  if (max_pages <= 0 || new_max_pages <= 0 || num_pages <= 0)
+    return invalid("max_pages, new_max_pages and num_pages must be positive");
+  if (budget <= 0) return invalid("budget must be positive");
+  if (sinks < 0 || recent < 0 || (long long)sinks + recent > budget)
+    return invalid("sinks and recent must be >= 0 and fit the budget");
+  if (!weights || !seq_lens || !block_table || !cache || !new_block_table || !kept || !new_seq_lens)
+    return invalid("null pointer");
+  if (new_block_table == block_table && new_max_pages != max_pages)
+    return invalid("in place (new_block_table == block_table) new_max_pages must be max_pages");
+  if (new_weights == weights && new_max_pages != max_pages)
+    return invalid("new_weights may be weights only if new_max_pages is max_pages");
+  if ((long long)max_pages * cfg->page_size > kEvictMaxKeys)
+    return unsupported("max_pages * page_size above 393216 tokens");
+  if ((long long)num_pages * cfg->page_size > 0x7FFFFFFFLL)
+    return unsupported("num_pages * page_size above 2^31 - 1");
+  if (((uintptr_t)cache & (cfg->cache_dtype == MLA_F32 ? 15 : 3)) != 0)
+    return invalid("cache must be 16-byte aligned (fp32) or 4-byte aligned");
+  EvictParams p;
+  p.weights = weights;
+  p.seq_lens = seq_lens;
+  p.block_table = block_table;
+  p.new_block_table = new_block_table;
+  p.max_pages = max_pages;
+  p.new_max_pages = new_max_pages;
+  p.num_pages = num_pages;
+  p.batch = batch;
+  p.budget = budget;
+  p.sinks = sinks;
+  p.recent = recent;
+  p.rotate = rotate ? 1 : 0;
+  p.P = cfg->page_size;
+  p.d_c = cfg->d_latent;
+  p.d_r = cfg->d_rope;
+  p.row_bytes = (long long)cache_row_bytes(cfg);
+  p.cache = cache;
+  p.new_weights = new_weights;
+  p.kept = kept;
+  p.new_seq_lens = new_seq_lens;
+  p.tt = turn_table(cfg);
+  p.status = dev_status;
+  cudaError_t e = launch_evict(cfg->cache_dtype, p, (cudaStream_t)stream);
+  return e == cudaSuccess ? MLA_OK : cuda_fail(e, "mla_evict_cache");
 }
 
 mla_status mla_read_device_status(const void* status_word, void* stream, int* code) {

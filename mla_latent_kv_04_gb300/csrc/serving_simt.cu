@@ -1,0 +1,274 @@
+// SIMT kernels of the shared-prefix and key-weight calls: every activation and cache format
+// and every head shape, fp32 sums. The tensor-core kernels (prefix_tc.cu, key_weights_tc.cu)
+// take the DeepSeek-V2 head shape in bf16; these serve the rest and cross-check them.
+#include <math.h>
+
+#include "internal.h"
+#include "page_elem.cuh"
+
+namespace mla {
+namespace {
+
+// ======================================================================== prefix expansion
+// keys[h][l] = c_l W_UK[:, h], values[h][l] = c_l W_UV[:, h] (huny.dev "DeepSeek MLA 해부"
+// §2-1: k^C = c W^UK, v^C = c W^UV). 64 x 64 output tile per block; z = 0 keys, 1 values.
+template <typename AT, typename CT>
+__global__ void __launch_bounds__(256) expand_simt_kernel(PrefixExpandParams p) {
+  __shared__ float As[16][64 + 4], Bs[16][64 + 4];
+  const int dh = blockIdx.z ? p.d_v : p.d_n;
+  const int N = p.H * dh;
+  const int n0 = blockIdx.x * 64, l0 = blockIdx.y * 64;
+  if (n0 >= N) return;
+  const AT* W = reinterpret_cast<const AT*>(blockIdx.z ? p.W_UV : p.W_UK);
+  AT* out = reinterpret_cast<AT*>(blockIdx.z ? p.values : p.keys);
+  const int tid = threadIdx.x, tx = tid % 16, ty = tid / 16;
+  float acc[4][4] = {};
+  for (int k0 = 0; k0 < p.d_c; k0 += 16) {
+    for (int i = tid; i < 64 * 16; i += 256) {
+      const int r = i / 16, k = k0 + i % 16, l = l0 + r;
+      float v = 0.f;
+      if (l < p.L && k < p.d_c) {
+        const int page = p.table[l / p.P];
+        if (page >= 0 && page < p.num_pages) {
+          const uint8_t* row = reinterpret_cast<const uint8_t*>(p.cache) +
+                               ((long long)page * p.P + l % p.P) * p.row_bytes;
+          v = PageElem<CT>::get(reinterpret_cast<const uint32_t*>(row), k, p.d_c);
+        } else if (i % 16 == 0 && k0 == 0 && l % p.P == 0) {
+          flag_status(p.status, MLA_ERR_DEVICE_GUARD);
+        }
+      }
+      As[i % 16][r] = v;
+    }
+    for (int i = tid; i < 16 * 64; i += 256) {
+      const int k = k0 + i / 64, n = n0 + i % 64;
+      Bs[i / 64][i % 64] = (k < p.d_c && n < N) ? to_f32(W[(long long)k * N + n]) : 0.f;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int kk = 0; kk < 16; ++kk) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(As[kk][ty * 4 + i], Bs[kk][tx * 4 + j], acc[i][j]);
+    }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int l = l0 + ty * 4 + i;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int n = n0 + tx * 4 + j;
+      if (l < p.L && n < N)
+        out[((long long)(n / dh) * p.L + l) * dh + n % dh] = from_f32<AT>(acc[i][j] * p.cache_scale);
+    }
+  }
+}
+
+// k_pe[l] = the cache's rotated key of token l, in the activation type. Block per token.
+template <typename AT, typename CT>
+__global__ void __launch_bounds__(64) expand_rope_kernel(PrefixExpandParams p) {
+  const int l = blockIdx.x;
+  const int page = p.table[l / p.P];
+  const bool ok = page >= 0 && page < p.num_pages;
+  if (!ok && threadIdx.x == 0) flag_status(p.status, MLA_ERR_DEVICE_GUARD);
+  const uint32_t* row = reinterpret_cast<const uint32_t*>(
+      reinterpret_cast<const uint8_t*>(p.cache) + ((long long)(ok ? page : 0) * p.P + l % p.P) * p.row_bytes);
+  AT* out = reinterpret_cast<AT*>(p.k_pe) + (long long)l * p.d_r;
+  for (int k = threadIdx.x; k < p.d_r; k += blockDim.x)
+    out[k] = from_f32<AT>(ok ? page_rope_elem<CT>(row, k, p.d_c) * p.cache_scale : 0.f);
+}
+
+// ======================================================================== prefix attention
+// Block per (query row, head): 128 keys at a time, one per thread, with the running maximum
+// and sum of the softmax; the output's dims over the threads.
+template <typename AT>
+__global__ void __launch_bounds__(128) attend_simt_kernel(PrefixAttendParams p) {
+  extern __shared__ float sm[];
+  float* q = sm;                               // [d_n + d_r]
+  float* o = q + p.d_n + p.d_r;                // [d_v]
+  __shared__ float ps[128], red[4];
+  const int r = blockIdx.x, h = blockIdx.y, tid = threadIdx.x;
+  const int S = p.seq_lens[r / p.q_len];
+  AT* out = reinterpret_cast<AT*>(p.u) + ((long long)r * p.H + h) * p.d_v;
+  float* lse = p.lse + (long long)r * p.H + h;
+  if (S < p.q_len || p.L == 0) {               // an empty request (or a bad length): no keys
+    if (S != 0 && S < p.q_len && h == 0 && tid == 0) flag_status(p.status, MLA_ERR_DEVICE_GUARD);
+    for (int v = tid; v < p.d_v; v += 128) out[v] = from_f32<AT>(0.f);
+    if (tid == 0) *lse = -INFINITY;
+    return;
+  }
+  const long long pos = (long long)p.L + S - p.q_len + r % p.q_len;
+  const AT* qn = reinterpret_cast<const AT*>(p.q_nope) + ((long long)r * p.H + h) * p.d_n;
+  const AT* qr = reinterpret_cast<const AT*>(p.q_pe) + ((long long)r * p.H + h) * p.d_r;
+  for (int i = tid; i < p.d_n; i += 128) q[i] = to_f32(qn[i]);
+  for (int k = tid; k < p.d_r / 2; k += 128) {
+    float sn, cs;
+    turn_sincos<sizeof(AT) == 4>(p.tt, k, pos, &sn, &cs);
+    const float x0 = to_f32(qr[2 * k]), x1 = to_f32(qr[2 * k + 1]);
+    q[p.d_n + 2 * k] = x0 * cs - x1 * sn;
+    q[p.d_n + 2 * k + 1] = x0 * sn + x1 * cs;
+  }
+  for (int v = tid; v < p.d_v; v += 128) o[v] = 0.f;
+  __syncthreads();
+  const AT* K = reinterpret_cast<const AT*>(p.keys) + (long long)h * p.L * p.d_n;
+  const AT* V = reinterpret_cast<const AT*>(p.values) + (long long)h * p.L * p.d_v;
+  const AT* kp = reinterpret_cast<const AT*>(p.k_pe);
+  float m = -INFINITY, l = 0.f;
+  for (int l0 = 0; l0 < p.L; l0 += 128) {
+    const int j = l0 + tid;
+    float s = -INFINITY;
+    if (j < p.L) {
+      float acc = 0.f;
+      for (int i = 0; i < p.d_n; ++i) acc = fmaf(q[i], to_f32(K[(long long)j * p.d_n + i]), acc);
+      for (int i = 0; i < p.d_r; ++i) acc = fmaf(q[p.d_n + i], to_f32(kp[(long long)j * p.d_r + i]), acc);
+      s = acc * p.scale_log2;
+    }
+    const float wm = warp_max(s);
+    __syncthreads();
+    if ((tid & 31) == 0) red[tid >> 5] = wm;
+    __syncthreads();
+    const float m_new = fmaxf(m, fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])));
+    // no finite score so far (all -inf): keep the sums at zero
+    const float ref = m_new == -INFINITY ? 0.f : m_new;
+    const float a = exp2f(m - ref), e = exp2f(s - ref);
+    ps[tid] = e;
+    const float ws = warp_sum(e);
+    __syncthreads();
+    if ((tid & 31) == 0) red[tid >> 5] = ws;
+    __syncthreads();
+    l = l * a + ((red[0] + red[1]) + (red[2] + red[3]));
+    const int n = min(128, p.L - l0);
+    for (int v = tid; v < p.d_v; v += 128) {
+      float acc = o[v] * a;
+      for (int i = 0; i < n; ++i) acc = fmaf(ps[i], to_f32(V[(long long)(l0 + i) * p.d_v + v]), acc);
+      o[v] = acc;
+    }
+    m = m_new;
+  }
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  for (int v = tid; v < p.d_v; v += 128) out[v] = from_f32<AT>(o[v] * inv);
+  if (tid == 0) *lse = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+}
+
+// ======================================================================== key weights
+// Block per (request, page): the page's rows in shared memory (odd word stride), one head's
+// query per warp at a time, two tokens per lane; the warps' sums meet in warp order.
+template <typename AT, typename CT>
+__global__ void __launch_bounds__(256) key_weights_simt_kernel(KeyWeightParams p) {
+  extern __shared__ __align__(16) uint32_t smem_kw[];
+  const int row_words = (int)(p.row_bytes / 4), stride = row_words | 1;
+  uint32_t* page_s = smem_kw;                                     // [P][stride]
+  float* q_s = reinterpret_cast<float*>(smem_kw + p.P * stride);   // [8][D]
+  float* red = q_s + 8 * p.D;                                     // [8][P]
+  const int b = blockIdx.x / p.max_pages, pg = blockIdx.x % p.max_pages;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int S = p.seq_lens[b];
+  if (S == 0) return;
+  if (S < p.q_len || S > (long long)p.max_pages * p.P) {
+    if (pg == 0 && threadIdx.x == 0) flag_status(p.status, MLA_ERR_DEVICE_GUARD);
+    return;
+  }
+  if ((long long)pg * p.P >= S) return;
+  const int page = p.block_table[(long long)b * p.max_pages + pg];
+  if (page < 0 || page >= p.num_pages) {
+    if (threadIdx.x == 0) flag_status(p.status, MLA_ERR_DEVICE_GUARD);
+    return;
+  }
+  const int ntok = min(p.P, S - pg * p.P);
+  const uint32_t* src = reinterpret_cast<const uint32_t*>(reinterpret_cast<const uint8_t*>(p.cache) +
+                                                          (long long)page * p.P * p.row_bytes);
+  for (int i = threadIdx.x; i < ntok * row_words; i += blockDim.x)
+    page_s[(i / row_words) * stride + i % row_words] = src[i];
+  __syncthreads();
+  float* q = q_s + warp * p.D;
+  float w0 = 0.f, w1 = 0.f;
+  for (int t = 0; t < p.q_len; ++t) {
+    const int last = S - p.q_len + t - pg * p.P;       // this query token sees tokens 0..last
+    const long long g = (long long)b * p.q_len + t;
+    for (int h = warp; h < p.H; h += 8) {
+      const AT* ql = reinterpret_cast<const AT*>(p.q_lat) + (g * p.H + h) * p.D;
+      __syncwarp();
+      for (int i = lane; i < p.D; i += 32) q[i] = to_f32(ql[i]);
+      __syncwarp();
+      const float off = p.lse[g * p.H + h] * kLog2e;
+      if (lane < ntok && lane <= last)
+        w0 += exp2f(PageElem<CT>::dot(page_s + lane * stride, q, p.D, p.d_c) * p.scale_log2 - off);
+      if (lane + 32 < ntok && lane + 32 <= last)
+        w1 += exp2f(PageElem<CT>::dot(page_s + (lane + 32) * stride, q, p.D, p.d_c) * p.scale_log2 - off);
+    }
+  }
+  if (lane < p.P) red[warp * p.P + lane] = w0;
+  if (lane + 32 < p.P) red[warp * p.P + lane + 32] = w1;
+  __syncthreads();
+  for (int i = threadIdx.x; i < ntok; i += blockDim.x) {
+    float mass = 0.f;
+    for (int w = 0; w < 8; ++w) mass += red[w * p.P + i];
+    const int j = pg * p.P + i;
+    float* dst = p.weights + (long long)b * p.max_pages * p.P + j;
+    // a token of this step has no earlier weight
+    *dst = (p.decay != 0.f && j < S - p.q_len) ? fmaf(p.decay, *dst, mass) : mass;
+  }
+}
+
+// A cache format's tag type, and the call f(tag of the activations, tag of the cache).
+template <typename F>
+cudaError_t by_format(mla_dtype act, mla_dtype cache, F f) {
+  if (act == MLA_F32) return f(float{}, float{});
+  if (cache == MLA_BF16) return f(bf16{}, bf16{});
+  if (cache == MLA_FP8_E4M3) return f(bf16{}, uint8_t{});
+  return f(bf16{}, E4m3B128{});
+}
+
+template <typename K>
+cudaError_t allow_smem(K kern, size_t bytes) {
+  if (bytes <= 48 * 1024) return cudaSuccess;
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+
+}  // namespace
+
+cudaError_t launch_prefix_expand_simt(mla_dtype act, mla_dtype cache, const PrefixExpandParams& p,
+                                      cudaStream_t s) {
+  if (p.L <= 0) return cudaSuccess;
+  return by_format(act, cache, [&](auto a, auto c) {
+    using AT = decltype(a);
+    using CT = decltype(c);
+    const int cols = p.H * (p.d_n > p.d_v ? p.d_n : p.d_v);
+    // one launch covers 65535 x 64 tokens
+    expand_simt_kernel<AT, CT><<<dim3((cols + 63) / 64, (p.L + 63) / 64, 2), 256, 0, s>>>(p);
+    note_launch();
+    expand_rope_kernel<AT, CT><<<p.L, 64, 0, s>>>(p);
+    note_launch();
+    return cudaGetLastError();
+  });
+}
+
+cudaError_t launch_prefix_attend_simt(mla_dtype act, const PrefixAttendParams& p, cudaStream_t s) {
+  const size_t smem = (size_t)(p.d_n + p.d_r + p.d_v) * 4;
+  auto go = [&](auto a) {
+    using AT = decltype(a);
+    cudaError_t e = allow_smem(attend_simt_kernel<AT>, smem);
+    if (e != cudaSuccess) return e;
+    attend_simt_kernel<AT><<<dim3(p.rows, p.H), 128, smem, s>>>(p);
+    note_launch();
+    return cudaGetLastError();
+  };
+  return act == MLA_F32 ? go(float{}) : go(bf16{});
+}
+
+cudaError_t launch_key_weights_simt(mla_dtype act, mla_dtype cache, const KeyWeightParams& p,
+                                    cudaStream_t s) {
+  const size_t smem = ((size_t)p.P * ((p.row_bytes / 4) | 1) + 8ull * p.D + 8ull * p.P) * 4;
+  return by_format(act, cache, [&](auto a, auto c) {
+    using AT = decltype(a);
+    using CT = decltype(c);
+    cudaError_t e = allow_smem(key_weights_simt_kernel<AT, CT>, smem);
+    if (e != cudaSuccess) return e;
+    key_weights_simt_kernel<AT, CT><<<(unsigned)((long long)p.batch * p.max_pages), 256, smem, s>>>(p);
+    note_launch();
+    return cudaGetLastError();
+  });
+}
+
+}  // namespace mla
