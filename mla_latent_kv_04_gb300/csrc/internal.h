@@ -212,6 +212,11 @@ struct PrefixAttendParams {
 };
 cudaError_t launch_prefix_attend_simt(mla_dtype act, const PrefixAttendParams& p, cudaStream_t s);
 
+// The tensor-core form (bf16, d_n 128, d_r 64, d_v 128) and its workspace (fp32 pieces).
+bool prefix_attend_tc_supported(const mla_config* c);
+size_t prefix_attend_tc_workspace(int rows, int H, int L);
+cudaError_t launch_prefix_attend_tc(const PrefixAttendParams& p, void* workspace, cudaStream_t s);
+
 struct KeyWeightParams {
   const void* q_lat;          // [batch * q_len][H][D]
   const float* lse;           // [batch * q_len][H], natural log

@@ -696,7 +696,9 @@ mla_status mla_prefix_attend_workspace_size(const mla_config* cfg, int batch, in
   if (st == MLA_OK) st = check_prefix(cfg, prefix_len);
   if (st != MLA_OK) return st;
   if (!bytes) return invalid("bytes is NULL");
-  *bytes = 0;
+  *bytes = prefix_attend_tc_supported(cfg)
+               ? prefix_attend_tc_workspace(batch * q_len, cfg->num_heads, prefix_len)
+               : 0;
   return MLA_OK;
 }
 
@@ -735,7 +737,9 @@ mla_status mla_prefix_attend(const mla_config* cfg, const void* q_nope, const vo
   p.scale_log2 = softmax_scale_of(cfg) * kLog2e;
   p.tt = turn_table(cfg);
   p.status = dev_status;
-  cudaError_t e = launch_prefix_attend_simt(cfg->act_dtype, p, (cudaStream_t)stream);
+  cudaError_t e = prefix_attend_tc_supported(cfg) && prefix_len > 0
+                      ? launch_prefix_attend_tc(p, workspace, (cudaStream_t)stream)
+                      : launch_prefix_attend_simt(cfg->act_dtype, p, (cudaStream_t)stream);
   return e == cudaSuccess ? MLA_OK : cuda_fail(e, "mla_prefix_attend");
 }
 
