@@ -196,6 +196,10 @@ struct PrefixExpandParams {
 cudaError_t launch_prefix_expand_simt(mla_dtype act, mla_dtype cache, const PrefixExpandParams& p,
                                       cudaStream_t s);
 
+// The tensor-core form: bf16 activations, 64-token pages, DeepSeek-V2 head shape, any cache.
+bool prefix_expand_tc_supported(const mla_config* c, long long num_pages);
+cudaError_t launch_prefix_expand_tc(mla_dtype cache, const PrefixExpandParams& p, cudaStream_t s);
+
 struct PrefixAttendParams {
   const void* q_nope;         // [rows][H][d_n], row b * q_len + t
   const void* q_pe;           // [rows][H][d_r], not rotated
