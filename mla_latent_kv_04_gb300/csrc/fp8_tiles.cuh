@@ -16,15 +16,16 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&b);
 }
 
-// One token row of a 64-dim chunk: the codes, in a tile of 64-byte rows with the 64-byte
+// Half a token row (32 dims, half 0 or 1) of a 64-dim chunk: the codes, in a tile of 64-byte rows with the 64-byte
 // swizzle, times `scale` as bf16 into a tile of 128-byte rows with the 128-byte swizzle. With
 // `lo`, what the rounding left over goes to that second tile as another bf16 (the two add up
 // to the product within 2^-17 of it). Without a scale (scale == 1) the codes are exact.
 template <bool kScaled, bool kLow>
-__device__ __forceinline__ void expand_codes_row(const uint8_t* codes, uint8_t* hi, uint8_t* lo, int row,
-                                                 float scale) {
+__device__ __forceinline__ void expand_codes_half_row(const uint8_t* codes, uint8_t* hi, uint8_t* lo,
+                                                      int row, int half, float scale) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int ii = 0; ii < 2; ++ii) {
+    const int i = 2 * half + ii;
     const uint4 c = *reinterpret_cast<const uint4*>(codes + row * 64 + ((i ^ ((row >> 1) & 3)) << 4));
     const uint32_t w[4] = {c.x, c.y, c.z, c.w};
     uint32_t h[8], l[8];

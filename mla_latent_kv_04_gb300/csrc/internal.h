@@ -237,9 +237,10 @@ struct KeyWeightParams {
 cudaError_t launch_key_weights_simt(mla_dtype act, mla_dtype cache, const KeyWeightParams& p,
                                     cudaStream_t s);
 
-// The tensor-core form: bf16 cache, 64-token pages, d_c 512, d_r 64, 16 to 128 heads by 16.
-bool key_weights_tc_supported(const mla_config* c);
-cudaError_t launch_key_weights_tc(const KeyWeightParams& p, cudaStream_t s);
+// The tensor-core form: bf16 activations, any cache, 64-token pages, d_c 512, d_r 64, 16 to 128
+// heads by 16.
+bool key_weights_tc_supported(const mla_config* c, long long num_pages);
+cudaError_t launch_key_weights_tc(mla_dtype cache, const KeyWeightParams& p, cudaStream_t s);
 
 struct EvictParams {
   const float* weights;       // [batch][max_pages * P]

@@ -776,8 +776,8 @@ mla_status mla_key_weights(const mla_config* cfg, const void* q_lat, const float
   p.decay = decay;
   p.weights = weights;
   p.status = dev_status;
-  cudaError_t e = key_weights_tc_supported(cfg)
-                      ? launch_key_weights_tc(p, (cudaStream_t)stream)
+  cudaError_t e = key_weights_tc_supported(cfg, num_pages)
+                      ? launch_key_weights_tc(cfg->cache_dtype, p, (cudaStream_t)stream)
                       : launch_key_weights_simt(cfg->act_dtype, cfg->cache_dtype, p, (cudaStream_t)stream);
   return e == cudaSuccess ? MLA_OK : cuda_fail(e, "mla_key_weights");
 }
