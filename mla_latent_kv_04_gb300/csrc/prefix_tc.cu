@@ -112,122 +112,131 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto wait = [&](int i, uint32_t parity) { return bounded_wait(bar(i), parity, abort, p.status); };
   Segments seg(work, blockIdx.x);
 
-  if (warp == 0) {
-    if (lane == 0) {                               // keys
-      const uint64_t pol = ptx::l2_policy_evict_first();
-      const bool once = work.row_tiles == 1;       // each key is read by one tile
-      uint32_t g = 0;
-      while (seg.next()) {
-        const int h = seg.tile / work.row_tiles;
-        bool ok = true;
-        for (int kb = seg.k0; kb < seg.k1 && (ok = wait(B_KEMPTY + (g & 1), ((g >> 1) & 1) ^ 1)); ++kb, ++g) {
-          const uint32_t st = base + kOffK + (g & 1) * 3 * kBox, full = bar(B_KFULL + (g & 1));
-          ptx::mbar_arrive_expect_tx(full, 3 * kBox);
-          if (once) {
-            ptx::tma_load_3d_hint(st, &tm_k, 0, kb * kBN, h, full, pol);
-            ptx::tma_load_3d_hint(st + kBox, &tm_k, 64, kb * kBN, h, full, pol);
-          } else {
-            ptx::tma_load_3d(st, &tm_k, 0, kb * kBN, h, full);
-            ptx::tma_load_3d(st + kBox, &tm_k, 64, kb * kBN, h, full);
+  // registers: the softmax warps hold a row of scores (launched with 168 x 384; 88 x 128 + 200 x
+  // 256 = 62464 of the 64512 after the split)
+  if (warp < 4) {
+    ptx::setmaxnreg_dec<88>();
+    if (warp == 0) {
+      if (lane == 0) {                               // keys
+        const uint64_t pol = ptx::l2_policy_evict_first();
+        const bool once = work.row_tiles == 1;       // each key is read by one tile
+        uint32_t g = 0;
+        while (seg.next()) {
+          const int h = seg.tile / work.row_tiles;
+          bool ok = true;
+          for (int kb = seg.k0; kb < seg.k1 && (ok = wait(B_KEMPTY + (g & 1), ((g >> 1) & 1) ^ 1)); ++kb, ++g) {
+            const uint32_t st = base + kOffK + (g & 1) * 3 * kBox, full = bar(B_KFULL + (g & 1));
+            ptx::mbar_arrive_expect_tx(full, 3 * kBox);
+            if (once) {
+              ptx::tma_load_3d_hint(st, &tm_k, 0, kb * kBN, h, full, pol);
+              ptx::tma_load_3d_hint(st + kBox, &tm_k, 64, kb * kBN, h, full, pol);
+            } else {
+              ptx::tma_load_3d(st, &tm_k, 0, kb * kBN, h, full);
+              ptx::tma_load_3d(st + kBox, &tm_k, 64, kb * kBN, h, full);
+            }
+            ptx::tma_load_3d(st + 2 * kBox, &tm_pe, 0, kb * kBN, 0, full);
           }
-          ptx::tma_load_3d(st + 2 * kBox, &tm_pe, 0, kb * kBN, 0, full);
+          if (!ok) break;
         }
-        if (!ok) break;
+        if (*abort)
+          for (uint32_t i = g > 2 ? g - 2 : 0; i < g; ++i) drain_wait(bar(B_KFULL + (i & 1)), (i >> 1) & 1);
       }
-      if (*abort)
-        for (uint32_t i = g > 2 ? g - 2 : 0; i < g; ++i) drain_wait(bar(B_KFULL + (i & 1)), (i >> 1) & 1);
-    }
-  } else if (warp == 3) {
-    if (lane == 0) {                               // values
-      const uint64_t pol = ptx::l2_policy_evict_first();
-      const bool once = work.row_tiles == 1;
-      uint32_t g = 0;
-      while (seg.next()) {
-        const int h = seg.tile / work.row_tiles;
-        bool ok = true;
-        for (int kb = seg.k0; kb < seg.k1 && (ok = wait(B_VEMPTY + (g & 1), ((g >> 1) & 1) ^ 1)); ++kb, ++g) {
-          const uint32_t st = base + kOffV + (g & 1) * 2 * kBox, full = bar(B_VFULL + (g & 1));
-          ptx::mbar_arrive_expect_tx(full, 2 * kBox);
-          if (once) {
-            ptx::tma_load_3d_hint(st, &tm_v, 0, kb * kBN, h, full, pol);
-            ptx::tma_load_3d_hint(st + kBox, &tm_v, 64, kb * kBN, h, full, pol);
-          } else {
-            ptx::tma_load_3d(st, &tm_v, 0, kb * kBN, h, full);
-            ptx::tma_load_3d(st + kBox, &tm_v, 64, kb * kBN, h, full);
+    } else if (warp == 3) {
+      if (lane == 0) {                               // values
+        const uint64_t pol = ptx::l2_policy_evict_first();
+        const bool once = work.row_tiles == 1;
+        uint32_t g = 0;
+        while (seg.next()) {
+          const int h = seg.tile / work.row_tiles;
+          bool ok = true;
+          for (int kb = seg.k0; kb < seg.k1 && (ok = wait(B_VEMPTY + (g & 1), ((g >> 1) & 1) ^ 1)); ++kb, ++g) {
+            const uint32_t st = base + kOffV + (g & 1) * 2 * kBox, full = bar(B_VFULL + (g & 1));
+            ptx::mbar_arrive_expect_tx(full, 2 * kBox);
+            if (once) {
+              ptx::tma_load_3d_hint(st, &tm_v, 0, kb * kBN, h, full, pol);
+              ptx::tma_load_3d_hint(st + kBox, &tm_v, 64, kb * kBN, h, full, pol);
+            } else {
+              ptx::tma_load_3d(st, &tm_v, 0, kb * kBN, h, full);
+              ptx::tma_load_3d(st + kBox, &tm_v, 64, kb * kBN, h, full);
+            }
           }
+          if (!ok) break;
         }
-        if (!ok) break;
+        if (*abort)
+          for (uint32_t i = g > 2 ? g - 2 : 0; i < g; ++i) drain_wait(bar(B_VFULL + (i & 1)), (i >> 1) & 1);
       }
-      if (*abort)
-        for (uint32_t i = g > 2 ? g - 2 : 0; i < g; ++i) drain_wait(bar(B_VFULL + (i & 1)), (i >> 1) & 1);
-    }
-  } else if (warp == 2) {
-    if (lane == 0) {                               // the content part of the queries
-      uint32_t s = 0;
-      while (seg.next() && wait(B_QEMPTY, (s & 1) ^ 1)) {
-        const int h = seg.tile / work.row_tiles, r0 = seg.tile % work.row_tiles * kBM;
-        ptx::mbar_arrive_expect_tx(bar(B_QFULL), 2 * kBox);
-        ptx::tma_load_3d(base + kOffQ, &tm_q, 0, r0, h, bar(B_QFULL));
-        ptx::tma_load_3d(base + kOffQ + kBox, &tm_q, 64, r0, h, bar(B_QFULL));
-        ++s;
+    } else if (warp == 2) {
+      if (lane == 0) {                               // the content part of the queries
+        uint32_t s = 0;
+        while (seg.next() && wait(B_QEMPTY, (s & 1) ^ 1)) {
+          const int h = seg.tile / work.row_tiles, r0 = seg.tile % work.row_tiles * kBM;
+          ptx::mbar_arrive_expect_tx(bar(B_QFULL), 2 * kBox);
+          ptx::tma_load_3d(base + kOffQ, &tm_q, 0, r0, h, bar(B_QFULL));
+          ptx::tma_load_3d(base + kOffQ + kBox, &tm_q, 64, r0, h, bar(B_QFULL));
+          ++s;
+        }
+        // after an abort the rotary part may never arrive: this wait may run its full second
+        if (*abort && s) drain_wait(bar(B_QFULL), (s - 1) & 1);
       }
-      // after an abort the rotary part may never arrive: this wait may run its full second
-      if (*abort && s) drain_wait(bar(B_QFULL), (s - 1) & 1);
-    }
-  } else if (warp == 1) {
-    if (lane == 0) {                               // MMAs: S(n), then O(n - 1)
-      uint32_t gk = 0, gv = 0, s = 0, cnt[2] = {0, 0};
-      bool ok = true;
-      auto out = [&](int n) {                      // O(n) += P(n) V(n); n: block of the segment
-        const int w = n & 1;
-        if (!wait(B_PREADY + w, (cnt[w] - 1) & 1) || !wait(B_VFULL + (gv & 1), (gv >> 1) & 1)) return false;
-        ptx::tc_fence_after();
-        const uint32_t v = base + kOffV + (gv & 1) * 2 * kBox;
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          ptx::mma_bf16_ts(tmem + 256 + 128 * w, tmem + 128 * w + 8 * k,
-                           ptx::smem_desc(v + 2048 * k, kBox, 1024, ptx::kSwizzle128), kIdescO,
-                           (n >= 2 || k) ? 1u : 0u);
-        ptx::mma_commit(bar(B_VEMPTY + (gv & 1)));
-        ptx::mma_commit(bar(B_ODONE + w));
-        ++gv;
-        return true;
-      };
-      while (ok && seg.next()) {
-        ok = wait(B_QFULL, s & 1);
-        const int nb = seg.k1 - seg.k0;
-        for (int n = 0; ok && n < nb; ++n) {
-          if (!(ok = wait(B_KFULL + (gk & 1), (gk >> 1) & 1))) break;
+    } else if (warp == 1) {
+      if (lane == 0) {                               // MMAs: S(n), then O(n - 1)
+        uint32_t gk = 0, gv = 0, s = 0, cnt[2] = {0, 0};
+        bool ok = true;
+        auto out = [&](int n) {                      // O(n) += P(n) V(n); n: block of the segment
+          const int w = n & 1;
+          if (!wait(B_PREADY + w, (cnt[w] - 1) & 1) || !wait(B_VFULL + (gv & 1), (gv >> 1) & 1)) return false;
           ptx::tc_fence_after();
-          // S(n) overwrites S and P of block n - 2, whose product was issued before
-          const uint32_t q = base + kOffQ, k0 = base + kOffK + (gk & 1) * 3 * kBox;
+          uint32_t v = base + kOffV + (gv & 1) * 2 * kBox;
+          asm volatile("" : "+r"(v));
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const uint32_t kbox = j < 12 ? j >> 2 : 2;       // the low rotary term meets k_pe again
-            ptx::mma_bf16_ss(tmem + 128 * (n & 1),
-                             ptx::smem_desc(q + (j >> 2) * kBox + 32 * (j & 3), 16, 1024, ptx::kSwizzle128),
-                             ptx::smem_desc(k0 + kbox * kBox + 32 * (j & 3), 16, 1024, ptx::kSwizzle128),
-                             kIdescS, j ? 1u : 0u);
+          for (int k = 0; k < 8; ++k)
+            ptx::mma_bf16_ts(tmem + 256 + 128 * w, tmem + 128 * w + 8 * k,
+                             ptx::smem_desc(v + 2048 * k, kBox, 1024, ptx::kSwizzle128), kIdescO,
+                             (n >= 2 || k) ? 1u : 0u);
+          ptx::mma_commit(bar(B_VEMPTY + (gv & 1)));
+          ptx::mma_commit(bar(B_ODONE + w));
+          ++gv;
+          return true;
+        };
+        while (ok && seg.next()) {
+          ok = wait(B_QFULL, s & 1);
+          const int nb = seg.k1 - seg.k0;
+          for (int n = 0; ok && n < nb; ++n) {
+            if (!(ok = wait(B_KFULL + (gk & 1), (gk >> 1) & 1))) break;
+            ptx::tc_fence_after();
+            // S(n) overwrites S and P of block n - 2, whose product was issued before
+            uint32_t q = base + kOffQ, k0 = base + kOffK + (gk & 1) * 3 * kBox;
+            // (hides the loop-invariant part: 16 descriptors held in registers would spill)
+            asm volatile("" : "+r"(q), "+r"(k0));
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const uint32_t kbox = j < 12 ? j >> 2 : 2;       // the low rotary term meets k_pe again
+              ptx::mma_bf16_ss(tmem + 128 * (n & 1),
+                               ptx::smem_desc(q + (j >> 2) * kBox + 32 * (j & 3), 16, 1024, ptx::kSwizzle128),
+                               ptx::smem_desc(k0 + kbox * kBox + 32 * (j & 3), 16, 1024, ptx::kSwizzle128),
+                               kIdescS, j ? 1u : 0u);
+            }
+            ptx::mma_commit(bar(B_KEMPTY + (gk & 1)));
+            ptx::mma_commit(bar(B_SFULL + (n & 1)));
+            if (n == nb - 1) ptx::mma_commit(bar(B_QEMPTY));
+            ++cnt[n & 1];
+            ++gk;
+            if (n > 0) {
+              // P(n - 1): the count of its warpgroup has not moved since S(n - 1)
+              ok = out(n - 1);
+            }
           }
-          ptx::mma_commit(bar(B_KEMPTY + (gk & 1)));
-          ptx::mma_commit(bar(B_SFULL + (n & 1)));
-          if (n == nb - 1) ptx::mma_commit(bar(B_QEMPTY));
-          ++cnt[n & 1];
-          ++gk;
-          if (n > 0) {
-            // P(n - 1): the count of its warpgroup has not moved since S(n - 1)
-            ok = out(n - 1);
-          }
+          if (ok) ok = out(nb - 1);
+          ++s;
         }
-        if (ok) ok = out(nb - 1);
-        ++s;
-      }
-      if (*abort) {
-        ptx::mma_commit(bar(B_TEAR));
-        drain_wait(bar(B_TEAR), 0);
+        if (*abort) {
+          ptx::mma_commit(bar(B_TEAR));
+          drain_wait(bar(B_TEAR), 0);
+        }
       }
     }
   } else {
+    ptx::setmaxnreg_inc<200>();
     // softmax warpgroup w: thread = row of the tile = lane of tensor memory
     const int w = warp >= 8 ? 1 : 0, quad = warp & 3, row = 32 * quad + lane;
     const uint32_t t_lane = tmem + ((uint32_t)(32 * quad) << 16);
@@ -290,20 +299,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(ok = wait_w(B_SFULL + w, cnt & 1))) break;
         ptx::tc_fence_after();
         const int valid = min(kBN, p.L - (seg.k0 + n) * kBN);
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        // the whole row at once: one wait for tensor memory instead of one per 32 columns
+        uint32_t v[4][32];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint32_t v[32];
-          ptx::tmem_ld32(t_s + 32 * q, v);
-          ptx::tmem_wait_ld();
-          if (valid < kBN) {
+        for (int q = 0; q < 4; ++q) ptx::tmem_ld32(t_s + 32 * q, v[q]);
+        ptx::tmem_wait_ld();
+        if (valid < kBN) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-              if (32 * q + j >= valid) v[j] = 0xFF800000u;
-          }
-#pragma unroll
-          for (int j = 0; j < 32; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(v[j]));
+              if (32 * q + j >= valid) v[q][j] = 0xFF800000u;
         }
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int j = 0; j < 32; j += 2)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            mx[q] = fmaxf(mx[q], fmaxf(__uint_as_float(v[q][j]), __uint_as_float(v[q][j + 1])));
         const float mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
         if (n == w) {
           m = mb;
@@ -315,13 +328,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::tc_fence_after();
             const float a = grow ? (m == -INFINITY ? 0.f : ptx::ex2((m - mb) * c)) : 1.f;
 #pragma unroll 1
-            for (int q = 0; q < 4; ++q) {
-              uint32_t v[32];
-              ptx::tmem_ld32(t_o + 32 * q, v);
+            for (int q = 0; q < 8; ++q) {
+              uint32_t o[16];
+              ptx::tmem_ld16(t_o + 16 * q, o);
               ptx::tmem_wait_ld();
 #pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * a);
-              ptx::tmem_st32(t_o + 32 * q, v);
+              for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * a);
+              ptx::tmem_st16(t_o + 16 * q, o);
             }
             ptx::tmem_wait_st();
             l *= a;
@@ -332,23 +345,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          uint32_t v[32], pk[16];
-          ptx::tmem_ld32(t_s + 32 * q, v);
-          ptx::tmem_wait_ld();
+          uint32_t pk[16];
 #pragma unroll
           for (int j = 0; j < 32; j += 2) {
-            float e0 = ptx::ex2(fmaf(__uint_as_float(v[j]), c, -off));
-            float e1 = ptx::ex2(fmaf(__uint_as_float(v[j + 1]), c, -off));
-            if (valid < kBN) {
-              if (32 * q + j >= valid) e0 = 0.f;
-              if (32 * q + j + 1 >= valid) e1 = 0.f;
-            }
+            // columns behind the prefix hold -infinity: exp2 gives 0
+            const float e0 = ptx::ex2(fmaf(__uint_as_float(v[q][j]), c, -off));
+            const float e1 = ptx::ex2(fmaf(__uint_as_float(v[q][j + 1]), c, -off));
             sum[j & 2] += e0;
             sum[(j & 2) + 1] += e1;
             const __nv_bfloat162 b2 = __floats2bfloat162_rn(e0, e1);
             pk[j >> 1] = *reinterpret_cast<const uint32_t*>(&b2);
           }
-          // P's columns 16 q .. trail the scores still to be read (32 (q + 1) ..)
           ptx::tmem_st16(t_s + 16 * q, pk);
         }
         ptx::tmem_wait_st();
