@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort = reinterpret_cast<volatile int*>(basep + kOffBar + 240);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(basep + kOffBar + 244);
   auto bar = [&](int i) { return base + kOffBar + 8 * i; };
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < B_COUNT; ++i) {
       const bool p_ready = i == B_PREADY || i == B_PREADY + 1;
@@ -110,6 +110,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   auto wait = [&](int i, uint32_t parity) { return bounded_wait(bar(i), parity, abort, p.status); };
+  // a warp goes on, or gives up, as one
+  auto wait_w = [&](int i, uint32_t parity) { return __all_sync(0xffffffffu, wait(i, parity)) != 0; };
   Segments seg(work, blockIdx.x);
 
   // registers: the softmax warps hold a row of scores (launched with 168 x 384; 88 x 128 + 200 x
@@ -179,15 +181,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (*abort && s) drain_wait(bar(B_QFULL), (s - 1) & 1);
       }
     } else if (warp == 1) {
-      if (lane == 0) {                               // MMAs: S(n), then O(n - 1)
-        uint32_t gk = 0, gv = 0, s = 0, cnt[2] = {0, 0};
-        bool ok = true;
-        auto out = [&](int n) {                      // O(n) += P(n) V(n); n: block of the segment
-          const int w = n & 1;
-          if (!wait(B_PREADY + w, (cnt[w] - 1) & 1) || !wait(B_VFULL + (gv & 1), (gv >> 1) & 1)) return false;
-          ptx::tc_fence_after();
-          uint32_t v = base + kOffV + (gv & 1) * 2 * kBox;
-          asm volatile("" : "+r"(v));
+      // MMAs: S(n), then O(n - 1)
+      uint32_t gk = 0, gv = 0, s = 0, cnt[2] = {0, 0};
+      bool ok = true;
+      auto out = [&](int n) {                        // O(n) += P(n) V(n); n: block of the segment
+        const int w = n & 1;
+        if (!wait_w(B_PREADY + w, ((w ? cnt[1] : cnt[0]) - 1) & 1) || !wait_w(B_VFULL + (gv & 1), (gv >> 1) & 1))
+          return false;
+        ptx::tc_fence_after();
+        const uint32_t v = base + kOffV + (gv & 1) * 2 * kBox;
+        if (ptx::elect_one()) {
 #pragma unroll
           for (int k = 0; k < 8; ++k)
             ptx::mma_bf16_ts(tmem + 256 + 128 * w, tmem + 128 * w + 8 * k,
@@ -195,22 +198,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                              (n >= 2 || k) ? 1u : 0u);
           ptx::mma_commit(bar(B_VEMPTY + (gv & 1)));
           ptx::mma_commit(bar(B_ODONE + w));
-          ++gv;
-          return true;
-        };
-        while (ok && seg.next()) {
-          ok = wait(B_QFULL, s & 1);
-          const int nb = seg.k1 - seg.k0;
-          for (int n = 0; ok && n < nb; ++n) {
-            if (!(ok = wait(B_KFULL + (gk & 1), (gk >> 1) & 1))) break;
-            ptx::tc_fence_after();
-            // S(n) overwrites S and P of block n - 2, whose product was issued before
-            uint32_t q = base + kOffQ, k0 = base + kOffK + (gk & 1) * 3 * kBox;
-            // (hides the loop-invariant part: 16 descriptors held in registers would spill)
-            asm volatile("" : "+r"(q), "+r"(k0));
+        }
+        __syncwarp();
+        ++gv;
+        return true;
+      };
+      while (ok && seg.next()) {
+        ok = wait_w(B_QFULL, s & 1);
+        const int nb = seg.k1 - seg.k0;
+        for (int n = 0; ok && n < nb; ++n) {
+          if (!(ok = wait_w(B_KFULL + (gk & 1), (gk >> 1) & 1))) break;
+          ptx::tc_fence_after();
+          // S(n) overwrites S and P of block n - 2, whose product was issued before
+          const uint32_t q = base + kOffQ, k0 = base + kOffK + (gk & 1) * 3 * kBox;
+          if (ptx::elect_one()) {
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
-              const uint32_t kbox = j < 12 ? j >> 2 : 2;       // the low rotary term meets k_pe again
+              const uint32_t kbox = j < 12 ? j >> 2 : 2;     // the low rotary term meets k_pe again
               ptx::mma_bf16_ss(tmem + 128 * (n & 1),
                                ptx::smem_desc(q + (j >> 2) * kBox + 32 * (j & 3), 16, 1024, ptx::kSwizzle128),
                                ptx::smem_desc(k0 + kbox * kBox + 32 * (j & 3), 16, 1024, ptx::kSwizzle128),
@@ -219,20 +223,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::mma_commit(bar(B_KEMPTY + (gk & 1)));
             ptx::mma_commit(bar(B_SFULL + (n & 1)));
             if (n == nb - 1) ptx::mma_commit(bar(B_QEMPTY));
-            ++cnt[n & 1];
-            ++gk;
-            if (n > 0) {
-              // P(n - 1): the count of its warpgroup has not moved since S(n - 1)
-              ok = out(n - 1);
-            }
           }
-          if (ok) ok = out(nb - 1);
-          ++s;
+          __syncwarp();
+          if (n & 1) ++cnt[1];
+          else ++cnt[0];
+          ++gk;
+          // P(n - 1): the count of its warpgroup has not moved since S(n - 1)
+          if (n > 0) ok = out(n - 1);
         }
-        if (*abort) {
-          ptx::mma_commit(bar(B_TEAR));
-          drain_wait(bar(B_TEAR), 0);
-        }
+        if (ok) ok = out(nb - 1);
+        ++s;
+      }
+      if (*abort) {
+        if (ptx::elect_one()) ptx::mma_commit(bar(B_TEAR));
+        __syncwarp();
+        drain_wait(bar(B_TEAR), 0);
       }
     }
   } else {
@@ -245,8 +250,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     float2* xch = reinterpret_cast<float2*>(basep + kOffX);
     uint32_t cnt = 0, cnt_other = 0, s = 0, meets = 0;
     bool ok = true;
-    // tensor-memory accesses are warp-wide: a warp goes on, or leaves, as one
-    auto wait_w = [&](int i, uint32_t parity) { return __all_sync(0xffffffffu, wait(i, parity)) != 0; };
     // both warpgroups meet (bounded, unlike a named barrier)
     auto meet = [&]() {
       __syncwarp();
