@@ -118,6 +118,13 @@ TurnTable turn_table(const mla_config* c) {
   return tt;
 }
 
+// The tensor-core kernels of the prefix and key-weight calls read and write 16 bytes at a time; tensors that start
+// elsewhere (views into a larger allocation) go to the SIMT kernels.
+template <typename... P>
+bool aligned16(P... p) {
+  return ((reinterpret_cast<uintptr_t>(p) | ...) & 15) == 0;
+}
+
 int default_workers(const mla_config* c, const mla_decode_opts* o, bool tc) {
   if (o && o->num_workers > 0) return o->num_workers;
   const int sms = device_sm_count();
@@ -667,6 +674,7 @@ mla_status mla_prefix_expand(const mla_config* cfg, const void* W_UK, const void
   if (prefix_len == 0) return MLA_OK;
   if (!W_UK || !W_UV || !cache || !prefix_pages || !keys || !values || !k_pe)
     return invalid("null pointer");
+  if (((uintptr_t)cache & 3) != 0) return invalid("cache must be 4-byte aligned");
   PrefixExpandParams p;
   p.W_UK = W_UK;
   p.W_UV = W_UV;
@@ -686,7 +694,7 @@ mla_status mla_prefix_expand(const mla_config* cfg, const void* W_UK, const void
   p.values = values;
   p.k_pe = k_pe;
   p.status = dev_status;
-  cudaError_t e = prefix_expand_tc_supported(cfg, num_pages)
+  cudaError_t e = prefix_expand_tc_supported(cfg, num_pages) && aligned16(W_UK, W_UV, cache, keys, values, k_pe)
                       ? launch_prefix_expand_tc(cfg->cache_dtype, p, (cudaStream_t)stream)
                       : launch_prefix_expand_simt(cfg->act_dtype, cfg->cache_dtype, p, (cudaStream_t)stream);
   return e == cudaSuccess ? MLA_OK : cuda_fail(e, "mla_prefix_expand");
@@ -739,7 +747,8 @@ mla_status mla_prefix_attend(const mla_config* cfg, const void* q_nope, const vo
   p.scale_log2 = softmax_scale_of(cfg) * kLog2e;
   p.tt = turn_table(cfg);
   p.status = dev_status;
-  cudaError_t e = prefix_attend_tc_supported(cfg) && prefix_len > 0
+  cudaError_t e = prefix_attend_tc_supported(cfg) && prefix_len > 0 &&
+                          aligned16(q_nope, q_pe, keys, values, k_pe, u)
                       ? launch_prefix_attend_tc(p, workspace, (cudaStream_t)stream)
                       : launch_prefix_attend_simt(cfg->act_dtype, p, (cudaStream_t)stream);
   return e == cudaSuccess ? MLA_OK : cuda_fail(e, "mla_prefix_attend");
@@ -757,6 +766,7 @@ mla_status mla_key_weights(const mla_config* cfg, const void* q_lat, const float
   if ((long long)batch * max_pages > 0x7FFFFFFFLL) return unsupported("batch * max_pages above 2^31 - 1");
   if ((long long)max_pages * cfg->page_size > 0x7FFFFFFFLL)
     return unsupported("max_pages * page_size above 2^31 - 1");
+  if (((uintptr_t)cache & 3) != 0) return invalid("cache must be 4-byte aligned");
   KeyWeightParams p;
   p.q_lat = q_lat;
   p.lse = lse;
@@ -776,7 +786,7 @@ mla_status mla_key_weights(const mla_config* cfg, const void* q_lat, const float
   p.decay = decay;
   p.weights = weights;
   p.status = dev_status;
-  cudaError_t e = key_weights_tc_supported(cfg, num_pages)
+  cudaError_t e = key_weights_tc_supported(cfg, num_pages) && aligned16(q_lat, cache)
                       ? launch_key_weights_tc(cfg->cache_dtype, p, (cudaStream_t)stream)
                       : launch_key_weights_simt(cfg->act_dtype, cfg->cache_dtype, p, (cudaStream_t)stream);
   return e == cudaSuccess ? MLA_OK : cuda_fail(e, "mla_key_weights");

@@ -128,7 +128,8 @@ def check_attend(d, x, lens, act, u, lse):
 @pytest.mark.parametrize("act,shape,H", [("f32", "tiny", 16), ("bf16", "tiny", 16), ("bf16", "v2", 16),
                                          ("bf16", "v2", 3), ("f32", "odd", 3)])
 @pytest.mark.parametrize("B,q,L", [(1, 1, 1), (3, 1, 64), (2, 3, 127), (5, 1, 128), (4, 2, 129), (3, 4, 700),
-                                   (128, 1, 257), (65, 2, 300), (43, 6, 200)])
+                                   (128, 1, 257), (65, 2, 300), (43, 6, 200),
+                                   (260, 1, 700), (300, 2, 130)])
 def test_attend(act, shape, H, B, q, L):
     rng = np.random.default_rng(B * 1000 + L)
     d = D.dims(shape, H)
@@ -219,6 +220,38 @@ def test_attend_same_bits_every_time_on_two_streams_and_captured():
     torch.cuda.synchronize()
     for o in (a, b, c):
         assert torch.equal(o[0], first[0]) and torch.equal(o[1], first[1])
+
+
+def shifted(t, elements=1):
+    """The same values at an address that is no multiple of 16 bytes."""
+    flat = torch.empty(t.numel() + 8, dtype=t.dtype, device=t.device)
+    view = flat[elements: elements + t.numel()].view(t.shape)
+    view.copy_(t)
+    return view
+
+
+def test_unaligned_views():
+    rng = np.random.default_rng(41)
+    d = D.dims("v2", 16)
+    x, lens = attend_inputs(rng, d, 5, 1, 130, "bf16", rng.integers(1, 90, 5))
+    cfg = M.make_config(d, "bf16", "bf16")
+    t = {k: shifted(D.dev(v, "bf16")) for k, v in x.items()}
+    u = shifted(torch.zeros(5, 1, 16, 128, dtype=torch.bfloat16, device="cuda"))
+    lse = shifted(torch.zeros(5, 1, 16, device="cuda"))
+    ws = torch.empty(max(256, M.mla_prefix_attend_workspace_size(cfg, 5, 1, 130)), dtype=torch.uint8, device="cuda")
+    M.mla_prefix_attend(cfg, t["q_nope"], t["q_pe"], t["keys"], t["values"], t["k_pe"], D.dev(lens), u, lse, ws)
+    torch.cuda.synchronize()
+    check_attend(d, x, lens, "bf16", u.double().cpu().numpy(), lse.double().cpu().numpy())
+    c = D.Cache(rng, "bf16", d, [130])
+    W_UK = D.draw(rng, (512, 16 * 128), "bf16", 512 ** -0.5)
+    W_UV = D.draw(rng, (512, 16 * 128), "bf16", 512 ** -0.5)
+    want = expand(c, cfg, W_UK, W_UV, 130)
+    got = [shifted(torch.zeros_like(y)) for y in want]
+    M.mla_prefix_expand(cfg, D.dev(W_UK, "bf16"), D.dev(W_UV, "bf16"), shifted(c.device(), 2), D.dev(c.table[0]), 130,
+                        *got)
+    torch.cuda.synchronize()
+    for g, y in zip(got, want):
+        assert (g.double() - y.double()).abs().max() <= 2.0 ** -7 * y.double().abs().max()
 
 
 # ----------------------------------------------------------------------------- joined projection

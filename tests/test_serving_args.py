@@ -56,7 +56,8 @@ OTHER = ctypes.c_void_p(1 << 21)
 I, U, Ws = M.MLA_ERR_INVALID, M.MLA_ERR_UNSUPPORTED, M.MLA_ERR_WORKSPACE
 REFUSED = [
     ("mla_prefix_expand", dict(prefix_len=-1), I), ("mla_prefix_expand", dict(prefix_len=(1 << 22) + 1), U),
-    ("mla_prefix_expand", dict(num_pages=0), I),
+    ("mla_prefix_expand", dict(num_pages=0), I), ("mla_prefix_expand", dict(cache=ODD_ADDRESS), I),
+    ("mla_key_weights", dict(cache=ODD_ADDRESS), I),
     ("mla_prefix_attend", dict(prefix_len=-1), I), ("mla_prefix_attend", dict(batch=0), I),
     ("mla_prefix_attend", dict(q_len=0), I), ("mla_prefix_attend", dict(batch=40000), U),
     ("mla_output_proj_prefix", dict(rows=-1), I), ("mla_output_proj_prefix", dict(bytes=100), Ws),
