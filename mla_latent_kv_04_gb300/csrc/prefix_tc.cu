@@ -72,7 +72,7 @@ struct Work {
   int workers;                                     // CTAs or pairs
   int pair;
   int whole;                                       // 1: cuts between tiles only
-  float* part_o;                                   // [2 CTAs][128][128]
+  float* part_o;                                   // [2 CTAs][32][128][4]: columns by 4, rows, column
   float* part_lse;                                 // [2 CTAs][128], log2 units
   __host__ __device__ long long begin(int c) const {
     return whole ? (long long)c * tiles / workers * blocks : (long long)c * tiles * blocks / workers;
@@ -288,8 +288,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float c = p.scale_log2;
     float* red = reinterpret_cast<float*>(basep + C::kOffRed);
     const uint32_t qfull = lead(B_QFULL), pready = lead(B_PREADY), ofree = lead(B_OFREE);
+    // What these arrivals announce lies in tensor memory (stores or loads already waited for), so
+    // the pair's need no release: one at cluster scope waits out the thread's memory traffic
+    // first (it cost 1.1 us of every block).
     auto arrive = [&](uint32_t b) {
-      if (kPair) ptx::mbar_arrive_remote(b);
+      if (kPair) ptx::mbar_arrive_remote_relaxed(b, 0u);
       else ptx::mbar_arrive(b);
     };
     uint32_t g = 0, x = 0, s = 0;                  // blocks, exchanges and segments so far
@@ -305,64 +308,63 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++x;
       return good;
     };
-    while (ok && seg.next()) {
+    // The row's query, raw: dims 64 w .. of the content part, pairs 16 w .. of the rotary part. It is
+    // asked for before the segment before it is written out.
+    uint4 qn[8], qr[4];
+    int S = 0;                                     // own length of the row's request
+    bool live = false;
+    auto fetch = [&](const Segments& sg) {
+      const int h = sg.tile / work.row_tiles;
+      const int r = (sg.tile % work.row_tiles * C::kCtas + rank) * 128 + row;
+      S = r < p.rows ? p.seq_lens[r / p.q_len] : 0;
+      live = r < p.rows && S >= p.q_len;
+      if (r < p.rows && S != 0 && S < p.q_len && h == 0 && sg.k0 == 0) flag_status(p.status, MLA_ERR_DEVICE_GUARD);
+      const uint4* n = reinterpret_cast<const uint4*>(reinterpret_cast<const bf16*>(p.q_nope) +
+                                                      ((long long)r * p.H + h) * 128 + 64 * w);
+      const uint4* e = reinterpret_cast<const uint4*>(reinterpret_cast<const bf16*>(p.q_pe) +
+                                                      ((long long)r * p.H + h) * 64 + 32 * w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) qn[i] = r < p.rows ? n[i] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) qr[i] = r < p.rows ? e[i] : make_uint4(0u, 0u, 0u, 0u);
+    };
+    bool more = seg.next();
+    if (more) fetch(seg);
+    while (ok && more) {
       const int h = seg.tile / work.row_tiles;
       const int r = (seg.tile % work.row_tiles * C::kCtas + rank) * 128 + row;
       const int nb = seg.k1 - seg.k0;
-      int S = 0;
-      if (r < p.rows) S = p.seq_lens[r / p.q_len];
-      const bool live = r < p.rows && S >= p.q_len;
-      if (r < p.rows && S != 0 && S < p.q_len && h == 0 && seg.k0 == 0) flag_status(p.status, MLA_ERR_DEVICE_GUARD);
-      // the row's query into tensor memory: one half stores the content part, the other turns the
-      // rotary part and stores its high and low term
+      const bool full = seg.k0 == 0 && seg.k1 == work.blocks;
+      const int k_first = seg.k0;
+      const bool row_live = live;
       {
-        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-        uint32_t q[64];
-        if (w == 0) {
-          const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const bf16*>(p.q_nope) +
-                                                            ((long long)r * p.H + h) * 128);
+        uint32_t hi[16], lo[16], raw_n[32];
+        const long long pos = (long long)p.L + S - p.q_len + r % p.q_len;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const uint4 y = live ? src[i] : zero;
-            q[4 * i] = y.x;
-            q[4 * i + 1] = y.y;
-            q[4 * i + 2] = y.z;
-            q[4 * i + 3] = y.w;
-          }
-        } else {
-          const long long pos = (long long)p.L + S - p.q_len + r % p.q_len;
-          const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const bf16*>(p.q_pe) +
-                                                            ((long long)r * p.H + h) * 64);
+        for (int i = 0; i < 8; ++i) {
+          raw_n[4 * i] = qn[i].x;
+          raw_n[4 * i + 1] = qn[i].y;
+          raw_n[4 * i + 2] = qn[i].z;
+          raw_n[4 * i + 3] = qn[i].w;
+        }
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint4 y = live ? src[i] : zero;
-            q[4 * i] = y.x;
-            q[4 * i + 1] = y.y;
-            q[4 * i + 2] = y.z;
-            q[4 * i + 3] = y.w;
-          }
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            float sn, cs;
-            turn_sincos<false>(p.tt, i, pos, &sn, &cs);
-            const float a = __uint_as_float(q[i] << 16), b = __uint_as_float(q[i] & 0xFFFF0000u);
-            const float y0 = a * cs - b * sn, y1 = a * sn + b * cs;
-            const __nv_bfloat162 t = __floats2bfloat162_rn(y0, y1);
-            const float2 f = __bfloat1622float2(t);
-            const __nv_bfloat162 u = __floats2bfloat162_rn(y0 - f.x, y1 - f.y);
-            q[i] = *reinterpret_cast<const uint32_t*>(&t);
-            q[32 + i] = *reinterpret_cast<const uint32_t*>(&u);
-          }
+        for (int i = 0; i < 16; ++i) {
+          const uint32_t y = (i & 3) == 0 ? qr[i >> 2].x : ((i & 3) == 1 ? qr[i >> 2].y : ((i & 3) == 2 ? qr[i >> 2].z : qr[i >> 2].w));
+          float sn, cs;
+          turn_sincos<false>(p.tt, 16 * w + i, pos, &sn, &cs);
+          const float a = __uint_as_float(y << 16), b = __uint_as_float(y & 0xFFFF0000u);
+          const float y0 = a * cs - b * sn, y1 = a * sn + b * cs;
+          const __nv_bfloat162 t = __floats2bfloat162_rn(y0, y1);
+          const float2 f = __bfloat1622float2(t);
+          const __nv_bfloat162 u = __floats2bfloat162_rn(y0 - f.x, y1 - f.y);
+          hi[i] = *reinterpret_cast<const uint32_t*>(&t);
+          lo[i] = *reinterpret_cast<const uint32_t*>(&u);
         }
         if (!(ok = wait_w(B_QEMPTY, (s & 1) ^ 1))) break;
         ptx::tc_fence_after();
-        uint32_t half[32];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) half[i] = q[32 * k + i];
-          ptx::tmem_st32(t_lane + kColQ + 64 * w + 32 * k, half);
-        }
+        ptx::tmem_st32(t_lane + kColQ + 32 * w, raw_n);
+        ptx::tmem_st16(t_lane + kColQ + 64 + 16 * w, hi);
+        ptx::tmem_st16(t_lane + kColQ + 96 + 16 * w, lo);
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
         __syncwarp();
@@ -377,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::tmem_ld32(t_s, v[0]);
         ptx::tmem_ld32(t_s + 32, v[1]);
         ptx::tmem_wait_ld();
-        const int valid = p.L - (seg.k0 + n) * kBN - 64 * w;
+        const int valid = p.L - (k_first + n) * kBN - 64 * w;
         if (valid < 64) {
 #pragma unroll
           for (int q = 0; q < 2; ++q)
@@ -450,18 +452,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) arrive(pready + 8 * (g & 1));
       }
       if (!ok) break;
+      more = seg.next();
+      if (more) fetch(seg);                        // (the tile's own h, r and row_live are kept above)
       float l_other = 0.f;
       if (!(ok = swap(l, &l_other))) break;
       const float L = w ? l_other + l : l + l_other;
       const float inv = L > 0.f ? 1.f / L : 0.f;
       if (!(ok = wait_w(B_ODONE + ((g - 1) & 1), ((g - 1) >> 1) & 1))) break;
       ptx::tc_fence_after();
-      const bool full = seg.k0 == 0 && seg.k1 == work.blocks;
-      const long long slot = 2LL * blockIdx.x + (seg.k0 == 0 ? 1 : 0);
+      const long long slot = 2LL * blockIdx.x + (k_first == 0 ? 1 : 0);
       if (w == 0) {
         const float lse2 = L > 0.f ? m * c + log2f(L) : -INFINITY;
         if (!full) work.part_lse[slot * 128 + row] = lse2;
-        else if (r < p.rows) p.lse[(long long)r * p.H + h] = live ? lse2 * kLn2 : -INFINITY;
+        else if (r < p.rows) p.lse[(long long)r * p.H + h] = row_live ? lse2 * kLn2 : -INFINITY;
       }
       uint32_t o[2][32];                           // output columns 64 w .. 64 w + 63
       ptx::tmem_ld32(t_o, o[0]);
@@ -472,12 +475,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) arrive(ofree);
       if (r < p.rows) {
         if (!full) {
-          float4* dst = reinterpret_cast<float4*>(work.part_o + (slot * 128 + row) * 128 + 64 * w);
+          // [slot][column / 4][row] float4: a warp's rows side by side
+          float4* dst = reinterpret_cast<float4*>(work.part_o) + (slot * 32 + 16 * w) * 128 + row;
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
             const uint32_t* y = &o[j >> 3][4 * (j & 7)];
-            dst[j] = make_float4(__uint_as_float(y[0]) * inv, __uint_as_float(y[1]) * inv,
-                                 __uint_as_float(y[2]) * inv, __uint_as_float(y[3]) * inv);
+            dst[j * 128] = make_float4(__uint_as_float(y[0]) * inv, __uint_as_float(y[1]) * inv,
+                                       __uint_as_float(y[2]) * inv, __uint_as_float(y[3]) * inv);
           }
         } else {
           uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<bf16*>(p.u) + ((long long)r * p.H + h) * 128 + 64 * w);
@@ -487,8 +491,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const uint32_t* y = &o[j >> 2][8 * (j & 3) + 2 * i];
-              const __nv_bfloat162 b2 = __floats2bfloat162_rn(live ? __uint_as_float(y[0]) * inv : 0.f,
-                                                              live ? __uint_as_float(y[1]) * inv : 0.f);
+              const __nv_bfloat162 b2 = __floats2bfloat162_rn(row_live ? __uint_as_float(y[0]) * inv : 0.f,
+                                                              row_live ? __uint_as_float(y[1]) * inv : 0.f);
               k[i] = *reinterpret_cast<const uint32_t*>(&b2);
             }
             dst[j] = make_uint4(k[0], k[1], k[2], k[3]);
@@ -509,11 +513,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Joins the pieces of a tile that was cut: out = sum_s w_s o_s, w_s = 2^(lse_s - L). Warp per row.
+// Joins the pieces of a tile that was cut: out = sum_s w_s o_s, w_s = 2^(lse_s - L). Block (tile, 16
+// columns), thread per row.
 __global__ void __launch_bounds__(256) attend_merge_kernel(const PrefixAttendParams p, const Work work) {
+  ptx::griddep_launch_dependents();
   ptx::griddep_wait();
-  const int tile = blockIdx.x, rows = work.pair ? 256 : 128;
-  const int tr = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;   // row of the tile
+  const int tile = blockIdx.x, rows = work.pair ? 256 : 128, tr = threadIdx.x;
   const int h = tile / work.row_tiles, r = tile % work.row_tiles * rows + tr;
   if (r >= p.rows) return;
   const long long t0 = (long long)tile * work.blocks, t1 = t0 + work.blocks;
@@ -530,31 +535,42 @@ __global__ void __launch_bounds__(256) attend_merge_kernel(const PrefixAttendPar
   const int rank = tr >> 7, row = tr & 127;
   auto slot = [&](int c) {
     const int cta = work.pair ? 2 * c + rank : c;
-    return (2LL * cta + (c == c0 ? 1 : 0)) * 128 + row;
+    return 2LL * cta + (c == c0 ? 1 : 0);
   };
   const int S = p.seq_lens[r / p.q_len];
   float m = -INFINITY;
-  for (int c = c0; c <= c1; ++c) m = fmaxf(m, work.part_lse[slot(c)]);
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int c = c0; c <= c1; ++c) m = fmaxf(m, work.part_lse[slot(c) * 128 + row]);
+  float acc[16] = {};
   float sum = 0.f;
   const bool live = S >= p.q_len && m > -INFINITY;
   if (live) {
     for (int c = c0; c <= c1; ++c) {
-      const float w = ptx::ex2(work.part_lse[slot(c)] - m);
-      const float4 o = *reinterpret_cast<const float4*>(work.part_o + slot(c) * 128 + 4 * lane);
-      acc.x = fmaf(w, o.x, acc.x);
-      acc.y = fmaf(w, o.y, acc.y);
-      acc.z = fmaf(w, o.z, acc.z);
-      acc.w = fmaf(w, o.w, acc.w);
+      const float w = ptx::ex2(work.part_lse[slot(c) * 128 + row] - m);
+      const float4* o = reinterpret_cast<const float4*>(work.part_o) + (slot(c) * 32 + 4 * blockIdx.y) * 128 + row;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 y = o[i * 128];
+        acc[4 * i] = fmaf(w, y.x, acc[4 * i]);
+        acc[4 * i + 1] = fmaf(w, y.y, acc[4 * i + 1]);
+        acc[4 * i + 2] = fmaf(w, y.z, acc[4 * i + 2]);
+        acc[4 * i + 3] = fmaf(w, y.w, acc[4 * i + 3]);
+      }
       sum += w;
     }
   }
   const float inv = live ? 1.f / sum : 0.f;
-  const __nv_bfloat162 x = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
-  const __nv_bfloat162 y = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-  *reinterpret_cast<uint2*>(reinterpret_cast<bf16*>(p.u) + ((long long)r * p.H + h) * 128 + 4 * lane) =
-      make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
-  if (lane == 0) p.lse[(long long)r * p.H + h] = live ? (m + log2f(sum)) * kLn2 : -INFINITY;
+  uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<bf16*>(p.u) + ((long long)r * p.H + h) * 128 + 16 * blockIdx.y);
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    uint32_t k[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 b2 = __floats2bfloat162_rn(acc[8 * j + 2 * i] * inv, acc[8 * j + 2 * i + 1] * inv);
+      k[i] = *reinterpret_cast<const uint32_t*>(&b2);
+    }
+    dst[j] = make_uint4(k[0], k[1], k[2], k[3]);
+  }
+  if (blockIdx.y == 0) p.lse[(long long)r * p.H + h] = live ? (m + log2f(sum)) * kLn2 : -INFINITY;
 }
 
 // Cuts between tiles unless that leaves a worker this many blocks more than an even share: a cut
@@ -603,9 +619,8 @@ static cudaError_t run(const CUtensorMap& k, const CUtensorMap& pe, const CUtens
   if (e != cudaSuccess) return e;
   note_launch();
   if (w.whole) return cudaSuccess;
-  const int rows = 128 * C::kCtas, groups = ((p.rows < rows ? p.rows : rows) + 7) / 8;
-  cfg.gridDim = dim3((unsigned)w.tiles, (unsigned)groups, 1);
-  cfg.blockDim = dim3(256, 1, 1);
+  cfg.gridDim = dim3((unsigned)w.tiles, 8, 1);
+  cfg.blockDim = dim3(128 * C::kCtas, 1, 1);
   cfg.dynamicSmemBytes = 0;
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, attend_merge_kernel, p, w);
