@@ -16,18 +16,17 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&b);
 }
 
-// Half a token row (32 dims, half 0 or 1) of a 64-dim chunk: the codes, in a tile of 64-byte rows with the 64-byte
-// swizzle, times `scale` as bf16 into a tile of 128-byte rows with the 128-byte swizzle. With
-// `lo`, what the rounding left over goes to that second tile as another bf16 (the two add up
-// to the product within 2^-17 of it). Without a scale (scale == 1) the codes are exact.
+// Half a token row (32 dims, half 0 or 1) of a 64-dim chunk: the 32 codes times `scale` as bf16
+// into a tile of 128-byte rows with the 128-byte swizzle. With kLow, what the rounding left over
+// goes to that second tile as another bf16 (the two add up to the product within 2^-17 of it).
+// Without a scale the codes are exact.
 template <bool kScaled, bool kLow>
-__device__ __forceinline__ void expand_codes_half_row(const uint8_t* codes, uint8_t* hi, uint8_t* lo,
-                                                      int row, int half, float scale) {
+__device__ __forceinline__ void expand_codes_half_row(const uint4 (&code)[2], uint8_t* hi, uint8_t* lo, int row,
+                                                      int half, float scale) {
 #pragma unroll
   for (int ii = 0; ii < 2; ++ii) {
     const int i = 2 * half + ii;
-    const uint4 c = *reinterpret_cast<const uint4*>(codes + row * 64 + ((i ^ ((row >> 1) & 3)) << 4));
-    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+    const uint32_t w[4] = {code[ii].x, code[ii].y, code[ii].z, code[ii].w};
     uint32_t h[8], l[8];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -52,6 +51,13 @@ __device__ __forceinline__ void expand_codes_half_row(const uint8_t* codes, uint
         *reinterpret_cast<uint4*>(lo + at) = make_uint4(l[4 * k], l[4 * k + 1], l[4 * k + 2], l[4 * k + 3]);
     }
   }
+}
+
+// The codes of half a token row in a tile of 64-byte rows with the 64-byte swizzle.
+__device__ __forceinline__ void load_codes_half_row(const uint8_t* codes, int row, int half, uint4 (&code)[2]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    code[i] = *reinterpret_cast<const uint4*>(codes + row * 64 + (((2 * half + i) ^ ((row >> 1) & 3)) << 4));
 }
 
 }  // namespace mla

@@ -340,7 +340,8 @@ __global__ void __launch_bounds__(Ring<kKind>::kThreads, 1)
             const uint32_t rs = gr % R::kRaw, st = g % R::kTiles, st2 = (g + 1) % R::kTiles;
             if (!(ok = wait_w(B_RAWFULL + rs, (gr / R::kRaw) & 1))) break;
             if (!(ok = wait_w(B_EMPTY + st, ((g / R::kTiles) & 1) ^ 1))) break;
-            const uint8_t* codes = basep + R::kOffRaw + rs * (kStage / 2);
+            uint4 codes[2];
+            load_codes_half_row(basep + R::kOffRaw + rs * (kStage / 2), row, half, codes);
             if (kKind == 1) {
               expand_codes_half_row<false, false>(codes, basep + kOffRing + st * kStage, nullptr, row, half, 1.f);
               done(st);

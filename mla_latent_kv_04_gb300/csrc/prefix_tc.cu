@@ -316,9 +316,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto fetch = [&](const Segments& sg) {
       const int h = sg.tile / work.row_tiles;
       const int r = (sg.tile % work.row_tiles * C::kCtas + rank) * 128 + row;
-      S = r < p.rows ? p.seq_lens[r / p.q_len] : 0;
-      live = r < p.rows && S >= p.q_len;
-      if (r < p.rows && S != 0 && S < p.q_len && h == 0 && sg.k0 == 0) flag_status(p.status, MLA_ERR_DEVICE_GUARD);
       const uint4* n = reinterpret_cast<const uint4*>(reinterpret_cast<const bf16*>(p.q_nope) +
                                                       ((long long)r * p.H + h) * 128 + 64 * w);
       const uint4* e = reinterpret_cast<const uint4*>(reinterpret_cast<const bf16*>(p.q_pe) +
@@ -327,6 +324,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < 8; ++i) qn[i] = r < p.rows ? n[i] : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
       for (int i = 0; i < 4; ++i) qr[i] = r < p.rows ? e[i] : make_uint4(0u, 0u, 0u, 0u);
+      S = r < p.rows ? p.seq_lens[r / p.q_len] : 0;
+      live = r < p.rows && S >= p.q_len;
+      if (r < p.rows && S != 0 && S < p.q_len && h == 0 && sg.k0 == 0) flag_status(p.status, MLA_ERR_DEVICE_GUARD);
     };
     bool more = seg.next();
     if (more) fetch(seg);
@@ -573,9 +573,11 @@ __global__ void __launch_bounds__(256) attend_merge_kernel(const PrefixAttendPar
   if (blockIdx.y == 0) p.lse[(long long)r * p.H + h] = live ? (m + log2f(sum)) * kLn2 : -INFINITY;
 }
 
-// Cuts between tiles unless that leaves a worker this many blocks more than an even share: a cut
-// tile costs its pieces' way through the workspace and the merge.
-constexpr int kCutGain = 4;
+// Cuts between tiles unless that leaves a worker this many blocks (of about a microsecond) more
+// than an even share: a cut tile costs a second epilogue and query load, its pieces' way through
+// the workspace and the merge, 10 us in all. Measured where whole tiles leave 64 blocks instead of
+// 54: 90.4 us uncut and 99.7 cut at 128 rows x 8192 keys, 83.3 and 86.7 at 256 rows x 4096 keys.
+constexpr int kCutGain = 12;
 
 static Work plan(int rows, int H, int L) {
   Work w{};
