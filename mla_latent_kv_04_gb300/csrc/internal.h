@@ -197,7 +197,7 @@ cudaError_t launch_prefix_expand_simt(mla_dtype act, mla_dtype cache, const Pref
                                       cudaStream_t s);
 
 // The tensor-core form: bf16 activations, 64-token pages, DeepSeek-V2 head shape, any cache.
-bool prefix_expand_tc_supported(const mla_config* c, long long num_pages);
+bool prefix_expand_tc_supported(const mla_config* c);
 cudaError_t launch_prefix_expand_tc(mla_dtype cache, const PrefixExpandParams& p, cudaStream_t s);
 
 struct PrefixAttendParams {

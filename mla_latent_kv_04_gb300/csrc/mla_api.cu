@@ -694,7 +694,7 @@ mla_status mla_prefix_expand(const mla_config* cfg, const void* W_UK, const void
   p.values = values;
   p.k_pe = k_pe;
   p.status = dev_status;
-  cudaError_t e = prefix_expand_tc_supported(cfg, num_pages) && aligned16(W_UK, W_UV, cache, keys, values, k_pe)
+  cudaError_t e = prefix_expand_tc_supported(cfg) && aligned16(W_UK, W_UV, cache, keys, values, k_pe)
                       ? launch_prefix_expand_tc(cfg->cache_dtype, p, (cudaStream_t)stream)
                       : launch_prefix_expand_simt(cfg->act_dtype, cfg->cache_dtype, p, (cudaStream_t)stream);
   return e == cudaSuccess ? MLA_OK : cuda_fail(e, "mla_prefix_expand");

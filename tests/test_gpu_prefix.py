@@ -50,7 +50,7 @@ def expand_bound(mag, x, act, cache_kind, d_c):
 @pytest.mark.parametrize("cache,shape,H", [("f32", "tiny", 16), ("bf16", "tiny", 16), ("bf16", "v2", 128),
                                            ("bf16", "v2", 16), ("fp8_e4m3", "v2", 32),
                                            ("fp8_e4m3_b128", "v2", 32), ("f32", "odd", 3), ("fp8_e4m3_b128", "odd128", 3)])
-@pytest.mark.parametrize("L", [1, 63, 64, 129, 400])
+@pytest.mark.parametrize("L", [1, 63, 64, 129, 400, 700, 1800])
 def test_expand(cache, shape, H, L):
     rng = np.random.default_rng(L)
     d = D.dims(shape, H)
