@@ -221,6 +221,15 @@ bool prefix_attend_tc_supported(const mla_config* c);
 size_t prefix_attend_tc_workspace(int rows, int H, int L);
 cudaError_t launch_prefix_attend_tc(const PrefixAttendParams& p, void* workspace, cudaStream_t s);
 
+// u and out of the joined projection on the tensor cores (bf16, d_v 128, d_c a multiple of 64), and
+// the fp32 pieces that the product with W_O needs (0 bytes up to 128 rows).
+bool prefix_join_tc_supported(const mla_config* c);
+size_t prefix_join_tc_workspace(int rows, int H, int d_v, int N);
+cudaError_t launch_prefix_join_tc(const void* o_lat, const void* W_UV, int rows, int H, int d_c, const PrefixJoin& j,
+                                  void* u, int32_t* status, cudaStream_t s);
+cudaError_t launch_prefix_project_tc(const void* u, const void* W_O, int rows, int K, int N, void* out, void* part,
+                                     int32_t* status, cudaStream_t s);
+
 struct KeyWeightParams {
   const void* q_lat;          // [batch * q_len][H][D]
   const float* lse;           // [batch * q_len][H], natural log

@@ -499,14 +499,17 @@ mla_status mla_output_proj_unfolded_workspace_size(const mla_config* cfg, int ro
   return MLA_OK;
 }
 
-static mla_status output_proj_unfolded(const mla_config* cfg, const void* out_latent, const void* W_UV,
-                                       const void* W_O, int rows, void* out, void* workspace,
-                                       size_t workspace_bytes, void* stream, const PrefixJoin* join,
-                                       const char* name) {
+mla_status mla_output_proj_unfolded(const mla_config* cfg, const void* out_latent, const void* W_UV,
+                                    const void* W_O, int rows, void* out, void* workspace,
+                                    size_t workspace_bytes, void* stream) {
+  mla_status st = check_config(cfg);
+  if (st != MLA_OK) return st;
+  if (rows < 0) return invalid("rows must be >= 0");
+  if (rows == 0) return MLA_OK;
   if (!out_latent || !W_UV || !W_O || !out) return invalid("null pointer");
   const size_t acc_bytes = unfolded_acc_bytes(cfg, rows);
   if (!workspace || workspace_bytes < acc_bytes + 256 + unfolded_u_bytes(cfg, rows)) {
-    g_last_error = std::string("workspace smaller than ") + name + "_workspace_size";
+    g_last_error = "workspace smaller than mla_output_proj_unfolded_workspace_size";
     return MLA_ERR_WORKSPACE;
   }
   if (((uintptr_t)workspace & 255) != 0) return invalid("workspace must be 256-byte aligned");
@@ -517,43 +520,66 @@ static mla_status output_proj_unfolded(const mla_config* cfg, const void* out_la
   const int H = cfg->num_heads, d_c = cfg->d_latent, d_v = cfg->d_v, d = cfg->d_model;
   cudaError_t e;
   if (cfg->act_dtype == MLA_BF16 && d_c % 64 == 0 && d_v % 64 == 0) {
-    e = launch_lift_tc(out_latent, W_UV, rows, H, d_c, d_v, u, status, s, join);
+    e = launch_lift_tc(out_latent, W_UV, rows, H, d_c, d_v, u, status, s);
     if (e == cudaSuccess) e = launch_output_proj_tc(u, W_O, rows, H * d_v, d, out, status, s);
   } else {
-    e = launch_lift_simt(cfg->act_dtype, out_latent, W_UV, rows, H, d_c, d_v, u, s, join);
+    e = launch_lift_simt(cfg->act_dtype, out_latent, W_UV, rows, H, d_c, d_v, u, s);
     if (e == cudaSuccess)
       e = launch_output_proj_simt_ws(cfg->act_dtype, u, W_O, rows, H * d_v, d, out, acc, s);
   }
-  return e == cudaSuccess ? MLA_OK : cuda_fail(e, name);
+  return e == cudaSuccess ? MLA_OK : cuda_fail(e, "mla_output_proj_unfolded");
 }
 
-mla_status mla_output_proj_unfolded(const mla_config* cfg, const void* out_latent, const void* W_UV,
-                                    const void* W_O, int rows, void* out, void* workspace,
-                                    size_t workspace_bytes, void* stream) {
-  mla_status st = check_config(cfg);
-  if (st != MLA_OK) return st;
-  if (rows < 0) return invalid("rows must be >= 0");
-  if (rows == 0) return MLA_OK;
-  return output_proj_unfolded(cfg, out_latent, W_UV, W_O, rows, out, workspace, workspace_bytes,
-                              stream, nullptr, "mla_output_proj_unfolded");
+// the unfolded projection's workspace, then the joined projection's fp32 pieces
+static size_t prefix_pieces_bytes(const mla_config* c, int rows) {
+  return prefix_join_tc_supported(c) && rows > 0
+             ? prefix_join_tc_workspace(rows, c->num_heads, c->d_v, c->d_model)
+             : 0;
 }
 
 mla_status mla_output_proj_prefix_workspace_size(const mla_config* cfg, int rows, size_t* bytes) {
-  return mla_output_proj_unfolded_workspace_size(cfg, rows, bytes);
+  mla_status st = mla_output_proj_unfolded_workspace_size(cfg, rows, bytes);
+  if (st != MLA_OK) return st;
+  *bytes += prefix_pieces_bytes(cfg, rows);
+  return MLA_OK;
 }
 
 mla_status mla_output_proj_prefix(const mla_config* cfg, const void* out_latent, const float* lse,
                                   const void* u_prefix, const float* lse_prefix, const void* W_UV,
                                   const void* W_O, int rows, void* out, void* workspace,
                                   size_t workspace_bytes, void* stream) {
-  mla_status st = check_config(cfg);
+  size_t need = 0;
+  mla_status st = mla_output_proj_prefix_workspace_size(cfg, rows, &need);
   if (st != MLA_OK) return st;
-  if (rows < 0) return invalid("rows must be >= 0");
   if (rows == 0) return MLA_OK;
-  if (!lse || !u_prefix || !lse_prefix) return invalid("null pointer");
+  if (!out_latent || !lse || !u_prefix || !lse_prefix || !W_UV || !W_O || !out) return invalid("null pointer");
+  if (!workspace || workspace_bytes < need) {
+    g_last_error = "workspace smaller than mla_output_proj_prefix_workspace_size";
+    return MLA_ERR_WORKSPACE;
+  }
+  if (((uintptr_t)workspace & 255) != 0) return invalid("workspace must be 256-byte aligned");
+  cudaStream_t s = (cudaStream_t)stream;
+  const size_t acc_bytes = unfolded_acc_bytes(cfg, rows);
+  float* acc = (float*)workspace;
+  int32_t* status = (int32_t*)((char*)workspace + acc_bytes);
+  char* u = (char*)workspace + acc_bytes + 256;
+  const int H = cfg->num_heads, d_c = cfg->d_latent, d_v = cfg->d_v, d = cfg->d_model;
   const PrefixJoin join{u_prefix, lse, lse_prefix};
-  return output_proj_unfolded(cfg, out_latent, W_UV, W_O, rows, out, workspace, workspace_bytes,
-                              stream, &join, "mla_output_proj_prefix");
+  const bool rows16 = aligned16(out_latent, u_prefix, W_UV, W_O, out) && d % 8 == 0;
+  cudaError_t e;
+  if (prefix_join_tc_supported(cfg) && rows16) {
+    e = launch_prefix_join_tc(out_latent, W_UV, rows, H, d_c, join, u, status, s);
+    if (e == cudaSuccess)
+      e = launch_prefix_project_tc(u, W_O, rows, H * d_v, d, out, u + unfolded_u_bytes(cfg, rows), status, s);
+  } else if (cfg->act_dtype == MLA_BF16 && d_c % 64 == 0 && d_v % 64 == 0 && rows16) {
+    e = launch_lift_tc(out_latent, W_UV, rows, H, d_c, d_v, u, status, s, &join);
+    if (e == cudaSuccess) e = launch_output_proj_tc(u, W_O, rows, H * d_v, d, out, status, s);
+  } else {
+    e = launch_lift_simt(cfg->act_dtype, out_latent, W_UV, rows, H, d_c, d_v, u, s, &join);
+    if (e == cudaSuccess)
+      e = launch_output_proj_simt_ws(cfg->act_dtype, u, W_O, rows, H * d_v, d, out, acc, s);
+  }
+  return e == cudaSuccess ? MLA_OK : cuda_fail(e, "mla_output_proj_prefix");
 }
 
 // Query side: three GEMMs through fp32 accumulators, one accumulator region reused in stream

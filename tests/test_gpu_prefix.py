@@ -258,7 +258,7 @@ def test_unaligned_views():
 
 @pytest.mark.parametrize("act,shape,H", [("f32", "tiny", 16), ("bf16", "tiny", 16), ("bf16", "v2", 16),
                                          ("bf16", "v2", 128)])
-@pytest.mark.parametrize("rows", [1, 33, 130])
+@pytest.mark.parametrize("rows", [1, 33, 130, 300])
 def test_output_proj_prefix(act, shape, H, rows):
     rng = np.random.default_rng(rows)
     d = D.dims(shape, H)

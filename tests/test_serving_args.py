@@ -111,8 +111,11 @@ def test_fp32_cache_alignment(lib):
 
 
 def test_workspace_sizes(lib):
-    assert M.mla_output_proj_prefix_workspace_size(cfg(), 32) == \
-        M.mla_output_proj_unfolded_workspace_size(cfg(), 32)
+    for rows in (1, 32, 128):
+        assert M.mla_output_proj_prefix_workspace_size(cfg(), rows) == \
+            M.mla_output_proj_unfolded_workspace_size(cfg(), rows)
+    # more rows: fp32 pieces of the product with W_O
+    assert M.mla_output_proj_prefix_workspace_size(cfg(), 129) > M.mla_output_proj_unfolded_workspace_size(cfg(), 129)
     n = ctypes.c_size_t(0)
     assert lib.mla_prefix_attend_workspace_size(ctypes.byref(cfg()), 4, 1, -1, ctypes.byref(n)) == I
     assert lib.mla_prefix_attend_workspace_size(ctypes.byref(cfg()), 4, 1, 10, None) == I
