@@ -16,6 +16,7 @@
 
 #include "internal.h"
 #include "sm100_ptx.cuh"
+#include "tc_host.h"
 
 namespace mla {
 namespace {
@@ -78,6 +79,8 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(EvictParam
   extern __shared__ float w_s[];
   __shared__ SelShared sh;
   const int b = blockIdx.x / C, rank = blockIdx.x % C, tid = threadIdx.x;
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
   const int S = p.seq_lens[b];
   int32_t* kept = p.kept + (long long)b * p.budget;
   const float* w = p.weights + (long long)b * p.max_pages * p.P;
@@ -235,20 +238,17 @@ template <int VB> struct Vec;
 template <> struct Vec<16> { typedef uint4 type; };
 template <> struct Vec<4> { typedef uint32_t type; };
 
-// Turns the pairs of the rotary part inside one vector of VB bytes at byte `off` of a row,
-// by `delta` positions. Kind: 0 fp32, 1 bf16, 2 e4m3 (codes; the scale cancels), 3 block-scaled
-// rows (rotary part in bf16). kpe: byte offset of the rotary part.
+// Turns the pairs of one vector of VB bytes at byte `off` of the rotary part, by `delta` positions.
+// Kind: 0 fp32, 1 bf16, 2 e4m3 (codes; the scale cancels), 3 block-scaled rows (rotary part in
+// bf16).
 template <int kKind, int VB>
-__device__ __forceinline__ void turn_vector(typename Vec<VB>::type& vec, int off, int kpe,
-                                            const TurnTable& tt, int delta) {
+__device__ __forceinline__ void turn_vector(typename Vec<VB>::type& vec, int off, const TurnTable& tt, int delta) {
   constexpr int kPairBytes = kKind == 0 ? 8 : (kKind == 2 ? 2 : 4);
   uint32_t* words = reinterpret_cast<uint32_t*>(&vec);
 #pragma unroll
   for (int q = 0; q < VB / kPairBytes; ++q) {
-    const int at = off + q * kPairBytes - kpe;           // byte offset inside the rotary part
-    if (at < 0) continue;
     float sn, cs;
-    turn_sincos<kKind == 0>(tt, at / kPairBytes, delta, &sn, &cs);
+    turn_sincos<kKind == 0>(tt, off / kPairBytes + q, delta, &sn, &cs);
     if constexpr (kKind == 0) {
       const float x0 = __uint_as_float(words[2 * q]), x1 = __uint_as_float(words[2 * q + 1]);
       words[2 * q] = __float_as_uint(x0 * cs - x1 * sn);
@@ -268,36 +268,45 @@ __device__ __forceinline__ void turn_vector(typename Vec<VB>::type& vec, int off
 }
 
 constexpr int kMoveThreads = 256;
-constexpr int kMoveRows = 1024;                // rows whose places are looked up at a time
+constexpr int kMoveRows = 2048;                // rows whose places are looked up at a time
 constexpr int kMoveU = 4;                      // vectors in flight per thread and chunk
 
-// CTA (column slice of W vectors, row part, request): copies its slice of rows kept[i] -> i.
-// The slices of a row never meet, so in place a CTA only has to order itself: new places are
-// at or before old ones, a chunk's rows are all read (a barrier) before the chunk is written,
-// and later chunks read only rows behind it. The next chunk's loads are issued before this
-// chunk's stores.
+// CTA (column slice, row part, request): copies its slice of rows kept[i] -> i. Slices of W vectors
+// of the latent part come first, then slices of Wk vectors of the rotary part (narrower: their
+// sines and cosines would otherwise make a few CTAs last). The slices of a row never meet, so in
+// place a CTA only has to order itself: new places are at or before old ones, a chunk's rows are
+// all read (a barrier) before the chunk is written, and later chunks read only rows behind it.
+// The next chunk's loads are issued before this chunk's stores.
 template <int kKind, int VB>
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(EvictParams p, int W, int parts,
+__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(EvictParams p, int W, int Wk, int parts,
                                                                   int in_place) {
   typedef typename Vec<VB>::type V;
-  __shared__ int src_s[kMoveRows], dst_s[kMoveRows], delta_s[kMoveRows];
-  const int nvec = (int)(p.row_bytes / VB);
+  __shared__ int src_s[kMoveRows], dst_s[kMoveRows];
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();                         // the selection's kept tokens
+  constexpr int kElem = kKind == 0 ? 4 : (kKind == 2 ? 1 : 2);
+  const int nvec = (int)(p.row_bytes / VB), kvec = p.d_r * kElem / VB, lvec = nvec - kvec;
+  const int lslices = (lvec + W - 1) / W;
+  const bool rope = (int)blockIdx.x >= lslices;
+  const int w = rope ? Wk : W, v0 = rope ? lvec + ((int)blockIdx.x - lslices) * Wk : (int)blockIdx.x * W;
   const int b = blockIdx.z, tid = threadIdx.x;
-  const int vec = blockIdx.x * W + tid % W, lane_row = tid / W, rows_u = kMoveThreads / W;
+  const int vec = v0 + tid % w, lane_row = tid / w, rows_u = kMoveThreads / w;
+  const bool mine = vec < (rope ? nvec : lvec);
   const int chunk = rows_u * kMoveU;
+  const bool turn = rope && p.rotate;
   const int32_t* kept = p.kept + (long long)b * p.budget;
   // rows of this request: the new length, unless the request was skipped (kept[0] = -1)
-  int n = min(p.new_seq_lens[b], p.budget);
+  const int n = min(p.new_seq_lens[b], p.budget);
   if (n <= 0 || kept[0] < 0) return;
   const int r0 = (int)((long long)n * blockIdx.y / parts), r1 = (int)((long long)n * (blockIdx.y + 1) / parts);
   const int32_t* bt = p.block_table + (long long)b * p.max_pages;
   const int32_t* nt = p.new_block_table + (long long)b * p.new_max_pages;
   V* cache = reinterpret_cast<V*>(p.cache);
-  const int kpe = kKind == 0 ? 4 * p.d_c : (kKind == 1 ? 2 * p.d_c : (kKind == 2 ? p.d_c : p.d_c + p.d_c / 32));
   for (int base = r0; base < r1; base += kMoveRows) {
     const int m = min(kMoveRows, r1 - base);
     int moved = 0;
     __syncthreads();
+#pragma unroll 8
     for (int x = tid; x < m; x += kMoveThreads) {
       const int i = base + x, j = kept[i];
       const int ps = bt[j / p.P], pd = nt[i / p.P];
@@ -311,66 +320,73 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(EvictParams p,
       }
       src_s[x] = src;
       dst_s[x] = dst;
-      delta_s[x] = i - j;
       moved |= src >= 0;
     }
     if (!__syncthreads_or(moved)) continue;
     V cur[kMoveU], nxt[kMoveU];
-    auto load = [&](V* v, int c) {
+    int from[kMoveU], from_nxt[kMoveU];
+    auto load = [&](V* v, int* f, int c) {
 #pragma unroll
       for (int u = 0; u < kMoveU; ++u) {
         const int x = c + lane_row + u * rows_u;
-        if (x < m && vec < nvec && src_s[x] >= 0) v[u] = cache[(long long)src_s[x] * nvec + vec];
+        f[u] = mine && x < m ? src_s[x] : -1;
+        if (f[u] >= 0) v[u] = cache[(long long)f[u] * nvec + vec];
       }
     };
-    load(cur, 0);
+    load(cur, from, 0);
     for (int c = 0; c < m; c += chunk) {
-      if (c + chunk < m) load(nxt, c + chunk);
-      // rows of this chunk turned (which waits for its loads), then every thread's loads of the
-      // chunk are done at the barrier
+      if (c + chunk < m) load(nxt, from_nxt, c + chunk);
+      if (turn) {
 #pragma unroll
-      for (int u = 0; u < kMoveU; ++u) {
-        const int x = c + lane_row + u * rows_u;
-        if (p.rotate && (vec + 1) * VB > kpe && x < m && vec < nvec && src_s[x] >= 0 && delta_s[x] != 0)
-          turn_vector<kKind, VB>(cur[u], vec * VB, kpe, p.tt, delta_s[x]);
+        for (int u = 0; u < kMoveU; ++u) {
+          const int i = base + c + lane_row + u * rows_u;
+          if (from[u] < 0) continue;
+          const int delta = i - kept[i];
+          if (delta != 0) turn_vector<kKind, VB>(cur[u], (vec - lvec) * VB, p.tt, delta);
+        }
       }
       if (in_place) __syncthreads();
 #pragma unroll
-      for (int u = 0; u < kMoveU; ++u) {
-        const int x = c + lane_row + u * rows_u;
-        if (x < m && vec < nvec && src_s[x] >= 0) cache[(long long)dst_s[x] * nvec + vec] = cur[u];
-      }
+      for (int u = 0; u < kMoveU; ++u)
+        if (from[u] >= 0) cache[(long long)dst_s[c + lane_row + u * rows_u] * nvec + vec] = cur[u];
 #pragma unroll
-      for (int u = 0; u < kMoveU; ++u) cur[u] = nxt[u];
+      for (int u = 0; u < kMoveU; ++u) {
+        cur[u] = nxt[u];
+        from[u] = from_nxt[u];
+      }
     }
   }
 }
 
-int sm_count() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return 148;
-  return n;
-}
-
 template <int kKind, int VB>
 cudaError_t move(const EvictParams& p, cudaStream_t s) {
-  const int nvec = (int)(p.row_bytes / VB), sms = sm_count();
+  constexpr int kElem = kKind == 0 ? 4 : (kKind == 2 ? 1 : 2);
+  const int nvec = (int)(p.row_bytes / VB), kvec = p.d_r * kElem / VB, lvec = nvec - kvec, sms = device_sms();
   const int in_place = p.new_block_table == p.block_table;
-  int W = 128 / VB;
-  int parts = 1;
+  int W = 128 / VB, parts = 1;
+  const int Wk = 32 / VB;
+  auto slices = [&]() { return (lvec + W - 1) / W + (kvec + Wk - 1) / Wk; };
   if (in_place) {
     // narrower slices until the CTAs cover the SMs twice, down to 32-byte sectors
-    while (W > 32 / VB && (long long)p.batch * ((nvec + W - 1) / W) < 2LL * sms) W /= 2;
+    while (W > 32 / VB && (long long)p.batch * slices() < 2LL * sms) W /= 2;
   } else {
-    const long long ctas = (long long)p.batch * ((nvec + W - 1) / W);
-    parts = (int)min((long long)((p.budget + 255) / 256), max(1LL, 8LL * sms / ctas));
+    // the rows in parts, until there are 8 CTAs per SM, of at least 256 rows
+    const long long ctas = (long long)p.batch * slices(), most = (p.budget + 255) / 256;
+    const long long want = 8LL * sms / ctas;
+    parts = (int)(want < 1 ? 1 : (want < most ? want : most));
   }
-  const dim3 grid((nvec + W - 1) / W, parts, p.batch);
-  evict_move_kernel<kKind, VB><<<grid, kMoveThreads, 0, s>>>(p, W, parts, in_place);
-  note_launch();
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)slices(), (unsigned)parts, (unsigned)p.batch);
+  cfg.blockDim = dim3(kMoveThreads, 1, 1);
+  cfg.stream = s;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, evict_move_kernel<kKind, VB>, p, W, Wk, parts, in_place);
+  if (e == cudaSuccess) note_launch();
+  return e;
 }
 
 }  // namespace
@@ -390,17 +406,21 @@ cudaError_t launch_evict(mla_dtype cache, const EvictParams& p, cudaStream_t s) 
   cfg.blockDim = dim3(kSelThreads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = (unsigned)C;
-  attr.val.clusterDim.y = 1;
-  attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = C > 1 ? 1 : 0;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)C;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = C > 1 ? 2 : 1;
   e = cudaLaunchKernelEx(&cfg, evict_select_kernel, p, C);
   if (e != cudaSuccess) return e;
   note_launch();
-  const bool wide = p.row_bytes % 16 == 0 && ((uintptr_t)p.cache & 15) == 0;
+  // 16 bytes at a time where the rows and both of their parts allow it
+  const int kpe = p.d_r * (cache == MLA_FP8_E4M3 ? 1 : 2);
+  const bool wide = p.row_bytes % 16 == 0 && kpe % 16 == 0 && ((uintptr_t)p.cache & 15) == 0;
   switch (cache) {
     case MLA_F32: return move<0, 16>(p, s);
     case MLA_BF16: return wide ? move<1, 16>(p, s) : move<1, 4>(p, s);
