@@ -250,6 +250,7 @@ cudaError_t launch_key_weights_simt(mla_dtype act, mla_dtype cache, const KeyWei
 // heads by 16.
 bool key_weights_tc_supported(const mla_config* c, long long num_pages);
 cudaError_t launch_key_weights_tc(mla_dtype cache, const KeyWeightParams& p, cudaStream_t s);
+cudaError_t launch_key_weights_fp8(mla_dtype cache, const KeyWeightParams& p, cudaStream_t s);
 
 struct EvictParams {
   const float* weights;       // [batch][max_pages * P]
