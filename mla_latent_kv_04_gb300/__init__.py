@@ -190,12 +190,14 @@ def _ptr(x, name, dtypes=None, numel=None, allow_none=False):
         raise ValueError(f"{name} has dtype {x.dtype}, expected one of {dtypes}")
     if numel is not None and x.numel() != numel:
         raise ValueError(f"{name} has {x.numel()} elements, expected {numel}")
-    return ctypes.c_void_p(x.data_ptr())
+    return x.data_ptr()
 
 
 def _stream(stream):
     if stream is None:
-        return ctypes.c_void_p(_torch().cuda.current_stream().cuda_stream)
+        # the current stream of the current device, without the Stream object around it (4 us a call)
+        c = _torch()._C
+        return c._cuda_getCurrentRawStream(c._cuda_getDevice())
     if isinstance(stream, int):
         return ctypes.c_void_p(stream)
     return ctypes.c_void_p(stream.cuda_stream)

@@ -5,6 +5,7 @@
 
 #include "internal.h"
 #include "page_elem.cuh"
+#include "sm100_ptx.cuh"
 
 namespace mla {
 namespace {
@@ -81,13 +82,17 @@ __global__ void __launch_bounds__(64) expand_rope_kernel(PrefixExpandParams p) {
 
 // ======================================================================== prefix attention
 // Block per (query row, head): 128 keys at a time, one per thread, with the running maximum
-// and sum of the softmax; the output's dims over the threads.
+// and sum of the softmax; the output's dims over the threads, narrow values several times, each
+// copy of the threads taking every so manyth key. Small calls are bound by the latency of their
+// loads, which the unrolled loops keep in flight together.
 template <typename AT>
 __global__ void __launch_bounds__(128) attend_simt_kernel(PrefixAttendParams p) {
   extern __shared__ float sm[];
   float* q = sm;                               // [d_n + d_r]
   float* o = q + p.d_n + p.d_r;                // [d_v]
-  __shared__ float ps[128], red[4];
+  __shared__ float ps[128], red[4], acc_s[128];
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
   const int r = blockIdx.x, h = blockIdx.y, tid = threadIdx.x;
   const int S = p.seq_lens[r / p.q_len];
   AT* out = reinterpret_cast<AT*>(p.u) + ((long long)r * p.H + h) * p.d_v;
@@ -114,13 +119,18 @@ __global__ void __launch_bounds__(128) attend_simt_kernel(PrefixAttendParams p) 
   const AT* K = reinterpret_cast<const AT*>(p.keys) + (long long)h * p.L * p.d_n;
   const AT* V = reinterpret_cast<const AT*>(p.values) + (long long)h * p.L * p.d_v;
   const AT* kp = reinterpret_cast<const AT*>(p.k_pe);
+  int width = 128;                             // threads that cover the output's dims once
+  while (width > 1 && width / 2 >= p.d_v) width /= 2;
+  const int copies = 128 / width;
   float m = -INFINITY, l = 0.f;
   for (int l0 = 0; l0 < p.L; l0 += 128) {
     const int j = l0 + tid;
     float s = -INFINITY;
     if (j < p.L) {
       float acc = 0.f;
+#pragma unroll 16
       for (int i = 0; i < p.d_n; ++i) acc = fmaf(q[i], to_f32(K[(long long)j * p.d_n + i]), acc);
+#pragma unroll 16
       for (int i = 0; i < p.d_r; ++i) acc = fmaf(q[p.d_n + i], to_f32(kp[(long long)j * p.d_r + i]), acc);
       s = acc * p.scale_log2;
     }
@@ -139,14 +149,29 @@ __global__ void __launch_bounds__(128) attend_simt_kernel(PrefixAttendParams p) 
     __syncthreads();
     l = l * a + ((red[0] + red[1]) + (red[2] + red[3]));
     const int n = min(128, p.L - l0);
-    for (int v = tid; v < p.d_v; v += 128) {
-      float acc = o[v] * a;
-      for (int i = 0; i < n; ++i) acc = fmaf(ps[i], to_f32(V[(long long)(l0 + i) * p.d_v + v]), acc);
-      o[v] = acc;
+    for (int v0 = 0; v0 < p.d_v; v0 += 128) {
+      const int v = v0 + tid % width;
+      float acc = 0.f;
+      if (v < p.d_v) {
+#pragma unroll 8
+        for (int i = tid / width; i < n; i += copies)
+          acc = fmaf(ps[i], to_f32(V[(long long)(l0 + i) * p.d_v + v]), acc);
+      }
+      if (copies > 1) {
+        __syncthreads();
+        acc_s[tid] = acc;
+        __syncthreads();
+        if (tid < width) {
+          acc = 0.f;
+          for (int g = 0; g < copies; ++g) acc += acc_s[g * width + tid];
+        }
+      }
+      if (tid < width && v < p.d_v) o[v] = o[v] * a + acc;
     }
     m = m_new;
   }
   const float inv = l > 0.f ? 1.f / l : 0.f;
+  __syncthreads();
   for (int v = tid; v < p.d_v; v += 128) out[v] = from_f32<AT>(o[v] * inv);
   if (tid == 0) *lse = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
 }
@@ -250,9 +275,19 @@ cudaError_t launch_prefix_attend_simt(mla_dtype act, const PrefixAttendParams& p
     using AT = decltype(a);
     cudaError_t e = allow_smem(attend_simt_kernel<AT>, smem);
     if (e != cudaSuccess) return e;
-    attend_simt_kernel<AT><<<dim3(p.rows, p.H), 128, smem, s>>>(p);
-    note_launch();
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)p.rows, (unsigned)p.H, 1);
+    cfg.blockDim = dim3(128, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, attend_simt_kernel<AT>, p);
+    if (e == cudaSuccess) note_launch();
+    return e;
   };
   return act == MLA_F32 ? go(float{}) : go(bf16{});
 }
