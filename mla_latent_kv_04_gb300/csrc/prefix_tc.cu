@@ -17,10 +17,10 @@
 // Tensor memory (512 columns): Q 128 (the A operand of S; from shared memory it would take half
 // of that memory's read rate), S two buffers of 128, O 128. P (bf16) takes the place of its S.
 // The MMA warp issues S(n + 1), then O(n): the softmax of a block runs under the next block's
-// scores. Two threads per row, 64 columns each, in two warpgroups; they share the row maximum
-// through shared memory, and form P against the running reference while the other half's maximum
-// is on its way: the reference moves only when the maximum grows by more than 2^8 (then P is
-// formed again and O rescaled in tensor memory).
+// scores. Two threads per row, 64 columns each, in two warpgroups, share the row maximum through
+// shared memory; the reference m moves only when the maximum grows by more than 2^8 (O is then
+// rescaled in tensor memory). P is handed to the MMAs in two parts, since the time from S to P is
+// what the pipeline waits for.
 //
 // Work: the (head, row tile, key block) triples in this order are cut into one contiguous range
 // per CTA (or pair); a range may start and end inside a tile, whose pieces then go to the
@@ -64,7 +64,7 @@ constexpr float kRescale = 8.f;                    // log2 units
 // both; the MMAs' commits (KEMPTY, VEMPTY, QEMPTY, SFULL, ODONE) go to both. SFULL, PREADY and ODONE
 // are per S buffer: a wait is never two phases behind, since S(n) is complete only after O(n - 2).
 enum { B_KFULL = 0, B_KEMPTY = 5, B_VFULL = 10, B_VEMPTY = 14, B_QFULL = 18, B_QEMPTY, B_SFULL, B_PREADY = 22,
-       B_ODONE = 24, B_OFREE = 26, B_RED, B_TEAR = B_RED + 8, B_COUNT };
+       B_ODONE = 26, B_OFREE = 28, B_RED, B_TEAR = B_RED + 8, B_COUNT };
 static_assert(B_COUNT * 8 <= 480, "barrier area");
 
 struct Work {
@@ -225,23 +225,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       auto out = [&](bool first) {
         const uint32_t b = no & 1, st = no % C::kNV;
-        if (!wait_lead(B_PREADY + b, (no >> 1) & 1) || !wait_lead(B_VFULL + st, (no / C::kNV) & 1)) return false;
+        if (!wait_lead(B_VFULL + st, (no / C::kNV) & 1)) return false;
         // a segment's first product overwrites O: its owners have read the one before
         if (first && !wait_lead(B_OFREE, (s & 1) ^ 1)) return false;
-        ptx::tc_fence_after();
         const uint32_t v = base + C::kOffV + st * C::kVStage;
-        if (ptx::elect_one()) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {            // keys 16 k ..: P of the first 64 keys, of the rest
-            const uint32_t a = tmem + kColS + 128 * b + (k < 4 ? 8 * k : 64 + 8 * (k - 4));
-            const uint64_t bd = ptx::smem_desc(v + 2048 * k, C::kVBox, 1024, ptx::kSwizzle128);
-            if (kPair) ptx::mma_bf16_ts_pair(tmem + kColO, a, bd, C::kIdescO, (!first || k) ? 1u : 0u);
-            else ptx::mma_bf16_ts(tmem + kColO, a, bd, C::kIdescO, (!first || k) ? 1u : 0u);
+        for (int part = 0; part < 2; ++part) {     // keys 0-31 and 64-95 of the block, then the rest
+          if (!wait_lead(B_PREADY + 2 * part + b, (no >> 1) & 1)) return false;
+          ptx::tc_fence_after();
+          if (ptx::elect_one()) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int k = 2 * part + (i & 1) + 4 * (i >> 1);       // keys 16 k ..
+              const uint32_t a = tmem + kColS + 128 * b + (k < 4 ? 8 * k : 64 + 8 * (k - 4));
+              const uint64_t bd = ptx::smem_desc(v + 2048 * k, C::kVBox, 1024, ptx::kSwizzle128);
+              if (kPair) ptx::mma_bf16_ts_pair(tmem + kColO, a, bd, C::kIdescO, (!first || k) ? 1u : 0u);
+              else ptx::mma_bf16_ts(tmem + kColO, a, bd, C::kIdescO, (!first || k) ? 1u : 0u);
+            }
+            if (part == 1) {
+              commit(B_VEMPTY + st);
+              commit(B_ODONE + b);
+            }
           }
-          commit(B_VEMPTY + st);
-          commit(B_ODONE + b);
+          __syncwarp();
         }
-        __syncwarp();
         ++no;
         return true;
       };
@@ -395,61 +402,58 @@ __global__ void __launch_bounds__(kThreads, 1)
             mx[q] = fmaxf(mx[q], fmaxf(__uint_as_float(v[q >> 1][j + 2 * (q & 1)]),
                                        __uint_as_float(v[q >> 1][j + 2 * (q & 1) + 1])));
         float mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        uint32_t pk[2][16];
-        float sum;
-        auto form = [&]() {                        // P against the reference m (columns behind the
-          const float off = m == -INFINITY ? 0.f : m * c;   // prefix hold -infinity: 0)
-          float part[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int q = 0; q < 2; ++q)
-#pragma unroll
-            for (int j = 0; j < 32; j += 2) {
-              const float e0 = ptx::ex2(fmaf(__uint_as_float(v[q][j]), c, -off));
-              const float e1 = ptx::ex2(fmaf(__uint_as_float(v[q][j + 1]), c, -off));
-              part[j & 2] += e0;
-              part[(j & 2) + 1] += e1;
-              const __nv_bfloat162 b2 = __floats2bfloat162_rn(e0, e1);
-              pk[q][j >> 1] = *reinterpret_cast<const uint32_t*>(&b2);
-            }
-          sum = (part[0] + part[1]) + (part[2] + part[3]);
-        };
         const uint32_t b = x & 1;
         red[b * 256 + w * 128 + row] = mb;
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(bar(B_RED + 2 * quad + b));
-        if (n > 0) form();
         if (!(ok = wait_w(B_RED + 2 * quad + b, (x >> 1) & 1))) break;
         mb = fmaxf(mb, red[b * 256 + (w ^ 1) * 128 + row]);
         ++x;
-        const bool grow = n > 0 && (mb - m) * c > kRescale;
         if (n == 0) {
           m = mb;
-          form();
-        } else if (__any_sync(0xffffffffu, grow)) {
+        } else {
+          const bool grow = (mb - m) * c > kRescale;
           // tensor-memory accesses are warp-wide: a warp's rows are rescaled together
-          if (!(ok = wait_w(B_ODONE + ((g - 1) & 1), ((g - 1) >> 1) & 1))) break;
-          ptx::tc_fence_after();
-          const float a = grow ? (m == -INFINITY ? 0.f : ptx::ex2((m - mb) * c)) : 1.f;
+          if (__any_sync(0xffffffffu, grow)) {
+            if (!(ok = wait_w(B_ODONE + ((g - 1) & 1), ((g - 1) >> 1) & 1))) break;
+            ptx::tc_fence_after();
+            const float a = grow ? (m == -INFINITY ? 0.f : ptx::ex2((m - mb) * c)) : 1.f;
 #pragma unroll 1
-          for (int q = 0; q < 4; ++q) {
-            uint32_t o[16];
-            ptx::tmem_ld16(t_o + 16 * q, o);
-            ptx::tmem_wait_ld();
+            for (int q = 0; q < 4; ++q) {
+              uint32_t o[16];
+              ptx::tmem_ld16(t_o + 16 * q, o);
+              ptx::tmem_wait_ld();
 #pragma unroll
-            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * a);
-            ptx::tmem_st16(t_o + 16 * q, o);
+              for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * a);
+              ptx::tmem_st16(t_o + 16 * q, o);
+            }
+            l *= a;
+            if (grow) m = mb;
           }
-          l *= a;
-          if (grow) m = mb;
-          form();
         }
-        ptx::tmem_st16(t_s, pk[0]);
-        ptx::tmem_st16(t_s + 16, pk[1]);
-        ptx::tmem_wait_st();
-        l += sum;
-        ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) arrive(pready + 8 * (g & 1));
+        // P against the reference m (columns behind the prefix hold -infinity: 0), handed over in
+        // two parts: the product with the first 32 columns' keys runs while the rest are formed
+        const float off = m == -INFINITY ? 0.f : m * c;
+        float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) {
+            const float e0 = ptx::ex2(fmaf(__uint_as_float(v[q][j]), c, -off));
+            const float e1 = ptx::ex2(fmaf(__uint_as_float(v[q][j + 1]), c, -off));
+            part[j & 2] += e0;
+            part[(j & 2) + 1] += e1;
+            const __nv_bfloat162 b2 = __floats2bfloat162_rn(e0, e1);
+            pk[j >> 1] = *reinterpret_cast<const uint32_t*>(&b2);
+          }
+          ptx::tmem_st16(t_s + 16 * q, pk);
+          ptx::tmem_wait_st();
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive(pready + 8 * (2 * q + (g & 1)));
+        }
+        l += (part[0] + part[1]) + (part[2] + part[3]);
       }
       if (!ok) break;
       more = seg.next();
