@@ -21,7 +21,6 @@
 namespace mla {
 namespace {
 
-constexpr int kSelThreads = 1024;
 constexpr int kBins = 2048;
 constexpr int kMaxCluster = 8;
 constexpr int kSegMax = (int)(kEvictMaxKeys / kMaxCluster);   // weights one CTA holds in shared memory
@@ -34,7 +33,8 @@ __device__ __forceinline__ uint32_t weight_key(float f) {
   return (u >> 31) ? ~u : (u | 0x80000000u);
 }
 
-// Exclusive prefix sum of v over the block's 1024 threads; *total gets the sum.
+// Exclusive prefix sum of v over the block's threads; *total gets the sum.
+template <int kSelThreads>
 __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* warp_tot, uint32_t* total) {
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   uint32_t x = v;
@@ -47,7 +47,7 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* warp_tot, u
   if (lane == 31) warp_tot[wid] = x;
   __syncthreads();
   if (wid == 0) {
-    uint32_t w = warp_tot[lane];
+    uint32_t w = lane < kSelThreads / 32 ? warp_tot[lane] : 0u;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const uint32_t y = __shfl_up_sync(0xffffffffu, w, o);
@@ -75,7 +75,9 @@ __device__ __forceinline__ uint32_t ld_dsmem_u32(uint32_t addr) {
 
 // Cluster of C CTAs per request (blockIdx.x / C); CTA r holds the r-th contiguous segment of
 // the tokens that are neither sinks nor recent.
-__global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(EvictParams p, int C) {
+template <int kSelThreads>
+__global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) evict_select_kernel(EvictParams p, int C) {
+  constexpr int kBinsPer = kBins / kSelThreads;
   extern __shared__ float w_s[];
   __shared__ SelShared sh;
   const int b = blockIdx.x / C, rank = blockIdx.x % C, tid = threadIdx.x;
@@ -133,27 +135,29 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(EvictParam
       }
       if (C > 1) ptx::cluster_sync();
       else __syncthreads();
-      // bins from the top: thread t has bins (descending) 2 t and 2 t + 1
-      const uint32_t d0 = kBins - 1 - 2 * tid, d1 = d0 - 1;
-      uint32_t c0 = 0, c1 = 0;
-      if (C == 1) {
-        c0 = hist[d0];
-        c1 = hist[d1];
-      } else {
-        const uint32_t a0 = ptx::smem_u32(&hist[d0]), a1 = ptx::smem_u32(&hist[d1]);
-        for (int r = 0; r < C; ++r) {
-          c0 += ld_dsmem_u32(ptx::map_to_rank(a0, (uint32_t)r));
-          c1 += ld_dsmem_u32(ptx::map_to_rank(a1, (uint32_t)r));
+      // bins from the top: thread t has (descending) the kBinsPer ones from its first
+      const uint32_t d0 = kBins - 1 - kBinsPer * tid;
+      uint32_t c[kBinsPer], sum = 0;
+#pragma unroll
+      for (int i = 0; i < kBinsPer; ++i) {
+        c[i] = 0;
+        if (C == 1) {
+          c[i] = hist[d0 - i];
+        } else {
+          const uint32_t a = ptx::smem_u32(&hist[d0 - i]);
+          for (int r = 0; r < C; ++r) c[i] += ld_dsmem_u32(ptx::map_to_rank(a, (uint32_t)r));
         }
+        sum += c[i];
       }
       uint32_t total;
-      const uint32_t above = block_scan(c0 + c1, sh.warp_tot, &total);
-      if (above < want && want <= above + c0) {
-        sh.digit = d0;
-        sh.left = want - above;
-      } else if (above + c0 < want && want <= above + c0 + c1) {
-        sh.digit = d1;
-        sh.left = want - above - c0;
+      uint32_t above = block_scan<kSelThreads>(sum, sh.warp_tot, &total);
+#pragma unroll
+      for (int i = 0; i < kBinsPer; ++i) {
+        if (above < want && want <= above + c[i]) {
+          sh.digit = d0 - i;
+          sh.left = want - above;
+        }
+        above += c[i];
       }
       __syncthreads();
       prefix |= sh.digit << shift;
@@ -178,7 +182,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(EvictParam
   }
   uint32_t total;
   // both counts of a CTA stay below 2^16: one scan for the two
-  const uint32_t before = block_scan(gt | (eq << 16), sh.warp_tot, &total);
+  const uint32_t before = block_scan<kSelThreads>(gt | (eq << 16), sh.warp_tot, &total);
   uint32_t gt_before = before & 0xFFFFu, eq_before = before >> 16, out0 = 0;
   if (C > 1) {
     if (tid == 0) {
@@ -278,7 +282,7 @@ constexpr int kMoveU = 4;                      // vectors in flight per thread a
 // all read (a barrier) before the chunk is written, and later chunks read only rows behind it.
 // The next chunk's loads are issued before this chunk's stores.
 template <int kKind, int VB>
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(EvictParams p, int W, int Wk, int parts,
+__global__ void __launch_bounds__(kMoveThreads, 3) evict_move_kernel(EvictParams p, int W, int Wk, int parts,
                                                                   int in_place) {
   typedef typename Vec<VB>::type V;
   __shared__ int src_s[kMoveRows], dst_s[kMoveRows];
@@ -302,6 +306,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(EvictParams p,
   const int32_t* bt = p.block_table + (long long)b * p.max_pages;
   const int32_t* nt = p.new_block_table + (long long)b * p.new_max_pages;
   V* cache = reinterpret_cast<V*>(p.cache);
+  const int shift = (p.P & (p.P - 1)) == 0 ? 31 - __clz(p.P) : -1;   // (a division costs 20 instructions)
   for (int base = r0; base < r1; base += kMoveRows) {
     const int m = min(kMoveRows, r1 - base);
     int moved = 0;
@@ -309,13 +314,14 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(EvictParams p,
 #pragma unroll 8
     for (int x = tid; x < m; x += kMoveThreads) {
       const int i = base + x, j = kept[i];
-      const int ps = bt[j / p.P], pd = nt[i / p.P];
+      const int jp = shift >= 0 ? j >> shift : j / p.P, ip = shift >= 0 ? i >> shift : i / p.P;
+      const int ps = bt[jp], pd = nt[ip];
       int src = -1, dst = -1;
       if (ps < 0 || ps >= p.num_pages || pd < 0 || pd >= p.num_pages) {
         if (blockIdx.x == 0) flag_status(p.status, MLA_ERR_DEVICE_GUARD);
       } else {
-        src = ps * p.P + j % p.P;
-        dst = pd * p.P + i % p.P;
+        src = ps * p.P + (j - jp * p.P);
+        dst = pd * p.P + (i - ip * p.P);
         if (src == dst) src = -1;              // already in its place
       }
       src_s[x] = src;
@@ -363,12 +369,14 @@ cudaError_t move(const EvictParams& p, cudaStream_t s) {
   constexpr int kElem = kKind == 0 ? 4 : (kKind == 2 ? 1 : 2);
   const int nvec = (int)(p.row_bytes / VB), kvec = p.d_r * kElem / VB, lvec = nvec - kvec, sms = device_sms();
   const int in_place = p.new_block_table == p.block_table;
-  int W = 128 / VB, parts = 1;
+  // a line of a row at a time in place (32 requests of 4096 tokens 46 us; with 64 bytes 52, with 256
+  // 56, with 512 84), two lines into new pages (181 us against 187 and 185)
+  int W = (in_place ? 128 : 256) / VB, parts = 1;
   const int Wk = 32 / VB;
   auto slices = [&]() { return (lvec + W - 1) / W + (kvec + Wk - 1) / Wk; };
   if (in_place) {
-    // narrower slices until the CTAs cover the SMs twice, down to 32-byte sectors
-    while (W > 32 / VB && (long long)p.batch * slices() < 2LL * sms) W /= 2;
+    // narrower slices for few requests, until the CTAs cover the SMs, down to 32-byte sectors
+    while (W > 32 / VB && (long long)p.batch * slices() < sms) W /= 2;
   } else {
     // the rows in parts, until there are 8 CTAs per SM, of at least 256 rows
     const long long ctas = (long long)p.batch * slices(), most = (p.budget + 255) / 256;
@@ -389,17 +397,11 @@ cudaError_t move(const EvictParams& p, cudaStream_t s) {
   return e;
 }
 
-}  // namespace
-
-cudaError_t launch_evict(mla_dtype cache, const EvictParams& p, cudaStream_t s) {
-  const long long keys = (long long)p.max_pages * p.P;
-  int C = 1;
-  while (C < kMaxCluster && keys > 16384LL * C) C *= 2;
-  const int seg = (int)((keys + C - 1) / C);
-  if (seg > kSegMax) return cudaErrorInvalidValue;
+template <int kSelThreads>
+cudaError_t select(const EvictParams& p, int C, int seg, cudaStream_t s) {
+  auto kern = evict_select_kernel<kSelThreads>;
   const size_t smem = (size_t)(seg > 1 ? seg : 1) * 4;
-  cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)smem);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(p.batch * C), 1, 1);
@@ -415,9 +417,23 @@ cudaError_t launch_evict(mla_dtype cache, const EvictParams& p, cudaStream_t s) 
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = C > 1 ? 2 : 1;
-  e = cudaLaunchKernelEx(&cfg, evict_select_kernel, p, C);
+  e = cudaLaunchKernelEx(&cfg, kern, p, C);
+  if (e == cudaSuccess) note_launch();
+  return e;
+}
+
+}  // namespace
+
+cudaError_t launch_evict(mla_dtype cache, const EvictParams& p, cudaStream_t s) {
+  const long long keys = (long long)p.max_pages * p.P;
+  int C = 1;
+  while (C < kMaxCluster && keys > 16384LL * C) C *= 2;
+  const int seg = (int)((keys + C - 1) / C);
+  if (seg > kSegMax) return cudaErrorInvalidValue;
+  // 1024 threads where every CTA has an SM to itself; otherwise 512, two of which fit on one (256
+  // requests of up to 8192 tokens: one wave instead of two, 20 us instead of 25)
+  cudaError_t e = p.batch * C <= device_sms() ? select<1024>(p, C, seg, s) : select<512>(p, C, seg, s);
   if (e != cudaSuccess) return e;
-  note_launch();
   // 16 bytes at a time where the rows and both of their parts allow it
   const int kpe = p.d_r * (cache == MLA_FP8_E4M3 ? 1 : 2);
   const bool wide = p.row_bytes % 16 == 0 && kpe % 16 == 0 && ((uintptr_t)p.cache & 15) == 0;
