@@ -184,6 +184,8 @@ def _ptr(x, name, dtypes=None, numel=None, allow_none=False):
         raise ValueError(f"{name} is required")
     if not x.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
+    if x.get_device() != _torch()._C._cuda_getDevice():
+        raise ValueError(f"{name} is on cuda:{x.get_device()}, which is not the current device")
     if not x.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if dtypes is not None and x.dtype not in dtypes:

@@ -829,6 +829,7 @@ mla_status mla_evict_cache(const mla_config* cfg, const float* weights, const in
   if (max_pages <= 0 || new_max_pages <= 0 || num_pages <= 0)
     return invalid("max_pages, new_max_pages and num_pages must be positive");
   if (budget <= 0) return invalid("budget must be positive");
+  if (budget > (1 << 30)) return unsupported("budget above 2^30");
   if (sinks < 0 || recent < 0 || (long long)sinks + recent > budget)
     return invalid("sinks and recent must be >= 0 and fit the budget");
   if (!weights || !seq_lens || !block_table || !cache || !new_block_table || !kept || !new_seq_lens)

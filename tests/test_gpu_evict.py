@@ -6,6 +6,7 @@ import torch
 
 import mla_latent_kv_04_gb300 as M
 import oracle
+import workloads as W
 from oracle import serving as ref
 from tests import serving_data as D
 
@@ -106,14 +107,49 @@ def test_key_weights_guards(kind, shape, H):
     assert np.array_equal(got[2:], old[2:])
 
 
-def test_key_weights_long_request_and_many_short_ones():
+@pytest.mark.parametrize("kind", ["bf16", "fp8_e4m3", "fp8_e4m3_b128"])
+@pytest.mark.parametrize("lens", ["many", "few", "equal"])
+def test_key_weights_shares_of_the_work(kind, lens):
+    """More requests than SMs, few long ones, and equal ones (CTAs of their own)."""
     rng = np.random.default_rng(9)
-    lens = [9000] + list(rng.integers(1, 140, 300))
-    c = D.Cache(rng, "bf16", D.dims("v2", 16), lens)
+    lens = {"many": [9000] + list(rng.integers(1, 140, 300)), "few": [9000, 130, 4100],
+            "equal": [1500] * 20}[lens]
+    c = D.Cache(rng, kind, D.dims("v2", 16), lens)
     q_lat, lse, scale = weigh_inputs(rng, c, 1)
     old = rng.random((len(lens), c.max_pages * 64)).astype(np.float32)
     got = weigh(c, 1, q_lat, lse, old, 0.5)
     check_weights(c, 1, q_lat, lse, scale, old, 0.5, got)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8_e4m3", "fp8_e4m3_b128"])
+def test_key_weights_several_tokens_over_long_runs(kind):
+    """Four query tokens of requests longer than a run, which is passed over once per token."""
+    rng = np.random.default_rng(12)
+    c = D.Cache(rng, kind, D.dims("v2", 16), [30000, 5001])
+    q_lat, lse, scale = weigh_inputs(rng, c, 4)
+    old = rng.random((2, c.max_pages * 64)).astype(np.float32)
+    got = weigh(c, 4, q_lat, lse, old, 1.0)
+    check_weights(c, 4, q_lat, lse, scale, old, 1.0, got)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8_e4m3", "fp8_e4m3_b128"])
+def test_key_weights_queries_of_any_magnitude(kind):
+    """Heads of zeros, of tiny and of large values, and heads whose elements span 2^30."""
+    rng = np.random.default_rng(15)
+    c = D.Cache(rng, kind, D.dims("v2", 16), [200, 70])
+    q_lat, lse, scale = weigh_inputs(rng, c, 1)
+    size = np.ones((16, 1), np.float32)
+    size[0], size[1], size[2], size[3] = 0.0, 2.0 ** -100, 2.0 ** 7, 2.0 ** -126
+    q_lat = W.round_bf16(q_lat * size)
+    spread = np.float32(2.0) ** -rng.integers(0, 30, q_lat[:, :, 4:8].shape)
+    q_lat[:, :, 4:8] = W.round_bf16(q_lat[:, :, 4:8] * spread)
+    for b, n in enumerate(c.lens):                 # the LSE of these scores, so that none overflows
+        z = scale * (q_lat[b, 0].astype(np.float64) @ c.values[b].T)
+        m = z.max(1)
+        lse[b, 0] = m + np.log(np.exp(z - m[:, None]).sum(1))
+    old = np.full((2, c.max_pages * 64), np.nan, np.float32)
+    got = weigh(c, 1, q_lat, lse, old, 0.0)
+    check_weights(c, 1, q_lat, lse, scale, old, 0.0, got)
 
 
 @pytest.mark.parametrize("act,shape,H", [("f32", "tiny", 16), ("bf16", "v2", 128), ("bf16", "tiny", 16)])

@@ -72,6 +72,7 @@ REFUSED = [
     ("mla_evict_cache", dict(batch=32769), I), ("mla_evict_cache", dict(max_pages=7000, new_table=OTHER), U),
     ("mla_evict_cache", dict(new_max_pages=3), I), ("mla_evict_cache", dict(new_table=OTHER, new_max_pages=0), I),
     ("mla_evict_cache", dict(new_table=OTHER, new_max_pages=3, new_weights=FAKE), I),
+    ("mla_evict_cache", dict(budget=(1 << 30) + 1), U),
     ("mla_evict_cache", dict(num_pages=1 << 26), U), ("mla_evict_cache", dict(cache=ODD_ADDRESS), I),
 ]
 OPTIONAL = {"status", "stream", "new_weights", "workspace"}
@@ -119,6 +120,30 @@ def test_workspace_sizes(lib):
     n = ctypes.c_size_t(0)
     assert lib.mla_prefix_attend_workspace_size(ctypes.byref(cfg()), 4, 1, -1, ctypes.byref(n)) == I
     assert lib.mla_prefix_attend_workspace_size(ctypes.byref(cfg()), 4, 1, 10, None) == I
+
+
+def test_binding_refuses_tensors_of_another_device(monkeypatch):
+    import torch
+
+    class OnDevice:
+        is_cuda = True
+
+        def __init__(self, device):
+            self.device = device
+
+        def get_device(self):
+            return self.device
+
+        def is_contiguous(self):
+            return True
+
+        def data_ptr(self):
+            return 4096
+
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    assert M._ptr(OnDevice(0), "x") == 4096
+    with pytest.raises(ValueError, match="not the current device"):
+        M._ptr(OnDevice(1), "x")
 
 
 # ----------------------------------------------------------------------------- reference pins
