@@ -1,9 +1,9 @@
-// How the key-weight kernels share out their work. Tiles are 128 tokens (two pages); a CTA's tiles
-// of one request, for which it prepares the request's query, are a run. Either the tiles of all
-// requests in order are cut into one contiguous range per CTA, all of the same length, or every
-// request gets CTAs of its own, as many as a common quota of tiles asks for: fuller CTAs by up to
-// the rounding, but one run each instead of up to two and more. With several query tokens a run is
-// limited in length and passed over once per query token.
+// How the key-weight kernels share out their work: the tiles of 128 tokens (two pages) of all
+// requests in order, cut into one contiguous range per CTA; a CTA's tiles of one request, for which
+// it prepares the request's query, are a run. The cuts are at equal cost, where a request costs
+// its tiles plus the preparation of a query, in tiles (every CTA pays one for its first run anyway;
+// the requests' own charges are for the further runs of the CTAs that they begin in). With several
+// query tokens a run is limited in length and passed over once per query token.
 #pragma once
 #include "internal.h"
 #include "prologue.cuh"
@@ -54,76 +54,51 @@ struct Runs {
   }
 };
 
-// Sum of v over the block (tmp: 32 ints).
-__device__ __forceinline__ int block_sum(int v, int* tmp) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) tmp[threadIdx.x >> 5] = v;
-  __syncthreads();
-  int sum = 0;
-  for (int i = 0; i < (int)(blockDim.x + 31) / 32; ++i) sum += tmp[i];
-  return sum;
-}
-
-// The CTA's range. scratch: batch + 1 ints of shared memory. run_cost: what preparing a query
-// costs, in tiles (0: no quotas); run_limit: the longest run with several query tokens. Called by the whole CTA,
-// which it synchronises; the caller synchronises again before the scratch is used for something
-// else.
+// The CTA's range. scratch: 2 (batch + 1) ints of shared memory, or batch + 1 if batch is above
+// kCostBatch (run_cost then counts as 0: CTAs have several runs each, whichever way they are cut).
+// run_limit: the longest run with several query tokens. Called by the whole CTA, which it
+// synchronises; the caller synchronises again before the scratch is used for something else.
+constexpr int kCostBatch = 8192;
 __device__ __forceinline__ Runs first_run(const KeyWeightParams& p, int* scratch, int run_cost, int run_limit) {
-  __shared__ int tmp[32], start[2];
-  int* cu = scratch;
-  const int ctas = gridDim.x, nt = blockDim.x;
-  int tiles = 0;
-  for (int b = threadIdx.x; b < p.batch; b += nt) {
-    const int S = p.seq_lens[b];
-    cu[b + 1] = request_tiles(p, b);
-    tiles += cu[b + 1];
-    if (blockIdx.x == 0 && S != 0 && cu[b + 1] == 0) flag_status(p.status, MLA_ERR_DEVICE_GUARD);
+  __shared__ int warp_tot[32], start[3];
+  const bool costs = run_cost > 0 && p.batch <= kCostBatch;
+  int* tiles = scratch;                                // [batch + 1] prefix sums of the tiles
+  int* cost = costs ? tiles + p.batch + 1 : tiles;     // and of the cost
+  for (int b = threadIdx.x; b < p.batch; b += blockDim.x) {
+    const int S = p.seq_lens[b], n = request_tiles(p, b);
+    tiles[b + 1] = n;
+    if (costs) cost[b + 1] = n > 0 ? n + run_cost : 0;
+    if (blockIdx.x == 0 && S != 0 && n == 0) flag_status(p.status, MLA_ERR_DEVICE_GUARD);
   }
-  if (threadIdx.x == 0) cu[0] = 0;
-  const int total = block_sum(tiles, tmp);
-  // the smallest quota, up to run_cost tiles above an even share, with CTAs enough
-  int quota = 0;
-  const int even = (total + ctas - 1) / ctas;
-  if (run_cost > 0 && p.batch <= ctas && total > 0) {
-    int lo = even, hi = even + run_cost + 1;           // hi: none
-    while (lo < hi) {
-      const int mid = (lo + hi) / 2;
-      int n = 0;
-      for (int b = threadIdx.x; b < p.batch; b += nt) n += (cu[b + 1] + mid - 1) / mid;
-      if (block_sum(n, tmp) <= ctas) hi = mid;
-      else lo = mid + 1;
-    }
-    if (lo <= even + run_cost) quota = lo;
+  if (threadIdx.x == 0) tiles[0] = cost[0] = 0;
+  __syncthreads();
+  block_inclusive_scan(tiles + 1, p.batch, warp_tot);
+  if (costs) block_inclusive_scan(cost + 1, p.batch, warp_tot);
+  // the tile at cost floor(V k / CTAs) (a cut inside a request's charge falls on its first tile)
+  const long long V = cost[p.batch];
+  auto cut = [&](int k, int* b) {
+    *b = p.batch;
+    if (k == (int)gridDim.x || V == 0) return tiles[p.batch];
+    const long long c = V * k / (int)gridDim.x;
+    *b = last_at_most(cost, p.batch, c);               // its last request with cost[b] <= c: not empty
+    const long long in = c - cost[*b] - (costs ? run_cost : 0);
+    return tiles[*b] + (int)(in < 0 ? 0 : in);
+  };
+  if (threadIdx.x == 0) {
+    int b0, b1;
+    const int t0 = cut(blockIdx.x, &b0), t1 = cut(blockIdx.x + 1, &b1);
+    start[0] = b0;
+    start[1] = t1 > t0 ? t0 - tiles[b0] : 0;
+    start[2] = t1 - t0;
   }
+  __syncthreads();
   Runs run;
   run.p = &p;
   run.limit = p.q_len > 1 ? run_limit : 0x7FFFFFFF;
-  if (quota > 0) {
-    __syncthreads();
-    for (int b = threadIdx.x; b < p.batch; b += nt) cu[b + 1] = (cu[b + 1] + quota - 1) / quota;
-    __syncthreads();
-  }
-  block_inclusive_scan(cu + 1, p.batch, tmp);
-  const int units = cu[p.batch];                       // CTAs in use (quota), or tiles
-  const int u0 = quota ? (int)blockIdx.x : (int)((long long)total * blockIdx.x / ctas);
-  const int u1 = quota ? min(u0 + 1, units) : (int)((long long)total * (blockIdx.x + 1) / ctas);
-  if (threadIdx.x == 0 && u1 > u0) {
-    const int b = last_at_most(cu, p.batch, u0);       // its last request with cu[b] <= u0: not empty
-    start[0] = b;
-    start[1] = u0 - cu[b];
-  }
-  __syncthreads();
-  run.left = u1 > u0 ? u1 - u0 : 0;
+  run.left = start[2];
   run.b = run.left > 0 ? start[0] : 0;
   run.at = run.left > 0 ? start[1] : 0;
   run.tiles = run.left > 0 ? request_tiles(p, run.b) : 0;
-  if (quota && run.left > 0) {                         // part `at` of the request's n
-    const int n = cu[run.b + 1] - cu[run.b], i = run.at;
-    run.at = (int)((long long)run.tiles * i / n);
-    run.left = (int)((long long)run.tiles * (i + 1) / n) - run.at;
-  }
   return run;
 }
 

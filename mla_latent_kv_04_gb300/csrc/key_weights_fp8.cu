@@ -14,7 +14,7 @@
 // scale is one number per thread); the bf16 rotary part is a bf16 product.
 //
 // Against expanding the codes to bf16 in shared memory (converter warps), 64 requests of 1000 to
-// 8192 tokens take 47 us instead of 70. Bound: the cache's bytes, 74 KB (84 KB) a tile, then the
+// 8192 tokens take 44 us instead of 70. Bound: the cache's bytes, 74 KB (84 KB) a tile, then the
 // conversion of a run's query (H x 576 values), about 6 us of integer arithmetic; the MMAs take
 // 2304 cycles a tile.
 #include <math.h>
@@ -110,7 +110,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
-  Runs run = weigh::first_run(p, reinterpret_cast<int*>(basep), 4, 16);
+  // a query's conversion counts as 5 tiles (64 requests of 1000 to 8192 tokens: 44.4 us; as 3 or 7
+  // 45.5, as none 50.5)
+  Runs run = weigh::first_run(p, reinterpret_cast<int*>(basep), 5, 16);
   ptx::tc_fence_before();
   ptx::fence_proxy_async_smem();
   __syncthreads();

@@ -63,8 +63,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
-  // the scan's scratch is the query's place, not yet in use
-  Runs run = first_run(p, reinterpret_cast<int*>(basep), 0, 8);
+  // the scan's scratch is the query's place, not yet in use; a query's load costs about a tile
+  Runs run = first_run(p, reinterpret_cast<int*>(basep), 1, 8);
   ptx::tc_fence_before();
   // the scratch is done with before the query's copy (through the async proxy) may land on it
   ptx::fence_proxy_async_smem();
