@@ -177,15 +177,26 @@ def _cache_row_elems(cfg):
     return cfg.d_latent + cfg.d_rope
 
 
+_device_query = None
+
+
+def _current_device() -> int:
+    global _device_query
+    if _device_query is None:
+        _device_query = _torch()._C._cuda_getDevice if _torch().cuda.is_available() else lambda: 0
+    return _device_query()
+
+
 def _ptr(x, name, dtypes=None, numel=None, allow_none=False):
     if x is None:
         if allow_none:
             return None
         raise ValueError(f"{name} is required")
-    if not x.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if x.get_device() != _torch()._C._cuda_getDevice():
-        raise ValueError(f"{name} is on cuda:{x.get_device()}, which is not the current device")
+    device = x.get_device()
+    if device != _current_device():
+        if not x.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        raise ValueError(f"{name} is on cuda:{device}, which is not the current device")
     if not x.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if dtypes is not None and x.dtype not in dtypes:
@@ -198,8 +209,7 @@ def _ptr(x, name, dtypes=None, numel=None, allow_none=False):
 def _stream(stream):
     if stream is None:
         # the current stream of the current device, without the Stream object around it (4 us a call)
-        c = _torch()._C
-        return c._cuda_getCurrentRawStream(c._cuda_getDevice())
+        return _torch()._C._cuda_getCurrentRawStream(_current_device())
     if isinstance(stream, int):
         return ctypes.c_void_p(stream)
     return ctypes.c_void_p(stream.cuda_stream)

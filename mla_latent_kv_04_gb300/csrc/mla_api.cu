@@ -106,8 +106,14 @@ RopeTable rope_table(const mla_config* c) {
 }
 
 // The frequencies as fractions of a turn in units of 2^-64 (TurnTable), from the same doubles.
-TurnTable turn_table(const mla_config* c) {
-  TurnTable tt;
+// The last table of each thread is kept (its 32 powers are a tenth of a small call's host time).
+const TurnTable& turn_table(const mla_config* c) {
+  static thread_local TurnTable tt;
+  static thread_local float theta = -1.f;
+  static thread_local int d_rope = -1;
+  if (theta == c->rope_theta && d_rope == c->d_rope) return tt;
+  theta = c->rope_theta;
+  d_rope = c->d_rope;
   memset(&tt, 0, sizeof(tt));
   const RopeTable rt = rope_table(c);
   tt.pairs = rt.pairs;

@@ -123,13 +123,9 @@ def test_workspace_sizes(lib):
 
 
 def test_binding_refuses_tensors_of_another_device(monkeypatch):
-    import torch
-
     class OnDevice:
-        is_cuda = True
-
         def __init__(self, device):
-            self.device = device
+            self.device, self.is_cuda = device, device >= 0
 
         def get_device(self):
             return self.device
@@ -140,7 +136,9 @@ def test_binding_refuses_tensors_of_another_device(monkeypatch):
         def data_ptr(self):
             return 4096
 
-    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(M, "_device_query", lambda: 0)
+    with pytest.raises(ValueError, match="must be a CUDA tensor"):
+        M._ptr(OnDevice(-1), "x")
     assert M._ptr(OnDevice(0), "x") == 4096
     with pytest.raises(ValueError, match="not the current device"):
         M._ptr(OnDevice(1), "x")
