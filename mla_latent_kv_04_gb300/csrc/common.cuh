@@ -100,11 +100,11 @@ __device__ __forceinline__ float warp_sum(float v) {
 // Softmax weights of two disjoint key sets from their natural-log LSEs (-inf: no keys; both
 // -inf: both weights 0).
 __device__ __forceinline__ void merge_weights(float lse_a, float lse_b, float* a, float* b) {
-  const float m = fmaxf(lse_a, lse_b);
-  if (m == -INFINITY) {
+  if (lse_a == -INFINITY && lse_b == -INFINITY) {
     *a = *b = 0.f;
     return;
   }
+  const float m = fmaxf(lse_a, lse_b);         // (of NaN and -inf: -inf, and both weights NaN)
   const float ea = expf(lse_a - m), eb = expf(lse_b - m), inv = 1.f / (ea + eb);
   *a = ea * inv;
   *b = eb * inv;

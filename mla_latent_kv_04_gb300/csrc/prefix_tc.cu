@@ -461,12 +461,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       float l_other = 0.f;
       if (!(ok = swap(l, &l_other))) break;
       const float L = w ? l_other + l : l + l_other;
-      const float inv = L > 0.f ? 1.f / L : 0.f;
+      const float inv = L == 0.f ? 0.f : 1.f / L;      // (a NaN in the scores stays one)
       if (!(ok = wait_w(B_ODONE + ((g - 1) & 1), ((g - 1) >> 1) & 1))) break;
       ptx::tc_fence_after();
       const long long slot = 2LL * blockIdx.x + (k_first == 0 ? 1 : 0);
       if (w == 0) {
-        const float lse2 = L > 0.f ? m * c + log2f(L) : -INFINITY;
+        const float lse2 = L == 0.f ? -INFINITY : (m == -INFINITY ? 0.f : m * c) + log2f(L);
         if (!full) work.part_lse[slot * 128 + row] = lse2;
         else if (r < p.rows) p.lse[(long long)r * p.H + h] = row_live ? lse2 * kLn2 : -INFINITY;
       }
@@ -543,10 +543,15 @@ __global__ void __launch_bounds__(256) attend_merge_kernel(const PrefixAttendPar
   };
   const int S = p.seq_lens[r / p.q_len];
   float m = -INFINITY;
-  for (int c = c0; c <= c1; ++c) m = fmaxf(m, work.part_lse[slot(c) * 128 + row]);
+  bool nan = false;
+  for (int c = c0; c <= c1; ++c) {
+    const float lse = work.part_lse[slot(c) * 128 + row];
+    nan |= lse != lse;
+    m = fmaxf(m, lse);
+  }
   float acc[16] = {};
   float sum = 0.f;
-  const bool live = S >= p.q_len && m > -INFINITY;
+  const bool live = S >= p.q_len && (nan || m > -INFINITY);
   if (live) {
     for (int c = c0; c <= c1; ++c) {
       const float w = ptx::ex2(work.part_lse[slot(c) * 128 + row] - m);

@@ -170,10 +170,10 @@ __global__ void __launch_bounds__(128) attend_simt_kernel(PrefixAttendParams p) 
     }
     m = m_new;
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const float inv = l == 0.f ? 0.f : 1.f / l;  // (a NaN in the scores stays one)
   __syncthreads();
   for (int v = tid; v < p.d_v; v += 128) out[v] = from_f32<AT>(o[v] * inv);
-  if (tid == 0) *lse = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+  if (tid == 0) *lse = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 // ======================================================================== key weights

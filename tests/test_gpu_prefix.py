@@ -185,6 +185,28 @@ def test_attend_growing_and_large_scores(act, shape, H):
     check_attend(d, x, lens, act, u, lse)
 
 
+@pytest.mark.parametrize("act,shape,H,B,L", [("f32", "tiny", 16, 4, 300), ("bf16", "tiny", 16, 4, 300),
+                                             ("bf16", "v2", 16, 4, 90), ("bf16", "v2", 16, 4, 2100),
+                                             ("bf16", "v2", 16, 140, 2100)])
+def test_attend_nan_shows_in_output_and_lse(act, shape, H, B, L):
+    """A NaN query makes its own row NaN, a NaN key its head's rows, and nothing else; neither may
+    pass for an empty key set (lse -inf), which the joined projection would leave out."""
+    rng = np.random.default_rng(B + L)
+    d = D.dims(shape, H)
+    x, lens = attend_inputs(rng, d, B, 1, L, act, rng.integers(1, 90, B))
+    cfg = M.make_config(d, act, act)
+    bad = {k: v.copy() for k, v in x.items()}
+    bad["q_nope"][2, 0, 0, 5] = np.nan
+    bad["q_pe"][3, 0, 1, 1] = np.nan
+    bad["keys"][2, L - 1, 0] = np.nan
+    u, lse = attend(cfg, bad, lens, act)
+    hit = np.zeros((B, 1, H), bool)
+    hit[2, 0, 0] = hit[3, 0, 1] = hit[:, 0, 2] = True
+    assert np.isnan(u[hit]).all() and np.isnan(lse[hit]).all()
+    good_u, good_lse = attend(cfg, x, lens, act)
+    assert np.array_equal(u[~hit], good_u[~hit]) and np.array_equal(lse[~hit], good_lse[~hit])
+
+
 def test_attend_same_bits_every_time_on_two_streams_and_captured():
     rng = np.random.default_rng(21)
     d = D.dims("v2", 16)
@@ -291,6 +313,27 @@ def test_output_proj_prefix(act, shape, H, rows):
     tol = du.reshape(rows, -1) @ np.abs(W_O).astype(np.float64) + 4 * H * d.d_v * 2.0 ** -24 * mag + \
         D.EPS[act] * np.abs(want)
     assert_within(out.double().cpu().numpy(), want, tol * 1.01, "out")
+
+
+@pytest.mark.parametrize("act,shape", [("f32", "tiny"), ("bf16", "tiny"), ("bf16", "v2")])
+@pytest.mark.parametrize("rows", [3, 150])
+def test_output_proj_prefix_nan_lse(act, shape, rows):
+    """A NaN LSE, beside an empty key set or another, makes its row NaN and no other."""
+    rng = np.random.default_rng(rows)
+    d = D.dims(shape, 16)
+    o_lat = D.draw(rng, (rows, 16, d.d_latent), act, 0.1)
+    up = D.draw(rng, (rows, 16, d.d_v), act, 0.1)
+    lse, lsep = np.zeros((2, rows, 16), np.float32)
+    lse[0, 0], lsep[0, 0] = -np.inf, np.nan
+    lse[1, 3] = np.nan
+    cfg = M.make_config(d, act, act)
+    out = torch.zeros((rows, d.d_model), dtype=D.torch_type(act), device="cuda")
+    ws = torch.empty(M.mla_output_proj_prefix_workspace_size(cfg, rows), dtype=torch.uint8, device="cuda")
+    M.mla_output_proj_prefix(cfg, D.dev(o_lat, act), D.dev(lse), D.dev(up, act), D.dev(lsep),
+                             D.dev(D.draw(rng, (d.d_latent, 16 * d.d_v), act), act),
+                             D.dev(D.draw(rng, (16 * d.d_v, d.d_model), act), act), out, ws)
+    torch.cuda.synchronize()
+    assert out[:2].isnan().all() and out[2:].isfinite().all()
 
 
 # ----------------------------------------------------------------------------- the three together
