@@ -214,6 +214,7 @@ struct PrefixAttendParams {
   TurnTable tt;
   int32_t* status;
 };
+constexpr int kPrefixShort = 3;        // prefixes of up to so many keys have a kernel of their own
 cudaError_t launch_prefix_attend_simt(mla_dtype act, const PrefixAttendParams& p, cudaStream_t s);
 
 // The tensor-core form (bf16, d_n 128, d_r 64, d_v 128) and its workspace (fp32 pieces).

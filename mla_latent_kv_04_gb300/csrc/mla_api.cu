@@ -779,7 +779,7 @@ mla_status mla_prefix_attend(const mla_config* cfg, const void* q_nope, const vo
   p.scale_log2 = softmax_scale_of(cfg) * kLog2e;
   p.tt = turn_table(cfg);
   p.status = dev_status;
-  cudaError_t e = prefix_attend_tc_supported(cfg) && prefix_len > 0 &&
+  cudaError_t e = prefix_attend_tc_supported(cfg) && prefix_len > kPrefixShort &&
                           aligned16(q_nope, q_pe, keys, values, k_pe, u)
                       ? launch_prefix_attend_tc(p, workspace, (cudaStream_t)stream)
                       : launch_prefix_attend_simt(cfg->act_dtype, p, (cudaStream_t)stream);

@@ -18,7 +18,7 @@ __global__ void __launch_bounds__(256) expand_simt_kernel(PrefixExpandParams p) 
   __shared__ float As[16][64 + 4], Bs[16][64 + 4];
   const int dh = blockIdx.z ? p.d_v : p.d_n;
   const int N = p.H * dh;
-  const int n0 = blockIdx.x * 64, l0 = blockIdx.y * 64;
+  const int n0 = blockIdx.y * 64, l0 = blockIdx.x * 64;
   if (n0 >= N) return;
   const AT* W = reinterpret_cast<const AT*>(blockIdx.z ? p.W_UV : p.W_UK);
   AT* out = reinterpret_cast<AT*>(blockIdx.z ? p.values : p.keys);
@@ -176,6 +176,68 @@ __global__ void __launch_bounds__(128) attend_simt_kernel(PrefixAttendParams p) 
   if (tid == 0) *lse = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
+// The same for a prefix of up to kPrefixShort keys: warp per (query row, head), dims over the lanes,
+// the scores in registers. For every format: the tensor-core kernel's query, two bf16 terms, is
+// too coarse for an LSE of one key, which may be near 0 (relative error 1.4e-6 over normal inputs,
+// 1e-6 with two keys and 6e-7 with three, against 1e-7 here). 128 rows x 128 heads x 1 key take 11.7
+// us (a block per row and head: 69).
+template <typename AT>
+__global__ void __launch_bounds__(256) attend_short_kernel(PrefixAttendParams p) {
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  const int lane = threadIdx.x & 31;
+  const long long g = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);   // row * H + head
+  if (g >= (long long)p.rows * p.H) return;
+  const int r = (int)(g / p.H), h = (int)(g - (long long)r * p.H), S = p.seq_lens[r / p.q_len];
+  AT* out = reinterpret_cast<AT*>(p.u) + g * p.d_v;
+  if (S < p.q_len) {
+    if (S != 0 && h == 0 && lane == 0) flag_status(p.status, MLA_ERR_DEVICE_GUARD);
+    for (int v = lane; v < p.d_v; v += 32) out[v] = from_f32<AT>(0.f);
+    if (lane == 0) p.lse[g] = -INFINITY;
+    return;
+  }
+  const long long pos = (long long)p.L + S - p.q_len + r % p.q_len;
+  const AT* qn = reinterpret_cast<const AT*>(p.q_nope) + g * p.d_n;
+  const AT* qr = reinterpret_cast<const AT*>(p.q_pe) + g * p.d_r;
+  const AT* K = reinterpret_cast<const AT*>(p.keys) + (long long)h * p.L * p.d_n;
+  const AT* V = reinterpret_cast<const AT*>(p.values) + (long long)h * p.L * p.d_v;
+  const AT* kp = reinterpret_cast<const AT*>(p.k_pe);
+  float s[kPrefixShort] = {};
+  for (int i = lane; i < p.d_n; i += 32) {
+    const float x = to_f32(qn[i]);
+#pragma unroll
+    for (int j = 0; j < kPrefixShort; ++j)
+      if (j < p.L) s[j] = fmaf(x, to_f32(K[j * p.d_n + i]), s[j]);
+  }
+  for (int k = lane; k < p.d_r / 2; k += 32) {
+    float sn, cs;
+    turn_sincos<sizeof(AT) == 4>(p.tt, k, pos, &sn, &cs);
+    const float x0 = to_f32(qr[2 * k]), x1 = to_f32(qr[2 * k + 1]);
+    const float y0 = x0 * cs - x1 * sn, y1 = x0 * sn + x1 * cs;
+#pragma unroll
+    for (int j = 0; j < kPrefixShort; ++j)
+      if (j < p.L) s[j] = fmaf(y1, to_f32(kp[j * p.d_r + 2 * k + 1]), fmaf(y0, to_f32(kp[j * p.d_r + 2 * k]), s[j]));
+  }
+  float m = -INFINITY, l = 0.f;
+#pragma unroll
+  for (int j = 0; j < kPrefixShort; ++j) {
+    s[j] = j < p.L ? warp_sum(s[j]) * p.scale_log2 : -INFINITY;
+    m = fmaxf(m, s[j]);
+  }
+  const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll
+  for (int j = 0; j < kPrefixShort; ++j) l += s[j] = exp2f(s[j] - ref);
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  for (int v = lane; v < p.d_v; v += 32) {
+    float o = 0.f;
+#pragma unroll
+    for (int j = 0; j < kPrefixShort; ++j)
+      if (j < p.L) o = fmaf(s[j], to_f32(V[j * p.d_v + v]), o);
+    out[v] = from_f32<AT>(o * inv);
+  }
+  if (lane == 0) p.lse[g] = l == 0.f ? -INFINITY : (ref + log2f(l)) * kLn2;
+}
+
 // ======================================================================== key weights
 // Block per (request, page): the page's rows in shared memory (odd word stride), one head's
 // query per warp at a time, two tokens per lane; the warps' sums meet in warp order.
@@ -260,8 +322,7 @@ cudaError_t launch_prefix_expand_simt(mla_dtype act, mla_dtype cache, const Pref
     using AT = decltype(a);
     using CT = decltype(c);
     const int cols = p.H * (p.d_n > p.d_v ? p.d_n : p.d_v);
-    // one launch covers 65535 x 64 tokens
-    expand_simt_kernel<AT, CT><<<dim3((cols + 63) / 64, (p.L + 63) / 64, 2), 256, 0, s>>>(p);
+    expand_simt_kernel<AT, CT><<<dim3((p.L + 63) / 64, (cols + 63) / 64, 2), 256, 0, s>>>(p);
     note_launch();
     expand_rope_kernel<AT, CT><<<p.L, 64, 0, s>>>(p);
     note_launch();
@@ -270,14 +331,17 @@ cudaError_t launch_prefix_expand_simt(mla_dtype act, mla_dtype cache, const Pref
 }
 
 cudaError_t launch_prefix_attend_simt(mla_dtype act, const PrefixAttendParams& p, cudaStream_t s) {
-  const size_t smem = (size_t)(p.d_n + p.d_r + p.d_v) * 4;
+  const bool brief = p.L > 0 && p.L <= kPrefixShort;
+  const size_t smem = brief ? 0 : (size_t)(p.d_n + p.d_r + p.d_v) * 4;
   auto go = [&](auto a) {
     using AT = decltype(a);
-    cudaError_t e = allow_smem(attend_simt_kernel<AT>, smem);
+    auto kern = brief ? attend_short_kernel<AT> : attend_simt_kernel<AT>;
+    cudaError_t e = allow_smem(kern, smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)p.rows, (unsigned)p.H, 1);
-    cfg.blockDim = dim3(128, 1, 1);
+    cfg.gridDim = brief ? dim3((unsigned)(((long long)p.rows * p.H + 7) / 8), 1, 1)
+                        : dim3((unsigned)p.rows, (unsigned)p.H, 1);
+    cfg.blockDim = dim3(brief ? 256 : 128, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr;
@@ -285,7 +349,7 @@ cudaError_t launch_prefix_attend_simt(mla_dtype act, const PrefixAttendParams& p
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, attend_simt_kernel<AT>, p);
+    e = cudaLaunchKernelEx(&cfg, kern, p);
     if (e == cudaSuccess) note_launch();
     return e;
   };

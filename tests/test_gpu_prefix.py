@@ -127,7 +127,7 @@ def check_attend(d, x, lens, act, u, lse):
 
 @pytest.mark.parametrize("act,shape,H", [("f32", "tiny", 16), ("bf16", "tiny", 16), ("bf16", "v2", 16),
                                          ("bf16", "v2", 3), ("f32", "odd", 3)])
-@pytest.mark.parametrize("B,q,L", [(1, 1, 1), (3, 1, 64), (2, 3, 127), (5, 1, 128), (4, 2, 129), (3, 4, 700),
+@pytest.mark.parametrize("B,q,L", [(1, 1, 1), (7, 2, 2), (1, 3, 3), (2, 1, 4), (130, 1, 1), (3, 1, 64), (2, 3, 127), (5, 1, 128), (4, 2, 129), (3, 4, 700),
                                    (128, 1, 257), (65, 2, 300), (43, 6, 200),
                                    (260, 1, 700), (300, 2, 130)])
 def test_attend(act, shape, H, B, q, L):
@@ -150,10 +150,11 @@ def test_attend_all_heads_and_long_prefix(L):
 
 
 @pytest.mark.parametrize("act,shape,H", [("f32", "tiny", 16), ("bf16", "v2", 16)])
-def test_attend_empty_and_bad_lengths(act, shape, H):
+@pytest.mark.parametrize("L", [150, 2])
+def test_attend_empty_and_bad_lengths(act, shape, H, L):
     rng = np.random.default_rng(3)
     d = D.dims(shape, H)
-    x, lens = attend_inputs(rng, d, 6, 2, 150, act, [0, 2, 1, 9, 0, -5])
+    x, lens = attend_inputs(rng, d, 6, 2, L, act, [0, 2, 1, 9, 0, -5])
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
     u, lse = attend(M.make_config(d, act, act), x, lens, act, status=status)
     assert M.mla_read_device_status(status) == M.MLA_ERR_DEVICE_GUARD
@@ -186,6 +187,7 @@ def test_attend_growing_and_large_scores(act, shape, H):
 
 
 @pytest.mark.parametrize("act,shape,H,B,L", [("f32", "tiny", 16, 4, 300), ("bf16", "tiny", 16, 4, 300),
+                                             ("f32", "tiny", 16, 4, 1), ("bf16", "v2", 16, 4, 3),
                                              ("bf16", "v2", 16, 4, 90), ("bf16", "v2", 16, 4, 2100),
                                              ("bf16", "v2", 16, 140, 2100)])
 def test_attend_nan_shows_in_output_and_lse(act, shape, H, B, L):
