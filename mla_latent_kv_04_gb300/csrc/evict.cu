@@ -64,7 +64,7 @@ struct SelShared {
   uint32_t hist[2][kBins];
   uint32_t warp_tot[32];
   uint32_t counts[2];                          // this CTA's weights above / at the threshold
-  uint32_t digit, left;                        // the chosen digit, and how many are left below it
+  uint32_t digit, left, whole;                 // the chosen digit, how many of it are kept, and whether all
 };
 
 __device__ __forceinline__ uint32_t ld_dsmem_u32(uint32_t addr) {
@@ -156,6 +156,7 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) evict_select_
         if (above < want && want <= above + c[i]) {
           sh.digit = d0 - i;
           sh.left = want - above;
+          sh.whole = want == above + c[i];
         }
         above += c[i];
       }
@@ -163,7 +164,13 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) evict_select_
       prefix |= sh.digit << shift;
       mask |= (bins - 1) << shift;
       want = sh.left;
+      const bool whole = sh.whole && prefix > 0;
       __syncthreads();
+      if (whole) {                             // all weights of these digits are kept: no need of the rest
+        prefix -= 1;                           // (those above this one)
+        want = 0;
+        break;
+      }
     }
   } else {
     __syncthreads();
