@@ -17,7 +17,7 @@ constexpr int kTile = 128;
 __device__ __forceinline__ int request_tiles(const KeyWeightParams& p, int b) {
   const int S = p.seq_lens[b];
   if (S < p.q_len || S <= 0 || S > (long long)p.max_pages * p.P) return 0;
-  return (S + kTile - 1) / kTile;
+  return (S - 1) / kTile + 1;
 }
 
 // A CTA's runs in order: tiles [t0, t1) of request rb, of length S.

@@ -173,13 +173,6 @@ __device__ __forceinline__ bool elect_one() {
   return ok != 0;
 }
 
-// 32-byte global store (32-byte aligned).
-__device__ __forceinline__ void st_global_32b(void* p, const uint32_t (&v)[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
-               ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-               : "memory");
-}
-
 // ---- tcgen05: tensor memory ---------------------------------------------------------------
 __device__ __forceinline__ void tmem_alloc(uint32_t dst_smem, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
@@ -304,11 +297,6 @@ __device__ __forceinline__ void mma_commit(uint32_t bar) {
                ::"r"(bar) : "memory");
 }
 
-// Arrive (release) on another CTA's mbarrier (an address from map_to_rank).
-__device__ __forceinline__ void mbar_arrive_remote(uint32_t remote_bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote_bar) : "memory");
-}
-
 // ---- tcgen05 on a CTA pair (cta_group::2) --------------------------------------------------
 // One MMA over both CTAs' tensor memories: A's M rows and B's N rows are split between the two
 // CTAs' shared memories (same offsets), D's rows between their tensor memories. Issued by one
@@ -340,12 +328,11 @@ __device__ __forceinline__ void mma_bf16_ts_pair(uint32_t d_tmem, uint32_t a_tme
       "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
       ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
 }
-// Arrive on the barrier at this offset of every CTA in the cluster's `mask` (the pair of ranks 0
-// and 1 by default) when every MMA issued so far is done.
-__device__ __forceinline__ void mma_commit_pair(uint32_t bar, uint16_t mask = 3) {
+// Arrive on the barrier at this offset of both CTAs of the pair when every MMA issued so far is done.
+__device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
-      ::"r"(bar), "h"(mask) : "memory");
+      ::"r"(bar), "h"((uint16_t)3) : "memory");
 }
 // TMA load into this CTA's shared memory, the bytes counted on a barrier of either CTA of the pair
 // (an address from map_to_rank).
@@ -362,18 +349,6 @@ __device__ __forceinline__ void tma_load_3d_pair_hint(uint32_t dst, const CUtens
       "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
       " [%0], [%1, {%2, %3, %4}], [%5], %6;"
       ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar), "l"(policy)
-      : "memory");
-}
-
-// The same into every CTA of the cluster's `mask`, at the same offset. Each CTA's bytes are counted
-// on the barrier at `bar`'s offset in it or, `bar` being the even CTA's of the issuer's own pair, in
-// the even CTA of its pair.
-__device__ __forceinline__ void tma_load_3d_pair_multicast(uint32_t dst, const CUtensorMap* map, int x, int y,
-                                                           int z, uint32_t bar, uint16_t mask) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster"
-      " [%0], [%1, {%2, %3, %4}], [%5], %6;"
-      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar), "h"(mask)
       : "memory");
 }
 
