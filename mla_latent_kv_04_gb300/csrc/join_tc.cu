@@ -15,7 +15,8 @@
 // shared memory takes 48 + 64 bytes a cycle instead of 64 + 64. The (tile, 64-deep chunk) units are
 // cut into one contiguous range per pair; pieces of a tile go to the workspace in fp32 and
 // gemm_merge_kernel adds them in order. Fewer rows are bound by W_O's bytes and take the cluster
-// split-K GEMM (gemm_tc.cu).
+// split-K GEMM (gemm_tc.cu). 512 rows take 90 us (join 25, product 54, merge 12, each by itself); 32
+// rows 35 us.
 #include "fp8_tiles.cuh"
 #include "internal.h"
 #include "sm100_ptx.cuh"

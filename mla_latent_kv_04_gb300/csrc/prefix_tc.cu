@@ -27,8 +27,10 @@
 // workspace (fp32) and are merged by attend_merge_kernel. If whole tiles spread evenly enough,
 // the cuts are put between tiles.
 //
-// Bound: at up to about 200 rows the keys' and values' bytes (64 KB per head and block), then
-// the MMAs.
+// Bound: at up to about 200 rows the keys' and values' bytes (64 KB per head and block): 128 rows x
+// 8192 keys take 90 us, 6.1 TB/s. Above, the MMAs would be (54 us for 256 rows x 4096 keys with the
+// low term); it takes 80, since a block's softmax, about as long as its MMAs, overlaps them in part only
+// and 128 heads are two rounds of 76 pairs.
 #include <math.h>
 
 #include "internal.h"
@@ -585,7 +587,7 @@ __global__ void __launch_bounds__(256) attend_merge_kernel(const PrefixAttendPar
 // Cuts between tiles unless that leaves a worker this many blocks (of about a microsecond) more
 // than an even share: a cut tile costs a second epilogue and query load, its pieces' way through
 // the workspace and the merge, 10 us in all. Measured where whole tiles leave 64 blocks instead of
-// 54: 90.4 us uncut and 99.7 cut at 128 rows x 8192 keys, 83.3 and 86.7 at 256 rows x 4096 keys.
+// 54: 90.1 us uncut and 96.8 cut at 128 rows x 8192 keys, 79.9 and 82.6 at 256 rows x 4096 keys.
 constexpr int kCutGain = 12;
 
 static Work plan(int rows, int H, int L) {
