@@ -290,7 +290,19 @@ mla_status mla_query_from_hidden(const mla_config* cfg, int d_q, const void* h, 
  * tokens needs no offset), and mla_prefix_attend rotates the query of token t at
  * prefix_len + seq_lens[b] - q_len + t, where seq_lens counts own tokens only, as given to
  * mla_decode. Every prefix key is visible to every query token. Several prefixes in one
- * batch: one mla_prefix_attend per prefix, on the rows of its requests. */
+ * batch: one mla_prefix_attend per prefix, on the rows of its requests.
+ *
+ * For these calls and those of eviction below: the tensor-core kernels serve bf16 activations at
+ * DeepSeek-V2's head shape (d_n 128, d_r 64, d_v 128, d_c 512, 64-token pages, any number of heads;
+ * key weights 16 to 128 heads by 16) and tensors that start at multiples of 16 bytes; any other
+ * shape, fp32, or a tensor that starts elsewhere takes SIMT kernels with the same results up to
+ * rounding, many times slower at large sizes. The cache has to start at a multiple of 4 bytes (eviction
+ * from an fp32 cache: 16). batch * q_len is limited to 32768 as in mla_decode. A tensor-core
+ * kernel's waits are bounded: should one run out (2 s), the call's work is left undone and
+ * MLA_ERR_TIMEOUT is OR-ed into *dev_status (mla_output_proj_prefix has no such word). Sums are
+ * made in one order, so that every run gives the same bits (except where SIMT kernels serve
+ * mla_output_proj_prefix: like mla_output_proj's, they add the parts of a sum by atomics). Inputs
+ * and outputs must not overlap unless a call says so. */
 
 /* Expand the prefix's cached rows, once per prefix (and weights):
  *   keys[i][l] = c_l W_UK[:, i*d_n : (i+1)*d_n],  values[i][l] = c_l W_UV[:, i*d_v : (i+1)*d_v],
@@ -321,7 +333,8 @@ mla_status mla_prefix_attend_workspace_size(const mla_config* cfg, int batch, in
  *   dtype), lse [batch][q_len][H] (fp32) outputs.
  * The softmax's weights are rounded to the act dtype for the product with the values; scores,
  * maxima, sums and the rotated query are held in fp32 precision (bf16: the rotated query as
- * the sum of two bf16 terms), so lse is an fp32 result.
+ * the sum of two bf16 terms, with an error of 2^-18 of a term; up to 3 keys in fp32), so lse is an
+ * fp32 result. A NaN score makes its row's u and lse NaN.
  * seq_lens[b] == 0 marks an empty request (u = 0, lse = -inf), as does prefix_len == 0 for
  * every request; 0 < seq_lens[b] < q_len is a guard error (same outputs). workspace: 256-byte
  * aligned device buffer of mla_prefix_attend_workspace_size bytes (NULL if that is 0), any
@@ -332,7 +345,9 @@ mla_status mla_prefix_attend(const mla_config* cfg, const void* q_nope, const vo
                              void* workspace, size_t workspace_bytes, int32_t* dev_status,
                              void* stream);
 
-/* Bytes of workspace mla_output_proj_prefix needs for `rows` rows. */
+/* Bytes of workspace mla_output_proj_prefix needs for `rows` rows: u and an fp32 accumulator as
+ * mla_output_proj_unfolded, and with bf16 activations above 128 rows fp32 pieces of the product, up to
+ * 80 MB. */
 mla_status mla_output_proj_prefix_workspace_size(const mla_config* cfg, int rows, size_t* bytes);
 
 /* mla_output_proj_unfolded of the attention over both key sets, own tokens and prefix:
@@ -376,7 +391,8 @@ mla_status mla_absorb_query(const mla_config* cfg, const void* q_nope, const voi
  *   for tokens that were never cached before.
  * Sums are fp32, in a fixed order (the same bits every time). seq_lens[b] == 0: nothing is
  * written. Requests with a bad length and tokens on a bad page are left out, with
- * MLA_ERR_DEVICE_GUARD in *dev_status (optional, OR-ed in). */
+ * MLA_ERR_DEVICE_GUARD in *dev_status (optional, OR-ed in). MLA_ERR_UNSUPPORTED: batch * max_pages
+ * or max_pages * P above 2^31 - 1. */
 mla_status mla_key_weights(const mla_config* cfg, const void* q_lat, const float* lse,
                            const void* cache, int num_pages, const int32_t* block_table,
                            int max_pages, const int32_t* seq_lens, int batch, int q_len, float decay,
@@ -403,7 +419,8 @@ mla_status mla_key_weights(const mla_config* cfg, const void* q_lat, const float
  * A request with seq_lens[b] outside [0, max_pages * P], or more kept tokens than
  * new_max_pages * P, is left alone (kept all -1, new length the old one), and a row whose old
  * or new page is out of range is not moved: MLA_ERR_DEVICE_GUARD in *dev_status (optional,
- * OR-ed in). MLA_ERR_UNSUPPORTED: max_pages * P above 393216. No workspace. */
+ * OR-ed in). MLA_ERR_UNSUPPORTED: max_pages * P above 393216 tokens,
+ * num_pages * P above 2^31 - 1, budget above 2^30. budget > 0, batch at most 32768. No workspace. */
 mla_status mla_evict_cache(const mla_config* cfg, const float* weights, const int32_t* seq_lens,
                            const int32_t* block_table, int max_pages, int batch, int budget,
                            int sinks, int recent, int rotate, void* cache, int num_pages,
