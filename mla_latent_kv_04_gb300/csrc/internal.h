@@ -238,6 +238,7 @@ struct KeyWeightParams {
   const int32_t* block_table;
   const int32_t* seq_lens;
   int max_pages, num_pages, batch, q_len, H, d_c, D, P;
+  int passes, cols;           // tensor-core kernels: passes over a tile, query rows of each
   long long row_bytes;
   float scale_log2;           // softmax scale * log2(e) (* the scale of a per-tensor fp8 cache)
   float decay;
@@ -250,7 +251,7 @@ cudaError_t launch_key_weights_simt(mla_dtype act, mla_dtype cache, const KeyWei
 // The tensor-core form: bf16 activations, any cache, 64-token pages, d_c 512, d_r 64, 16 to 128
 // heads by 16.
 bool key_weights_tc_supported(const mla_config* c, long long num_pages);
-cudaError_t launch_key_weights_tc(mla_dtype cache, const KeyWeightParams& p, cudaStream_t s);
+cudaError_t launch_key_weights_tc(mla_dtype cache, KeyWeightParams p, cudaStream_t s);
 cudaError_t launch_key_weights_fp8(mla_dtype cache, const KeyWeightParams& p, cudaStream_t s);
 
 struct EvictParams {

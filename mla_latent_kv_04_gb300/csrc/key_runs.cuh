@@ -2,8 +2,10 @@
 // requests in order, cut into one contiguous range per CTA; a CTA's tiles of one request, for which
 // it prepares the request's query, are a run. The cuts are at equal cost, where a request costs
 // its tiles plus the preparation of a query, in tiles (every CTA pays one for its first run anyway;
-// the requests' own charges are for the further runs of the CTAs that they begin in). With several
-// query tokens a run is limited in length and passed over once per query token.
+// the requests' own charges are for the further runs of the CTAs that they begin in).
+//
+// Several query tokens are columns of one product as far as they fit (heads * tokens <= 128);
+// otherwise a run is limited in length and passed over once per query token.
 #pragma once
 #include "internal.h"
 #include "prologue.cuh"
@@ -56,7 +58,7 @@ struct Runs {
 
 // The CTA's range. scratch: 2 (batch + 1) ints of shared memory, or batch + 1 if batch is above
 // kCostBatch (run_cost then counts as 0: CTAs have several runs each, whichever way they are cut).
-// run_limit: the longest run with several query tokens. Called by the whole CTA, which it
+// run_limit: the longest run with several passes. Called by the whole CTA, which it
 // synchronises; the caller synchronises again before the scratch is used for something else.
 constexpr int kCostBatch = 8192;
 __device__ __forceinline__ Runs first_run(const KeyWeightParams& p, int* scratch, int run_cost, int run_limit) {
@@ -94,12 +96,27 @@ __device__ __forceinline__ Runs first_run(const KeyWeightParams& p, int* scratch
   __syncthreads();
   Runs run;
   run.p = &p;
-  run.limit = p.q_len > 1 ? run_limit : 0x7FFFFFFF;
+  run.limit = p.passes > 1 ? run_limit : 0x7FFFFFFF;
   run.left = start[2];
   run.b = run.left > 0 ? start[0] : 0;
   run.at = run.left > 0 ? start[1] : 0;
   run.tiles = run.left > 0 ? request_tiles(p, run.b) : 0;
   return run;
+}
+
+// Passes and columns (64 requests of 300 tokens, 16 heads, 4 query tokens: @@A us at once, @@B us in
+// passes).
+inline void set_passes(KeyWeightParams& p) {
+  const bool once = (long long)p.H * p.q_len <= 128;
+  p.passes = once ? 1 : p.q_len;
+  p.cols = once ? p.H * p.q_len : p.H;
+}
+// The first column that counts for token j in pass t (those before belong to query tokens that do
+// not see it).
+__device__ __forceinline__ int first_column(const KeyWeightParams& p, int S, int j, int t) {
+  const int past = j - (S - p.q_len);                  // it is seen from query token `past` on
+  if (p.passes > 1) return past <= t ? 0 : p.cols;
+  return past > 0 ? past * p.H : 0;
 }
 
 // One CTA per SM, and no more than tiles that the tables can hold.

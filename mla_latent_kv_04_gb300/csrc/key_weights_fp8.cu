@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   auto wait = [&](int i, uint32_t parity) { return bounded_wait(bar(i), parity, abort, p.status); };
   auto wait_w = [&](int i, uint32_t parity) { return __all_sync(0xffffffffu, wait(i, parity)) != 0; };
-  const int N = 2 * p.H;
+  const int N = 2 * p.cols;
 
   if (warp == 0) {
     if (lane == 0) {
@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t g = 0;
       bool ok = true;
       while (ok && run.next()) {
-        for (int t = 0; ok && t < p.q_len; ++t) {
+        for (int t = 0; ok && t < p.passes; ++t) {
           int y0 = run.row_of(2 * run.t0), y1 = run.row_of(2 * run.t0 + 1);
           for (int tile = run.t0; ok && tile < run.t1; ++tile) {
             const bool two = (long long)(2 * tile + 1) * 64 < run.S;
@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const CUtensorMap* tm = c < 4 ? &tm_x : &tm_pe;
               const int x = c < 4 ? 128 * c : (kB128 ? 528 : 512);
               ptx::mbar_arrive_expect_tx(full, two ? 2 * half : half);
-              if (p.q_len > 1) {
+              if (p.passes > 1) {
                 ptx::tma_load_3d(dst, tm, x, y0, 0, full);
                 if (two) ptx::tma_load_3d(dst + half, tm, x, y1, 0, full);
               } else {
@@ -163,11 +163,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           drain_wait(bar(B_FULL + i % kStages), (i / kStages) & 1);
     }
   } else if (warp == 1) {
-    const uint32_t idesc = idesc_e4m3(128, N), idesc_pe = ptx::idesc_bf16_f32(128, p.H, false, false);
+    const uint32_t idesc = idesc_e4m3(128, N), idesc_pe = ptx::idesc_bf16_f32(128, p.cols, false, false);
     uint32_t g = 0, q_iter = 0, z = 0;
     bool ok = true;
     while (ok && run.next()) {
-      for (int t = 0; ok && t < p.q_len; ++t, ++q_iter) {
+      for (int t = 0; ok && t < p.passes; ++t, ++q_iter) {
         if (!(ok = wait_w(B_QFULL, q_iter & 1))) break;
         for (int tile = run.t0; ok && tile < run.t1; ++tile) {
           for (int c = 0; c < 5; ++c, ++g) {
@@ -218,27 +218,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     // scores were read (accumulator z - 1).
     auto convert = [&](const Runs& r, int t, uint32_t q_iter, uint32_t z) {
       const int qw = warp - 2;
-      const long long g = (long long)r.rb * p.q_len + t;
+      const long long g = (long long)r.rb * p.passes + t;
       bool good = wait_w(B_QEMPTY, (q_iter & 1) ^ 1);
       if (good && z > 0) good = wait_w(B_ZFREE + ((z - 1) & 1), ((z - 1) >> 1) & 1);
       if (!good) return false;
-      for (int hb = qw; hb < p.H; hb += kQAtOnce * kQWarps) {
+      for (int hb = qw; hb < p.cols; hb += kQAtOnce * kQWarps) {
         uint4 a[kQAtOnce], b[kQAtOnce];
         uint32_t e[kQAtOnce];
         float off[kQAtOnce];
 #pragma unroll
         for (int i = 0; i < kQAtOnce; ++i) {
-          const int h = min(hb + i * kQWarps, p.H - 1);
-          const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const bf16*>(p.q_lat) + (g * p.H + h) * 576);
+          const int h = min(hb + i * kQWarps, p.cols - 1);
+          const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const bf16*>(p.q_lat) + (g * p.cols + h) * 576);
           a[i] = src[2 * lane];
           b[i] = src[2 * lane + 1];
           e[i] = reinterpret_cast<const uint32_t*>(src + 64)[lane];
-          off[i] = p.lse[g * p.H + h] * kLog2e;
+          off[i] = p.lse[g * p.cols + h] * kLog2e;
         }
 #pragma unroll
         for (int i = 0; i < kQAtOnce; ++i) {
           const int h = hb + i * kQWarps;
-          if (h >= p.H) break;
+          if (h >= p.cols) break;
           const uint32_t pe = e[i];
           const uint32_t v[8] = {a[i].x, a[i].y, a[i].z, a[i].w, b[i].x, b[i].y, b[i].z, b[i].w};
           // the largest magnitude, two at a time; the warp's by its bits (NaN above all: kept)
@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int k = 0; k < 4; ++k) split4(v[2 * k], v[2 * k + 1], s, &hi[k], &lo[k]);
           uint8_t* q = basep + (lane >> 3) * kQChunk;
-          const int unit = lane & 7, r1 = h + p.H;
+          const int unit = lane & 7, r1 = h + p.cols;
           *reinterpret_cast<uint4*>(q + h * 128 + ((unit ^ (h & 7)) << 4)) =
               make_uint4(hi[0], hi[1], hi[2], hi[3]);
           *reinterpret_cast<uint4*>(q + r1 * 128 + ((unit ^ (r1 & 7)) << 4)) =
@@ -281,19 +281,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     // the query after this one into L2
     auto prefetch = [&](Runs r, int t) {
-      if (++t == p.q_len) {
+      if (++t == p.passes) {
         if (!r.next()) return;
         t = 0;
       }
-      ptx::bulk_prefetch_l2(reinterpret_cast<const bf16*>(p.q_lat) + ((long long)r.rb * p.q_len + t) * p.H * 576,
-                            (uint32_t)(p.H * 576 * 2));
+      ptx::bulk_prefetch_l2(reinterpret_cast<const bf16*>(p.q_lat) + ((long long)r.rb * p.passes + t) * p.cols * 576,
+                            (uint32_t)(p.cols * 576 * 2));
     };
     constexpr uint32_t kZ = kB128 ? 5 : 1;             // accumulators of a tile
     if (warp < 4 || warp >= 12) {
       uint32_t q_iter = 0, z = 0;
       bool ok = true;
       while (ok && run.next()) {
-        for (int t = 0; ok && t < p.q_len; ++t, ++q_iter) {
+        for (int t = 0; ok && t < p.passes; ++t, ++q_iter) {
           if (!(ok = convert(run, t, q_iter, z))) break;
           z += kZ * (uint32_t)(run.t1 - run.t0);
           if (warp == 2 && lane == 0) prefetch(run, t);
@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // two threads per token: heads H/2 part .. of it
       const int quad = warp & 3, part = warp >= 8 ? 1 : 0, row = 32 * quad + lane;
       const uint32_t t_row = tmem + ((uint32_t)(32 * quad) << 16);
-      const int hh = p.H / 2, h0 = part * hh;            // heads of this thread (a multiple of 8)
+      const int hh = p.cols / 2, h0 = part * hh;         // columns of this thread (a multiple of 8)
       float* half_sum = reinterpret_cast<float*>(basep + kOffSum);
       uint32_t z = 0, x = 0, q_iter = 0;
       bool ok = true;
@@ -312,10 +312,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int32_t* bt = p.block_table + (long long)run.rb * p.max_pages;
         const int S = run.S;
         float* w = p.weights + (long long)run.rb * p.max_pages * p.P;
-        for (int t = 0; ok && t < p.q_len; ++t, ++q_iter) {
+        for (int t = 0; ok && t < p.passes; ++t, ++q_iter) {
           if (!(ok = convert(run, t, q_iter, z) && wait_w(B_QFULL, q_iter & 1))) break;
           for (int tile = run.t0; ok && tile < run.t1; ++tile) {
-            const int j = tile * kTile + row;
+            const int j = tile * kTile + row, from = weigh::first_column(p, S, j, t);
             int page = j < S ? bt[j / 64] : -1;
             if (page >= p.num_pages) page = -1;
             float4 sc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -331,14 +331,17 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int h = h0; h < h0 + hh; h += 8) {
                 uint32_t hi[8], lo[8];
                 ptx::tmem_ld8(d + h, hi);
-                ptx::tmem_ld8(d + p.H + h, lo);
+                ptx::tmem_ld8(d + p.cols + h, lo);
                 ptx::tmem_wait_ld();
+                const bool sees = h >= from;           // (a query token's columns are a multiple of 16)
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                   const float2 f = head[h + i];
                   const float v = fmaf(__uint_as_float(lo[i]), 0.0625f, __uint_as_float(hi[i]));
-                  s4[i & 3] += ptx::ex2(fmaf(v, f.x, -f.y));
+                  const float e = ptx::ex2(fmaf(v, f.x, -f.y));
+                  s4[i & 3] += sees ? e : 0.f;
                 }
+                __syncwarp();                          // the next load is warp-wide
               }
               sum = (s4[0] + s4[1]) + (s4[2] + s4[3]);
               ptx::tc_fence_before();
@@ -361,17 +364,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (i >= hh) break;
                     uint32_t hi[8], lo[8];
                     ptx::tmem_ld8(d + h0 + i, hi);
-                    if (c < 4) ptx::tmem_ld8(d + p.H + h0 + i, lo);
+                    if (c < 4) ptx::tmem_ld8(d + p.cols + h0 + i, lo);
                     ptx::tmem_wait_ld();
+                    // (the last chunk: a query token's columns are a multiple of 16)
+                    if (c < 4) {
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                      if (c < 4) {
+                      for (int k = 0; k < 8; ++k)
                         acc[i + k] = fmaf(s, fmaf(__uint_as_float(lo[k]), 0.0625f, __uint_as_float(hi[k])), acc[i + k]);
-                      } else {
+                    } else if (h0 + i >= from) {
+#pragma unroll
+                      for (int k = 0; k < 8; ++k) {
                         const float2 f = head[h0 + i + k];           // factor 2^-e, offset
                         sum += ptx::ex2(fmaf(fmaf(acc[i + k], f.x, __uint_as_float(hi[k])), p.scale_log2, -f.y));
                       }
                     }
+                    if (c == 4) __syncwarp();                        // the next load is warp-wide
                   }
                   ptx::tc_fence_before();
                   __syncwarp();
@@ -396,10 +403,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) ptx::mbar_arrive(bar(B_TAKEN + quad));
             ++x;
             if (page >= 0) {
-              const bool sees = j <= S - p.q_len + t;
-              const float mass = sees ? sum + other : 0.f;
+              const float mass = sum + other;
               if (t == 0) w[j] = (p.decay != 0.f && j < S - p.q_len) ? fmaf(p.decay, w[j], mass) : mass;
-              else if (sees) w[j] += mass;
+              else if (from == 0) w[j] += mass;
             }
           }
         }

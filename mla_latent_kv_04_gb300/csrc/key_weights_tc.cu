@@ -9,9 +9,10 @@
 // q_lat is an operand as given (bf16), products are exact and sums fp32, so the weights are
 // fp32 results.
 //
-// A run of tiles (key_runs.cuh) loads its request's query (H x 576) once. With several query
-// tokens a run is passed over once per query token (the later passes read its pages from L2), each
-// pass adding to the weights that the same thread wrote before: no atomics, one order of sums.
+// A run of tiles (key_runs.cuh) loads its request's query (H x 576) once; several query tokens are
+// further columns as far as they fit. Otherwise a run is passed over once per query token (the later
+// passes read its pages from L2), each pass adding to the weights that the same thread wrote before:
+// no atomics, one order of sums.
 //
 // Bound: the cache is read once, 147 KB a tile; the MMAs take a third of that time. 32 x 4096
 // tokens take 28.5 us, 5.5 TB/s; four requests of 32K to 128K tokens 76 us, 6.1 TB/s.
@@ -81,7 +82,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t g = 0;
       bool ok = true;
       while (ok && run.next()) {
-        for (int t = 0; ok && t < p.q_len; ++t) {
+        for (int t = 0; ok && t < p.passes; ++t) {
           int y0 = run.row_of(2 * run.t0), y1 = run.row_of(2 * run.t0 + 1);
           for (int tile = run.t0; ok && tile < run.t1; ++tile) {
             const bool two = (long long)(2 * tile + 1) * 64 < run.S;
@@ -91,7 +92,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (!(ok = wait(B_EMPTY + st, ((g / kStages) & 1) ^ 1))) break;
               const uint32_t dst = base + kOffRing + st * kStage, full = bar(B_FULL + st);
               ptx::mbar_arrive_expect_tx(full, two ? kStage : kStage / 2);
-              if (p.q_len > 1) {
+              if (p.passes > 1) {
                 ptx::tma_load_3d(dst, &tm_x, 64 * c, y0, 0, full);
                 if (two) ptx::tma_load_3d(dst + kStage / 2, &tm_x, 64 * c, y1, 0, full);
               } else {
@@ -113,17 +114,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           drain_wait(bar(B_FULL + i % kStages), (i / kStages) & 1);
     }
   } else if (warp == 1) {
-    const uint32_t idesc = ptx::idesc_bf16_f32(128, p.H, false, false);
+    const uint32_t idesc = ptx::idesc_bf16_f32(128, p.cols, false, false);
     uint32_t g = 0, q_iter = 0, z = 0;
     bool ok = true;
     while (ok && run.next()) {
-      for (int t = 0; ok && t < p.q_len; ++t, ++q_iter) {
+      for (int t = 0; ok && t < p.passes; ++t, ++q_iter) {
         // the query of this run and token: B_QEMPTY says that the MMAs on the one before are done
         if (!(ok = wait_w(B_QEMPTY, (q_iter & 1) ^ 1))) break;
         if (ptx::elect_one()) {
-          ptx::mbar_arrive_expect_tx(bar(B_QFULL), kChunks * p.H * 128);
+          ptx::mbar_arrive_expect_tx(bar(B_QFULL), kChunks * p.cols * 128);
           for (int c = 0; c < kChunks; ++c)
-            ptx::tma_load_3d(base + c * kQChunk, &tm_q, 64 * c, 0, run.rb * p.q_len + t, bar(B_QFULL));
+            ptx::tma_load_3d(base + c * kQChunk, &tm_q, 64 * c, 0, run.rb * p.passes + t, bar(B_QFULL));
         }
         __syncwarp();
         if (!(ok = wait_w(B_QFULL, q_iter & 1))) break;
@@ -173,39 +174,42 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int32_t* bt = p.block_table + (long long)run.rb * p.max_pages;
       const int S = run.S;
       float* w = p.weights + (long long)run.rb * p.max_pages * p.P;
-      for (int t = 0; ok && t < p.q_len; ++t) {
-        const float* lse = p.lse + ((long long)run.rb * p.q_len + t) * p.H;
+      for (int t = 0; ok && t < p.passes; ++t) {
+        const float* lse = p.lse + ((long long)run.rb * p.passes + t) * p.cols;
         if (!(ok = meet())) break;
-        if (row < p.H) lse_s[row] = lse[row] * kLog2e;
+        if (row < p.cols) lse_s[row] = lse[row] * kLog2e;
         if (!(ok = meet())) break;
         for (int tile = run.t0; tile < run.t1; ++tile, ++z) {
           if (!(ok = wait_w(B_ZFULL + (z & 1), (z >> 1) & 1))) break;
           ptx::tc_fence_after();
+          const int j = tile * kTile + row, from = first_column(p, S, j, t);
           float sum[4] = {0.f, 0.f, 0.f, 0.f};
-          for (int h0 = 0; h0 < p.H; h0 += 16) {
+          for (int h0 = 0; h0 < p.cols; h0 += 16) {
             uint32_t v[16];
             ptx::tmem_ld16(t_row + 128 * (z & 1) + h0, v);
             ptx::tmem_wait_ld();
+            const bool sees = h0 >= from;              // (a query token's columns are a multiple of 16)
 #pragma unroll
             for (int j = 0; j < 16; j += 4) {
               const float4 off = *reinterpret_cast<const float4*>(lse_s + h0 + j);
-              sum[0] += ptx::ex2(fmaf(__uint_as_float(v[j]), p.scale_log2, -off.x));
-              sum[1] += ptx::ex2(fmaf(__uint_as_float(v[j + 1]), p.scale_log2, -off.y));
-              sum[2] += ptx::ex2(fmaf(__uint_as_float(v[j + 2]), p.scale_log2, -off.z));
-              sum[3] += ptx::ex2(fmaf(__uint_as_float(v[j + 3]), p.scale_log2, -off.w));
+              const float e[4] = {ptx::ex2(fmaf(__uint_as_float(v[j]), p.scale_log2, -off.x)),
+                                  ptx::ex2(fmaf(__uint_as_float(v[j + 1]), p.scale_log2, -off.y)),
+                                  ptx::ex2(fmaf(__uint_as_float(v[j + 2]), p.scale_log2, -off.z)),
+                                  ptx::ex2(fmaf(__uint_as_float(v[j + 3]), p.scale_log2, -off.w))};
+#pragma unroll
+              for (int k = 0; k < 4; ++k) sum[k] += sees ? e[k] : 0.f;
             }
+            __syncwarp();                              // the next load is warp-wide
           }
           ptx::tc_fence_before();
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(bar(B_ZFREE + (z & 1)));
-          const int j = tile * kTile + row;
           if (j < S) {
             const int page = bt[j / 64];
             if (page >= 0 && page < p.num_pages) {
-              const bool sees = j <= S - p.q_len + t;
-              const float mass = sees ? (sum[0] + sum[1]) + (sum[2] + sum[3]) : 0.f;
+              const float mass = (sum[0] + sum[1]) + (sum[2] + sum[3]);
               if (t == 0) w[j] = (p.decay != 0.f && j < S - p.q_len) ? fmaf(p.decay, w[j], mass) : mass;
-              else if (sees) w[j] += mass;
+              else if (from == 0) w[j] += mass;
             }
           }
         }
@@ -228,14 +232,15 @@ bool key_weights_tc_supported(const mla_config* c, long long num_pages) {
          c->num_heads % 16 == 0 && c->num_heads <= 128 && num_pages * 64 <= 0x7FFFFF00LL;
 }
 
-cudaError_t launch_key_weights_tc(mla_dtype cache, const KeyWeightParams& p, cudaStream_t s) {
+cudaError_t launch_key_weights_tc(mla_dtype cache, KeyWeightParams p, cudaStream_t s) {
   using namespace weigh;
+  set_passes(p);
   if (cache != MLA_BF16) return launch_key_weights_fp8(cache, p, s);
   CUtensorMap x, q;
   const uint64_t rows = (uint64_t)p.num_pages * 64;
   if (!tensor_map_bf16(&x, p.cache, kD, rows, 1, kD * 2, rows * kD * 2, 64, 64) ||
-      !tensor_map_bf16(&q, p.q_lat, kD, (uint64_t)p.H, (uint64_t)p.batch * p.q_len, kD * 2,
-                       (uint64_t)p.H * kD * 2, 64, (uint32_t)p.H))
+      !tensor_map_bf16(&q, p.q_lat, kD, (uint64_t)p.cols, (uint64_t)p.batch * p.passes, kD * 2,
+                       (uint64_t)p.cols * kD * 2, 64, (uint32_t)p.cols))
     return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(key_weights_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;

@@ -3,6 +3,8 @@
 // take the DeepSeek-V2 head shape in bf16; these serve the rest and cross-check them.
 #include <math.h>
 
+#include <type_traits>
+
 #include "internal.h"
 #include "page_elem.cuh"
 #include "sm100_ptx.cuh"
@@ -11,11 +13,33 @@ namespace mla {
 namespace {
 
 // ======================================================================== prefix expansion
+template <typename AT, typename CT>
+__device__ __forceinline__ void expand_rope(const PrefixExpandParams& p, int l0) {
+  const int n = min(64, p.L - l0) * p.d_r;
+  for (int i = threadIdx.x; i < n; i += blockDim.x) {
+    const int l = l0 + i / p.d_r, k = i % p.d_r;
+    const int page = p.table[l / p.P];
+    const bool ok = page >= 0 && page < p.num_pages;
+    if (!ok && k == 0) flag_status(p.status, MLA_ERR_DEVICE_GUARD);
+    const uint32_t* row = reinterpret_cast<const uint32_t*>(
+        reinterpret_cast<const uint8_t*>(p.cache) + ((long long)(ok ? page : 0) * p.P + l % p.P) * p.row_bytes);
+    reinterpret_cast<AT*>(p.k_pe)[(long long)l * p.d_r + k] =
+        from_f32<AT>(ok ? page_rope_elem<CT>(row, k, p.d_c) * p.cache_scale : 0.f);
+  }
+}
+
 // keys[h][l] = c_l W_UK[:, h], values[h][l] = c_l W_UV[:, h] (huny.dev "DeepSeek MLA 해부"
-// §2-1: k^C = c W^UK, v^C = c W^UV). 64 x 64 output tile per block; z = 0 keys, 1 values.
+// §2-1: k^C = c W^UK, v^C = c W^UV). 64 x 64 output tile per block; z = 0 keys, 1 values, 2 the
+// rotated keys as cached, k_pe[l], of 64 tokens.
 template <typename AT, typename CT>
 __global__ void __launch_bounds__(256) expand_simt_kernel(PrefixExpandParams p) {
   __shared__ float As[16][64 + 4], Bs[16][64 + 4];
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  if (blockIdx.z == 2) {
+    if (blockIdx.y == 0) expand_rope<AT, CT>(p, blockIdx.x * 64);
+    return;
+  }
   const int dh = blockIdx.z ? p.d_v : p.d_n;
   const int N = p.H * dh;
   const int n0 = blockIdx.y * 64, l0 = blockIdx.x * 64;
@@ -23,28 +47,38 @@ __global__ void __launch_bounds__(256) expand_simt_kernel(PrefixExpandParams p) 
   const AT* W = reinterpret_cast<const AT*>(blockIdx.z ? p.W_UV : p.W_UK);
   AT* out = reinterpret_cast<AT*>(blockIdx.z ? p.values : p.keys);
   const int tid = threadIdx.x, tx = tid % 16, ty = tid / 16;
-  float acc[4][4] = {};
-  for (int k0 = 0; k0 < p.d_c; k0 += 16) {
-    for (int i = tid; i < 64 * 16; i += 256) {
-      const int r = i / 16, k = k0 + i % 16, l = l0 + r;
-      float v = 0.f;
-      if (l < p.L && k < p.d_c) {
-        const int page = p.table[l / p.P];
-        if (page >= 0 && page < p.num_pages) {
-          const uint8_t* row = reinterpret_cast<const uint8_t*>(p.cache) +
-                               ((long long)page * p.P + l % p.P) * p.row_bytes;
-          v = PageElem<CT>::get(reinterpret_cast<const uint32_t*>(row), k, p.d_c);
-        } else if (i % 16 == 0 && k0 == 0 && l % p.P == 0) {
-          flag_status(p.status, MLA_ERR_DEVICE_GUARD);
-        }
-      }
-      As[i % 16][r] = v;
+  // a thread loads dim k0 + tx of four tokens and column tid % 64 of four dims, a step ahead
+  const uint32_t* row[4];
+#pragma unroll
+  for (int m = 0; m < 4; ++m) {
+    const int l = l0 + ty + 16 * m, page = l < p.L ? p.table[l / p.P] : -1;
+    row[m] = nullptr;
+    if (page >= 0 && page < p.num_pages)
+      row[m] = reinterpret_cast<const uint32_t*>(reinterpret_cast<const uint8_t*>(p.cache) +
+                                                 ((long long)page * p.P + l % p.P) * p.row_bytes);
+    else if (tx == 0 && l < p.L && l % p.P == 0)
+      flag_status(p.status, MLA_ERR_DEVICE_GUARD);
+  }
+  float a[4], w[4];
+  auto load = [&](int k0) {
+    const int n = n0 + tid % 64;
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      const int k = k0 + tid / 64 + 4 * m;
+      a[m] = row[m] && k0 + tx < p.d_c ? PageElem<CT>::get(row[m], k0 + tx, p.d_c) : 0.f;
+      w[m] = k < p.d_c && n < N ? to_f32(W[(long long)k * N + n]) : 0.f;
     }
-    for (int i = tid; i < 16 * 64; i += 256) {
-      const int k = k0 + i / 64, n = n0 + i % 64;
-      Bs[i / 64][i % 64] = (k < p.d_c && n < N) ? to_f32(W[(long long)k * N + n]) : 0.f;
+  };
+  float acc[4][4] = {};
+  load(0);
+  for (int k0 = 0; k0 < p.d_c; k0 += 16) {
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      As[tx][ty + 16 * m] = a[m];
+      Bs[tid / 64 + 4 * m][tid % 64] = w[m];
     }
     __syncthreads();
+    if (k0 + 16 < p.d_c) load(k0 + 16);
 #pragma unroll
     for (int kk = 0; kk < 16; ++kk) {
 #pragma unroll
@@ -64,20 +98,6 @@ __global__ void __launch_bounds__(256) expand_simt_kernel(PrefixExpandParams p) 
         out[((long long)(n / dh) * p.L + l) * dh + n % dh] = from_f32<AT>(acc[i][j] * p.cache_scale);
     }
   }
-}
-
-// k_pe[l] = the cache's rotated key of token l, in the activation type. Block per token.
-template <typename AT, typename CT>
-__global__ void __launch_bounds__(64) expand_rope_kernel(PrefixExpandParams p) {
-  const int l = blockIdx.x;
-  const int page = p.table[l / p.P];
-  const bool ok = page >= 0 && page < p.num_pages;
-  if (!ok && threadIdx.x == 0) flag_status(p.status, MLA_ERR_DEVICE_GUARD);
-  const uint32_t* row = reinterpret_cast<const uint32_t*>(
-      reinterpret_cast<const uint8_t*>(p.cache) + ((long long)(ok ? page : 0) * p.P + l % p.P) * p.row_bytes);
-  AT* out = reinterpret_cast<AT*>(p.k_pe) + (long long)l * p.d_r;
-  for (int k = threadIdx.x; k < p.d_r; k += blockDim.x)
-    out[k] = from_f32<AT>(ok ? page_rope_elem<CT>(row, k, p.d_c) * p.cache_scale : 0.f);
 }
 
 // ======================================================================== prefix attention
@@ -239,15 +259,41 @@ __global__ void __launch_bounds__(256) attend_short_kernel(PrefixAttendParams p)
 }
 
 // ======================================================================== key weights
-// Block per (request, page): the page's rows in shared memory (odd word stride), one head's
-// query per warp at a time, two tokens per lane; the warps' sums meet in warp order.
-template <typename AT, typename CT>
-__global__ void __launch_bounds__(256) key_weights_simt_kernel(KeyWeightParams p) {
+// Elements e .. e + 3 of a row in shared memory (e a multiple of 4, as d_c and d_r are).
+template <typename CT>
+__device__ __forceinline__ float4 row_quad(const uint32_t* row, int e, int d_c) {
+  if constexpr (sizeof(CT) == 4 || sizeof(CT) == 2) {
+    return make_float4(PageElem<CT>::get(row, e, d_c), PageElem<CT>::get(row, e + 1, d_c),
+                       PageElem<CT>::get(row, e + 2, d_c), PageElem<CT>::get(row, e + 3, d_c));
+  } else if constexpr (std::is_same<CT, E4m3B128>::value) {
+    if (e >= d_c)
+      return make_float4(page_rope_elem<CT>(row, e - d_c, d_c), page_rope_elem<CT>(row, e - d_c + 1, d_c),
+                         page_rope_elem<CT>(row, e - d_c + 2, d_c), page_rope_elem<CT>(row, e - d_c + 3, d_c));
+    const float4 c = row_quad<uint8_t>(row, e, d_c);
+    const float s = __uint_as_float(row[(d_c >> 2) + (e >> 7)]);
+    return make_float4(c.x * s, c.y * s, c.z * s, c.w * s);
+  } else {
+    const uint32_t w = row[e >> 2];
+    return make_float4(fp8_to_f32((uint8_t)w), fp8_to_f32((uint8_t)(w >> 8)), fp8_to_f32((uint8_t)(w >> 16)),
+                       fp8_to_f32((uint8_t)(w >> 24)));
+  }
+}
+
+// Block per (request, page): the page's rows in shared memory (odd word stride), kQ queries (query
+// token, head) per warp at a time, two tokens per lane: a row's element is read once for kQ products;
+// the warps' sums meet in warp order. Few pages are bound by the latency of a warp's queries in turn,
+// many by shared memory's reads. fp32 tiny shape, 16 heads, 4 query tokens: 2 requests of 319 tokens
+// @@C us, 64 of up to 1000 @@D (one query at a time in 8 warps: 26.5 and 72).
+template <typename AT, typename CT, int kQ>
+__global__ void __launch_bounds__(1024) key_weights_simt_kernel(KeyWeightParams p) {
   extern __shared__ __align__(16) uint32_t smem_kw[];
   const int row_words = (int)(p.row_bytes / 4), stride = row_words | 1;
   uint32_t* page_s = smem_kw;                                     // [P][stride]
-  float* q_s = reinterpret_cast<float*>(smem_kw + p.P * stride);   // [8][D]
-  float* red = q_s + 8 * p.D;                                     // [8][P]
+  const int warps = blockDim.x >> 5;
+  float* q_s = reinterpret_cast<float*>(smem_kw + ((p.P * stride + 3) & ~3));   // [warps][kQ][D]
+  float* red = q_s + warps * kQ * p.D;                            // [warps][P]
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
   const int b = blockIdx.x / p.max_pages, pg = blockIdx.x % p.max_pages;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int S = p.seq_lens[b];
@@ -268,21 +314,36 @@ __global__ void __launch_bounds__(256) key_weights_simt_kernel(KeyWeightParams p
   for (int i = threadIdx.x; i < ntok * row_words; i += blockDim.x)
     page_s[(i / row_words) * stride + i % row_words] = src[i];
   __syncthreads();
-  float* q = q_s + warp * p.D;
+  float* q = q_s + warp * kQ * p.D;
+  const uint32_t* row0 = page_s + min(lane, p.P - 1) * stride;
+  const uint32_t* row1 = page_s + min(lane + 32, p.P - 1) * stride;
+  const int queries = p.q_len * p.H;
+  const AT* ql = reinterpret_cast<const AT*>(p.q_lat) + (long long)b * queries * p.D;
+  const float* lse = p.lse + (long long)b * queries;
   float w0 = 0.f, w1 = 0.f;
-  for (int t = 0; t < p.q_len; ++t) {
-    const int last = S - p.q_len + t - pg * p.P;       // this query token sees tokens 0..last
-    const long long g = (long long)b * p.q_len + t;
-    for (int h = warp; h < p.H; h += 8) {
-      const AT* ql = reinterpret_cast<const AT*>(p.q_lat) + (g * p.H + h) * p.D;
-      __syncwarp();
-      for (int i = lane; i < p.D; i += 32) q[i] = to_f32(ql[i]);
-      __syncwarp();
-      const float off = p.lse[g * p.H + h] * kLog2e;
-      if (lane < ntok && lane <= last)
-        w0 += exp2f(PageElem<CT>::dot(page_s + lane * stride, q, p.D, p.d_c) * p.scale_log2 - off);
-      if (lane + 32 < ntok && lane + 32 <= last)
-        w1 += exp2f(PageElem<CT>::dot(page_s + (lane + 32) * stride, q, p.D, p.d_c) * p.scale_log2 - off);
+  for (int x0 = warp * kQ; x0 < queries; x0 += warps * kQ) {
+    const int nq = min(kQ, queries - x0);
+    __syncwarp();
+    for (int i = lane; i < kQ * p.D; i += 32) q[i] = i < nq * p.D ? to_f32(ql[(long long)x0 * p.D + i]) : 0.f;
+    __syncwarp();
+    float a0[kQ] = {}, a1[kQ] = {};
+#pragma unroll 2
+    for (int e = 0; e < p.D; e += 4) {
+      const float4 r0 = row_quad<CT>(row0, e, p.d_c), r1 = row_quad<CT>(row1, e, p.d_c);
+#pragma unroll
+      for (int k = 0; k < kQ; ++k) {
+        const float4 y = *reinterpret_cast<const float4*>(q + k * p.D + e);
+        a0[k] = fmaf(y.w, r0.w, fmaf(y.z, r0.z, fmaf(y.y, r0.y, fmaf(y.x, r0.x, a0[k]))));
+        a1[k] = fmaf(y.w, r1.w, fmaf(y.z, r1.z, fmaf(y.y, r1.y, fmaf(y.x, r1.x, a1[k]))));
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kQ; ++k) {
+      if (k >= nq) break;
+      const int last = S - p.q_len + (x0 + k) / p.H - pg * p.P;   // its query token sees tokens 0..last
+      const float off = lse[x0 + k] * kLog2e;
+      if (lane < ntok && lane <= last) w0 += exp2f(a0[k] * p.scale_log2 - off);
+      if (lane + 32 < ntok && lane + 32 <= last) w1 += exp2f(a1[k] * p.scale_log2 - off);
     }
   }
   if (lane < p.P) red[warp * p.P + lane] = w0;
@@ -290,7 +351,7 @@ __global__ void __launch_bounds__(256) key_weights_simt_kernel(KeyWeightParams p
   __syncthreads();
   for (int i = threadIdx.x; i < ntok; i += blockDim.x) {
     float mass = 0.f;
-    for (int w = 0; w < 8; ++w) mass += red[w * p.P + i];
+    for (int w = 0; w < warps; ++w) mass += red[w * p.P + i];
     const int j = pg * p.P + i;
     float* dst = p.weights + (long long)b * p.max_pages * p.P + j;
     // a token of this step has no earlier weight
@@ -322,11 +383,18 @@ cudaError_t launch_prefix_expand_simt(mla_dtype act, mla_dtype cache, const Pref
     using AT = decltype(a);
     using CT = decltype(c);
     const int cols = p.H * (p.d_n > p.d_v ? p.d_n : p.d_v);
-    expand_simt_kernel<AT, CT><<<dim3((p.L + 63) / 64, (cols + 63) / 64, 2), 256, 0, s>>>(p);
-    note_launch();
-    expand_rope_kernel<AT, CT><<<p.L, 64, 0, s>>>(p);
-    note_launch();
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((p.L + 63) / 64), (unsigned)((cols + 63) / 64), 3);
+    cfg.blockDim = dim3(256, 1, 1);
+    cfg.stream = s;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, expand_simt_kernel<AT, CT>, p);
+    if (e == cudaSuccess) note_launch();
+    return e;
   });
 }
 
@@ -358,15 +426,33 @@ cudaError_t launch_prefix_attend_simt(mla_dtype act, const PrefixAttendParams& p
 
 cudaError_t launch_key_weights_simt(mla_dtype act, mla_dtype cache, const KeyWeightParams& p,
                                     cudaStream_t s) {
-  const size_t smem = ((size_t)p.P * ((p.row_bytes / 4) | 1) + 8ull * p.D + 8ull * p.P) * 4;
+  // up to 32 warps of 4 queries each, as many as there are queries and as fit beside the page
+  int warps = 32, at_once = 4;
+  auto bytes = [&]() {
+    return (((size_t)p.P * ((p.row_bytes / 4) | 1) + 3) / 4 * 4 + (size_t)warps * (at_once * p.D + p.P)) * 4;
+  };
+  while (warps > 8 && (bytes() > 200 * 1024 || warps / 2 * at_once >= p.q_len * p.H)) warps /= 2;
+  if (bytes() > 220 * 1024) at_once = 1;
+  const size_t smem = bytes();
   return by_format(act, cache, [&](auto a, auto c) {
     using AT = decltype(a);
     using CT = decltype(c);
-    cudaError_t e = allow_smem(key_weights_simt_kernel<AT, CT>, smem);
+    auto kern = at_once == 4 ? key_weights_simt_kernel<AT, CT, 4> : key_weights_simt_kernel<AT, CT, 1>;
+    cudaError_t e = allow_smem(kern, smem);
     if (e != cudaSuccess) return e;
-    key_weights_simt_kernel<AT, CT><<<(unsigned)((long long)p.batch * p.max_pages), 256, smem, s>>>(p);
-    note_launch();
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((long long)p.batch * p.max_pages), 1, 1);
+    cfg.blockDim = dim3(32 * warps, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kern, p);
+    if (e == cudaSuccess) note_launch();
+    return e;
   });
 }
 

@@ -24,6 +24,7 @@ def _built():
 
 FORMATS = [("f32", "tiny", 16), ("bf16", "tiny", 16), ("bf16", "v2", 128), ("bf16", "v2", 16),
            ("fp8_e4m3", "v2", 128), ("fp8_e4m3_b128", "v2", 128), ("fp8_e4m3_b128", "v2", 32),
+           ("bf16", "v2", 32), ("bf16", "v2", 48), ("fp8_e4m3", "v2", 32), ("fp8_e4m3", "v2", 64),
            ("bf16", "v2", 10), ("f32", "odd", 3), ("fp8_e4m3", "odd", 3), ("fp8_e4m3_b128", "odd128", 3)]
 LENS = {1: (1, 63, 64, 65, 130, 700, 0), 2: (2, 3, 64, 129, 0, 517), 4: (4, 5, 127, 128, 300)}
 
@@ -122,10 +123,12 @@ def test_key_weights_shares_of_the_work(kind, lens):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "fp8_e4m3", "fp8_e4m3_b128"])
-def test_key_weights_several_tokens_over_long_runs(kind):
-    """Four query tokens of requests longer than a run, which is passed over once per token."""
+@pytest.mark.parametrize("H", [16, 48])
+def test_key_weights_several_tokens_over_long_runs(kind, H):
+    """Four query tokens of requests longer than a run, which is passed over once per token where their
+    heads do not fit one product."""
     rng = np.random.default_rng(12)
-    c = D.Cache(rng, kind, D.dims("v2", 16), [30000, 5001])
+    c = D.Cache(rng, kind, D.dims("v2", H), [30000, 5001])
     q_lat, lse, scale = weigh_inputs(rng, c, 4)
     old = rng.random((2, c.max_pages * 64)).astype(np.float32)
     got = weigh(c, 4, q_lat, lse, old, 1.0)
