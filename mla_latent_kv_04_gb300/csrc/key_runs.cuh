@@ -104,7 +104,7 @@ __device__ __forceinline__ Runs first_run(const KeyWeightParams& p, int* scratch
   return run;
 }
 
-// Passes and columns (64 requests of 300 tokens, 16 heads, 4 query tokens: @@A us at once, @@B us in
+// Passes and columns (64 requests of 300 tokens, 16 heads, 4 query tokens: 10.5 us at once, 24 in
 // passes).
 inline void set_passes(KeyWeightParams& p) {
   const bool once = (long long)p.H * p.q_len <= 128;
