@@ -238,7 +238,7 @@ struct KeyWeightParams {
   const int32_t* block_table;
   const int32_t* seq_lens;
   int max_pages, num_pages, batch, q_len, H, d_c, D, P;
-  int passes, cols;           // tensor-core kernels: passes over a tile, query rows of each
+  int passes, tokens, cols;   // tensor-core kernels: passes over a tile, query tokens and rows of each
   long long row_bytes;
   float scale_log2;           // softmax scale * log2(e) (* the scale of a per-tensor fp8 cache)
   float decay;

@@ -4,8 +4,8 @@
 // its tiles plus the preparation of a query, in tiles (every CTA pays one for its first run anyway;
 // the requests' own charges are for the further runs of the CTAs that they begin in).
 //
-// Several query tokens are columns of one product as far as they fit (heads * tokens <= 128);
-// otherwise a run is limited in length and passed over once per query token.
+// Several query tokens are columns of one product as far as they fit (heads * tokens <= 128); with more,
+// a run is limited in length and passed over several times.
 #pragma once
 #include "internal.h"
 #include "prologue.cuh"
@@ -104,18 +104,20 @@ __device__ __forceinline__ Runs first_run(const KeyWeightParams& p, int* scratch
   return run;
 }
 
-// Passes and columns (64 requests of 300 tokens, 16 heads, 4 query tokens: 10.5 us at once, 24 in
-// passes).
+// Query tokens of a pass: the largest divisor of q_len with which the columns stay within 128 (64 requests
+// of 300 tokens, 16 heads, 4 query tokens: 10.5 us at once, 24 in four passes).
 inline void set_passes(KeyWeightParams& p) {
-  const bool once = (long long)p.H * p.q_len <= 128;
-  p.passes = once ? 1 : p.q_len;
-  p.cols = once ? p.H * p.q_len : p.H;
+  int m = 1;
+  for (int k = 2; k <= p.q_len && (long long)k * p.H <= 128; ++k)
+    if (p.q_len % k == 0) m = k;
+  p.tokens = m;
+  p.passes = p.q_len / m;
+  p.cols = p.H * m;
 }
-// The first column that counts for token j in pass t (those before belong to query tokens that do
-// not see it).
+// The first column of pass t that counts for token j (those before it, possibly all, belong to query
+// tokens that do not see j).
 __device__ __forceinline__ int first_column(const KeyWeightParams& p, int S, int j, int t) {
-  const int past = j - (S - p.q_len);                  // it is seen from query token `past` on
-  if (p.passes > 1) return past <= t ? 0 : p.cols;
+  const int past = j - (S - p.q_len) - t * p.tokens;
   return past > 0 ? past * p.H : 0;
 }
 

@@ -405,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (page >= 0) {
               const float mass = sum + other;
               if (t == 0) w[j] = (p.decay != 0.f && j < S - p.q_len) ? fmaf(p.decay, w[j], mass) : mass;
-              else if (from == 0) w[j] += mass;
+              else if (from < p.cols) w[j] += mass;
             }
           }
         }

@@ -10,9 +10,9 @@
 // fp32 results.
 //
 // A run of tiles (key_runs.cuh) loads its request's query (H x 576) once; several query tokens are
-// further columns as far as they fit. Otherwise a run is passed over once per query token (the later
-// passes read its pages from L2), each pass adding to the weights that the same thread wrote before:
-// no atomics, one order of sums.
+// further columns as far as they fit. With more a run is passed over several times (the later passes
+// read its pages from L2), each pass adding to the weights that the same thread wrote before: no
+// atomics, one order of sums.
 //
 // Bound: the cache is read once, 147 KB a tile; the MMAs take a third of that time. 32 x 4096
 // tokens take 28.5 us, 5.5 TB/s; four requests of 32K to 128K tokens 76 us, 6.1 TB/s.
@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (page >= 0 && page < p.num_pages) {
               const float mass = (sum[0] + sum[1]) + (sum[2] + sum[3]);
               if (t == 0) w[j] = (p.decay != 0.f && j < S - p.q_len) ? fmaf(p.decay, w[j], mass) : mass;
-              else if (from == 0) w[j] += mass;
+              else if (from < p.cols) w[j] += mass;
             }
           }
         }

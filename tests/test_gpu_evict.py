@@ -123,16 +123,16 @@ def test_key_weights_shares_of_the_work(kind, lens):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "fp8_e4m3", "fp8_e4m3_b128"])
-@pytest.mark.parametrize("H", [16, 48])
-def test_key_weights_several_tokens_over_long_runs(kind, H):
-    """Four query tokens of requests longer than a run, which is passed over once per token where their
-    heads do not fit one product."""
+@pytest.mark.parametrize("H,q_len", [(16, 4), (48, 4), (64, 3), (32, 6)])
+def test_key_weights_several_tokens_over_long_runs(kind, H, q_len):
+    """Several query tokens of requests longer than a run, which is passed over several times where
+    their heads do not fit one product (one, two or three tokens a pass)."""
     rng = np.random.default_rng(12)
-    c = D.Cache(rng, kind, D.dims("v2", H), [30000, 5001])
-    q_lat, lse, scale = weigh_inputs(rng, c, 4)
+    c = D.Cache(rng, kind, D.dims("v2", H), [12000, 5001])
+    q_lat, lse, scale = weigh_inputs(rng, c, q_len)
     old = rng.random((2, c.max_pages * 64)).astype(np.float32)
-    got = weigh(c, 4, q_lat, lse, old, 1.0)
-    check_weights(c, 4, q_lat, lse, scale, old, 1.0, got)
+    got = weigh(c, q_len, q_lat, lse, old, 1.0)
+    check_weights(c, q_len, q_lat, lse, scale, old, 1.0, got)
 
 
 @pytest.mark.parametrize("kind", ["bf16", "fp8_e4m3", "fp8_e4m3_b128"])
