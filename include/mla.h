@@ -300,9 +300,8 @@ mla_status mla_query_from_hidden(const mla_config* cfg, int d_q, const void* h, 
  * from an fp32 cache: 16). batch * q_len is limited to 32768 as in mla_decode. A tensor-core
  * kernel's waits are bounded: should one run out (2 s), the call's work is left undone and
  * MLA_ERR_TIMEOUT is OR-ed into *dev_status (mla_output_proj_prefix has no such word). Sums are
- * made in one order, so that every run gives the same bits (except where SIMT kernels serve
- * mla_output_proj_prefix: like mla_output_proj's, they add the parts of a sum by atomics). Inputs
- * and outputs must not overlap unless a call says so. */
+ * made in one order, so that every run gives the same bits. Inputs and outputs must not overlap
+ * unless a call says so. */
 
 /* Expand the prefix's cached rows, once per prefix (and weights):
  *   keys[i][l] = c_l W_UK[:, i*d_n : (i+1)*d_n],  values[i][l] = c_l W_UV[:, i*d_v : (i+1)*d_v],

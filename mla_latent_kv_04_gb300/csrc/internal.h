@@ -231,6 +231,9 @@ cudaError_t launch_prefix_join_tc(const void* o_lat, const void* W_UV, int rows,
 cudaError_t launch_prefix_project_tc(const void* u, const void* W_O, int rows, int K, int N, void* out, void* part,
                                      int32_t* status, cudaStream_t s);
 
+cudaError_t launch_prefix_project_simt(mla_dtype act, const void* u, const void* W_O, int rows, int K, int N,
+                                       void* out, cudaStream_t s);
+
 struct KeyWeightParams {
   const void* q_lat;          // [batch * q_len][H][D]
   const float* lse;           // [batch * q_len][H], natural log

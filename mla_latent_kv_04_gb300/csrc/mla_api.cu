@@ -566,7 +566,6 @@ mla_status mla_output_proj_prefix(const mla_config* cfg, const void* out_latent,
   if (((uintptr_t)workspace & 255) != 0) return invalid("workspace must be 256-byte aligned");
   cudaStream_t s = (cudaStream_t)stream;
   const size_t acc_bytes = unfolded_acc_bytes(cfg, rows);
-  float* acc = (float*)workspace;
   int32_t* status = (int32_t*)((char*)workspace + acc_bytes);
   char* u = (char*)workspace + acc_bytes + 256;
   const int H = cfg->num_heads, d_c = cfg->d_latent, d_v = cfg->d_v, d = cfg->d_model;
@@ -582,8 +581,7 @@ mla_status mla_output_proj_prefix(const mla_config* cfg, const void* out_latent,
     if (e == cudaSuccess) e = launch_output_proj_tc(u, W_O, rows, H * d_v, d, out, status, s);
   } else {
     e = launch_lift_simt(cfg->act_dtype, out_latent, W_UV, rows, H, d_c, d_v, u, s, &join);
-    if (e == cudaSuccess)
-      e = launch_output_proj_simt_ws(cfg->act_dtype, u, W_O, rows, H * d_v, d, out, acc, s);
+    if (e == cudaSuccess) e = launch_prefix_project_simt(cfg->act_dtype, u, W_O, rows, H * d_v, d, out, s);
   }
   return e == cudaSuccess ? MLA_OK : cuda_fail(e, "mla_output_proj_prefix");
 }

@@ -8,6 +8,7 @@
 #include "internal.h"
 #include "page_elem.cuh"
 #include "sm100_ptx.cuh"
+#include "tc_host.h"
 
 namespace mla {
 namespace {
@@ -101,40 +102,40 @@ __global__ void __launch_bounds__(256) expand_simt_kernel(PrefixExpandParams p) 
 }
 
 // ======================================================================== prefix attention
-// Block per (query row, head): 128 keys at a time, one per thread, with the running maximum
-// and sum of the softmax; the output's dims over the threads, narrow values several times, each
-// copy of the threads taking every so manyth key. Small calls are bound by the latency of their
-// loads, which the unrolled loops keep in flight together.
-template <typename AT>
+// Block per (kR query rows, head): 128 keys at a time, one per thread, with the running maximum and
+// sum of the softmax; the output's dims over the threads, narrow values several times, each copy of
+// the threads taking every so manyth key. Small calls are bound by the latency of their loads, which
+// the unrolled loops keep in flight together; large ones by the loads of keys (a thread reads a row of
+// its own), which several query rows share: 64 rows x 16 heads, tiny shape, 1000 keys @@F us with 4 rows
+// a block, 201 with one.
+template <typename AT, int kR>
 __global__ void __launch_bounds__(128) attend_simt_kernel(PrefixAttendParams p) {
-  extern __shared__ float sm[];
-  float* q = sm;                               // [d_n + d_r]
-  float* o = q + p.d_n + p.d_r;                // [d_v]
-  __shared__ float ps[128], red[4], acc_s[128];
+  extern __shared__ __align__(16) float sm[];
+  const int dn4 = (p.d_n + 3) & ~3, dq = dn4 + p.d_r;
+  float* q = sm;                               // [kR][dq]: content, zeros up to dn4, rotary
+  float* o = q + kR * dq;                      // [kR][d_v]
+  __shared__ float ps[kR][128], red[kR][4], acc_s[128];
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
-  const int r = blockIdx.x, h = blockIdx.y, tid = threadIdx.x;
-  const int S = p.seq_lens[r / p.q_len];
-  AT* out = reinterpret_cast<AT*>(p.u) + ((long long)r * p.H + h) * p.d_v;
-  float* lse = p.lse + (long long)r * p.H + h;
-  if (S < p.q_len || p.L == 0) {               // an empty request (or a bad length): no keys
+  const int r0 = blockIdx.x * kR, nr = min(kR, p.rows - r0), h = blockIdx.y, tid = threadIdx.x;
+  auto own = [&](int r) { return p.seq_lens[(r0 + r) / p.q_len]; };
+  for (int r = 0; r < nr; ++r) {
+    const int S = own(r);
+    const AT* qn = reinterpret_cast<const AT*>(p.q_nope) + ((long long)(r0 + r) * p.H + h) * p.d_n;
+    const AT* qr = reinterpret_cast<const AT*>(p.q_pe) + ((long long)(r0 + r) * p.H + h) * p.d_r;
+    const long long pos = (long long)p.L + S - p.q_len + (r0 + r) % p.q_len;
+    for (int i = tid; i < dn4; i += 128) q[r * dq + i] = i < p.d_n ? to_f32(qn[i]) : 0.f;
+    for (int k = tid; k < p.d_r / 2; k += 128) {
+      float sn, cs;
+      turn_sincos<sizeof(AT) == 4>(p.tt, k, pos, &sn, &cs);
+      const float x0 = to_f32(qr[2 * k]), x1 = to_f32(qr[2 * k + 1]);
+      q[r * dq + dn4 + 2 * k] = x0 * cs - x1 * sn;
+      q[r * dq + dn4 + 2 * k + 1] = x0 * sn + x1 * cs;
+    }
     if (S != 0 && S < p.q_len && h == 0 && tid == 0) flag_status(p.status, MLA_ERR_DEVICE_GUARD);
-    for (int v = tid; v < p.d_v; v += 128) out[v] = from_f32<AT>(0.f);
-    if (tid == 0) *lse = -INFINITY;
-    return;
   }
-  const long long pos = (long long)p.L + S - p.q_len + r % p.q_len;
-  const AT* qn = reinterpret_cast<const AT*>(p.q_nope) + ((long long)r * p.H + h) * p.d_n;
-  const AT* qr = reinterpret_cast<const AT*>(p.q_pe) + ((long long)r * p.H + h) * p.d_r;
-  for (int i = tid; i < p.d_n; i += 128) q[i] = to_f32(qn[i]);
-  for (int k = tid; k < p.d_r / 2; k += 128) {
-    float sn, cs;
-    turn_sincos<sizeof(AT) == 4>(p.tt, k, pos, &sn, &cs);
-    const float x0 = to_f32(qr[2 * k]), x1 = to_f32(qr[2 * k + 1]);
-    q[p.d_n + 2 * k] = x0 * cs - x1 * sn;
-    q[p.d_n + 2 * k + 1] = x0 * sn + x1 * cs;
-  }
-  for (int v = tid; v < p.d_v; v += 128) o[v] = 0.f;
+  for (int i = nr * dq + tid; i < kR * dq; i += 128) q[i] = 0.f;
+  for (int i = tid; i < kR * p.d_v; i += 128) o[i] = 0.f;
   __syncthreads();
   const AT* K = reinterpret_cast<const AT*>(p.keys) + (long long)h * p.L * p.d_n;
   const AT* V = reinterpret_cast<const AT*>(p.values) + (long long)h * p.L * p.d_v;
@@ -142,58 +143,104 @@ __global__ void __launch_bounds__(128) attend_simt_kernel(PrefixAttendParams p) 
   int width = 128;                             // threads that cover the output's dims once
   while (width > 1 && width / 2 >= p.d_v) width /= 2;
   const int copies = 128 / width;
-  float m = -INFINITY, l = 0.f;
+  float m[kR], l[kR], a[kR];
+#pragma unroll
+  for (int r = 0; r < kR; ++r) {
+    m[r] = -INFINITY;
+    l[r] = 0.f;
+  }
   for (int l0 = 0; l0 < p.L; l0 += 128) {
     const int j = l0 + tid;
-    float s = -INFINITY;
+    float s[kR] = {};
     if (j < p.L) {
-      float acc = 0.f;
-#pragma unroll 16
-      for (int i = 0; i < p.d_n; ++i) acc = fmaf(q[i], to_f32(K[(long long)j * p.d_n + i]), acc);
-#pragma unroll 16
-      for (int i = 0; i < p.d_r; ++i) acc = fmaf(q[p.d_n + i], to_f32(kp[(long long)j * p.d_r + i]), acc);
-      s = acc * p.scale_log2;
+      auto add = [&](const float (&k)[4], int at) {
+#pragma unroll
+        for (int r = 0; r < kR; ++r) {
+          const float4 y = *reinterpret_cast<const float4*>(q + r * dq + at);
+          s[r] = fmaf(y.w, k[3], fmaf(y.z, k[2], fmaf(y.y, k[1], fmaf(y.x, k[0], s[r]))));
+        }
+      };
+#pragma unroll 4
+      for (int i = 0; i < dn4; i += 4) {
+        float k[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) k[t] = i + t < p.d_n ? to_f32(K[(long long)j * p.d_n + i + t]) : 0.f;
+        add(k, i);
+      }
+#pragma unroll 4
+      for (int i = 0; i < p.d_r; i += 4) {
+        float k[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) k[t] = to_f32(kp[(long long)j * p.d_r + i + t]);
+        add(k, dn4 + i);
+      }
     }
-    const float wm = warp_max(s);
     __syncthreads();
-    if ((tid & 31) == 0) red[tid >> 5] = wm;
+#pragma unroll
+    for (int r = 0; r < kR; ++r) {
+      s[r] = j < p.L ? s[r] * p.scale_log2 : -INFINITY;
+      const float wm = warp_max(s[r]);
+      if ((tid & 31) == 0) red[r][tid >> 5] = wm;
+    }
     __syncthreads();
-    const float m_new = fmaxf(m, fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])));
-    // no finite score so far (all -inf): keep the sums at zero
-    const float ref = m_new == -INFINITY ? 0.f : m_new;
-    const float a = exp2f(m - ref), e = exp2f(s - ref);
-    ps[tid] = e;
-    const float ws = warp_sum(e);
+    float ws[kR];
+#pragma unroll
+    for (int r = 0; r < kR; ++r) {
+      const float m_new = fmaxf(m[r], fmaxf(fmaxf(red[r][0], red[r][1]), fmaxf(red[r][2], red[r][3])));
+      // no finite score so far (all -inf): keep the sums at zero
+      const float ref = m_new == -INFINITY ? 0.f : m_new;
+      a[r] = exp2f(m[r] - ref);
+      const float e = exp2f(s[r] - ref);
+      ps[r][tid] = e;
+      ws[r] = warp_sum(e);
+      m[r] = m_new;
+    }
     __syncthreads();
-    if ((tid & 31) == 0) red[tid >> 5] = ws;
+#pragma unroll
+    for (int r = 0; r < kR; ++r)
+      if ((tid & 31) == 0) red[r][tid >> 5] = ws[r];
     __syncthreads();
-    l = l * a + ((red[0] + red[1]) + (red[2] + red[3]));
+#pragma unroll
+    for (int r = 0; r < kR; ++r) l[r] = l[r] * a[r] + ((red[r][0] + red[r][1]) + (red[r][2] + red[r][3]));
     const int n = min(128, p.L - l0);
     for (int v0 = 0; v0 < p.d_v; v0 += 128) {
       const int v = v0 + tid % width;
-      float acc = 0.f;
+      float acc[kR] = {};
       if (v < p.d_v) {
 #pragma unroll 8
-        for (int i = tid / width; i < n; i += copies)
-          acc = fmaf(ps[i], to_f32(V[(long long)(l0 + i) * p.d_v + v]), acc);
-      }
-      if (copies > 1) {
-        __syncthreads();
-        acc_s[tid] = acc;
-        __syncthreads();
-        if (tid < width) {
-          acc = 0.f;
-          for (int g = 0; g < copies; ++g) acc += acc_s[g * width + tid];
+        for (int i = tid / width; i < n; i += copies) {
+          const float y = to_f32(V[(long long)(l0 + i) * p.d_v + v]);
+#pragma unroll
+          for (int r = 0; r < kR; ++r) acc[r] = fmaf(ps[r][i], y, acc[r]);
         }
       }
-      if (tid < width && v < p.d_v) o[v] = o[v] * a + acc;
+#pragma unroll
+      for (int r = 0; r < kR; ++r) {
+        if (copies > 1) {
+          __syncthreads();
+          acc_s[tid] = acc[r];
+          __syncthreads();
+          if (tid < width) {
+            acc[r] = 0.f;
+            for (int g = 0; g < copies; ++g) acc[r] += acc_s[g * width + tid];
+          }
+        }
+        if (tid < width && v < p.d_v) o[r * p.d_v + v] = o[r * p.d_v + v] * a[r] + acc[r];
+      }
     }
-    m = m_new;
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;  // (a NaN in the scores stays one)
   __syncthreads();
-  for (int v = tid; v < p.d_v; v += 128) out[v] = from_f32<AT>(o[v] * inv);
-  if (tid == 0) *lse = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+#pragma unroll
+  for (int r = 0; r < kR; ++r) {
+    if (r >= nr) break;
+    // an empty request (or a bad length), or no prefix: no keys
+    const bool live = own(r) >= p.q_len && p.L > 0;
+    const long long g = (long long)(r0 + r) * p.H + h;
+    AT* out = reinterpret_cast<AT*>(p.u) + g * p.d_v;
+    const float inv = l[r] == 0.f ? 0.f : 1.f / l[r];      // (a NaN in the scores stays one)
+    for (int v = tid; v < p.d_v; v += 128) out[v] = from_f32<AT>(live ? o[r * p.d_v + v] * inv : 0.f);
+    if (tid == 0) p.lse[g] = !live || l[r] == 0.f ? -INFINITY : (m[r] + log2f(l[r])) * kLn2;
+  }
 }
 
 // The same for a prefix of up to kPrefixShort keys: warp per (query row, head), dims over the lanes,
@@ -256,6 +303,54 @@ __global__ void __launch_bounds__(256) attend_short_kernel(PrefixAttendParams p)
     out[v] = from_f32<AT>(o * inv);
   }
   if (lane == 0) p.lse[g] = l == 0.f ? -INFINITY : (ref + log2f(l)) * kLn2;
+}
+
+// ======================================================================== u W_O
+// out = u W_O for the joined projection, the sum over K in one order (the split-K form of the other
+// projections adds by atomics, in three launches). Block: 16 rows x 32 columns, 512 of K at a time; a
+// warp has 64 of them, a lane a column, and the warps' sums meet in warp order. Bound by the
+// weights' loads where rows are few: fp32 tiny shape (512 x 256), 32 rows: the whole call @@E us, by
+// atomics 32.
+constexpr int kProjRows = 16, kProjCols = 32, kProjK = 512;
+template <typename AT>
+__global__ void __launch_bounds__(256) project_simt_kernel(const AT* u, const AT* W, AT* out, int rows, int K, int N) {
+  __shared__ __align__(16) float us[kProjRows * kProjK];
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int n = blockIdx.x * kProjCols + lane, r0 = blockIdx.y * kProjRows;
+  float acc[kProjRows] = {};
+  for (int kc = 0; kc < K; kc += kProjK) {
+    __syncthreads();
+#pragma unroll 16
+    for (int i = threadIdx.x; i < kProjRows * kProjK; i += 256) {
+      const int r = r0 + i / kProjK, k = kc + i % kProjK;
+      us[i] = r < rows && k < K ? to_f32(u[(long long)r * K + k]) : 0.f;
+    }
+    __syncthreads();
+    const int k0 = 64 * warp;
+#pragma unroll 8
+    for (int k = k0; k < k0 + 64; k += 4) {
+      float w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = kc + k + j < K && n < N ? to_f32(W[(long long)(kc + k + j) * N + n]) : 0.f;
+#pragma unroll
+      for (int r = 0; r < kProjRows; ++r) {
+        const float4 y = *reinterpret_cast<const float4*>(us + r * kProjK + k);
+        acc[r] = fmaf(y.w, w[3], fmaf(y.z, w[2], fmaf(y.y, w[1], fmaf(y.x, w[0], acc[r]))));
+      }
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < kProjRows; ++r) us[(warp * kProjRows + r) * kProjCols + lane] = acc[r];
+  __syncthreads();
+  for (int i = threadIdx.x; i < kProjRows * kProjCols; i += 256) {
+    const int r = r0 + i / kProjCols, c = blockIdx.x * kProjCols + i % kProjCols;
+    float sum = 0.f;
+    for (int w = 0; w < 8; ++w) sum += us[w * kProjRows * kProjCols + i];
+    if (r < rows && c < N) out[(long long)r * N + c] = from_f32<AT>(sum);
+  }
 }
 
 // ======================================================================== key weights
@@ -400,15 +495,20 @@ cudaError_t launch_prefix_expand_simt(mla_dtype act, mla_dtype cache, const Pref
 
 cudaError_t launch_prefix_attend_simt(mla_dtype act, const PrefixAttendParams& p, cudaStream_t s) {
   const bool brief = p.L > 0 && p.L <= kPrefixShort;
-  const size_t smem = brief ? 0 : (size_t)(p.d_n + p.d_r + p.d_v) * 4;
+  // rows of a block: as many as leave a block per SM
+  int at_once = 8;
+  while (at_once > 1 && (long long)((p.rows + at_once - 1) / at_once) * p.H < device_sms()) at_once /= at_once == 8 ? 2 : 4;
+  const size_t smem = brief ? 0 : (size_t)at_once * (((p.d_n + 3) & ~3) + p.d_r + p.d_v) * 4;
   auto go = [&](auto a) {
     using AT = decltype(a);
-    auto kern = brief ? attend_short_kernel<AT> : attend_simt_kernel<AT>;
+    auto kern = brief ? attend_short_kernel<AT>
+                      : (at_once == 8 ? attend_simt_kernel<AT, 8>
+                                      : (at_once == 4 ? attend_simt_kernel<AT, 4> : attend_simt_kernel<AT, 1>));
     cudaError_t e = allow_smem(kern, smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = brief ? dim3((unsigned)(((long long)p.rows * p.H + 7) / 8), 1, 1)
-                        : dim3((unsigned)p.rows, (unsigned)p.H, 1);
+                        : dim3((unsigned)((p.rows + at_once - 1) / at_once), (unsigned)p.H, 1);
     cfg.blockDim = dim3(brief ? 256 : 128, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
@@ -418,6 +518,27 @@ cudaError_t launch_prefix_attend_simt(mla_dtype act, const PrefixAttendParams& p
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, kern, p);
+    if (e == cudaSuccess) note_launch();
+    return e;
+  };
+  return act == MLA_F32 ? go(float{}) : go(bf16{});
+}
+
+cudaError_t launch_prefix_project_simt(mla_dtype act, const void* u, const void* W_O, int rows, int K, int N,
+                                       void* out, cudaStream_t s) {
+  auto go = [&](auto a) {
+    using AT = decltype(a);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((N + kProjCols - 1) / kProjCols), (unsigned)((rows + kProjRows - 1) / kProjRows), 1);
+    cfg.blockDim = dim3(256, 1, 1);
+    cfg.stream = s;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, project_simt_kernel<AT>, reinterpret_cast<const AT*>(u),
+                                       reinterpret_cast<const AT*>(W_O), reinterpret_cast<AT*>(out), rows, K, N);
     if (e == cudaSuccess) note_launch();
     return e;
   };

@@ -24,7 +24,7 @@ def _built():
 
 FORMATS = [("f32", "tiny", 16), ("bf16", "tiny", 16), ("bf16", "v2", 128), ("bf16", "v2", 16),
            ("fp8_e4m3", "v2", 128), ("fp8_e4m3_b128", "v2", 128), ("fp8_e4m3_b128", "v2", 32),
-           ("bf16", "v2", 32), ("bf16", "v2", 48), ("fp8_e4m3", "v2", 32), ("fp8_e4m3", "v2", 64),
+           ("f32", "v2", 4), ("bf16", "v2", 32), ("bf16", "v2", 48), ("fp8_e4m3", "v2", 32), ("fp8_e4m3", "v2", 64),
            ("bf16", "v2", 10), ("f32", "odd", 3), ("fp8_e4m3", "odd", 3), ("fp8_e4m3_b128", "odd128", 3)]
 LENS = {1: (1, 63, 64, 65, 130, 700, 0), 2: (2, 3, 64, 129, 0, 517), 4: (4, 5, 127, 128, 300)}
 

@@ -281,7 +281,7 @@ def test_unaligned_views():
 # ----------------------------------------------------------------------------- joined projection
 
 @pytest.mark.parametrize("act,shape,H", [("f32", "tiny", 16), ("bf16", "tiny", 16), ("bf16", "v2", 16),
-                                         ("bf16", "v2", 128)])
+                                         ("bf16", "v2", 128), ("f32", "odd", 5), ("f32", "v2", 5)])
 @pytest.mark.parametrize("rows", [1, 33, 130, 300])
 def test_output_proj_prefix(act, shape, H, rows):
     rng = np.random.default_rng(rows)
@@ -315,6 +315,10 @@ def test_output_proj_prefix(act, shape, H, rows):
     tol = du.reshape(rows, -1) @ np.abs(W_O).astype(np.float64) + 4 * H * d.d_v * 2.0 ** -24 * mag + \
         D.EPS[act] * np.abs(want)
     assert_within(out.double().cpu().numpy(), want, tol * 1.01, "out")
+    again = torch.empty_like(out)
+    M.mla_output_proj_prefix(cfg, D.dev(o_lat, act), D.dev(lse), D.dev(up, act), D.dev(lsep),
+                             D.dev(W_UV, act), D.dev(W_O, act), again, ws)
+    assert torch.equal(out, again)                     # same bits
 
 
 @pytest.mark.parametrize("act,shape", [("f32", "tiny"), ("bf16", "tiny"), ("bf16", "v2")])
