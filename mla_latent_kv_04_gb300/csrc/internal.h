@@ -163,13 +163,12 @@ struct PrefixJoin {
 };
 
 // u[r][h][:] = o_lat[r][h][:] . W_i^UV (the latent output lifted to the value width):
-// tensor-core GEMM for bf16 (d_c and d_v multiples of 64), SIMT GEMM otherwise. join: u is
-// the two parts' sum under their softmax weights.
+// tensor-core GEMM for bf16 (d_c and d_v multiples of 64; join: u is the two parts' sum under their
+// softmax weights), SIMT GEMM otherwise.
 cudaError_t launch_lift_tc(const void* o_lat, const void* W_UV, int rows, int H, int d_c, int d_v,
                            void* u, int32_t* status, cudaStream_t s, const PrefixJoin* join = nullptr);
 cudaError_t launch_lift_simt(mla_dtype act, const void* o_lat, const void* W_UV, int rows, int H,
-                             int d_c, int d_v, void* u, cudaStream_t s,
-                             const PrefixJoin* join = nullptr);
+                             int d_c, int d_v, void* u, cudaStream_t s);
 
 // out = o_lat . W_comb; `acc` is an fp32 [rows][N] accumulator in the caller's workspace.
 cudaError_t launch_output_proj_simt_ws(mla_dtype act, const void* o_lat, const void* W_comb,
@@ -231,8 +230,9 @@ cudaError_t launch_prefix_join_tc(const void* o_lat, const void* W_UV, int rows,
 cudaError_t launch_prefix_project_tc(const void* u, const void* W_O, int rows, int K, int N, void* out, void* part,
                                      int32_t* status, cudaStream_t s);
 
-cudaError_t launch_prefix_project_simt(mla_dtype act, const void* u, const void* W_O, int rows, int K, int N,
-                                       void* out, cudaStream_t s);
+cudaError_t launch_prefix_project_simt(mla_dtype act, const void* o_lat, const void* W_UV, const void* W_O, int rows,
+                                       int H, int d_c, int d_v, int N, const PrefixJoin& join, void* u, void* out,
+                                       cudaStream_t s);
 
 struct KeyWeightParams {
   const void* q_lat;          // [batch * q_len][H][D]

@@ -98,27 +98,6 @@ struct StoreEpi {
   }
 };
 
-// Head z's lifted output joined with that of a shared prefix under the two parts' softmax
-// weights, into C[row * ldc + z * dv + col].
-template <typename TC>
-struct JoinEpi {
-  TC* C;
-  const TC* u_prefix;
-  const float* lse;
-  const float* lse_prefix;
-  int heads, dv;
-  __device__ void operator()(int z, int row, int col0, const float* v, int N) const {
-    float a, b;
-    merge_weights(lse[(long long)row * heads + z], lse_prefix[(long long)row * heads + z], &a, &b);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (col0 + j >= N) break;
-      const long long i = ((long long)row * heads + z) * dv + col0 + j;
-      C[i] = from_f32<TC>(merge_parts(a, v[j], b, to_f32(u_prefix[i])));
-    }
-  }
-};
-
 // fp32 atomic accumulation (split-K partial sums).
 struct AtomicAddEpi {
   float* C;
@@ -837,14 +816,7 @@ static cudaError_t output_proj_t(const void* o_lat, const void* W_comb, int rows
 // u[r][h][0:d_v] = o_lat[r][h][:] . W_UV[:, h d_v : (h + 1) d_v], one batch entry per head.
 template <typename T>
 static cudaError_t lift_t(const void* o_lat, const void* W_UV, int rows, int H, int d_c, int d_v,
-                          void* u, cudaStream_t s, const PrefixJoin* join) {
-  if (join) {
-    JoinEpi<T> epi{reinterpret_cast<T*>(u), reinterpret_cast<const T*>(join->u_prefix), join->lse,
-                   join->lse_prefix, H, d_v};
-    return simt_gemm(reinterpret_cast<const T*>(o_lat), (long long)H * d_c, (long long)d_c,
-                     reinterpret_cast<const T*>(W_UV), (long long)H * d_v, (long long)d_v, rows, d_v,
-                     d_c, H, 1, epi, s);
-  }
+                          void* u, cudaStream_t s) {
   StoreEpi<T> epi{reinterpret_cast<T*>(u), (long long)H * d_v, (long long)d_v};
   return simt_gemm(reinterpret_cast<const T*>(o_lat), (long long)H * d_c, (long long)d_c,
                    reinterpret_cast<const T*>(W_UV), (long long)H * d_v, (long long)d_v, rows, d_v,
@@ -852,10 +824,10 @@ static cudaError_t lift_t(const void* o_lat, const void* W_UV, int rows, int H, 
 }
 
 cudaError_t launch_lift_simt(mla_dtype act, const void* o_lat, const void* W_UV, int rows, int H,
-                             int d_c, int d_v, void* u, cudaStream_t s, const PrefixJoin* join) {
+                             int d_c, int d_v, void* u, cudaStream_t s) {
   if (rows <= 0) return cudaSuccess;
-  if (act == MLA_F32) return lift_t<float>(o_lat, W_UV, rows, H, d_c, d_v, u, s, join);
-  return lift_t<bf16>(o_lat, W_UV, rows, H, d_c, d_v, u, s, join);
+  if (act == MLA_F32) return lift_t<float>(o_lat, W_UV, rows, H, d_c, d_v, u, s);
+  return lift_t<bf16>(o_lat, W_UV, rows, H, d_c, d_v, u, s);
 }
 
 cudaError_t launch_output_proj_simt_ws(mla_dtype act, const void* o_lat, const void* W_comb,

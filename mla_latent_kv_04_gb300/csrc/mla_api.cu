@@ -580,8 +580,7 @@ mla_status mla_output_proj_prefix(const mla_config* cfg, const void* out_latent,
     e = launch_lift_tc(out_latent, W_UV, rows, H, d_c, d_v, u, status, s, &join);
     if (e == cudaSuccess) e = launch_output_proj_tc(u, W_O, rows, H * d_v, d, out, status, s);
   } else {
-    e = launch_lift_simt(cfg->act_dtype, out_latent, W_UV, rows, H, d_c, d_v, u, s, &join);
-    if (e == cudaSuccess) e = launch_prefix_project_simt(cfg->act_dtype, u, W_O, rows, H * d_v, d, out, s);
+    e = launch_prefix_project_simt(cfg->act_dtype, out_latent, W_UV, W_O, rows, H, d_c, d_v, d, join, u, out, s);
   }
   return e == cudaSuccess ? MLA_OK : cuda_fail(e, "mla_output_proj_prefix");
 }

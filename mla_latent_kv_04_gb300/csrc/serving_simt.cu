@@ -102,12 +102,26 @@ __global__ void __launch_bounds__(256) expand_simt_kernel(PrefixExpandParams p) 
 }
 
 // ======================================================================== prefix attention
+// Four elements, read at once.
+template <typename AT> struct Quads;
+template <> struct Quads<float> {
+  float4 v;
+  __device__ __forceinline__ float4 get() const { return v; }
+};
+template <> struct Quads<bf16> {
+  uint2 v;
+  __device__ __forceinline__ float4 get() const {
+    return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u), __uint_as_float(v.y << 16),
+                       __uint_as_float(v.y & 0xFFFF0000u));
+  }
+};
+
 // Block per (kR query rows, head): 128 keys at a time, one per thread, with the running maximum and
 // sum of the softmax; the output's dims over the threads, narrow values several times, each copy of
 // the threads taking every so manyth key. Small calls are bound by the latency of their loads, which
 // the unrolled loops keep in flight together; large ones by the loads of keys (a thread reads a row of
-// its own), which several query rows share: 64 rows x 16 heads, tiny shape, 1000 keys @@F us with 4 rows
-// a block, 201 with one.
+// its own), which several query rows share: 64 rows x 16 heads, tiny shape, 1000 keys 52 us with 4 rows
+// a block and four elements a load, 201 with one row and one element.
 template <typename AT, int kR>
 __global__ void __launch_bounds__(128) attend_simt_kernel(PrefixAttendParams p) {
   extern __shared__ __align__(16) float sm[];
@@ -140,6 +154,8 @@ __global__ void __launch_bounds__(128) attend_simt_kernel(PrefixAttendParams p) 
   const AT* K = reinterpret_cast<const AT*>(p.keys) + (long long)h * p.L * p.d_n;
   const AT* V = reinterpret_cast<const AT*>(p.values) + (long long)h * p.L * p.d_v;
   const AT* kp = reinterpret_cast<const AT*>(p.k_pe);
+  typedef Quads<AT> Quad;
+  const bool vec = p.d_n % 4 == 0 && ((reinterpret_cast<uintptr_t>(K) | reinterpret_cast<uintptr_t>(kp)) % sizeof(Quad)) == 0;
   int width = 128;                             // threads that cover the output's dims once
   while (width > 1 && width / 2 >= p.d_v) width /= 2;
   const int copies = 128 / width;
@@ -153,26 +169,32 @@ __global__ void __launch_bounds__(128) attend_simt_kernel(PrefixAttendParams p) 
     const int j = l0 + tid;
     float s[kR] = {};
     if (j < p.L) {
-      auto add = [&](const float (&k)[4], int at) {
+      auto add = [&](float4 k, int at) {
 #pragma unroll
         for (int r = 0; r < kR; ++r) {
           const float4 y = *reinterpret_cast<const float4*>(q + r * dq + at);
-          s[r] = fmaf(y.w, k[3], fmaf(y.z, k[2], fmaf(y.y, k[1], fmaf(y.x, k[0], s[r]))));
+          s[r] = fmaf(y.w, k.w, fmaf(y.z, k.z, fmaf(y.y, k.y, fmaf(y.x, k.x, s[r]))));
         }
       };
+      if (vec) {                               // four elements a load
+        const Quad* kq = reinterpret_cast<const Quad*>(K + (long long)j * p.d_n);
+        const Quad* kr = reinterpret_cast<const Quad*>(kp + (long long)j * p.d_r);
+#pragma unroll 8
+        for (int i = 0; i < p.d_n / 4; ++i) add(kq[i].get(), 4 * i);
+#pragma unroll 8
+        for (int i = 0; i < p.d_r / 4; ++i) add(kr[i].get(), dn4 + 4 * i);
+      } else {
 #pragma unroll 4
-      for (int i = 0; i < dn4; i += 4) {
-        float k[4];
+        for (int i = 0; i < dn4; i += 4) {
+          float k[4];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) k[t] = i + t < p.d_n ? to_f32(K[(long long)j * p.d_n + i + t]) : 0.f;
-        add(k, i);
-      }
-#pragma unroll 4
-      for (int i = 0; i < p.d_r; i += 4) {
-        float k[4];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) k[t] = to_f32(kp[(long long)j * p.d_r + i + t]);
-        add(k, dn4 + i);
+          for (int t = 0; t < 4; ++t) k[t] = i + t < p.d_n ? to_f32(K[(long long)j * p.d_n + i + t]) : 0.f;
+          add(make_float4(k[0], k[1], k[2], k[3]), i);
+        }
+        for (int i = 0; i < p.d_r; i += 4) {
+          const AT* k = kp + (long long)j * p.d_r + i;
+          add(make_float4(to_f32(k[0]), to_f32(k[1]), to_f32(k[2]), to_f32(k[3])), dn4 + i);
+        }
       }
     }
     __syncthreads();
@@ -305,38 +327,48 @@ __global__ void __launch_bounds__(256) attend_short_kernel(PrefixAttendParams p)
   if (lane == 0) p.lse[g] = l == 0.f ? -INFINITY : (ref + log2f(l)) * kLn2;
 }
 
-// ======================================================================== u W_O
-// out = u W_O for the joined projection, the sum over K in one order (the split-K form of the other
-// projections adds by atomics, in three launches). Block: 16 rows x 32 columns, 512 of K at a time; a
-// warp has 64 of them, a lane a column, and the warps' sums meet in warp order. Bound by the
-// weights' loads where rows are few: fp32 tiny shape (512 x 256), 32 rows: the whole call @@E us, by
-// atomics 32.
+// ======================================================================== joined projection
+// out[z] = x[z] W[z] in fp32 sums of one order (the split-K form of the other projections adds by
+// atomics, in three launches). With lse, the lift of head z joined with the prefix's part (`join`).
+// Block: 16 rows x 32 columns, up to 512 of K at a time, an eighth of them per warp and a column
+// per lane; the warps' sums meet in warp order. Few rows are bound by the latency of the loads: fp32
+// tiny shape (512 x 256), 32 rows: lift and product 12 us, by the split-K form 32.
+struct SimtProduct {
+  const void* x;
+  const void* W;
+  void* out;
+  int rows, K, N, heads;
+  long long ldx, ldw, ldo, zx, zw, zo;         // strides of rows and of z
+  PrefixJoin join;                             // lse null: no join
+};
 constexpr int kProjRows = 16, kProjCols = 32, kProjK = 512;
 template <typename AT>
-__global__ void __launch_bounds__(256) project_simt_kernel(const AT* u, const AT* W, AT* out, int rows, int K, int N) {
+__global__ void __launch_bounds__(256) product_simt_kernel(SimtProduct p) {
   __shared__ __align__(16) float us[kProjRows * kProjK];
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, z = blockIdx.z;
   const int n = blockIdx.x * kProjCols + lane, r0 = blockIdx.y * kProjRows;
+  const AT* x = reinterpret_cast<const AT*>(p.x) + z * p.zx;
+  const AT* W = reinterpret_cast<const AT*>(p.W) + z * p.zw;
+  const int chunk = min(kProjK, (p.K + 31) & ~31), slice = chunk / 8;
   float acc[kProjRows] = {};
-  for (int kc = 0; kc < K; kc += kProjK) {
+  for (int kc = 0; kc < p.K; kc += chunk) {
     __syncthreads();
-#pragma unroll 16
-    for (int i = threadIdx.x; i < kProjRows * kProjK; i += 256) {
-      const int r = r0 + i / kProjK, k = kc + i % kProjK;
-      us[i] = r < rows && k < K ? to_f32(u[(long long)r * K + k]) : 0.f;
+#pragma unroll 8
+    for (int i = threadIdx.x; i < kProjRows * chunk; i += 256) {
+      const int r = i / chunk, k = kc + i - r * chunk;
+      us[i] = r0 + r < p.rows && k < p.K ? to_f32(x[(r0 + r) * p.ldx + k]) : 0.f;
     }
     __syncthreads();
-    const int k0 = 64 * warp;
-#pragma unroll 8
-    for (int k = k0; k < k0 + 64; k += 4) {
+#pragma unroll 4
+    for (int k = slice * warp; k < slice * (warp + 1); k += 4) {
       float w[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) w[j] = kc + k + j < K && n < N ? to_f32(W[(long long)(kc + k + j) * N + n]) : 0.f;
+      for (int j = 0; j < 4; ++j) w[j] = kc + k + j < p.K && n < p.N ? to_f32(W[(kc + k + j) * p.ldw + n]) : 0.f;
 #pragma unroll
       for (int r = 0; r < kProjRows; ++r) {
-        const float4 y = *reinterpret_cast<const float4*>(us + r * kProjK + k);
+        const float4 y = *reinterpret_cast<const float4*>(us + r * chunk + k);
         acc[r] = fmaf(y.w, w[3], fmaf(y.z, w[2], fmaf(y.y, w[1], fmaf(y.x, w[0], acc[r]))));
       }
     }
@@ -349,7 +381,14 @@ __global__ void __launch_bounds__(256) project_simt_kernel(const AT* u, const AT
     const int r = r0 + i / kProjCols, c = blockIdx.x * kProjCols + i % kProjCols;
     float sum = 0.f;
     for (int w = 0; w < 8; ++w) sum += us[w * kProjRows * kProjCols + i];
-    if (r < rows && c < N) out[(long long)r * N + c] = from_f32<AT>(sum);
+    if (r >= p.rows || c >= p.N) continue;
+    const long long at = r * p.ldo + z * p.zo + c;
+    if (p.join.lse) {
+      float a, b;
+      merge_weights(p.join.lse[(long long)r * p.heads + z], p.join.lse_prefix[(long long)r * p.heads + z], &a, &b);
+      sum = merge_parts(a, sum, b, to_f32(reinterpret_cast<const AT*>(p.join.u_prefix)[at]));
+    }
+    reinterpret_cast<AT*>(p.out)[at] = from_f32<AT>(sum);
   }
 }
 
@@ -524,12 +563,12 @@ cudaError_t launch_prefix_attend_simt(mla_dtype act, const PrefixAttendParams& p
   return act == MLA_F32 ? go(float{}) : go(bf16{});
 }
 
-cudaError_t launch_prefix_project_simt(mla_dtype act, const void* u, const void* W_O, int rows, int K, int N,
-                                       void* out, cudaStream_t s) {
+static cudaError_t product_simt(mla_dtype act, const SimtProduct& p, int batch, cudaStream_t s) {
   auto go = [&](auto a) {
     using AT = decltype(a);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((N + kProjCols - 1) / kProjCols), (unsigned)((rows + kProjRows - 1) / kProjRows), 1);
+    cfg.gridDim = dim3((unsigned)((p.N + kProjCols - 1) / kProjCols),
+                       (unsigned)((p.rows + kProjRows - 1) / kProjRows), (unsigned)batch);
     cfg.blockDim = dim3(256, 1, 1);
     cfg.stream = s;
     cudaLaunchAttribute attr;
@@ -537,12 +576,22 @@ cudaError_t launch_prefix_project_simt(mla_dtype act, const void* u, const void*
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, project_simt_kernel<AT>, reinterpret_cast<const AT*>(u),
-                                       reinterpret_cast<const AT*>(W_O), reinterpret_cast<AT*>(out), rows, K, N);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, product_simt_kernel<AT>, p);
     if (e == cudaSuccess) note_launch();
     return e;
   };
   return act == MLA_F32 ? go(float{}) : go(bf16{});
+}
+
+cudaError_t launch_prefix_project_simt(mla_dtype act, const void* o_lat, const void* W_UV, const void* W_O, int rows,
+                                       int H, int d_c, int d_v, int N, const PrefixJoin& join, void* u, void* out,
+                                       cudaStream_t s) {
+  const SimtProduct lift{o_lat, W_UV, u, rows, d_c, d_v, H, (long long)H * d_c, (long long)H * d_v,
+                         (long long)H * d_v, d_c, d_v, d_v, join};
+  cudaError_t e = product_simt(act, lift, H, s);
+  if (e != cudaSuccess) return e;
+  const SimtProduct prod{u, W_O, out, rows, H * d_v, N, H, (long long)H * d_v, N, N, 0, 0, 0, {}};
+  return product_simt(act, prod, 1, s);
 }
 
 cudaError_t launch_key_weights_simt(mla_dtype act, mla_dtype cache, const KeyWeightParams& p,
