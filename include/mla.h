@@ -345,8 +345,8 @@ mla_status mla_prefix_attend(const mla_config* cfg, const void* q_nope, const vo
                              void* stream);
 
 /* Bytes of workspace mla_output_proj_prefix needs for `rows` rows: u and an fp32 accumulator as
- * mla_output_proj_unfolded, and with bf16 activations above 128 rows fp32 pieces of the product, up to
- * 80 MB. */
+ * mla_output_proj_unfolded, and with bf16 activations above 128 rows fp32 pieces of the product where
+ * it is cut, up to 80 MB. */
 mla_status mla_output_proj_prefix_workspace_size(const mla_config* cfg, int rows, size_t* bytes);
 
 /* mla_output_proj_unfolded of the attention over both key sets, own tokens and prefix:

@@ -14,7 +14,7 @@
 // row tiles, whose accumulators fill the tensor memory, so that the weights are read once and
 // shared memory takes 48 + 64 bytes a cycle instead of 64 + 64. The (tile, 64-deep chunk) units are
 // cut into one contiguous range per pair; pieces of a tile go to the workspace in fp32 and
-// gemm_merge_kernel adds them in order. Fewer rows are bound by W_O's bytes and take the cluster
+// gemm_merge_kernel adds them in order. Short products (few heads) take whole tiles instead. Fewer rows are bound by W_O's bytes and take the cluster
 // split-K GEMM (gemm_tc.cu). 512 rows take 90 us (join 25, product 54, merge 12, each by itself); 32
 // rows 35 us.
 #include "fp8_tiles.cuh"
@@ -175,12 +175,16 @@ enum { G_FULL = 0, G_EMPTY = 6, G_DFULL = 12, G_DFREE = 14, G_TEAR = 16, G_COUNT
 struct Work {
   int rows, K, N;
   int row_tiles, n_tiles, chunks, pairs;               // tile = n tile * row_tiles + row tile
+  int k_tiles;                                         // row tiles of 256 that share a weight chunk
+  int whole;                                           // 1: cuts between tiles only, no pieces
   bf16* out;
   float* part;                                         // [2 pairs][2 CTAs][kTiles][64][128][4]: columns
                                                        // by 4, rows, column
   int32_t* status;
   __host__ __device__ long long units() const { return (long long)row_tiles * n_tiles * chunks; }
-  __host__ __device__ long long begin(int w) const { return units() * w / pairs; }
+  __host__ __device__ long long begin(int w) const {
+    return whole ? (long long)row_tiles * n_tiles * w / pairs * chunks : units() * w / pairs;
+  }
 };
 
 struct Segment {
@@ -406,18 +410,27 @@ __global__ void __launch_bounds__(256) gemm_merge_kernel(const Work w) {
   }
 }
 
+// Whole tiles of 256 rows, or even cuts of tiles of 256 (more than 256 rows: 512), whose pieces cost a
+// way through the workspace and the merge, as long as some 30 chunks of a tile for every 256 rows: whichever
+// is shorter. 512 rows, the whole call: 16 heads 23 us whole and 36 cut, 32 heads 34.5 and 42; 64 and 128
+// heads are cut (56 and 90 us).
+constexpr int kMergeChunks = 30;
 static Work plan(int rows, int K, int N) {
   Work w{};
   w.rows = rows;
   w.K = K;
   w.N = N;
-  const int tile = rows > 256 ? 512 : 256;
-  w.row_tiles = (rows + tile - 1) / tile;
   w.n_tiles = (N + 255) / 256;
   w.chunks = (K + 63) / 64;
-  const long long units = w.units();
-  const int most = device_sms() > 1 ? device_sms() / 2 : 1;
-  w.pairs = (int)(units < most ? units : most);
+  const int most = device_sms() > 1 ? device_sms() / 2 : 1, k_tiles = rows > 256 ? 2 : 1;
+  auto tiles = [&](int k) { return (long long)((rows + 256 * k - 1) / (256 * k)) * w.n_tiles; };
+  const long long whole = (tiles(1) + most - 1) / most * w.chunks;
+  const long long cut = tiles(k_tiles) * w.chunks * k_tiles / most + kMergeChunks * k_tiles;
+  w.whole = whole <= cut;
+  w.k_tiles = w.whole ? 1 : k_tiles;
+  w.row_tiles = (rows + 256 * w.k_tiles - 1) / (256 * w.k_tiles);
+  const long long parts = w.whole ? tiles(1) : w.units();
+  w.pairs = (int)(parts < most ? parts : most);
   return w;
 }
 
@@ -440,6 +453,7 @@ static cudaError_t run(const CUtensorMap& x, const CUtensorMap& wm, const Work& 
   e = cudaLaunchKernelEx(&cfg, kern, x, wm, w);
   if (e != cudaSuccess) return e;
   note_launch();
+  if (w.whole) return cudaSuccess;
   cfg.gridDim = dim3((unsigned)(w.row_tiles * w.n_tiles), 16, kTiles);
   cfg.blockDim = dim3(256, 1, 1);
   cfg.dynamicSmemBytes = 0;
@@ -462,7 +476,7 @@ static bool pair_gemm(int rows, int N) { return rows > kPairRows && N % 8 == 0; 
 size_t prefix_join_tc_workspace(int rows, int H, int d_v, int N) {
   if (!pair_gemm(rows, N)) return 0;
   const join::gemm2::Work w = join::gemm2::plan(rows, H * d_v, N);
-  return (size_t)2 * w.pairs * 2 * (rows > 256 ? 2 : 1) * 256 * 128 * 4;
+  return w.whole ? 0 : (size_t)2 * w.pairs * 2 * w.k_tiles * 256 * 128 * 4;
 }
 
 cudaError_t launch_prefix_join_tc(const void* o_lat, const void* W_UV, int rows, int H, int d_c, const PrefixJoin& j,
@@ -510,7 +524,7 @@ cudaError_t launch_prefix_project_tc(const void* u, const void* W_O, int rows, i
   if (!tensor_map_bf16(&x, u, (uint64_t)K, (uint64_t)rows, 1, (uint64_t)K * 2, (uint64_t)K * rows * 2, 64, 128) ||
       !tensor_map_bf16(&wm, W_O, (uint64_t)N, (uint64_t)K, 1, (uint64_t)N * 2, (uint64_t)N * K * 2, 64, 64))
     return cudaErrorInvalidValue;
-  return rows > 256 ? gemm2::run<2>(x, wm, w, s) : gemm2::run<1>(x, wm, w, s);
+  return w.k_tiles == 2 ? gemm2::run<2>(x, wm, w, s) : gemm2::run<1>(x, wm, w, s);
 }
 
 }  // namespace mla

@@ -23,10 +23,14 @@ class Dims:
 # rows that are no multiple of 16 bytes
 ODD = W.Dims(num_heads=3, d_model=40, d_latent=60, d_rope=8, d_nope=20, d_v=12)
 ODD128 = W.Dims(num_heads=3, d_model=40, d_latent=128, d_rope=12, d_nope=20, d_v=12)
+# other value and latent widths that the tensor cores take in the joined projection
+VALUE64 = W.Dims(num_heads=5, d_model=256, d_latent=192, d_rope=16, d_nope=32, d_v=64)
+VALUE128 = W.Dims(num_heads=5, d_model=264, d_latent=192, d_rope=16, d_nope=32, d_v=128)
 
 
 def dims(shape, H):
-    return Dims(H, {"v2": W.V2, "tiny": W.TINY, "odd": ODD, "odd128": ODD128}[shape])
+    return Dims(H, {"v2": W.V2, "tiny": W.TINY, "odd": ODD, "odd128": ODD128, "value64": VALUE64,
+                    "value128": VALUE128}[shape])
 
 
 def act_of(cache):

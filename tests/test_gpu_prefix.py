@@ -281,7 +281,8 @@ def test_unaligned_views():
 # ----------------------------------------------------------------------------- joined projection
 
 @pytest.mark.parametrize("act,shape,H", [("f32", "tiny", 16), ("bf16", "tiny", 16), ("bf16", "v2", 16),
-                                         ("bf16", "v2", 128), ("f32", "odd", 5), ("f32", "v2", 5)])
+                                         ("bf16", "v2", 128), ("f32", "odd", 5), ("f32", "v2", 5),
+                                         ("bf16", "value64", 5), ("bf16", "value128", 5)])
 @pytest.mark.parametrize("rows", [1, 33, 130, 300])
 def test_output_proj_prefix(act, shape, H, rows):
     rng = np.random.default_rng(rows)
@@ -321,7 +322,7 @@ def test_output_proj_prefix(act, shape, H, rows):
     assert torch.equal(out, again)                     # same bits
 
 
-@pytest.mark.parametrize("act,shape", [("f32", "tiny"), ("bf16", "tiny"), ("bf16", "v2")])
+@pytest.mark.parametrize("act,shape", [("f32", "tiny"), ("bf16", "tiny"), ("bf16", "v2"), ("bf16", "value64")])
 @pytest.mark.parametrize("rows", [3, 150])
 def test_output_proj_prefix_nan_lse(act, shape, rows):
     """A NaN LSE, beside an empty key set or another, makes its row NaN and no other."""
