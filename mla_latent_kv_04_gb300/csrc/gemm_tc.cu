@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
       const int r = (int)blockIdx.x - main_end;
       const RopeJob& q = gp.rope;
-      if (q.d_r % 16 == 0)
+      if (q.vec)
         rope_body_bf16x8(q.q_pe, q.seq_lens, q.q_len, q.H, q.d_c, q.d_r, q.rt, q.qs, q.planar, q.q_lat,
                          r / q.hblocks, r % q.hblocks, 32, q.f16);
       else

@@ -375,6 +375,7 @@ mla_status mla_decode_ex(const mla_config* cfg, const void* q_nope, const void* 
       rj.planar = planar;
       rj.hblocks = (cfg->num_heads + 31) / 32;
       rj.f16 = f16;
+      rj.vec = rope_vec16(q_pe, rj.q_lat, rj.d_c, rj.d_r);
       rj.qs = q_scale;
       rj.rt = rt;
       e = launch_query_absorb_tc(q_nope, W_UK_abs, batch * q_len, cfg->num_heads, cfg->d_nope,
@@ -655,7 +656,10 @@ mla_status mla_absorb_query(const mla_config* cfg, const void* q_nope, const voi
   const RopeTable rt = rope_table(cfg);
   const int D = cfg->d_latent + cfg->d_rope;
   cudaError_t e;
-  if (cfg->act_dtype == MLA_BF16) {
+  // the tensor maps of the GEMM want 16-byte starts and row strides; the rotation and the stores to
+  // q_lat go element by element where they have to
+  if (cfg->act_dtype == MLA_BF16 && cfg->d_nope % 8 == 0 && cfg->d_latent % 8 == 0 &&
+      aligned16(q_nope, W_UK_abs)) {
     RopeJob rj;
     rj.q_pe = reinterpret_cast<const bf16*>(q_pe);
     rj.seq_lens = seq_lens;
@@ -668,6 +672,7 @@ mla_status mla_absorb_query(const mla_config* cfg, const void* q_nope, const voi
     rj.planar = 0;
     rj.hblocks = (cfg->num_heads + 31) / 32;
     rj.f16 = 0;
+    rj.vec = rope_vec16(q_pe, q_lat, rj.d_c, rj.d_r);
     rj.qs = 1.f;
     rj.rt = rt;
     e = launch_query_absorb_tc(q_nope, W_UK_abs, batch * q_len, cfg->num_heads, cfg->d_nope,

@@ -281,6 +281,13 @@ __device__ __forceinline__ void rope_body_bf16x8(const bf16* __restrict__ q_pe, 
   }
 }
 
+// Whether rope_body_bf16x8 may read q_pe and write q_lat: every run of 16 elements then starts at a
+// multiple of 16 bytes in both (D = d_c + d_r is a multiple of 8).
+inline bool rope_vec16(const void* q_pe, const void* q_lat, int d_c, int d_r) {
+  return d_r % 16 == 0 && d_c % 8 == 0 &&
+         ((reinterpret_cast<uintptr_t>(q_pe) | reinterpret_cast<uintptr_t>(q_lat)) & 15) == 0;
+}
+
 // One rotation job: q_pe of `groups` groups into the rotated part of q_lat, one block per
 // (group, 32 heads).
 struct RopeJob {
@@ -289,6 +296,7 @@ struct RopeJob {
   bf16* q_lat;
   int groups, q_len, H, d_c, d_r, planar, hblocks;
   int f16;     // store the rotated query as f16 (the tensor-core kernel on an e4m3 cache)
+  int vec;     // 16 bytes at a time (rope_vec16), else element by element
   float qs;
   RopeTable rt;
 };

@@ -136,3 +136,11 @@ def assert_within(got, ref, tol, what):
         f"{what}: off by {err[over.argmax()]:.3e}, allowed {tol[fin][over.argmax()]:.3e}, "
         f"{(over > 0).sum()} of {err.size} values")
     assert np.isfinite(got[fin]).all(), f"{what}: NaN or infinity"
+
+
+def shifted(t, elements=1):
+    """The same values at an address that is no multiple of 16 bytes."""
+    flat = torch.empty(t.numel() + 16, dtype=t.dtype, device=t.device)
+    view = flat[elements: elements + t.numel()].view(t.shape)
+    view.copy_(t)
+    return view
