@@ -61,12 +61,14 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* warp_tot, u
   return x - v + (wid ? warp_tot[wid - 1] : 0u);
 }
 
+constexpr int kSelStatic = 18 * 1024;          // of the selection's static shared memory, at most
 struct SelShared {
   uint32_t hist[2][kBins];
   uint32_t warp_tot[32];
   uint32_t counts[2];                          // this CTA's weights above / at the threshold
   uint32_t digit, left, whole;                 // the chosen digit, how many of it are kept, and whether all
 };
+static_assert(sizeof(SelShared) <= kSelStatic && kSegMax * 4 + kSelStatic <= (int)kSmemPerCta, "shared memory per CTA");
 
 __device__ __forceinline__ uint32_t ld_dsmem_u32(uint32_t addr) {
   uint32_t v;
@@ -409,7 +411,7 @@ template <int kSelThreads>
 cudaError_t select(const EvictParams& p, int C, int seg, cudaStream_t s) {
   auto kern = evict_select_kernel<kSelThreads>;
   const size_t smem = (size_t)(seg > 1 ? seg : 1) * 4;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = allow_smem(kern, smem, kSelStatic);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(p.batch * C), 1, 1);

@@ -13,6 +13,7 @@
 #include "page_elem.cuh"
 #include "prologue.cuh"
 #include "sm100_ptx.cuh"
+#include "tc_host.h"
 
 namespace mla {
 
@@ -545,11 +546,8 @@ __global__ void f32_to_act_kernel(const float* __restrict__ src, T* __restrict__
 // ======================================================================== launchers
 cudaError_t launch_plan(const PlanParams& p, cudaStream_t s) {
   const size_t smem = (size_t)(4 * (p.batch * p.q_len + 1) + 3 * (p.workers + 1) + 32) * sizeof(int);
-  if (smem > 48 * 1024) {
-    cudaError_t e = cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)smem);
-    if (e != cudaSuccess) return e;
-  }
+  cudaError_t e = allow_smem(plan_kernel, smem);
+  if (e != cudaSuccess) return e;
   plan_kernel<<<1, 256, smem, s>>>(p);
   note_launch();
   return cudaGetLastError();
@@ -583,10 +581,9 @@ cudaError_t launch_prep(const PlanParams& pp, const void* q_pe, const int32_t* s
   const bool plan = pp.workers > 0;
   const size_t smem = plan ? plan_smem_bytes(groups, pp.workers) : 0;
   auto kern = prep_kernel<bf16>;
-  if (smem > 48 * 1024) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-  }
+  // (the rotation's sines and cosines: 1 KB)
+  cudaError_t e = allow_smem(kern, smem, 2 * kMaxRopePairs * sizeof(float));
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((plan ? 1 : 0) + groups * hblocks, 1, 1);
   cfg.blockDim = dim3(256, 1, 1);
@@ -597,7 +594,7 @@ cudaError_t launch_prep(const PlanParams& pp, const void* q_pe, const int32_t* s
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = plan ? 0 : 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, kern, pp, reinterpret_cast<const bf16*>(q_pe), seq_lens, q_len,
+  e = cudaLaunchKernelEx(&cfg, kern, pp, reinterpret_cast<const bf16*>(q_pe), seq_lens, q_len,
                                      H, d_c, d_r, rt, q_scale, planar, reinterpret_cast<bf16*>(q_lat),
                                      hblocks, f16);
   note_launch();
@@ -637,10 +634,8 @@ static cudaError_t decode_simt_t(const DecodeParams& p, cudaStream_t s) {
   const int stride = row_words | 1;
   const size_t smem = (size_t)p.P * stride * 4 + (size_t)SIMT_HEADS * p.D * 4;
   auto kern = decode_simt_kernel<QT, CT, VPL>;
-  if (smem > 48 * 1024) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-  }
+  cudaError_t e = allow_smem(kern, smem);
+  if (e != cudaSuccess) return e;
   dim3 grid(p.workers, (p.H + SIMT_HEADS - 1) / SIMT_HEADS);
   kern<<<grid, 256, smem, s>>>(p);
   note_launch();

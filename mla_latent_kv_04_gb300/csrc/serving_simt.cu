@@ -502,12 +502,6 @@ cudaError_t by_format(mla_dtype act, mla_dtype cache, F f) {
   return f(bf16{}, E4m3B128{});
 }
 
-template <typename K>
-cudaError_t allow_smem(K kern, size_t bytes) {
-  if (bytes <= 48 * 1024) return cudaSuccess;
-  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-}
-
 }  // namespace
 
 cudaError_t launch_prefix_expand_simt(mla_dtype act, mla_dtype cache, const PrefixExpandParams& p,
@@ -543,7 +537,8 @@ cudaError_t launch_prefix_attend_simt(mla_dtype act, const PrefixAttendParams& p
     auto kern = brief ? attend_short_kernel<AT>
                       : (at_once == 8 ? attend_simt_kernel<AT, 8>
                                       : (at_once == 4 ? attend_simt_kernel<AT, 4> : attend_simt_kernel<AT, 1>));
-    cudaError_t e = allow_smem(kern, smem);
+    // (a block's static arrays: 528 bytes a row and 512, here rounded up)
+    cudaError_t e = allow_smem(kern, smem, 528 * at_once + 1024);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = brief ? dim3((unsigned)(((long long)p.rows * p.H + 7) / 8), 1, 1)

@@ -53,4 +53,16 @@ inline int device_sms() {
   return cached[dev];
 }
 
+// Shared memory of one CTA (227 KB), static and dynamic together.
+constexpr size_t kSmemPerCta = 232448;
+
+// Lets a kernel with `fixed` bytes of static shared memory have more than 48 KB in all. The limit
+// belongs to the kernel and not to a launch, so it goes to the most that any call may need: set to
+// one call's need, another host thread could lower it between this call's setting and its launch.
+template <typename K>
+inline cudaError_t allow_smem(K kern, size_t dynamic, size_t fixed = 0) {
+  if (dynamic + fixed <= 48 * 1024) return cudaSuccess;
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(kSmemPerCta - fixed));
+}
+
 }  // namespace mla

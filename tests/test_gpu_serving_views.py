@@ -1,5 +1,7 @@
 """The serving calls on tensors that start off a 16-byte boundary, on head shapes that no tensor map
 takes, and at the edges of their kernels' limits."""
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -7,6 +9,8 @@ import torch
 import mla_latent_kv_04_gb300 as M
 import oracle
 from tests import serving_data as D
+from tests import test_gpu_evict as evict
+from tests import test_gpu_prefix as prefix
 
 pytestmark = pytest.mark.gpu
 assert_within = D.assert_within
@@ -47,3 +51,96 @@ def test_absorb_query_off_the_tensor_map(shape, H, shift):
     tol = D.EPS["bf16"] * np.abs(want) * 1.01 + np.concatenate(
         [4 * d.d_nope * 2.0 ** -24 * mag, np.full(pe.shape, 6 * 2.0 ** -20)], -1)
     assert_within(t["q_lat"].double().cpu().numpy(), want, tol, "q_lat")
+
+
+# ----------------------------------------------------------------------------- several host threads
+
+def _evict_call(rng, keys):
+    """An eviction of two requests on tables of `keys` tokens: the call, and its outputs."""
+    d = D.dims("tiny", 16)
+    c = D.Cache(rng, "f32", d, (300, 200), max_pages=-(-keys // 64))
+    w, tab, ln = D.dev(D.draw(rng, (2, c.max_pages * 64), "f32")), D.dev(c.table), D.dev(np.array([300, 200], np.int32))
+    pool, cfg = c.device(), c.config()
+    new = D.dev(c.spare.reshape(2, 2).copy())          # into new pages: every call does the same
+    outs = torch.empty(2, 100, dtype=torch.int32, device="cuda"), torch.empty(2, dtype=torch.int32, device="cuda")
+    return lambda s: M.mla_evict_cache(cfg, w, ln, tab, pool, 100, *outs, new_block_table=new, sinks=2, recent=5,
+                                       stream=s), outs
+
+
+def _attend_call(rng, d_n):
+    d = D.dims("tiny", 16)
+    d.d_nope = d_n
+    x = [D.dev(D.draw(rng, s, "f32")) for s in ((80, 1, 16, d_n), (80, 1, 16, d.d_rope), (16, 9, d_n), (16, 9, d.d_v),
+                                                (9, d.d_rope))]
+    outs = torch.empty(80, 1, 16, d.d_v, device="cuda"), torch.empty(80, 1, 16, device="cuda")
+    ln, cfg = D.dev(np.full(80, 3, np.int32)), M.make_config(d, "f32", "f32")
+    return lambda s: M.mla_prefix_attend(cfg, *x, ln, *outs, stream=s), outs
+
+
+def _weigh_call(rng, d_c):
+    d = D.dims("tiny", 16)
+    d.d_latent = d_c
+    c = D.Cache(rng, "f32", d, (100,))
+    q, lse = D.dev(D.draw(rng, (1, 1, 16, d_c + d.d_rope), "f32", 0.1)), torch.zeros(1, 1, 16, device="cuda")
+    w, pool, cfg = torch.zeros(1, c.max_pages * 64, device="cuda"), c.device(), c.config()
+    tab, ln = D.dev(c.table), D.dev(np.array([100], np.int32))
+    return lambda s: M.mla_key_weights(cfg, q, lse, pool, tab, ln, w, decay=0.0, stream=s), (w,)
+
+
+@pytest.mark.parametrize("make,sizes", [(_evict_call, (640, 150000)), (_attend_call, (1600, 3200)),
+                                        (_weigh_call, (256, 512))], ids=["evict", "attend", "weigh"])
+def test_host_threads_with_other_sizes(make, sizes):
+    """Host threads whose calls need different amounts of shared memory of one kernel, on streams of
+    their own: no call fails, and all give what they give alone."""
+    calls = [make(np.random.default_rng(i), n) for i, n in enumerate(3 * sizes)]
+    streams = [torch.cuda.Stream() for _ in calls]
+    want = []
+    for call, outs in calls:
+        call(None)
+        torch.cuda.synchronize()
+        want.append([o.clone() for o in outs])
+    gate, errors = threading.Barrier(len(calls)), []
+
+    def loop(i):
+        try:
+            gate.wait()
+            for _ in range(5000):
+                calls[i][0](streams[i])
+        except Exception as e:                       # noqa: BLE001 (reported below)
+            errors.append(e)
+
+    threads = [threading.Thread(target=loop, args=(i,)) for i in range(len(calls))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors, errors
+    for (_, outs), w in zip(calls, want):
+        assert all(torch.equal(o, y) for o, y in zip(outs, w))
+
+
+@pytest.mark.parametrize("B,d_n", [(80, 1390), (80, 1400), (80, 1472), (80, 1488), (3, 1488)])
+def test_attend_widths_around_48_kb(B, d_n):
+    """Head widths whose query rows and outputs are just within 48 KB of dynamic shared memory, beside
+    the kernel's static arrays (d_n + d_r + d_v up to 1536 at 8 rows a block), and just above."""
+    rng = np.random.default_rng(d_n)
+    d = D.dims("tiny", 16)
+    d.d_nope = d_n
+    x = dict(q_nope=D.draw(rng, (B, 1, 16, d_n), "f32"), q_pe=D.draw(rng, (B, 1, 16, d.d_rope), "f32"),
+             keys=D.draw(rng, (16, 70, d_n), "f32"), values=D.draw(rng, (16, 70, d.d_v), "f32"),
+             k_pe=D.draw(rng, (70, d.d_rope), "f32"))
+    lens = rng.integers(1, 50, B).astype(np.int32)
+    u, lse = prefix.attend(M.make_config(d, "f32", "f32"), x, lens, "f32")
+    prefix.check_attend(d, x, lens, "f32", u, lse)
+
+
+@pytest.mark.parametrize("pages", [100, 112, 128, 140])
+def test_evict_many_requests_of_wide_tables(pages):
+    """More requests than SMs, with tables of 6400 to 8960 tokens: the selection's weights take about
+    48 KB beside its static arrays."""
+    rng = np.random.default_rng(pages)
+    c = D.Cache(rng, "f32", D.dims("tiny", 16), list(rng.integers(0, 200, 160)), max_pages=pages)
+    w = evict.draw_weights(rng, 160, pages * 64, "plain")
+    res = evict.run_evict(c, w, 70, 2, 8)
+    evict.check_evict(c, w, 70, 2, 8, res)
