@@ -329,7 +329,8 @@ mla_status mla_prefix_attend_workspace_size(const mla_config* cfg, int batch, in
  *   q_nope [batch][q_len][H][d_n], q_pe [batch][q_len][H][d_r] as given to mla_decode (not
  *   rotated); keys, values, k_pe from mla_prefix_expand; seq_lens [batch] int32 (device): each
  *   request's own cached tokens including this step's q_len; u [batch][q_len][H][d_v] (act
- *   dtype), lse [batch][q_len][H] (fp32) outputs.
+ *   dtype), lse [batch][q_len][H] (fp32) outputs. d_n + d_r + d_v above 57344:
+ *   MLA_ERR_UNSUPPORTED.
  * The softmax's weights are rounded to the act dtype for the product with the values; scores,
  * maxima, sums and the rotated query are held in fp32 precision (bf16: the rotated query as
  * the sum of two bf16 terms, with an error of 2^-18 of a term; up to 3 keys in fp32), so lse is an

@@ -213,6 +213,8 @@ struct PrefixAttendParams {
   TurnTable tt;
   int32_t* status;
 };
+// d_n + d_r + d_v up to which one query row of the SIMT kernel fits a block's shared memory.
+constexpr int kPrefixMaxWidth = 56 * 1024;
 constexpr int kPrefixShort = 3;        // prefixes of up to so many keys have a kernel of their own
 cudaError_t launch_prefix_attend_simt(mla_dtype act, const PrefixAttendParams& p, cudaStream_t s);
 

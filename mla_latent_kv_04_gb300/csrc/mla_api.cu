@@ -739,6 +739,8 @@ mla_status mla_prefix_attend_workspace_size(const mla_config* cfg, int batch, in
   mla_status st = check_decode_shape(cfg, batch, q_len);
   if (st == MLA_OK) st = check_prefix(cfg, prefix_len);
   if (st != MLA_OK) return st;
+  if ((long long)cfg->d_nope + cfg->d_rope + cfg->d_v > kPrefixMaxWidth)
+    return unsupported("d_nope + d_rope + d_v above 57344");
   if (!bytes) return invalid("bytes is NULL");
   *bytes = prefix_attend_tc_supported(cfg)
                ? prefix_attend_tc_workspace(batch * q_len, cfg->num_heads, prefix_len)

@@ -526,19 +526,25 @@ cudaError_t launch_prefix_expand_simt(mla_dtype act, mla_dtype cache, const Pref
   });
 }
 
+static_assert((kPrefixMaxWidth + 3) * 4 + 528 + 1024 <= kSmemPerCta, "a query row in shared memory");
+
 cudaError_t launch_prefix_attend_simt(mla_dtype act, const PrefixAttendParams& p, cudaStream_t s) {
   const bool brief = p.L > 0 && p.L <= kPrefixShort;
-  // rows of a block: as many as leave a block per SM
+  // rows of a block: as many as leave a block per SM and fit its shared memory (a block's static
+  // arrays: 528 bytes a row and 512, here rounded up)
   int at_once = 8;
-  while (at_once > 1 && (long long)((p.rows + at_once - 1) / at_once) * p.H < device_sms()) at_once /= at_once == 8 ? 2 : 4;
-  const size_t smem = brief ? 0 : (size_t)at_once * (((p.d_n + 3) & ~3) + p.d_r + p.d_v) * 4;
+  auto dynamic = [&]() { return (size_t)at_once * (((p.d_n + 3) & ~3) + p.d_r + p.d_v) * 4; };
+  auto fixed = [&]() { return (size_t)(528 * at_once + 1024); };
+  while (at_once > 1 && ((long long)((p.rows + at_once - 1) / at_once) * p.H < device_sms() ||
+                         dynamic() + fixed() > kSmemPerCta))
+    at_once /= at_once == 8 ? 2 : 4;
+  const size_t smem = brief ? 0 : dynamic();
   auto go = [&](auto a) {
     using AT = decltype(a);
     auto kern = brief ? attend_short_kernel<AT>
                       : (at_once == 8 ? attend_simt_kernel<AT, 8>
                                       : (at_once == 4 ? attend_simt_kernel<AT, 4> : attend_simt_kernel<AT, 1>));
-    // (a block's static arrays: 528 bytes a row and 512, here rounded up)
-    cudaError_t e = allow_smem(kern, smem, 528 * at_once + 1024);
+    cudaError_t e = allow_smem(kern, smem, fixed());
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = brief ? dim3((unsigned)(((long long)p.rows * p.H + 7) / 8), 1, 1)

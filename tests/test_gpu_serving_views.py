@@ -120,10 +120,12 @@ def test_host_threads_with_other_sizes(make, sizes):
         assert all(torch.equal(o, y) for o, y in zip(outs, w))
 
 
-@pytest.mark.parametrize("B,d_n", [(80, 1390), (80, 1400), (80, 1472), (80, 1488), (3, 1488)])
-def test_attend_widths_around_48_kb(B, d_n):
+@pytest.mark.parametrize("B,d_n", [(80, 1390), (80, 1400), (80, 1472), (80, 1488), (3, 1488), (80, 7000),
+                                   (80, 7200), (80, 14300), (80, 20000), (2, 50001)])
+def test_attend_widths_up_to_the_shared_memory(B, d_n):
     """Head widths whose query rows and outputs are just within 48 KB of dynamic shared memory, beside
-    the kernel's static arrays (d_n + d_r + d_v up to 1536 at 8 rows a block), and just above."""
+    the kernel's static arrays (d_n + d_r + d_v up to 1536 at 8 rows a block), and just above; widths
+    of which 8 rows, or 4, no longer fit a block."""
     rng = np.random.default_rng(d_n)
     d = D.dims("tiny", 16)
     d.d_nope = d_n
