@@ -329,6 +329,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
           }
         }
+        __syncwarp();                                  // the store is warp-wide (tokens on bad pages load nothing)
         ptx::tmem_st32(t_x + 32 * b, o);
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) cur[i] = nxt[i];

@@ -130,6 +130,7 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         uint32_t v[32];
+        __syncwarp();                                  // the load is warp-wide
         ptx::tmem_ld32(tmem + ((uint32_t)(32 * quad) << 16) + 32 * q, v);
         ptx::tmem_wait_ld();
         if (live) {
@@ -325,6 +326,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads2, 1)
 #pragma unroll 1
         for (int q = 0; q < 4; ++q) {
           uint32_t v[32];
+          __syncwarp();                                // the load is warp-wide (rows behind the last left early)
           ptx::tmem_ld32(d + 256 * i + 128 * part + 32 * q, v);
           ptx::tmem_wait_ld();
           if (i == kTiles - 1 && q == 3) {

@@ -420,6 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!(ok = wait_w(B_ODONE + ((g - 1) & 1), ((g - 1) >> 1) & 1))) break;
             ptx::tc_fence_after();
             const float a = grow ? (m == -INFINITY ? 0.f : ptx::ex2((m - mb) * c)) : 1.f;
+            __syncwarp();
 #pragma unroll 1
             for (int q = 0; q < 4; ++q) {
               uint32_t o[16];
@@ -473,6 +474,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         else if (r < p.rows) p.lse[(long long)r * p.H + h] = row_live ? lse2 * kLn2 : -INFINITY;
       }
       uint32_t o[2][32];                           // output columns 64 w .. 64 w + 63
+      __syncwarp();                                // the loads are warp-wide
       ptx::tmem_ld32(t_o, o[0]);
       ptx::tmem_ld32(t_o + 32, o[1]);
       ptx::tmem_wait_ld();

@@ -146,3 +146,57 @@ def test_evict_many_requests_of_wide_tables(pages):
     w = evict.draw_weights(rng, 160, pages * 64, "plain")
     res = evict.run_evict(c, w, 70, 2, 8)
     evict.check_evict(c, w, 70, 2, 8, res)
+
+
+# ----------------------------------------------------------------------------- rows inside a warp
+
+@pytest.mark.parametrize("shape,H", [("v2", 16), ("v2", 64), ("value64", 5), ("value128", 5)])
+@pytest.mark.parametrize("some,all_", [(131, 160), (129, 256), (283, 288), (33, 64), (5, 32)])
+def test_rows_that_end_inside_a_warp_have_the_bits_of_whole_ones(shape, H, some, all_):
+    """The joined projection of a batch whose last warp has few live rows equals, bit by bit, the same
+    rows of a batch that fills its warps (both cut the product alike)."""
+    rng = np.random.default_rng(some)
+    d = D.dims(shape, H)
+    cfg = M.make_config(d, "bf16", "bf16")
+    o, up = (D.dev(D.draw(rng, (all_, H, w), "bf16", 0.1), "bf16") for w in (d.d_latent, d.d_v))
+    lse, lsep = (D.dev((rng.standard_normal((all_, H)) * 3).astype(np.float32)) for _ in range(2))
+    W_UV = D.dev(D.draw(rng, (d.d_latent, H * d.d_v), "bf16", d.d_latent ** -0.5), "bf16")
+    W_O = D.dev(D.draw(rng, (H * d.d_v, d.d_model), "bf16", (H * d.d_v) ** -0.5), "bf16")
+
+    def project(n):
+        out = torch.full((n, d.d_model), float("nan"), dtype=torch.bfloat16, device="cuda")
+        ws = torch.empty(M.mla_output_proj_prefix_workspace_size(cfg, n), dtype=torch.uint8, device="cuda")
+        M.mla_output_proj_prefix(cfg, o[:n], lse[:n], up[:n], lsep[:n], W_UV, W_O, out, ws)
+        return out
+    got, want = project(some), project(all_)
+    torch.cuda.synchronize()
+    assert torch.isfinite(want).all() and torch.equal(got, want[:some])
+
+
+@pytest.mark.parametrize("some,all_,L", [(131, 160, 1500), (129, 256, 300), (33, 64, 5000), (5, 32, 260)])
+def test_attention_rows_that_end_inside_a_warp(some, all_, L):
+    rng = np.random.default_rng(some)
+    d = D.dims("v2", 16)
+    x, lens = prefix.attend_inputs(rng, d, all_, 1, L, "bf16", rng.integers(1, 900, all_))
+    cfg = M.make_config(d, "bf16", "bf16")
+    u, lse = prefix.attend(cfg, x, lens, "bf16")
+    x["q_nope"], x["q_pe"] = x["q_nope"][:some], x["q_pe"][:some]
+    su, slse = prefix.attend(cfg, x, lens[:some], "bf16")
+    assert np.array_equal(su, u[:some]) and np.array_equal(slse, lse[:some])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8_e4m3", "fp8_e4m3_b128"])
+def test_expansion_of_bad_pages_between_good_ones(kind):
+    """Bad pages in every place of a 256-token tile: their rows are zeros, the others' bits stay."""
+    rng = np.random.default_rng(7)
+    d = D.dims("v2", 16)
+    c = D.Cache(rng, kind, d, [600])
+    W_UK, W_UV = (D.draw(rng, (512, 16 * 128), "bf16", 512 ** -0.5) for _ in range(2))
+    good = prefix.expand(c, c.config(), W_UK, W_UV, 600)
+    for bad in ([0], [3], [1, 2, 6], [0, 1, 2, 3], [9]):
+        table = c.table[0].copy()
+        table[bad] = -1
+        gone = np.isin(np.arange(600) // 64, bad)
+        got = prefix.expand(c, c.config(), W_UK, W_UV, 600, table=table)
+        for g, w in zip(got[:2], good[:2]):
+            assert torch.equal(g[:, ~gone], w[:, ~gone]) and not g[:, gone].any()
