@@ -392,7 +392,8 @@ mla_status mla_absorb_query(const mla_config* cfg, const void* q_nope, const voi
  * Sums are fp32, in a fixed order (the same bits every time). seq_lens[b] == 0: nothing is
  * written. Requests with a bad length and tokens on a bad page are left out, with
  * MLA_ERR_DEVICE_GUARD in *dev_status (optional, OR-ed in). MLA_ERR_UNSUPPORTED: batch * max_pages
- * or max_pages * P above 2^31 - 1. */
+ * or max_pages * P above 2^31 - 1; rows so wide that a page of them and a query in fp32 do not fit
+ * 227 KB (64-token pages: d_c + d_r above 892 in fp32, 1756 in bf16, 3412 in e4m3, 3136 block-scaled). */
 mla_status mla_key_weights(const mla_config* cfg, const void* q_lat, const float* lse,
                            const void* cache, int num_pages, const int32_t* block_table,
                            int max_pages, const int32_t* seq_lens, int batch, int q_len, float decay,

@@ -250,6 +250,8 @@ struct KeyWeightParams {
   float* weights;             // [batch][max_pages * P]
   int32_t* status;
 };
+// Whether a page of such rows and one query fit a block's shared memory.
+bool key_weights_simt_fits(int P, long long row_bytes, long long D);
 cudaError_t launch_key_weights_simt(mla_dtype act, mla_dtype cache, const KeyWeightParams& p,
                                     cudaStream_t s);
 

@@ -802,6 +802,8 @@ mla_status mla_key_weights(const mla_config* cfg, const void* q_lat, const float
   if ((long long)batch * max_pages > 0x7FFFFFFFLL) return unsupported("batch * max_pages above 2^31 - 1");
   if ((long long)max_pages * cfg->page_size > 0x7FFFFFFFLL)
     return unsupported("max_pages * page_size above 2^31 - 1");
+  if (!key_weights_simt_fits(cfg->page_size, (long long)cache_row_bytes(cfg), (long long)cfg->d_latent + cfg->d_rope))
+    return unsupported("a page of the cache and a query do not fit 227 KB of shared memory");
   if (((uintptr_t)cache & 3) != 0) return invalid("cache must be 4-byte aligned");
   KeyWeightParams p;
   p.q_lat = q_lat;

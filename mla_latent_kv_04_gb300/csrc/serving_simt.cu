@@ -413,6 +413,11 @@ __device__ __forceinline__ float4 row_quad(const uint32_t* row, int e, int d_c) 
   }
 }
 
+// Bytes of shared memory: the page's rows (an odd number of words each), the warps' queries and sums.
+size_t key_weights_simt_smem(int P, long long row_bytes, long long D, int warps, int at_once) {
+  return (((size_t)P * ((row_bytes / 4) | 1) + 3) / 4 * 4 + (size_t)warps * ((size_t)at_once * D + P)) * 4;
+}
+
 // Block per (request, page): the page's rows in shared memory (odd word stride), kQ queries (query
 // token, head) per warp at a time, two tokens per lane: a row's element is read once for kQ products;
 // the warps' sums meet in warp order. Few pages are bound by the latency of a warp's queries in turn,
@@ -595,15 +600,19 @@ cudaError_t launch_prefix_project_simt(mla_dtype act, const void* o_lat, const v
   return product_simt(act, prod, 1, s);
 }
 
+bool key_weights_simt_fits(int P, long long row_bytes, long long D) {
+  return key_weights_simt_smem(P, row_bytes, D, 1, 1) <= kSmemPerCta;
+}
+
 cudaError_t launch_key_weights_simt(mla_dtype act, mla_dtype cache, const KeyWeightParams& p,
                                     cudaStream_t s) {
-  // up to 32 warps of 4 queries each, as many as there are queries and as fit beside the page
+  // up to 32 warps of 4 queries each, as many as there are queries and as fit beside the page; less
+  // than 8 warps of one query only beside the widest rows
   int warps = 32, at_once = 4;
-  auto bytes = [&]() {
-    return (((size_t)p.P * ((p.row_bytes / 4) | 1) + 3) / 4 * 4 + (size_t)warps * (at_once * p.D + p.P)) * 4;
-  };
+  auto bytes = [&]() { return key_weights_simt_smem(p.P, p.row_bytes, p.D, warps, at_once); };
   while (warps > 8 && (bytes() > 200 * 1024 || warps / 2 * at_once >= p.q_len * p.H)) warps /= 2;
   if (bytes() > 220 * 1024) at_once = 1;
+  while (warps > 1 && bytes() > kSmemPerCta) warps /= 2;
   const size_t smem = bytes();
   return by_format(act, cache, [&](auto a, auto c) {
     using AT = decltype(a);

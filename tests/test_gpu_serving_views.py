@@ -200,3 +200,20 @@ def test_expansion_of_bad_pages_between_good_ones(kind):
         got = prefix.expand(c, c.config(), W_UK, W_UV, 600, table=table)
         for g, w in zip(got[:2], good[:2]):
             assert torch.equal(g[:, ~gone], w[:, ~gone]) and not g[:, gone].any()
+
+
+# ----------------------------------------------------------------------------- wide rows
+
+@pytest.mark.parametrize("kind,d_c,H", [("f32", 768, 16), ("f32", 828, 3), ("bf16", 1400, 16), ("bf16", 1692, 3),
+                                        ("fp8_e4m3", 3348, 3), ("fp8_e4m3_b128", 2944, 3), ("f32", 704, 16)])
+def test_key_weights_of_rows_up_to_the_shared_memory(kind, d_c, H):
+    """Latents so wide that a page leaves room for 8 warps of one query, or for fewer."""
+    rng = np.random.default_rng(d_c)
+    d = D.dims("tiny", H)
+    d.d_latent, d.d_rope = d_c, 64
+    c = D.Cache(rng, kind, d, (70, 0, 5))
+    q_lat, lse, scale = evict.weigh_inputs(rng, c, 2)
+    q_lat, lse = q_lat * np.float32(0.25), np.zeros_like(lse)   # moderate scores; any LSE serves
+    old = rng.random((3, c.max_pages * 64)).astype(np.float32)
+    got = evict.weigh(c, 2, q_lat, lse, old, 0.5)
+    evict.check_weights(c, 2, q_lat, lse, scale, old, 0.5, got)
