@@ -348,7 +348,10 @@ __global__ void __launch_bounds__(256) product_simt_kernel(SimtProduct p) {
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, z = blockIdx.z;
-  const int n = blockIdx.x * kProjCols + lane, r0 = blockIdx.y * kProjRows;
+  // blockIdx.x: the column block, then the row block (any number of rows: y has 65535 blocks at most)
+  const int col_blocks = (p.N + kProjCols - 1) / kProjCols;
+  const int n0 = blockIdx.x % col_blocks * kProjCols, r0 = blockIdx.x / col_blocks * kProjRows;
+  const int n = n0 + lane;
   const AT* x = reinterpret_cast<const AT*>(p.x) + z * p.zx;
   const AT* W = reinterpret_cast<const AT*>(p.W) + z * p.zw;
   const int chunk = min(kProjK, (p.K + 31) & ~31), slice = chunk / 8;
@@ -378,7 +381,7 @@ __global__ void __launch_bounds__(256) product_simt_kernel(SimtProduct p) {
   for (int r = 0; r < kProjRows; ++r) us[(warp * kProjRows + r) * kProjCols + lane] = acc[r];
   __syncthreads();
   for (int i = threadIdx.x; i < kProjRows * kProjCols; i += 256) {
-    const int r = r0 + i / kProjCols, c = blockIdx.x * kProjCols + i % kProjCols;
+    const int r = r0 + i / kProjCols, c = n0 + i % kProjCols;
     float sum = 0.f;
     for (int w = 0; w < 8; ++w) sum += us[w * kProjRows * kProjCols + i];
     if (r >= p.rows || c >= p.N) continue;
@@ -573,8 +576,9 @@ static cudaError_t product_simt(mla_dtype act, const SimtProduct& p, int batch, 
   auto go = [&](auto a) {
     using AT = decltype(a);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((p.N + kProjCols - 1) / kProjCols),
-                       (unsigned)((p.rows + kProjRows - 1) / kProjRows), (unsigned)batch);
+    const long long blocks = (long long)((p.N + kProjCols - 1) / kProjCols) * ((p.rows + kProjRows - 1LL) / kProjRows);
+    if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
+    cfg.gridDim = dim3((unsigned)blocks, 1, (unsigned)batch);
     cfg.blockDim = dim3(256, 1, 1);
     cfg.stream = s;
     cudaLaunchAttribute attr;

@@ -217,3 +217,28 @@ def test_key_weights_of_rows_up_to_the_shared_memory(kind, d_c, H):
     old = rng.random((3, c.max_pages * 64)).astype(np.float32)
     got = evict.weigh(c, 2, q_lat, lse, old, 0.5)
     evict.check_weights(c, 2, q_lat, lse, scale, old, 0.5, got)
+
+
+# ----------------------------------------------------------------------------- many rows
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+def test_output_proj_prefix_of_a_million_rows(act):
+    """More rows than 65535 blocks of 16, at a small shape; every row equals that of a small batch."""
+    rng = np.random.default_rng(3)
+    d = D.dims("tiny", 2)
+    d.d_latent, d.d_nope, d.d_v, d.d_model = 8, 4, 4, 12
+    cfg, rows, few = M.make_config(d, act, act), 16 * 65535 + 21, 1000
+    o, up = (D.dev(D.draw(rng, (few, 2, w), act, 0.1), act) for w in (8, 4))
+    lse, lsep = (D.dev(rng.standard_normal((few, 2)).astype(np.float32)) for _ in range(2))
+    W_UV, W_O = D.dev(D.draw(rng, (8, 8), act), act), D.dev(D.draw(rng, (8, 12), act), act)
+
+    def project(at):
+        out = torch.full((len(at), 12), float("nan"), dtype=D.torch_type(act), device="cuda")
+        ws = torch.empty(M.mla_output_proj_prefix_workspace_size(cfg, len(at)), dtype=torch.uint8, device="cuda")
+        M.mla_output_proj_prefix(cfg, o[at], lse[at], up[at], lsep[at], W_UV, W_O, out, ws)
+        return out
+    want = project(torch.arange(few, device="cuda"))
+    at = torch.arange(rows, device="cuda") % few
+    got = project(at)
+    torch.cuda.synchronize()
+    assert torch.isfinite(want).all() and torch.equal(got, want[at])
