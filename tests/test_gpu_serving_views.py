@@ -8,6 +8,7 @@ import torch
 
 import mla_latent_kv_04_gb300 as M
 import oracle
+from oracle import serving as ref
 from tests import serving_data as D
 from tests import test_gpu_evict as evict
 from tests import test_gpu_prefix as prefix
@@ -242,3 +243,95 @@ def test_output_proj_prefix_of_a_million_rows(act):
     got = project(at)
     torch.cuda.synchronize()
     assert torch.isfinite(want).all() and torch.equal(got, want[at])
+
+
+# ----------------------------------------------------------------------------- other start addresses
+
+@pytest.mark.parametrize("which", ["W_UK", "W_UV", "cache", "keys", "values", "k_pe", "all"])
+def test_expand_off_16_bytes(which):
+    """Each tensor of an expansion off a 16-byte boundary, element by element against fp64."""
+    rng = np.random.default_rng(50)
+    d = D.dims("v2", 3)
+    c = D.Cache(rng, "bf16", d, [130])
+    W_UK, W_UV = (D.draw(rng, (512, 3 * 128), "bf16", 512 ** -0.5) for _ in range(2))
+    t = dict(W_UK=D.dev(W_UK, "bf16"), W_UV=D.dev(W_UV, "bf16"), cache=c.device(),
+             keys=torch.full((3, 130, 128), 7.0, dtype=torch.bfloat16, device="cuda"),
+             values=torch.full((3, 130, 128), 7.0, dtype=torch.bfloat16, device="cuda"),
+             k_pe=torch.full((130, 64), 7.0, dtype=torch.bfloat16, device="cuda"))
+    for name in t:
+        if which in (name, "all"):
+            t[name] = D.shifted(t[name], 2 if name == "cache" else 1)    # (a cache starts on 4 bytes)
+    M.mla_prefix_expand(c.config(), t["W_UK"], t["W_UV"], t["cache"], D.dev(c.table[0]), 130, t["keys"], t["values"],
+                        t["k_pe"])
+    torch.cuda.synchronize()
+    rows = c.values[0]
+    K, V, aK, aV = ref.expand_prefix(rows[:, :512], W_UK, W_UV, 3)
+    assert_within(t["keys"].double().cpu().numpy(), K, prefix.expand_bound(aK, K, "bf16", "bf16", 512), "keys")
+    assert_within(t["values"].double().cpu().numpy(), V, prefix.expand_bound(aV, V, "bf16", "bf16", 512), "values")
+    assert np.array_equal(t["k_pe"].double().cpu().numpy(), rows[:, 512:])
+
+
+@pytest.mark.parametrize("rows", [5, 150])
+@pytest.mark.parametrize("which", ["o", "lse", "up", "lsep", "W_UV", "W_O", "out", "all"])
+def test_output_proj_prefix_off_16_bytes(which, rows):
+    """The joined projection at the tensor cores' shape with each tensor off a 16-byte boundary."""
+    rng = np.random.default_rng(rows)
+    H = 3
+    d = D.dims("v2", H)
+    cfg = M.make_config(d, "bf16", "bf16")
+    h = dict(o=D.draw(rng, (rows, H, 512), "bf16", 0.1), up=D.draw(rng, (rows, H, 128), "bf16", 0.1),
+             lse=(rng.standard_normal((rows, H)) * 3).astype(np.float32),
+             lsep=(rng.standard_normal((rows, H)) * 3).astype(np.float32),
+             W_UV=D.draw(rng, (512, H * 128), "bf16", 512 ** -0.5),
+             W_O=D.draw(rng, (H * 128, d.d_model), "bf16", (H * 128) ** -0.5))
+    t = {k: D.dev(v, None if k.startswith("lse") else "bf16") for k, v in h.items()}
+    t["out"] = torch.full((rows, d.d_model), float("nan"), dtype=torch.bfloat16, device="cuda")
+    for name in t:
+        if which in (name, "all"):
+            t[name] = D.shifted(t[name])
+    ws = torch.full((M.mla_output_proj_prefix_workspace_size(cfg, rows),), 0xFF, dtype=torch.uint8, device="cuda")
+    M.mla_output_proj_prefix(cfg, t["o"], t["lse"], t["up"], t["lsep"], t["W_UV"], t["W_O"], t["out"], ws)
+    torch.cuda.synchronize()
+    lse, lsep, W_O = h["lse"].astype(np.float64), h["lsep"].astype(np.float64), h["W_O"].astype(np.float64)
+    u = ref.join_prefix(h["o"], lse, h["up"], lsep, h["W_UV"], H)
+    mag_u = ref.join_prefix(np.abs(h["o"]), lse, np.abs(h["up"]), lsep, np.abs(h["W_UV"]), H)
+    want, mag = u.reshape(rows, -1) @ W_O, np.abs(u).reshape(rows, -1) @ np.abs(W_O)
+    # u's rounding, its fp32 sums (weights to 2^-20), the projection's sums, the result's rounding
+    du = 2.0 ** -8 * np.abs(u) + (4 * 512 * 2.0 ** -24 + 2.0 ** -19) * mag_u
+    tol = du.reshape(rows, -1) @ np.abs(W_O) + 4 * H * 128 * 2.0 ** -24 * mag + 2.0 ** -8 * np.abs(want)
+    assert_within(t["out"].double().cpu().numpy(), want, tol * 1.01, "out")
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8_e4m3", "fp8_e4m3_b128"])
+@pytest.mark.parametrize("which", ["q_lat", "lse", "cache", "weights", "all"])
+def test_key_weights_off_16_bytes(kind, which):
+    """Key weights at the tensor cores' shape with each tensor off a 16-byte boundary (the cache by 4
+    bytes, its own alignment)."""
+    rng = np.random.default_rng(61)
+    c = D.Cache(rng, kind, D.dims("v2", 16), (130, 0, 65, 2), max_pages=3)
+    q_lat, lse, scale = evict.weigh_inputs(rng, c, 2)
+    old = rng.random((4, 192)).astype(np.float32)
+    t = dict(q_lat=D.dev(q_lat, "bf16"), lse=D.dev(lse), cache=c.device(), weights=D.dev(old))
+    for name in t:
+        if which in (name, "all"):
+            t[name] = D.shifted(t[name], 4 // c.device().element_size() if name == "cache" else 1)
+    M.mla_key_weights(c.config(), t["q_lat"], t["lse"], t["cache"], D.dev(c.table), D.dev(np.array(c.lens, np.int32)),
+                      t["weights"], decay=0.9)
+    torch.cuda.synchronize()
+    evict.check_weights(c, 2, q_lat, lse, scale, old, 0.9, t["weights"].cpu().numpy())
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8_e4m3", "fp8_e4m3_b128"])
+@pytest.mark.parametrize("in_place", [True, False], ids=["in_place", "new_pages"])
+def test_evict_off_16_bytes(kind, in_place, monkeypatch):
+    """Rows that could move 16 bytes at a time, in a cache that starts 4 bytes off: 4 at a time."""
+    rng = np.random.default_rng(62)
+    c = D.Cache(rng, kind, D.dims("v2", 16), evict.EVICT_LENS, max_pages=13, spare=40)
+    aligned = c.device
+    monkeypatch.setattr(c, "device", lambda: D.shifted(aligned(), 4 // aligned().element_size()))
+    assert c.device().data_ptr() % 16 == 4
+    w = evict.draw_weights(rng, len(c.lens), 13 * 64, "plain")
+    table = None if in_place else evict.fresh_table(c, c.lens, 130)
+    # (the helper reads the pool back through a byte view, which needs no alignment of its own)
+    res = evict.run_evict(c, w, 130, 4, 20, in_place=in_place, new_table=table)
+    evict.check_evict(c, w, 130, 4, 20, res)
