@@ -9,6 +9,7 @@ libmla.so has not been built the first call raises ``RuntimeError``.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
@@ -187,7 +188,8 @@ def _current_device() -> int:
     return _device_query()
 
 
-def _ptr(x, name, dtypes=None, numel=None, allow_none=False):
+def _ptr(x, name, dtypes=None, numel=None, allow_none=False, peer=False):
+    """peer: tensors of a device that the current one can access are let through."""
     if x is None:
         if allow_none:
             return None
@@ -196,7 +198,8 @@ def _ptr(x, name, dtypes=None, numel=None, allow_none=False):
     if device != _current_device():
         if not x.is_cuda:
             raise ValueError(f"{name} must be a CUDA tensor")
-        raise ValueError(f"{name} is on cuda:{device}, which is not the current device")
+        if not peer:
+            raise ValueError(f"{name} is on cuda:{device}, which is not the current device")
     if not x.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if dtypes is not None and x.dtype not in dtypes:
@@ -204,6 +207,10 @@ def _ptr(x, name, dtypes=None, numel=None, allow_none=False):
     if numel is not None and x.numel() != numel:
         raise ValueError(f"{name} has {x.numel()} elements, expected {numel}")
     return x.data_ptr()
+
+
+# The calls of ABI 1.02 and before leave a tensor's device to the caller.
+_peer_ptr = functools.partial(_ptr, peer=True)
 
 
 def _stream(stream):
@@ -235,9 +242,9 @@ def mla_absorb_weights(cfg, W_UK, W_UV, W_O, W_UK_abs, W_comb, stream=None):
     a = (_act_dtype(cfg),)
     H, d_c, d_n, d_v, d = cfg.num_heads, cfg.d_latent, cfg.d_nope, cfg.d_v, cfg.d_model
     _check(lib().mla_absorb_weights(
-        ctypes.byref(cfg), _ptr(W_UK, "W_UK", a, d_c * H * d_n), _ptr(W_UV, "W_UV", a, d_c * H * d_v),
-        _ptr(W_O, "W_O", a, H * d_v * d), _ptr(W_UK_abs, "W_UK_abs", a, H * d_n * d_c),
-        _ptr(W_comb, "W_comb", a, H * d_c * d), _stream(stream)), "mla_absorb_weights")
+        ctypes.byref(cfg), _peer_ptr(W_UK, "W_UK", a, d_c * H * d_n), _peer_ptr(W_UV, "W_UV", a, d_c * H * d_v),
+        _peer_ptr(W_O, "W_O", a, H * d_v * d), _peer_ptr(W_UK_abs, "W_UK_abs", a, H * d_n * d_c),
+        _peer_ptr(W_comb, "W_comb", a, H * d_c * d), _stream(stream)), "mla_absorb_weights")
 
 
 def _i32(t):
@@ -260,12 +267,12 @@ def mla_append_cache(cfg, h, W_DKV_KR, req_ids, positions, block_table, cache, d
     batch, max_pages = block_table.shape
     num_pages = cache.numel() // (cfg.page_size * _cache_row_elems(cfg))
     _check(lib().mla_append_cache(
-        ctypes.byref(cfg), _ptr(h, "h", a, T * cfg.d_model), _ptr(W_DKV_KR, "W_DKV_KR", a, cfg.d_model * D),
-        T, _ptr(req_ids, "req_ids", _i32(0), T), _ptr(positions, "positions", _i32(0), T),
-        _ptr(block_table, "block_table", _i32(0)), batch, max_pages,
-        _ptr(cache, "cache", _cache_dtypes(cfg), num_pages * cfg.page_size * _cache_row_elems(cfg)), num_pages,
-        _ptr(dev_status, "dev_status", _i32(0), allow_none=True),
-        _ptr(workspace, "workspace", (_torch().uint8,), allow_none=True),
+        ctypes.byref(cfg), _peer_ptr(h, "h", a, T * cfg.d_model), _peer_ptr(W_DKV_KR, "W_DKV_KR", a, cfg.d_model * D),
+        T, _peer_ptr(req_ids, "req_ids", _i32(0), T), _peer_ptr(positions, "positions", _i32(0), T),
+        _peer_ptr(block_table, "block_table", _i32(0)), batch, max_pages,
+        _peer_ptr(cache, "cache", _cache_dtypes(cfg), num_pages * cfg.page_size * _cache_row_elems(cfg)), num_pages,
+        _peer_ptr(dev_status, "dev_status", _i32(0), allow_none=True),
+        _peer_ptr(workspace, "workspace", (_torch().uint8,), allow_none=True),
         0 if workspace is None else workspace.numel(), _stream(stream)),
         "mla_append_cache")
 
@@ -278,11 +285,11 @@ def mla_append_cache_latent(cfg, c_kv, k_pe, req_ids, positions, block_table, ca
     batch, max_pages = block_table.shape
     num_pages = cache.numel() // (cfg.page_size * _cache_row_elems(cfg))
     _check(lib().mla_append_cache_latent(
-        ctypes.byref(cfg), _ptr(c_kv, "c_kv", a, T * cfg.d_latent), _ptr(k_pe, "k_pe", a, T * cfg.d_rope),
-        T, _ptr(req_ids, "req_ids", _i32(0), T), _ptr(positions, "positions", _i32(0), T),
-        _ptr(block_table, "block_table", _i32(0)), batch, max_pages,
-        _ptr(cache, "cache", _cache_dtypes(cfg), num_pages * cfg.page_size * _cache_row_elems(cfg)), num_pages,
-        1 if rotate else 0, _ptr(dev_status, "dev_status", _i32(0), allow_none=True),
+        ctypes.byref(cfg), _peer_ptr(c_kv, "c_kv", a, T * cfg.d_latent), _peer_ptr(k_pe, "k_pe", a, T * cfg.d_rope),
+        T, _peer_ptr(req_ids, "req_ids", _i32(0), T), _peer_ptr(positions, "positions", _i32(0), T),
+        _peer_ptr(block_table, "block_table", _i32(0)), batch, max_pages,
+        _peer_ptr(cache, "cache", _cache_dtypes(cfg), num_pages * cfg.page_size * _cache_row_elems(cfg)), num_pages,
+        1 if rotate else 0, _peer_ptr(dev_status, "dev_status", _i32(0), allow_none=True),
         _stream(stream)), "mla_append_cache_latent")
 
 
@@ -309,15 +316,15 @@ def mla_decode(cfg, q_nope, q_pe, W_UK_abs, cache, block_table, seq_lens, out_la
     max_pages = block_table.shape[1]
     o = _opts(num_workers, kernel, attn_events, wait_limit_us, withhold_page)
     _check(lib().mla_decode_ex(
-        ctypes.byref(cfg), _ptr(q_nope, "q_nope", a, batch * q_len * H * d_n),
-        _ptr(q_pe, "q_pe", a, batch * q_len * H * d_r),
-        _ptr(W_UK_abs, "W_UK_abs", a, H * d_n * d_c),
-        _ptr(cache, "cache", _cache_dtypes(cfg), num_pages * cfg.page_size * _cache_row_elems(cfg)), num_pages,
-        _ptr(block_table, "block_table", _i32(0), batch * max_pages), max_pages,
-        _ptr(seq_lens, "seq_lens", _i32(0), batch), batch, q_len,
-        _ptr(out_latent, "out_latent", a, batch * q_len * H * d_c),
-        _ptr(lse, "lse", (t.float32,), batch * q_len * H),
-        _ptr(workspace, "workspace", (t.uint8,)), workspace.numel(), ctypes.byref(o),
+        ctypes.byref(cfg), _peer_ptr(q_nope, "q_nope", a, batch * q_len * H * d_n),
+        _peer_ptr(q_pe, "q_pe", a, batch * q_len * H * d_r),
+        _peer_ptr(W_UK_abs, "W_UK_abs", a, H * d_n * d_c),
+        _peer_ptr(cache, "cache", _cache_dtypes(cfg), num_pages * cfg.page_size * _cache_row_elems(cfg)), num_pages,
+        _peer_ptr(block_table, "block_table", _i32(0), batch * max_pages), max_pages,
+        _peer_ptr(seq_lens, "seq_lens", _i32(0), batch), batch, q_len,
+        _peer_ptr(out_latent, "out_latent", a, batch * q_len * H * d_c),
+        _peer_ptr(lse, "lse", (t.float32,), batch * q_len * H),
+        _peer_ptr(workspace, "workspace", (t.uint8,)), workspace.numel(), ctypes.byref(o),
         _stream(stream)), "mla_decode")
 
 
@@ -334,14 +341,14 @@ def mla_decode_noalloc(cfg, q_nope, q_pe, W_UK_abs, cache, block_table, seq_lens
     num_pages = cache.numel() // (cfg.page_size * _cache_row_elems(cfg))
     max_pages = block_table.shape[1]
     _check(lib().mla_decode_noalloc(
-        ctypes.byref(cfg), _ptr(q_nope, "q_nope", a, batch * q_len * H * d_n),
-        _ptr(q_pe, "q_pe", a, batch * q_len * H * d_r),
-        _ptr(W_UK_abs, "W_UK_abs", a, H * d_n * d_c),
-        _ptr(cache, "cache", _cache_dtypes(cfg), num_pages * cfg.page_size * _cache_row_elems(cfg)), num_pages,
-        _ptr(block_table, "block_table", _i32(0), batch * max_pages), max_pages,
-        _ptr(seq_lens, "seq_lens", _i32(0), batch), batch, q_len,
-        _ptr(out_latent, "out_latent", a, batch * q_len * H * d_c),
-        _ptr(lse, "lse", (t.float32,), batch * q_len * H), _stream(stream)), "mla_decode_noalloc")
+        ctypes.byref(cfg), _peer_ptr(q_nope, "q_nope", a, batch * q_len * H * d_n),
+        _peer_ptr(q_pe, "q_pe", a, batch * q_len * H * d_r),
+        _peer_ptr(W_UK_abs, "W_UK_abs", a, H * d_n * d_c),
+        _peer_ptr(cache, "cache", _cache_dtypes(cfg), num_pages * cfg.page_size * _cache_row_elems(cfg)), num_pages,
+        _peer_ptr(block_table, "block_table", _i32(0), batch * max_pages), max_pages,
+        _peer_ptr(seq_lens, "seq_lens", _i32(0), batch), batch, q_len,
+        _peer_ptr(out_latent, "out_latent", a, batch * q_len * H * d_c),
+        _peer_ptr(lse, "lse", (t.float32,), batch * q_len * H), _stream(stream)), "mla_decode_noalloc")
 
 
 def mla_decode_noalloc_status(stream=None) -> int:
@@ -365,9 +372,9 @@ def mla_output_proj(cfg, out_latent, W_comb, out, workspace, stream=None):
     K = cfg.num_heads * cfg.d_latent
     rows = out_latent.numel() // K
     _check(lib().mla_output_proj(
-        ctypes.byref(cfg), _ptr(out_latent, "out_latent", a, rows * K),
-        _ptr(W_comb, "W_comb", a, K * cfg.d_model), rows, _ptr(out, "out", a, rows * cfg.d_model),
-        _ptr(workspace, "workspace", (_torch().uint8,)), workspace.numel(), _stream(stream)),
+        ctypes.byref(cfg), _peer_ptr(out_latent, "out_latent", a, rows * K),
+        _peer_ptr(W_comb, "W_comb", a, K * cfg.d_model), rows, _peer_ptr(out, "out", a, rows * cfg.d_model),
+        _peer_ptr(workspace, "workspace", (_torch().uint8,)), workspace.numel(), _stream(stream)),
         "mla_output_proj")
 
 
@@ -385,10 +392,10 @@ def mla_output_proj_unfolded(cfg, out_latent, W_UV, W_O, out, workspace, stream=
     HV = cfg.num_heads * cfg.d_v
     rows = out_latent.numel() // K
     _check(lib().mla_output_proj_unfolded(
-        ctypes.byref(cfg), _ptr(out_latent, "out_latent", a, rows * K),
-        _ptr(W_UV, "W_UV", a, cfg.d_latent * HV), _ptr(W_O, "W_O", a, HV * cfg.d_model), rows,
-        _ptr(out, "out", a, rows * cfg.d_model),
-        _ptr(workspace, "workspace", (_torch().uint8,)), workspace.numel(), _stream(stream)),
+        ctypes.byref(cfg), _peer_ptr(out_latent, "out_latent", a, rows * K),
+        _peer_ptr(W_UV, "W_UV", a, cfg.d_latent * HV), _peer_ptr(W_O, "W_O", a, HV * cfg.d_model), rows,
+        _peer_ptr(out, "out", a, rows * cfg.d_model),
+        _peer_ptr(workspace, "workspace", (_torch().uint8,)), workspace.numel(), _stream(stream)),
         "mla_output_proj_unfolded")
 
 
@@ -411,10 +418,10 @@ def mla_query_from_hidden(cfg, d_q, h, W_DQ, W_UQ, W_QR, q_nope, q_pe, workspace
     d, H = cfg.d_model, cfg.num_heads
     T = h.numel() // d
     _check(lib().mla_query_from_hidden(
-        ctypes.byref(cfg), int(d_q), _ptr(h, "h", a, T * d), _ptr(W_DQ, "W_DQ", a, d * d_q),
-        _ptr(W_UQ, "W_UQ", a, d_q * H * cfg.d_nope), _ptr(W_QR, "W_QR", a, d * H * cfg.d_rope), T,
-        _ptr(q_nope, "q_nope", a, T * H * cfg.d_nope), _ptr(q_pe, "q_pe", a, T * H * cfg.d_rope),
-        _ptr(workspace, "workspace", (_torch().uint8,)), workspace.numel(), _stream(stream)),
+        ctypes.byref(cfg), int(d_q), _peer_ptr(h, "h", a, T * d), _peer_ptr(W_DQ, "W_DQ", a, d * d_q),
+        _peer_ptr(W_UQ, "W_UQ", a, d_q * H * cfg.d_nope), _peer_ptr(W_QR, "W_QR", a, d * H * cfg.d_rope), T,
+        _peer_ptr(q_nope, "q_nope", a, T * H * cfg.d_nope), _peer_ptr(q_pe, "q_pe", a, T * H * cfg.d_rope),
+        _peer_ptr(workspace, "workspace", (_torch().uint8,)), workspace.numel(), _stream(stream)),
         "mla_query_from_hidden")
 
 
@@ -542,6 +549,6 @@ def mla_evict_cache(cfg, weights, seq_lens, block_table, cache, budget, kept, ne
 def mla_read_device_status(status_word, stream=None) -> int:
     """Synchronises the stream and returns (then clears) the device status code."""
     code = ctypes.c_int(0)
-    _check(lib().mla_read_device_status(_ptr(status_word, "status_word"), _stream(stream),
+    _check(lib().mla_read_device_status(_peer_ptr(status_word, "status_word"), _stream(stream),
                                         ctypes.byref(code)), "mla_read_device_status")
     return int(code.value)
