@@ -217,6 +217,8 @@ static mla_status check_append(const mla_config* cfg, int T, const int32_t* req_
     return invalid("null pointer");
   if (batch <= 0 || max_pages <= 0 || num_pages <= 0)
     return invalid("batch, max_pages and num_pages must be positive");
+  if (T > 0 && cfg->cache_dtype == MLA_FP8_E4M3_B128 && ((uintptr_t)cache & 3) != 0)
+    return invalid("a block-scaled cache must be 4-byte aligned");
   return MLA_OK;
 }
 
@@ -323,6 +325,8 @@ mla_status mla_decode_ex(const mla_config* cfg, const void* q_nope, const void* 
     return unsupported("the tensor-core decode kernel needs bf16 activations, 64-token pages and "
                        "the DeepSeek-V2 head shape (128 heads, d_c 512, d_r 64)");
   const bool tc = use_tc_kernel(cfg, opts);
+  if (tc && !aligned16(out_latent)) return invalid("out_latent must be 16-byte aligned");
+  if (!tc && ((uintptr_t)cache & 3) != 0) return invalid("cache must be 4-byte aligned");
   DecodeWorkspace w;
   decode_layout(cfg, batch, q_len, default_workers(cfg, opts, tc), &w);
   if (!workspace || workspace_bytes < w.total) {

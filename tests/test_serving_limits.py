@@ -29,6 +29,32 @@ def test_key_weights_refuses_rows_wider_than_its_shared_memory(lib, act, cache, 
     assert "shared memory" in M.mla_last_error()
 
 
+# ----------------------------------------------------------------------------- addresses
+
+def at(offset):
+    return ctypes.c_void_p((1 << 20) + offset)
+
+
+@pytest.mark.parametrize("kernel,out,cache,code", [(0, 2, 0, M.MLA_ERR_INVALID), (2, 8, 0, M.MLA_ERR_INVALID),
+                                                   (1, 2, 2, M.MLA_ERR_INVALID)])
+def test_decode_refuses_addresses_that_its_kernels_cannot_take(lib, kernel, out, cache, code):  # noqa: F811
+    """The tensor-core kernel writes out_latent 16 bytes at a time, the SIMT kernel reads the cache by
+    32-bit words; elsewhere these were misaligned accesses."""
+    opts = M._opts(0, kernel)
+    assert lib.mla_decode_ex(ctypes.byref(cfg()), at(0), at(0), at(0), at(cache), 4, at(0), 2, at(0), 4, 1, at(out), at(0),
+                             at(0), 1 << 40, ctypes.byref(opts), None) == code
+    assert "aligned" in M.mla_last_error()
+
+
+def test_append_refuses_addresses_that_its_kernels_cannot_take(lib):  # noqa: F811
+    c = cfg("bf16", "fp8_e4m3_b128")
+    assert lib.mla_append_cache_latent(ctypes.byref(c), at(0), at(0), 3, at(0), at(0), at(0), 1, 2, at(2), 4, 1, None,
+                                       None) == M.MLA_ERR_INVALID
+    assert lib.mla_append_cache(ctypes.byref(c), at(0), at(0), 3, at(0), at(0), at(0), 1, 2, at(2), 4, None, None, 0,
+                                None) == M.MLA_ERR_INVALID
+    assert "aligned" in M.mla_last_error()
+
+
 # ----------------------------------------------------------------------------- devices
 
 class Elsewhere:
