@@ -175,7 +175,7 @@ mla_status mla_decode_workspace_size(const mla_config* cfg, int batch, int q_len
  *   out_latent [batch][q_len][H][d_c] (act dtype), lse [batch][q_len][H] (fp32)  outputs.
  * seq_lens[b] == 0 marks an empty request: out_latent = 0, lse = -inf.
  * The cache has to start at a multiple of 4 bytes (a block-scaled one in the append calls too);
- * the tensor-core kernel's out_latent at one of 16.
+ * the tensor-core kernel's out_latent at one of 16. d_latent above 512: MLA_ERR_UNSUPPORTED.
  * workspace: device buffer of at least mla_decode_workspace_size bytes, 256-byte
  * aligned, owned by the caller, any initial contents; its first int32 is the device
  * status word, cleared by each call and then set by that call's guards. Calls that

@@ -297,9 +297,16 @@ static mla_status check_decode_shape(const mla_config* cfg, int batch, int q_len
   return MLA_OK;
 }
 
+// The SIMT decode kernel holds a latent of at most 512 elements in registers.
+static mla_status check_decode(const mla_config* cfg, int batch, int q_len) {
+  mla_status st = check_decode_shape(cfg, batch, q_len);
+  if (st == MLA_OK && cfg->d_latent > 512) st = unsupported("the decode takes d_latent up to 512");
+  return st;
+}
+
 mla_status mla_decode_workspace_size(const mla_config* cfg, int batch, int q_len,
                                      const mla_decode_opts* opts, size_t* bytes) {
-  mla_status st = check_decode_shape(cfg, batch, q_len);
+  mla_status st = check_decode(cfg, batch, q_len);
   if (st != MLA_OK) return st;
   if (!bytes) return invalid("bytes is NULL");
   const bool tc = use_tc_kernel(cfg, opts);
@@ -314,7 +321,7 @@ mla_status mla_decode_ex(const mla_config* cfg, const void* q_nope, const void* 
                          const int32_t* block_table, int max_pages, const int32_t* seq_lens,
                          int batch, int q_len, void* out_latent, float* lse, void* workspace,
                          size_t workspace_bytes, const mla_decode_opts* opts, void* stream) {
-  mla_status st = check_decode_shape(cfg, batch, q_len);
+  mla_status st = check_decode(cfg, batch, q_len);
   if (st != MLA_OK) return st;
   if (!q_nope || !q_pe || !W_UK_abs || !cache || !block_table || !seq_lens || !out_latent || !lse)
     return invalid("null pointer");

@@ -29,6 +29,15 @@ def test_key_weights_refuses_rows_wider_than_its_shared_memory(lib, act, cache, 
     assert "shared memory" in M.mla_last_error()
 
 
+def test_decode_refuses_latents_wider_than_its_registers(lib):  # noqa: F811
+    """The SIMT kernel's accumulators end at 512 elements: wider outputs were left unwritten."""
+    for act in ("f32", "bf16"):
+        c, n = cfg(act, act, d_latent=516), ctypes.c_size_t(0)
+        assert lib.mla_decode_workspace_size(ctypes.byref(c), 4, 1, None, ctypes.byref(n)) == U
+        assert lib.mla_decode(ctypes.byref(c), *[ctypes.c_void_p(1 << 20)] * 4, 4, ctypes.c_void_p(1 << 20), 2,
+                              ctypes.c_void_p(1 << 20), 4, 1, *[ctypes.c_void_p(1 << 20)] * 3, 1 << 40, None) == U
+
+
 # ----------------------------------------------------------------------------- addresses
 
 def at(offset):
