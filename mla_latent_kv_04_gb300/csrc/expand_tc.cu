@@ -296,7 +296,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     Units it(job, u0);
     for (int u = u0; ok && u < u1; ++u, it.next()) {
       if (u != u0 && !it.row_start()) continue;
-      const int l = it.tile * kTile + 128 * rank + row, page = page_of(l);
+      // a warp's 32 tokens lie on one page, so that its lanes go one way to the warp-wide stores below
+      // (rows behind the prefix, on its last page, are not written out)
+      const int l = it.tile * kTile + 128 * rank + row, page = page_of(l - lane);
       const uint8_t* row_p = reinterpret_cast<const uint8_t*>(p.cache) +
                              ((long long)(page < 0 ? 0 : page) * 64 + (l & 63)) * p.row_bytes;
       const uint4* src = reinterpret_cast<const uint4*>(row_p + (kKind ? 256 : 512) * half);
@@ -329,7 +331,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
           }
         }
-        __syncwarp();                                  // the store is warp-wide (tokens on bad pages load nothing)
         ptx::tmem_st32(t_x + 32 * b, o);
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) cur[i] = nxt[i];

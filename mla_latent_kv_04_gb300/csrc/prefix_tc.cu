@@ -419,8 +419,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (__any_sync(0xffffffffu, grow)) {
             if (!(ok = wait_w(B_ODONE + ((g - 1) & 1), ((g - 1) >> 1) & 1))) break;
             ptx::tc_fence_after();
-            const float a = grow ? (m == -INFINITY ? 0.f : ptx::ex2((m - mb) * c)) : 1.f;
-            __syncwarp();
+            // (no branch: the warp stays together for the accesses below; m = -infinity gives 0)
+            const float shrink = ptx::ex2((m - mb) * c), a = grow ? shrink : 1.f;
 #pragma unroll 1
             for (int q = 0; q < 4; ++q) {
               uint32_t o[16];
