@@ -281,8 +281,15 @@ mla_status mla_query_from_hidden(const mla_config* cfg, int d_q, const void* h, 
  * values (huny.dev §2-1: k^C = c W^UK, v^C = c W^UV), each step attends to those for every
  * request of the batch at once, and the result is joined with mla_decode's over the request's
  * own tokens. Per key, head and query this multiplies d_n + d_r + d_v elements instead of
- * the absorbed form's 2 d_c + d_r, and the prefix is read once per step instead of once per
- * request. A step is
+ * the absorbed form's 2 d_c + d_r, and a step reads the expanded prefix once, not once per
+ * request. But the expanded prefix is large: H (d_n + d_v) + d_r elements a token, 65.7 KB in bf16
+ * at DeepSeek-V2 shapes (57 times its cached row; 538 MB per layer for 8192 tokens), so that a
+ * step costs the same for one request as for 128. With few query tokens (batch * q_len) a plain
+ * mla_decode, with block tables that all name the prefix's pages in front of the request's own, is
+ * faster: measured, the attention to the prefix alone, it leads up to about 10 query tokens at 2048
+ * prefix tokens, 33 at 8192 and 40 at 32768, and nowhere at 512 (8192 tokens: 57 us against 93 for 16
+ * query tokens, 157 against 95 for 64, 287 against 99 for 128). (That form numbers a request's own
+ * tokens from prefix_len, which has to be a whole number of pages.) A step is
  *   mla_prefix_attend(..)        -> u_prefix, lse_prefix   (the shared tokens)
  *   mla_decode(..)               -> out_latent, lse        (each request's own tokens)
  *   mla_output_proj_prefix(..)   -> out
@@ -298,10 +305,12 @@ mla_status mla_query_from_hidden(const mla_config* cfg, int d_q, const void* h, 
  * DeepSeek-V2's head shape (d_n 128, d_r 64, d_v 128, d_c 512, 64-token pages, any number of heads;
  * key weights 16 to 128 heads by 16) and tensors that start at multiples of 16 bytes; any other
  * shape, fp32, or a tensor that starts elsewhere takes SIMT kernels with the same results up to
- * rounding, many times slower at large sizes. The cache has to start at a multiple of 4 bytes (eviction
+ * rounding, many times slower at large sizes. (mla_absorb_query takes the decode's GEMM for every bf16
+ * shape with d_n and d_c multiples of 8 and a q_nope and W_UK_abs that start at multiples of 16 bytes.) The cache has to start at a multiple of 4 bytes (eviction
  * from an fp32 cache: 16). batch * q_len is limited to 32768 as in mla_decode. A tensor-core
  * kernel's waits are bounded: should one run out (2 s), the call's work is left undone and
- * MLA_ERR_TIMEOUT is OR-ed into *dev_status (mla_output_proj_prefix has no such word). Sums are
+ * MLA_ERR_TIMEOUT is OR-ed into *dev_status (mla_output_proj_prefix and mla_absorb_query have no such
+ * word: their outputs are then not written). Sums are
  * made in one order, so that every run gives the same bits. Inputs and outputs must not overlap
  * unless a call says so. */
 
@@ -334,9 +343,8 @@ mla_status mla_prefix_attend_workspace_size(const mla_config* cfg, int batch, in
  *   dtype), lse [batch][q_len][H] (fp32) outputs. d_n + d_r + d_v above 57344:
  *   MLA_ERR_UNSUPPORTED.
  * The softmax's weights are rounded to the act dtype for the product with the values; scores,
- * maxima, sums and the rotated query are held in fp32 precision (bf16: the rotated query as
- * the sum of two bf16 terms, with an error of 2^-18 of a term; up to 3 keys in fp32), so lse is an
- * fp32 result. A NaN score makes its row's u and lse NaN.
+ * maxima and sums are held in fp32, and so is the rotated query up to 3 keys; above, with bf16, it is
+ * the sum of two bf16 terms, each element off by at most 2^-17 of itself (sine and cosine by 2^-21). A NaN score makes its row's u and lse NaN.
  * seq_lens[b] == 0 marks an empty request (u = 0, lse = -inf), as does prefix_len == 0 for
  * every request; 0 < seq_lens[b] < q_len is a guard error (same outputs). workspace: 256-byte
  * aligned device buffer of mla_prefix_attend_workspace_size bytes (NULL if that is 0), any
@@ -347,9 +355,9 @@ mla_status mla_prefix_attend(const mla_config* cfg, const void* q_nope, const vo
                              void* workspace, size_t workspace_bytes, int32_t* dev_status,
                              void* stream);
 
-/* Bytes of workspace mla_output_proj_prefix needs for `rows` rows: u and an fp32 accumulator as
- * mla_output_proj_unfolded, and with bf16 activations above 128 rows fp32 pieces of the product where
- * it is cut, up to 80 MB. */
+/* Bytes of workspace mla_output_proj_prefix needs for `rows` rows: as many as
+ * mla_output_proj_unfolded (whose accumulator's place this call leaves unused) and, with bf16
+ * activations above 128 rows, fp32 pieces of the product where it is cut, up to 80 MB. */
 mla_status mla_output_proj_prefix_workspace_size(const mla_config* cfg, int rows, size_t* bytes);
 
 /* mla_output_proj_unfolded of the attention over both key sets, own tokens and prefix:
@@ -389,8 +397,11 @@ mla_status mla_absorb_query(const mla_config* cfg, const void* q_nope, const voi
  * shared prefix joined in) it is the own tokens' share of it.
  *   q_lat [batch][q_len][H][d_c + d_r] (act dtype; mla_absorb_query), lse [batch][q_len][H]
  *   (fp32); cache, block_table, seq_lens, batch, q_len as in mla_decode; decay in [0, 1];
- *   weights [batch][max_pages * P] fp32 (device), updated in place: no initial contents needed
- *   for tokens that were never cached before.
+ *   weights [batch][max_pages * P] fp32 (device), updated in place. With decay > 0 the entries of
+ *   tokens cached before this step are read, so each has to be written first: by the call of the
+ *   step that cached the token, or by the caller (0, say) for tokens cached without one: a prompt,
+ *   or what was appended after an eviction, behind whose new lengths the old entries remain. Entries
+ *   of this step's tokens and behind the request, and all of them with decay == 0, may hold anything.
  * Sums are fp32, in a fixed order (the same bits every time). seq_lens[b] == 0: nothing is
  * written. Requests with a bad length and tokens on a bad page are left out, with
  * MLA_ERR_DEVICE_GUARD in *dev_status (optional, OR-ed in). MLA_ERR_UNSUPPORTED: batch * max_pages

@@ -36,9 +36,11 @@ __device__ __forceinline__ void rope_sincos(const RopeTable& rt, int k, int pos,
 
 // The same frequencies as binary fractions of a turn, turns[k] = theta^(-2k/d_r) / (2 pi) in
 // units of 2^-64 turn: the product with an integer position wraps to the angle modulo one
-// turn by itself, exactly up to |position| 2^-65 turns, in integer arithmetic (the double
-// reduction above costs three fp64 operations per angle, which this GPU runs at a 64th of
-// the fp32 rate: kernels that turn many rows are then bound by it).
+// turn by itself, in integer arithmetic (the double reduction above costs three fp64 operations per
+// angle, which this GPU runs at a 64th of the fp32 rate: kernels that turn many rows are then bound by
+// it). The table is made of doubles: an entry is off by up to 2^-55 turn, and the angle by |position|
+// times that, plus the 2^-32 turn to which it is cut (2^-24 turn at position 2^31), before it is
+// rounded to fp32.
 struct TurnTable {
   unsigned long long turns[kMaxRopePairs];
   int pairs;

@@ -24,8 +24,8 @@
 // (codes are exact in bf16); block scales multiply the codes and the product is rounded to bf16,
 // which adds as much error as the rounding of the result does.
 //
-// Bound: the MMAs (4096 cycles for 256 tokens and a head on two SMs): 8192 tokens take 167 us, 1650
-// TFLOP/s.
+// Bound: the MMAs (4096 cycles for 256 tokens and a head on two SMs): 8192 tokens take 165 to 175 us
+// in a graph of such calls (1570 to 1670 TFLOP/s, as the power cap lets it), a call by itself 184.
 #include "fp8_tiles.cuh"
 #include "internal.h"
 #include "sm100_ptx.cuh"

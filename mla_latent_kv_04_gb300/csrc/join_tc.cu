@@ -15,8 +15,9 @@
 // shared memory takes 48 + 64 bytes a cycle instead of 64 + 64. The (tile, 64-deep chunk) units are
 // cut into one contiguous range per pair; pieces of a tile go to the workspace in fp32 and
 // gemm_merge_kernel adds them in order. Short products (few heads) take whole tiles instead. Fewer rows are bound by W_O's bytes and take the cluster
-// split-K GEMM (gemm_tc.cu). 512 rows take 90 us (join 25, product 54, merge 12, each by itself); 32
-// rows 35 us.
+// split-K GEMM (gemm_tc.cu). In a graph of such calls 512 rows take 89 us (join 25, product 54, merge 12,
+// each by itself) and 32 rows 34; a call by itself 92 and 37. u is rounded to bf16 between the two
+// products, as in mla_output_proj_unfolded: W_O's MMAs take it as an operand.
 #include "fp8_tiles.cuh"
 #include "internal.h"
 #include "sm100_ptx.cuh"

@@ -5,9 +5,11 @@
 // values are read once for all of a tile's rows. Per head, row tile and block of 128 keys:
 //   S = [q_nope ; q_hi ; q_lo] [K ; k_pe ; k_pe]^T   (K = 128 + 64 + 64 of the MMA)
 //   P = exp2(c S - c m),  O += P V,  l += sum P      (c = softmax scale * log2 e)
-// The rotated query is the sum of two bf16 terms (residual 2^-16), so that the scores, and the
-// LSE, are fp32 results: q_nope and the keys are exact. The low term costs a fifth of the MMA
-// time; bf16 alone would put up to 2^-8 of the rotary score's terms into the LSE.
+// The rotated query is the sum of two bf16 terms (off by at most 2^-17 of an element; q_nope and the
+// keys are exact), since the LSE is joined with another one: the low term costs a fifth of the MMA
+// time; bf16 alone would put up to 2^-8 of the rotary score's terms into the LSE. P is rounded to
+// bf16 as the operand of O (its sum l is not): at most 2^-8 of a weight, about what the rounding of u
+// to bf16 does; a second term would double O's MMAs, and P and O have no tensor memory to spare.
 //
 // A tile is 128 rows on one CTA, or, with more than 128 rows in the batch, 256 rows on a CTA pair
 // whose MMAs run over both (cta_group::2, M = 256): each CTA holds half the keys of a block
@@ -27,6 +29,7 @@
 // workspace (fp32) and are merged by attend_merge_kernel. If whole tiles spread evenly enough,
 // the cuts are put between tiles.
 //
+// Times are those of a call in a graph of the same calls (a call by itself takes 7 us more).
 // Bound: at up to about 200 rows the keys' and values' bytes (64 KB per head and block): 128 rows x
 // 8192 keys take 90 us, 6.1 TB/s. Above, the MMAs would be (54 us for 256 rows x 4096 keys with the
 // low term); it takes 80, since a block's softmax, about as long as its MMAs, overlaps them in part only

@@ -120,8 +120,9 @@ template <> struct Quads<bf16> {
 // sum of the softmax; the output's dims over the threads, narrow values several times, each copy of
 // the threads taking every so manyth key. Small calls are bound by the latency of their loads, which
 // the unrolled loops keep in flight together; large ones by the loads of keys (a thread reads a row of
-// its own), which several query rows share: 64 rows x 16 heads, tiny shape, 1000 keys 52 us with 4 rows
-// a block and four elements a load, 201 with one row and one element.
+// its own), which several query rows share: 64 rows x 16 heads, tiny shape, 1000 keys 62 us with 4 rows
+// a block and four elements a load, 201 with one row and one element. (85 us among calls issued one by
+// one: the next call's blocks, started early, are spread unevenly over the SMs.)
 template <typename AT, int kR>
 __global__ void __launch_bounds__(128) attend_simt_kernel(PrefixAttendParams p) {
   extern __shared__ __align__(16) float sm[];
