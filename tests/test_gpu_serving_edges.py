@@ -362,3 +362,94 @@ def test_whole_step_captured_and_replayed(cache, act, shape, H):
     restore()
     step()
     same(results(), want)
+
+
+# ----------------------------------------------------------------------------- the largest batches
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8_e4m3"])
+def test_key_weights_of_more_requests_than_the_cost_table_holds(kind):
+    """Above 8192 requests the ranges are cut by tiles alone."""
+    rng = np.random.default_rng(1)
+    c = D.Cache(rng, kind, D.dims("v2", 16), list(rng.integers(0, 4, 8300)), max_pages=1)
+    q_lat = D.draw(rng, (8300, 1, 16, 576), "bf16", 0.6)
+    lse = rng.standard_normal((8300, 1, 16)).astype(np.float32)
+    old = rng.random((8300, 64)).astype(np.float32)
+    got = evict.weigh(c, 1, q_lat, lse, old, 0.5)
+    evict.check_weights(c, 1, q_lat, lse, oracle.softmax_scale(128, 64), old, 0.5, got)
+
+
+@pytest.mark.parametrize("B,q,L", [(32768, 1, 2), (32768, 1, 10), (8192, 4, 10)])
+@pytest.mark.parametrize("act,shape", [("bf16", "v2"), ("f32", "tiny")])
+def test_attend_of_the_largest_batch(act, shape, B, q, L):
+    rng = np.random.default_rng(L)
+    d = D.dims(shape, 1)
+    x, lens = prefix.attend_inputs(rng, d, B, q, L, act, rng.integers(q, 3000, B))
+    u, lse = prefix.attend(M.make_config(d, act, act), x, lens, act)
+    prefix.check_attend(d, x, lens, act, u, lse)
+
+
+@pytest.mark.parametrize("act,shape", [("bf16", "v2"), ("f32", "tiny"), ("bf16", "odd")])
+def test_absorb_query_of_the_largest_batch(act, shape):
+    rng = np.random.default_rng(2)
+    d, B = D.dims(shape, 2), 32768
+    qn, qp = D.draw(rng, (B, 1, 2, d.d_nope), act), D.draw(rng, (B, 1, 2, d.d_rope), act)
+    W_abs = D.draw(rng, (2, d.d_nope, d.d_latent), act, d.d_latent ** -0.5)
+    lens = rng.integers(1, 5000, B).astype(np.int32)
+    out = torch.empty(B, 1, 2, d.d_latent + d.d_rope, dtype=D.torch_type(act), device="cuda")
+    M.mla_absorb_query(M.make_config(d, act, act), D.dev(qn, act), D.dev(qp, act), D.dev(W_abs, act), D.dev(lens), out)
+    lat = np.einsum("bthn,hnc->bthc", qn.astype(np.float64), W_abs.astype(np.float64))
+    mag = np.einsum("bthn,hnc->bthc", np.abs(qn), np.abs(W_abs))
+    pe = oracle.rope(qp.astype(np.float64), np.repeat(lens.astype(np.int64)[:, None, None] - 1, 2, 2))
+    want = np.concatenate([lat, pe], -1)
+    # fp32 sums of d_n products; sine and cosine to 2^-20 of values below 7; one rounding
+    tol = D.EPS[act] * np.abs(want) * 1.01 + np.concatenate(
+        [4 * d.d_nope * 2.0 ** -24 * mag, np.full(pe.shape, 7 * 2.0 ** -20)], -1)
+    assert_within(out.double().cpu().numpy(), want, tol, "q_lat")
+
+
+def test_output_proj_prefix_of_many_rows():
+    """40000 rows on the tensor cores, against fp64 on the device."""
+    H, rows = 2, 40000
+    d = D.dims("v2", H)
+    cfg, g = M.make_config(d, "bf16", "bf16"), torch.Generator(device="cuda").manual_seed(3)
+
+    def rand(*shape, std=1.0, dtype=torch.bfloat16):
+        return (torch.randn(*shape, generator=g, device="cuda") * std).to(dtype)
+    o, up, W_UV, W_O = rand(rows, H, 512, std=0.1), rand(rows, H, 128, std=0.1), rand(512, H * 128, std=512 ** -0.5), rand(H * 128, 5120, std=1 / 16)
+    lse, lsep = rand(rows, H, std=3, dtype=torch.float32), rand(rows, H, std=3, dtype=torch.float32)
+    out = torch.full((rows, 5120), float("nan"), dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(M.mla_output_proj_prefix_workspace_size(cfg, rows), dtype=torch.uint8, device="cuda")
+    M.mla_output_proj_prefix(cfg, o, lse, up, lsep, W_UV, W_O, out, ws)
+    a = torch.sigmoid(lse.double() - lsep.double())[..., None]
+    W = W_UV.double().view(512, H, 128)
+
+    def joined(x, y, w):
+        return a * torch.einsum("rhc,chv->rhv", x, w) + (1 - a) * y
+    u = joined(o.double(), up.double(), W).view(rows, -1)
+    mag_u = joined(o.double().abs(), up.double().abs(), W.abs()).view(rows, -1)
+    O64 = W_O.double()
+    want = u @ O64
+    # u's rounding, its fp32 sums (weights to 2^-20), the projection's sums, the result's rounding
+    tol = (2.0 ** -8 * u.abs() + (4 * 512 * 2.0 ** -24 + 2.0 ** -19) * mag_u) @ O64.abs() + \
+        4 * H * 128 * 2.0 ** -24 * (u.abs() @ O64.abs()) + 2.0 ** -8 * want.abs()
+    assert ((out.double() - want).abs() <= tol * 1.01).all()
+
+
+@pytest.mark.parametrize("in_place", [True, False], ids=["in_place", "new_pages"])
+def test_evict_of_the_largest_batch(in_place):
+    """32768 requests of three tokens down to two, pages of four tokens."""
+    B, dims = 32768, D.dims("tiny", 16)
+    dims.page_size = 4
+    cfg, row = M.make_config(dims, "f32", "f32"), 80
+    g = torch.Generator(device="cuda").manual_seed(4)
+    pool = torch.randn(2 * B, 4, row, generator=g, device="cuda")
+    perm = torch.randperm(2 * B, generator=g, device="cuda").to(torch.int32)
+    table, new = perm[:B].view(B, 1).contiguous(), perm[B:].view(B, 1).contiguous()
+    w = torch.rand(B, 4, generator=g, device="cuda")
+    lens = torch.full((B,), 3, dtype=torch.int32, device="cuda")
+    kept, nl, before = torch.empty(B, 2, dtype=torch.int32, device="cuda"), torch.empty_like(lens), pool.clone()
+    M.mla_evict_cache(cfg, w, lens, table, pool, 2, kept, nl, new_block_table=table if in_place else new, rotate=False)
+    want = torch.sort(torch.topk(w[:, :3], 2).indices, 1).values
+    assert (nl == 2).all() and torch.equal(kept, want.int())
+    src = before[table[:, 0].long()[:, None], want]
+    assert torch.equal(pool[(table if in_place else new)[:, 0].long(), :2], src)
