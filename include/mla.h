@@ -402,8 +402,10 @@ mla_status mla_absorb_query(const mla_config* cfg, const void* q_nope, const voi
  *   step that cached the token, or by the caller (0, say) for tokens cached without one: a prompt,
  *   or what was appended after an eviction, behind whose new lengths the old entries remain. Entries
  *   of this step's tokens and behind the request, and all of them with decay == 0, may hold anything.
- * Sums are fp32, in a fixed order (the same bits every time). seq_lens[b] == 0: nothing is
- * written. Requests with a bad length and tokens on a bad page are left out, with
+ * Sums are fp32, in a fixed order (the same bits every time). On fp8 caches the tensor-core form
+ * takes each head's latent query (and rotary one, with a per-tensor scale) as the sum of two e4m3
+ * terms: exact for elements down to 2^-13 of the head's largest, smaller ones off by up to 2^-19 of
+ * it. seq_lens[b] == 0: nothing is written. Requests with a bad length and tokens on a bad page are left out, with
  * MLA_ERR_DEVICE_GUARD in *dev_status (optional, OR-ed in). MLA_ERR_UNSUPPORTED: batch * max_pages
  * or max_pages * P above 2^31 - 1; rows so wide that a page of them and a query in fp32 do not fit
  * 227 KB (64-token pages: d_c + d_r above 892 in fp32, 1756 in bf16, 3412 in e4m3, 3136 block-scaled). */
