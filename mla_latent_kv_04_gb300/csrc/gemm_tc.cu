@@ -234,7 +234,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
     for (int c = 0; c < BN; c += 32) {
       uint32_t v[32];
-      __syncwarp();                             // the load is warp-wide
       ptx::tmem_ld32(t_row + c, v);
       ptx::tmem_wait_ld();
       if (m < gp.M) {
@@ -244,6 +243,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (n < gp.N) epi(z, m, n, __uint_as_float(v[j]));
         }
       }
+      if (gp.M & 31) __syncwarp();              // rows end inside a warp: the next load is warp-wide
     }
   }
   ptx::tc_fence_before();
