@@ -226,9 +226,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   k_loop<BN, NS>(&tmA, &tmB, base, tmem, m0, n0, z, kb0, kb1, abort, gp.status);
   // epilogue: every thread owns one TMEM lane = one row m of D^T
-  ok = wait_bar(done, 0, abort, gp.status);
+  // (a warp reads the accumulator, or gives up, as one)
+  ok = __all_sync(0xffffffffu, wait_bar(done, 0, abort, gp.status) && !*abort) != 0;
   ptx::tc_fence_after();
-  if (ok && !*abort) {
+  if (ok) {
     const int m = m0 + 32 * warp + lane;
     const uint32_t t_row = tmem + ((uint32_t)(32 * warp) << 16);
 #pragma unroll 1

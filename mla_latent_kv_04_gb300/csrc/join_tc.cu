@@ -125,9 +125,9 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
       for (int i = 0; i < 16; ++i) up[i] = reinterpret_cast<const uint4*>(p.u_prefix + at)[i];
     }
-    const bool ok = __all_sync(0xffffffffu, wait(B_DONE, 0)) != 0;
+    const bool ok = __all_sync(0xffffffffu, wait(B_DONE, 0) && !*abort) != 0;   // (a warp reads, or gives up, as one)
     ptx::tc_fence_after();
-    if (ok && !*abort) {
+    if (ok) {
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         uint32_t v[32];
