@@ -443,6 +443,127 @@ mla_status mla_evict_cache(const mla_config* cfg, const float* weights, const in
                            const int32_t* new_block_table, int new_max_pages, float* new_weights,
                            int32_t* kept, int32_t* new_seq_lens, int32_t* dev_status, void* stream);
 
+/* ---- page-sparse decoding -----------------------------------------------------------------
+ * A long context's cache is read whole by every mla_decode. These calls let each query token read only
+ * the pages that an estimate finds worth reading: a summary of each page (mla_page_keys), the attention
+ * that the query would pay to each page by those summaries (mla_page_scores: 1/64 of the cache's bytes),
+ * the pages kept (mla_select_pages) and the attention over their tokens (mla_decode_pages). A step is
+ *   mla_append_cache(..), mla_page_keys(.., new_tokens = q_len, ..)
+ *   mla_absorb_query(..)  -> q_lat
+ *   mla_page_scores(..)   -> scores
+ *   mla_select_pages(..)  -> pages
+ *   mla_decode_pages(..)  -> out_latent, lse     (then an output projection as ever)
+ * The cache, its block tables and lengths are those of mla_append_cache and mla_decode and are not
+ * changed. A page is one of the cache's own, of P tokens: page p of a request holds its tokens
+ * p P .. p P + P - 1. Query token t of request b sits at seq_lens[b] - q_len + t and sees the pages
+ * 0 .. (seq_lens[b] - q_len + t) / P. Sums are made in one order: every run gives the same bits. Inputs
+ * and outputs must not overlap. *dev_status (optional, may be NULL) has MLA_ERR_DEVICE_GUARD OR-ed in. */
+
+/* The mean of a page's cached rows, latent and rotary part, as its key:
+ *   page_keys[page] = (1 / n) sum over its n cached tokens of the row   (fp8: the values of the codes)
+ * for every page that holds one of the request's last new_tokens tokens (all its pages if new_tokens >=
+ * seq_lens[b]: a prompt, or after mla_evict_cache); other rows are left as they are. fp32 sums, rounded
+ * once.
+ *   cache, num_pages, block_table, max_pages, seq_lens, batch as in mla_decode (batch at most 32768);
+ *   page_keys [num_pages][d_c + d_r] act dtype, indexed like the cache by physical page (a page that
+ *   several requests share has one key; the requests have to agree on how many of its tokens are cached).
+ * seq_lens[b] == 0: nothing is written; a length outside [0, max_pages * P] or a page id out of range is
+ * left out, with the guard. The cache has to start at a multiple of 4 bytes. MLA_ERR_UNSUPPORTED:
+ * d_c + d_r above 58112, max_pages * P above 2^31 - 1. No workspace. */
+mla_status mla_page_keys(const mla_config* cfg, const void* cache, int num_pages, const int32_t* block_table,
+                         int max_pages, const int32_t* seq_lens, int batch, int new_tokens, void* page_keys,
+                         int32_t* dev_status, void* stream);
+
+/* Bytes of workspace mla_page_scores needs for this batch on the current device (may be 0). */
+mla_status mla_page_scores_workspace_size(const mla_config* cfg, int batch, int q_len, int max_pages,
+                                          size_t* bytes);
+
+/* The attention that each query token would pay to each page if every token's key were its page's:
+ *   z_ip = softmax_scale * q_lat[b][t][i] . page_keys[page p],
+ *   scores[b][t][p] = sum over heads i of m_p exp(z_ip) / sum_p' m_p' exp(z_ip'),
+ * m_p the tokens of page p that the query sees (P, or fewer on its last page), over the pages it sees:
+ * they share out H. Entries behind them are left as they are.
+ *   q_lat [batch][q_len][H][d_c + d_r] (act dtype; mla_absorb_query); page_keys from mla_page_keys;
+ *   block_table, seq_lens as in mla_decode; scores [batch][q_len][max_pages] fp32.
+ * fp32 sums and softmax. A page with an id out of range scores 0, a request with seq_lens[b] < q_len or
+ * above max_pages * P is left out, both with the guard; seq_lens[b] == 0 is left out. workspace: 256-byte
+ * aligned device buffer of mla_page_scores_workspace_size bytes (NULL if that is 0), any contents; calls
+ * that share one must be ordered on the GPU. */
+mla_status mla_page_scores(const mla_config* cfg, const void* q_lat, const void* page_keys, int num_pages,
+                           const int32_t* block_table, int max_pages, const int32_t* seq_lens, int batch,
+                           int q_len, float* scores, void* workspace, size_t workspace_bytes,
+                           int32_t* dev_status, void* stream);
+
+/* The pages that each query token keeps: all it sees if they are at most `budget`, otherwise its first
+ * `sinks`, its last `recent` and, of those between, the budget - sinks - recent with the largest scores
+ * (equal scores: the lowest index first; NaN below every number).
+ *   scores [batch][q_len][max_pages] fp32; seq_lens [batch]; pages [batch][q_len][budget] int32: page
+ *   indices of the request, ascending, then -1.
+ * seq_lens[b] == 0 gives an empty list (all -1), as does a length below q_len or above max_pages * P, with
+ * the guard. MLA_ERR_UNSUPPORTED: max_pages above 49152. No workspace. Use recent >= 1 to keep the page of
+ * the query itself. */
+mla_status mla_select_pages(const mla_config* cfg, const float* scores, int max_pages, const int32_t* seq_lens,
+                            int batch, int q_len, int budget, int sinks, int recent, int32_t* pages,
+                            int32_t* dev_status, void* stream);
+
+/* Bytes of workspace mla_decode_pages needs for this batch on the current device. */
+mla_status mla_decode_pages_workspace_size(const mla_config* cfg, int batch, int q_len, int budget,
+                                           size_t* bytes);
+
+/* mla_decode over the tokens of chosen pages: query token t of request b attends to the tokens of the
+ * pages on its list that it sees (j <= seq_lens[b] - q_len + t),
+ *   s_j = softmax_scale * q_lat[b][t][i] . cache_row_j,  out_latent = sum_j softmax(s)_j c_j,
+ *   lse = ln sum_j exp(s_j).
+ *   q_lat [batch][q_len][H][d_c + d_r] as formed by mla_absorb_query (act dtype, rotated); pages
+ *   [batch][q_len][budget] int32: page indices of the request, ascending, -1 behind the end (from
+ *   mla_select_pages, or any other choice); the rest as in mla_decode. A list of all pages gives
+ *   mla_decode's result up to rounding.
+ * An empty list or seq_lens[b] == 0: out_latent = 0, lse = -inf. A length below q_len or above max_pages *
+ * P is skipped like an empty request, with the guard; a list that is not ascending or names a page that
+ * the query does not see sets the guard and leaves that query's result undefined. workspace: as in
+ * mla_decode (its first int32 is the call's status word, cleared by each call). MLA_ERR_UNSUPPORTED:
+ * d_latent above 512, batch * q_len above 8192. A cache that does not start at a multiple of 4 bytes is
+ * refused. */
+mla_status mla_decode_pages(const mla_config* cfg, const void* q_lat, const void* cache, int num_pages,
+                            const int32_t* block_table, int max_pages, const int32_t* seq_lens, int batch,
+                            int q_len, const int32_t* pages, int budget, void* out_latent, float* lse,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---- 4-bit weights ------------------------------------------------------------------------
+ * A weight W [K][N] (as every weight of this library: x W with x [rows][K]) as 4-bit floating point with
+ * microscaling: 17/32 of a byte an element instead of 2. Each block of 32 elements along K of one column
+ * has a scale 2^e and 32 codes of e2m1 (a sign and one of 0, 0.5, 1, 1.5, 2, 3, 4, 6); an element's value
+ * is code * 2^e. e is the exponent of the block's largest magnitude, rounded to two significant bits,
+ * less 2 (the largest magnitude then lies in [3.5, 7) scales; at most 125, at least -127), and codes
+ * round to nearest even, +-6 at most. A block that holds an infinity or NaN has the scale NaN.
+ *   codes [N][K / 2] bytes: column n contiguous, element 2 j in the low half of byte j, 2 j + 1 in the high;
+ *   scales [ceil(N / 128)][ceil(K / 128)][32][4][4] bytes, e + 127 (255: NaN): block kb = k / 32 of column
+ *   n at [n / 128][kb / 4][n % 32][(n % 128) / 32][kb % 4]; entries of columns behind N and blocks behind
+ *   K hold 127.
+ * K is a multiple of 32 (MLA_ERR_INVALID otherwise), K and N at most 8388608; codes and scales start at
+ * multiples of 16 bytes. Of cfg these calls use the act dtype (and refuse an invalid one). */
+
+/* Sizes of the two arrays. */
+mla_status mla_mx4_bytes(const mla_config* cfg, int K, int N, size_t* codes_bytes, size_t* scales_bytes);
+
+/* W [K][N] (act dtype) -> codes, scales; once at load, say for W_comb, W_O, W_DQ, W_UQ or W_QR. */
+mla_status mla_mx4_quantize(const mla_config* cfg, const void* W, int K, int N, void* codes, void* scales,
+                            void* stream);
+
+/* codes, scales -> the values W [K][N] (act dtype; every value is exact in bf16). */
+mla_status mla_mx4_dequantize(const mla_config* cfg, const void* codes, const void* scales, int K, int N, void* W,
+                              void* stream);
+
+/* Bytes of workspace mla_mx4_project needs for `rows` rows (may be 0). */
+mla_status mla_mx4_project_workspace_size(const mla_config* cfg, int K, int N, int rows, size_t* bytes);
+
+/* out = x W for a 4-bit W: x [rows][K], out [rows][N] (act dtype), fp32 sums. With W = W_comb and x =
+ * out_latent this is mla_output_proj with a quarter of its bytes to read.
+ *   workspace: 256-byte aligned device buffer of mla_mx4_project_workspace_size bytes (NULL if that is 0),
+ *   any contents; calls that share one must be ordered on the GPU. rows == 0 is a no-op. */
+mla_status mla_mx4_project(const mla_config* cfg, const void* x, const void* codes, const void* scales, int K,
+                           int N, int rows, void* out, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Wait for `stream`, then read the device status word at `status_word` (a decode
  * workspace or an append dev_status) into *code (an mla_status value, MLA_OK if clean)
  * and reset it to 0. */
@@ -455,7 +576,8 @@ const char* mla_status_string(mla_status status);
 const char* mla_last_error(void);
 
 /* Library ABI version (major * 100 + minor). 1.02: mla_append_cache needs no workspace
- * (its size is 0). 1.03: the shared-prefix and eviction calls. */
+ * (its size is 0). 1.03: the shared-prefix and eviction calls. 1.04: page-sparse decoding and 4-bit
+ * weights. */
 int mla_version(void);
 
 /* Number of CUDA kernels the library has launched in this process so far (all

@@ -93,6 +93,17 @@ _SIGNATURES = {
     "mla_key_weights": (_I, [_CFG, _P, _P, _P, _I, _P, _I, _P, _I, _I, ctypes.c_float, _P, _P, _P]),
     "mla_evict_cache": (_I, [_CFG, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _I, _P, _I, _P, _P, _P,
                              _P, _P]),
+    "mla_page_keys": (_I, [_CFG, _P, _I, _P, _I, _P, _I, _I, _P, _P, _P]),
+    "mla_page_scores_workspace_size": (_I, [_CFG, _I, _I, _I, ctypes.POINTER(_SZ)]),
+    "mla_page_scores": (_I, [_CFG, _P, _P, _I, _P, _I, _P, _I, _I, _P, _P, _SZ, _P, _P]),
+    "mla_select_pages": (_I, [_CFG, _P, _I, _P, _I, _I, _I, _I, _I, _P, _P, _P]),
+    "mla_decode_pages_workspace_size": (_I, [_CFG, _I, _I, _I, ctypes.POINTER(_SZ)]),
+    "mla_decode_pages": (_I, [_CFG, _P, _P, _I, _P, _I, _P, _I, _I, _P, _I, _P, _P, _P, _SZ, _P]),
+    "mla_mx4_bytes": (_I, [_CFG, _I, _I, ctypes.POINTER(_SZ), ctypes.POINTER(_SZ)]),
+    "mla_mx4_quantize": (_I, [_CFG, _P, _I, _I, _P, _P, _P]),
+    "mla_mx4_dequantize": (_I, [_CFG, _P, _P, _I, _I, _P, _P]),
+    "mla_mx4_project_workspace_size": (_I, [_CFG, _I, _I, _I, ctypes.POINTER(_SZ)]),
+    "mla_mx4_project": (_I, [_CFG, _P, _P, _P, _I, _I, _I, _P, _P, _SZ, _P]),
     "mla_read_device_status": (_I, [_P, _P, ctypes.POINTER(_I)]),
     "mla_status_string": (ctypes.c_char_p, [_I]),
     "mla_last_error": (ctypes.c_char_p, []),
@@ -544,6 +555,139 @@ def mla_evict_cache(cfg, weights, seq_lens, block_table, cache, budget, kept, ne
         _ptr(kept, "kept", _i32(0), batch * max(int(budget), 0)),
         _ptr(new_seq_lens, "new_seq_lens", _i32(0), batch),
         _ptr(dev_status, "dev_status", _i32(0), allow_none=True), _stream(stream)), "mla_evict_cache")
+
+
+def mla_page_keys(cfg, cache, block_table, seq_lens, page_keys, new_tokens=None, dev_status=None,
+                  stream=None):
+    """page_keys [num_pages][d_c + d_r]: means of the pages that hold any of each request's last
+    new_tokens tokens (None: of all its pages)."""
+    batch, max_pages = block_table.shape
+    num_pages = cache.numel() // (cfg.page_size * _cache_row_elems(cfg))
+    new = max_pages * cfg.page_size if new_tokens is None else new_tokens
+    _check(lib().mla_page_keys(
+        ctypes.byref(cfg),
+        _ptr(cache, "cache", _cache_dtypes(cfg), num_pages * cfg.page_size * _cache_row_elems(cfg)), num_pages,
+        _ptr(block_table, "block_table", _i32(0), batch * max_pages), max_pages,
+        _ptr(seq_lens, "seq_lens", _i32(0), batch), batch, min(int(new), 2 ** 31 - 1),
+        _ptr(page_keys, "page_keys", (_act_dtype(cfg),), num_pages * (cfg.d_latent + cfg.d_rope)),
+        _ptr(dev_status, "dev_status", _i32(0), allow_none=True), _stream(stream)), "mla_page_keys")
+
+
+def mla_page_scores_workspace_size(cfg, batch, q_len, max_pages) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().mla_page_scores_workspace_size(ctypes.byref(cfg), int(batch), int(q_len), int(max_pages),
+                                                ctypes.byref(n)), "mla_page_scores_workspace_size")
+    return int(n.value)
+
+
+def mla_page_scores(cfg, q_lat, page_keys, block_table, seq_lens, scores, workspace=None, dev_status=None,
+                    stream=None):
+    """q_lat [B][q_len][H][d_c + d_r] (mla_absorb_query) -> scores [B][q_len][max_pages] fp32. workspace:
+    uint8 device tensor of mla_page_scores_workspace_size bytes (None if 0)."""
+    a = (_act_dtype(cfg),)
+    t = _torch()
+    batch, q_len = q_lat.shape[0], q_lat.shape[1]
+    max_pages = block_table.shape[1]
+    D = cfg.d_latent + cfg.d_rope
+    num_pages = page_keys.numel() // D
+    _check(lib().mla_page_scores(
+        ctypes.byref(cfg), _ptr(q_lat, "q_lat", a, batch * q_len * cfg.num_heads * D),
+        _ptr(page_keys, "page_keys", a, num_pages * D), num_pages,
+        _ptr(block_table, "block_table", _i32(0), batch * max_pages), max_pages,
+        _ptr(seq_lens, "seq_lens", _i32(0), batch), batch, q_len,
+        _ptr(scores, "scores", (t.float32,), batch * q_len * max_pages),
+        _ptr(workspace, "workspace", (t.uint8,), allow_none=True),
+        0 if workspace is None else workspace.numel(),
+        _ptr(dev_status, "dev_status", _i32(0), allow_none=True), _stream(stream)), "mla_page_scores")
+
+
+def mla_select_pages(cfg, scores, seq_lens, pages, sinks=0, recent=1, dev_status=None, stream=None):
+    """scores [B][q_len][max_pages] fp32 -> pages [B][q_len][budget] int32, ascending, then -1."""
+    t = _torch()
+    batch, q_len, max_pages = scores.shape
+    budget = pages.shape[2]
+    _check(lib().mla_select_pages(
+        ctypes.byref(cfg), _ptr(scores, "scores", (t.float32,)), max_pages,
+        _ptr(seq_lens, "seq_lens", _i32(0), batch), batch, q_len, budget, int(sinks), int(recent),
+        _ptr(pages, "pages", _i32(0), batch * q_len * budget),
+        _ptr(dev_status, "dev_status", _i32(0), allow_none=True), _stream(stream)), "mla_select_pages")
+
+
+def mla_decode_pages_workspace_size(cfg, batch, q_len, budget) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().mla_decode_pages_workspace_size(ctypes.byref(cfg), int(batch), int(q_len), int(budget),
+                                                 ctypes.byref(n)), "mla_decode_pages_workspace_size")
+    return int(n.value)
+
+
+def mla_decode_pages(cfg, q_lat, cache, block_table, seq_lens, pages, out_latent, lse, workspace, stream=None):
+    """Attention over the pages [B][q_len][budget] of each query token; q_lat [B][q_len][H][d_c + d_r]
+    from mla_absorb_query. workspace: its first int32 is the call's status word, as in mla_decode."""
+    a = (_act_dtype(cfg),)
+    t = _torch()
+    batch, q_len = q_lat.shape[0], q_lat.shape[1]
+    H, d_c, D = cfg.num_heads, cfg.d_latent, cfg.d_latent + cfg.d_rope
+    budget, max_pages = pages.shape[2], block_table.shape[1]
+    num_pages = cache.numel() // (cfg.page_size * _cache_row_elems(cfg))
+    _check(lib().mla_decode_pages(
+        ctypes.byref(cfg), _ptr(q_lat, "q_lat", a, batch * q_len * H * D),
+        _ptr(cache, "cache", _cache_dtypes(cfg), num_pages * cfg.page_size * _cache_row_elems(cfg)), num_pages,
+        _ptr(block_table, "block_table", _i32(0), batch * max_pages), max_pages,
+        _ptr(seq_lens, "seq_lens", _i32(0), batch), batch, q_len,
+        _ptr(pages, "pages", _i32(0), batch * q_len * budget), budget,
+        _ptr(out_latent, "out_latent", a, batch * q_len * H * d_c),
+        _ptr(lse, "lse", (t.float32,), batch * q_len * H),
+        _ptr(workspace, "workspace", (t.uint8,)), workspace.numel(), _stream(stream)), "mla_decode_pages")
+
+
+def mla_mx4_bytes(cfg, K, N):
+    """Bytes of the codes and of the scales of a 4-bit weight [K][N]."""
+    c, s = ctypes.c_size_t(0), ctypes.c_size_t(0)
+    _check(lib().mla_mx4_bytes(ctypes.byref(cfg), int(K), int(N), ctypes.byref(c), ctypes.byref(s)),
+           "mla_mx4_bytes")
+    return int(c.value), int(s.value)
+
+
+def _mx4(cfg, K, N, codes, scales):
+    t = _torch()
+    c, s = mla_mx4_bytes(cfg, K, N)
+    return _ptr(codes, "codes", (t.uint8,), c), _ptr(scales, "scales", (t.uint8,), s)
+
+
+def mla_mx4_quantize(cfg, W, codes, scales, stream=None):
+    """W [K][N] -> codes [N][K / 2], scales (uint8 tensors of mla_mx4_bytes bytes)."""
+    K, N = W.shape
+    c, s = _mx4(cfg, K, N, codes, scales)
+    _check(lib().mla_mx4_quantize(ctypes.byref(cfg), _ptr(W, "W", (_act_dtype(cfg),), K * N), K, N, c, s,
+                                  _stream(stream)), "mla_mx4_quantize")
+
+
+def mla_mx4_dequantize(cfg, codes, scales, W, stream=None):
+    """codes, scales -> their values W [K][N]."""
+    K, N = W.shape
+    c, s = _mx4(cfg, K, N, codes, scales)
+    _check(lib().mla_mx4_dequantize(ctypes.byref(cfg), c, s, K, N, _ptr(W, "W", (_act_dtype(cfg),), K * N),
+                                    _stream(stream)), "mla_mx4_dequantize")
+
+
+def mla_mx4_project_workspace_size(cfg, K, N, rows) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().mla_mx4_project_workspace_size(ctypes.byref(cfg), int(K), int(N), int(rows), ctypes.byref(n)),
+           "mla_mx4_project_workspace_size")
+    return int(n.value)
+
+
+def mla_mx4_project(cfg, x, codes, scales, out, workspace=None, stream=None):
+    """out [rows][N] = x [rows][K] times the 4-bit weight. workspace: uint8 device tensor of
+    mla_mx4_project_workspace_size bytes (None if 0)."""
+    a = (_act_dtype(cfg),)
+    rows, K = x.shape
+    N = out.shape[1]
+    c, s = _mx4(cfg, K, N, codes, scales)
+    _check(lib().mla_mx4_project(
+        ctypes.byref(cfg), _ptr(x, "x", a, rows * K), c, s, K, N, rows, _ptr(out, "out", a, rows * N),
+        _ptr(workspace, "workspace", (_torch().uint8,), allow_none=True),
+        0 if workspace is None else workspace.numel(), _stream(stream)), "mla_mx4_project")
 
 
 def mla_read_device_status(status_word, stream=None) -> int:

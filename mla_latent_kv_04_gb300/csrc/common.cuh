@@ -87,6 +87,14 @@ template <> struct CacheCodec<uint8_t> {
   __device__ __forceinline__ static uint8_t encode(float v, float scale) { return f32_to_fp8(v / scale); }
 };
 
+// Order-preserving integer form: larger value, larger key; -0 as +0, NaN below everything.
+__device__ __forceinline__ uint32_t order_key(float f) {
+  uint32_t u = __float_as_uint(f);
+  if ((u & 0x7FFFFFFFu) > 0x7F800000u) return 0u;
+  if (u == 0x80000000u) u = 0u;
+  return (u >> 31) ? ~u : (u | 0x80000000u);
+}
+
 // ---- warp reductions ----------------------------------------------------------------
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll

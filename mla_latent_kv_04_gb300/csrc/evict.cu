@@ -26,14 +26,6 @@ constexpr int kBins = 2048;
 constexpr int kMaxCluster = 8;
 constexpr int kSegMax = (int)(kEvictMaxKeys / kMaxCluster);   // weights one CTA holds in shared memory
 
-// Order-preserving integer form: larger weight, larger key; -0 as +0, NaN below everything.
-__device__ __forceinline__ uint32_t weight_key(float f) {
-  uint32_t u = __float_as_uint(f);
-  if ((u & 0x7FFFFFFFu) > 0x7F800000u) return 0u;
-  if (u == 0x80000000u) u = 0u;
-  return (u >> 31) ? ~u : (u | 0x80000000u);
-}
-
 // Exclusive prefix sum of v over the block's threads; *total gets the sum.
 template <int kSelThreads>
 __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* warp_tot, uint32_t* total) {
@@ -125,7 +117,7 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) evict_select_
       const int steps = (len + kSelThreads - 1) / kSelThreads;
       for (int k = 0; k < steps; ++k) {
         const int i = k * kSelThreads + tid;
-        const uint32_t key = i < len ? weight_key(w_s[i]) : 0u;
+        const uint32_t key = i < len ? order_key(w_s[i]) : 0u;
         const bool in = i < len && (key & mask) == prefix;
         const uint32_t d = in ? (key >> shift) & (bins - 1) : kBins;
         int same;
@@ -185,7 +177,7 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) evict_select_
   uint32_t gt = 0, eq = 0;
   if (any) {
     for (int i = i0; i < i1; ++i) {
-      const uint32_t key = weight_key(w_s[i]);
+      const uint32_t key = order_key(w_s[i]);
       gt += key > prefix;
       eq += key == prefix;
     }
@@ -213,7 +205,7 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) evict_select_
   if (any) {
     uint32_t at = (uint32_t)p.sinks + out0 + gt_before + min(eq_before, want);
     for (int i = i0; i < i1; ++i) {
-      const uint32_t key = weight_key(w_s[i]);
+      const uint32_t key = order_key(w_s[i]);
       const bool take = key > prefix || (key == prefix && eq_before < want);
       eq_before += key == prefix;
       if (take) {

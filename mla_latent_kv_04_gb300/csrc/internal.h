@@ -45,6 +45,9 @@ struct PlanParams {
   int* group_last;
   int* group_kv;
   int32_t* status;
+  // the decode over chosen pages: each group's ascending page list, -1 behind its end
+  const int32_t* pages = nullptr;
+  int budget = 0;
 };
 
 struct DecodeParams {
@@ -278,5 +281,60 @@ struct EvictParams {
 // Weights of one request that the selection holds on chip: a cluster of 8 CTAs, 48 K each.
 constexpr long long kEvictMaxKeys = 8LL * 48 * 1024;
 cudaError_t launch_evict(mla_dtype cache, const EvictParams& p, cudaStream_t s);
+
+// ---- page-sparse decoding ------------------------------------------------------------------
+struct PageKeysParams {
+  const void* cache;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  int max_pages, num_pages, batch, new_tokens, P, d_c, d_r;
+  long long row_bytes;
+  float cache_scale;          // of a per-tensor fp8 cache, else 1
+  void* page_keys;            // [num_pages][d_c + d_r] act dtype
+  int32_t* status;
+};
+// Whether a row's sums fit a block's shared memory.
+bool page_keys_fits(int d_c, int d_r);
+cudaError_t launch_page_keys(mla_dtype act, mla_dtype cache, const PageKeysParams& p, cudaStream_t s);
+
+struct PageScoreParams {
+  const void* q_lat;          // [groups][H][D]
+  const void* page_keys;      // [num_pages][D]
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  int max_pages, num_pages, groups, q_len, H, D, P;
+  float scale_log2;           // softmax scale * log2(e)
+  float* scores;              // [groups][max_pages]
+  float* z;                   // workspace of the SIMT form: [groups][H][max_pages]
+  float* lse2;                // and [groups][H]
+  int32_t* status;
+};
+cudaError_t launch_page_scores_simt(mla_dtype act, const PageScoreParams& p, cudaStream_t s);
+
+struct SelectParams {
+  const float* scores;        // [groups][max_pages]
+  const int32_t* seq_lens;
+  int max_pages, q_len, budget, sinks, recent, P;
+  int32_t* pages;             // [groups][budget]
+  int32_t* status;
+};
+// Pages whose scores the selection holds in shared memory (and counts in 16 bits).
+constexpr int kSelectMaxPages = 49152;
+cudaError_t launch_select_pages(const SelectParams& p, int groups, cudaStream_t s);
+
+// Groups whose plan fits the shared memory of one block.
+constexpr int kPagesMaxGroups = 8192;
+// Plans the decode over the lists of pp.pages, and writes their physical pages to table
+// [groups][budget] (-1 for an entry out of order or out of sight).
+cudaError_t launch_pages_prep(const PlanParams& pp, const int32_t* block_table, int32_t* table, cudaStream_t s);
+
+// ---- 4-bit weights -------------------------------------------------------------------------
+// codes [N][K / 2], scales in tiles of 128 columns x 4 blocks (mla.h).
+cudaError_t launch_mx4_quantize(mla_dtype act, const void* W, int K, int N, void* codes, void* scales,
+                                cudaStream_t s);
+cudaError_t launch_mx4_dequantize(mla_dtype act, const void* codes, const void* scales, int K, int N, void* W,
+                                  cudaStream_t s);
+cudaError_t launch_mx4_project_simt(mla_dtype act, const void* x, const void* codes, const void* scales, int K,
+                                    int N, int rows, void* out, cudaStream_t s);
 
 }  // namespace mla

@@ -177,7 +177,7 @@ void set_last_error(const std::string& what) { g_last_error = what; }
 
 extern "C" {
 
-int mla_version(void) { return 103; }
+int mla_version(void) { return 104; }
 
 uint64_t mla_kernel_launches(void) { return (uint64_t)mla::g_launches.load(); }
 
@@ -892,6 +892,298 @@ mla_status mla_evict_cache(const mla_config* cfg, const float* weights, const in
   p.status = dev_status;
   cudaError_t e = launch_evict(cfg->cache_dtype, p, (cudaStream_t)stream);
   return e == cudaSuccess ? MLA_OK : cuda_fail(e, "mla_evict_cache");
+}
+
+// ------------------------------------------------------------------ page-sparse decoding
+
+static mla_status check_pages(const mla_config* cfg, int num_pages, int max_pages) {
+  if (num_pages <= 0 || max_pages <= 0) return invalid("num_pages and max_pages must be positive");
+  if ((long long)max_pages * cfg->page_size > 0x7FFFFFFFLL)
+    return unsupported("max_pages * page_size above 2^31 - 1");
+  return MLA_OK;
+}
+
+mla_status mla_page_keys(const mla_config* cfg, const void* cache, int num_pages, const int32_t* block_table,
+                         int max_pages, const int32_t* seq_lens, int batch, int new_tokens, void* page_keys,
+                         int32_t* dev_status, void* stream) {
+  mla_status st = check_config(cfg);
+  if (st == MLA_OK) st = check_pages(cfg, num_pages, max_pages);
+  if (st != MLA_OK) return st;
+  if (batch <= 0 || batch > 32768) return invalid("batch must be in [1, 32768]");
+  if (new_tokens < 0) return invalid("new_tokens must be >= 0");
+  if (new_tokens == 0) return MLA_OK;
+  if (!cache || !block_table || !seq_lens || !page_keys) return invalid("null pointer");
+  if (!page_keys_fits(cfg->d_latent, cfg->d_rope))
+    return unsupported("a row's sums do not fit 227 KB of shared memory");
+  if (((uintptr_t)cache & 3) != 0) return invalid("cache must be 4-byte aligned");
+  PageKeysParams p;
+  p.cache = cache;
+  p.block_table = block_table;
+  p.seq_lens = seq_lens;
+  p.max_pages = max_pages;
+  p.num_pages = num_pages;
+  p.batch = batch;
+  p.new_tokens = new_tokens;
+  p.P = cfg->page_size;
+  p.d_c = cfg->d_latent;
+  p.d_r = cfg->d_rope;
+  p.row_bytes = (long long)cache_row_bytes(cfg);
+  p.cache_scale = code_scale_of(cfg);
+  p.page_keys = page_keys;
+  p.status = dev_status;
+  cudaError_t e = launch_page_keys(cfg->act_dtype, cfg->cache_dtype, p, (cudaStream_t)stream);
+  return e == cudaSuccess ? MLA_OK : cuda_fail(e, "mla_page_keys");
+}
+
+// Scores of every head and page, and every head's sum (of the SIMT form).
+static size_t page_scores_z_bytes(const mla_config* c, int groups, int max_pages) {
+  return align256((size_t)groups * c->num_heads * max_pages * 4);
+}
+
+mla_status mla_page_scores_workspace_size(const mla_config* cfg, int batch, int q_len, int max_pages,
+                                          size_t* bytes) {
+  mla_status st = check_decode_shape(cfg, batch, q_len);
+  if (st == MLA_OK) st = check_pages(cfg, 1, max_pages);
+  if (st != MLA_OK) return st;
+  if (!bytes) return invalid("bytes is NULL");
+  *bytes = page_scores_z_bytes(cfg, batch * q_len, max_pages) + align256((size_t)batch * q_len * cfg->num_heads * 4);
+  return MLA_OK;
+}
+
+mla_status mla_page_scores(const mla_config* cfg, const void* q_lat, const void* page_keys, int num_pages,
+                           const int32_t* block_table, int max_pages, const int32_t* seq_lens, int batch,
+                           int q_len, float* scores, void* workspace, size_t workspace_bytes,
+                           int32_t* dev_status, void* stream) {
+  size_t need = 0;
+  mla_status st = mla_page_scores_workspace_size(cfg, batch, q_len, max_pages, &need);
+  if (st == MLA_OK) st = check_pages(cfg, num_pages, max_pages);
+  if (st != MLA_OK) return st;
+  if (!q_lat || !page_keys || !block_table || !seq_lens || !scores) return invalid("null pointer");
+  if (need > 0 && (!workspace || workspace_bytes < need)) {
+    g_last_error = "workspace smaller than mla_page_scores_workspace_size";
+    return MLA_ERR_WORKSPACE;
+  }
+  if (need > 0 && ((uintptr_t)workspace & 255) != 0) return invalid("workspace must be 256-byte aligned");
+  PageScoreParams p;
+  p.q_lat = q_lat;
+  p.page_keys = page_keys;
+  p.block_table = block_table;
+  p.seq_lens = seq_lens;
+  p.max_pages = max_pages;
+  p.num_pages = num_pages;
+  p.groups = batch * q_len;
+  p.q_len = q_len;
+  p.H = cfg->num_heads;
+  p.D = cfg->d_latent + cfg->d_rope;
+  p.P = cfg->page_size;
+  p.scale_log2 = softmax_scale_of(cfg) * kLog2e;
+  p.scores = scores;
+  p.z = (float*)workspace;
+  p.lse2 = (float*)((char*)workspace + page_scores_z_bytes(cfg, p.groups, max_pages));
+  p.status = dev_status;
+  cudaError_t e = launch_page_scores_simt(cfg->act_dtype, p, (cudaStream_t)stream);
+  return e == cudaSuccess ? MLA_OK : cuda_fail(e, "mla_page_scores");
+}
+
+static mla_status check_budget(const mla_config* cfg, int budget) {
+  if (budget <= 0) return invalid("budget must be positive");
+  if ((long long)budget * cfg->page_size > 0x7FFFFFFFLL) return unsupported("budget * page_size above 2^31 - 1");
+  return MLA_OK;
+}
+
+mla_status mla_select_pages(const mla_config* cfg, const float* scores, int max_pages, const int32_t* seq_lens,
+                            int batch, int q_len, int budget, int sinks, int recent, int32_t* pages,
+                            int32_t* dev_status, void* stream) {
+  mla_status st = check_decode_shape(cfg, batch, q_len);
+  if (st == MLA_OK) st = check_pages(cfg, 1, max_pages);
+  if (st == MLA_OK) st = check_budget(cfg, budget);
+  if (st != MLA_OK) return st;
+  if (sinks < 0 || recent < 0 || (long long)sinks + recent > budget)
+    return invalid("sinks and recent must be >= 0 and fit the budget");
+  if (max_pages > kSelectMaxPages) return unsupported("max_pages above 49152");
+  if (!scores || !seq_lens || !pages) return invalid("null pointer");
+  SelectParams p;
+  p.scores = scores;
+  p.seq_lens = seq_lens;
+  p.max_pages = max_pages;
+  p.q_len = q_len;
+  p.budget = budget;
+  p.sinks = sinks;
+  p.recent = recent;
+  p.P = cfg->page_size;
+  p.pages = pages;
+  p.status = dev_status;
+  cudaError_t e = launch_select_pages(p, batch * q_len, (cudaStream_t)stream);
+  return e == cudaSuccess ? MLA_OK : cuda_fail(e, "mla_select_pages");
+}
+
+// the decode's workspace without its query (which is given), then the physical pages of every list
+static mla_status pages_layout(const mla_config* cfg, int batch, int q_len, int budget, DecodeWorkspace* w,
+                               size_t* table) {
+  mla_status st = check_decode(cfg, batch, q_len);
+  if (st == MLA_OK) st = check_budget(cfg, budget);
+  if (st != MLA_OK) return st;
+  if (batch * q_len > kPagesMaxGroups) return unsupported("batch * q_len above 8192");
+  decode_layout(cfg, batch, q_len, default_workers(cfg, nullptr, false), w);
+  const size_t query = w->part_o - w->q_lat;
+  w->part_o -= query;
+  w->part_lse -= query;
+  *table = w->total - query;
+  w->total = align256(*table + (size_t)batch * q_len * budget * 4);
+  return MLA_OK;
+}
+
+mla_status mla_decode_pages_workspace_size(const mla_config* cfg, int batch, int q_len, int budget, size_t* bytes) {
+  mla_status st = check_config(cfg);
+  if (st != MLA_OK) return st;
+  DecodeWorkspace w;
+  size_t table;
+  st = pages_layout(cfg, batch, q_len, budget, &w, &table);
+  if (st != MLA_OK) return st;
+  if (!bytes) return invalid("bytes is NULL");
+  *bytes = w.total;
+  return MLA_OK;
+}
+
+mla_status mla_decode_pages(const mla_config* cfg, const void* q_lat, const void* cache, int num_pages,
+                            const int32_t* block_table, int max_pages, const int32_t* seq_lens, int batch,
+                            int q_len, const int32_t* pages, int budget, void* out_latent, float* lse,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+  size_t need = 0;
+  mla_status st = mla_decode_pages_workspace_size(cfg, batch, q_len, budget, &need);
+  if (st == MLA_OK) st = check_pages(cfg, num_pages, max_pages);
+  if (st != MLA_OK) return st;
+  if (!q_lat || !cache || !block_table || !seq_lens || !pages || !out_latent || !lse) return invalid("null pointer");
+  if (!workspace || workspace_bytes < need) {
+    g_last_error = "workspace smaller than mla_decode_pages_workspace_size";
+    return MLA_ERR_WORKSPACE;
+  }
+  if (((uintptr_t)workspace & 255) != 0) return invalid("workspace must be 256-byte aligned");
+  if (((uintptr_t)cache & 3) != 0) return invalid("cache must be 4-byte aligned");
+  DecodeWorkspace w;
+  size_t table;
+  pages_layout(cfg, batch, q_len, budget, &w, &table);
+  cudaStream_t s = (cudaStream_t)stream;
+  char* ws = (char*)workspace;
+  const float code_scale = code_scale_of(cfg);
+  PlanParams pp;
+  pp.seq_lens = seq_lens;
+  pp.batch = batch;
+  pp.q_len = q_len;
+  pp.page_size = cfg->page_size;
+  pp.max_pages = max_pages;
+  pp.workers = w.workers;
+  pp.worker_off = (int*)(ws + w.worker_off);
+  pp.items = (WorkItem*)(ws + w.items);
+  pp.group_first = (int*)(ws + w.group_first);
+  pp.group_last = (int*)(ws + w.group_last);
+  pp.group_kv = (int*)(ws + w.group_kv);
+  pp.status = (int32_t*)(ws + w.status);
+  pp.pages = pages;
+  pp.budget = budget;
+  int32_t* listed = (int32_t*)(ws + table);
+  cudaError_t e = launch_pages_prep(pp, block_table, listed, s);
+  if (e != cudaSuccess) return cuda_fail(e, "mla_decode_pages (prologue)");
+  // every query is a request of its own, with its list as its pages
+  DecodeParams dp;
+  dp.q_lat = q_lat;
+  dp.cache = cache;
+  dp.block_table = listed;
+  dp.max_pages = budget;
+  dp.num_pages = num_pages;
+  dp.batch = w.groups;
+  dp.q_len = 1;
+  dp.H = cfg->num_heads;
+  dp.d_c = cfg->d_latent;
+  dp.d_r = cfg->d_rope;
+  dp.D = cfg->d_latent + cfg->d_rope;
+  dp.P = cfg->page_size;
+  dp.row_bytes = (long long)cache_row_bytes(cfg);
+  dp.scale_log2 = softmax_scale_of(cfg) * code_scale * kLog2e;
+  dp.out_scale = code_scale;
+  dp.out_latent = out_latent;
+  dp.lse = lse;
+  dp.worker_off = pp.worker_off;
+  dp.items = pp.items;
+  dp.group_first = pp.group_first;
+  dp.group_last = pp.group_last;
+  dp.group_kv = pp.group_kv;
+  dp.part_o = (float*)(ws + w.part_o);
+  dp.part_lse = (float*)(ws + w.part_lse);
+  dp.status = pp.status;
+  dp.workers = w.workers;
+  dp.part_planar = 0;
+  dp.wait_limit_ns = 2000000000ull;
+  dp.withhold_page = 0;
+  e = launch_decode_simt(cfg->act_dtype, cfg->cache_dtype, dp, s);
+  if (e != cudaSuccess) return cuda_fail(e, "mla_decode_pages (attention)");
+  e = launch_combine(cfg->act_dtype, dp, w.groups, s);
+  return e == cudaSuccess ? MLA_OK : cuda_fail(e, "mla_decode_pages (combine)");
+}
+
+// ------------------------------------------------------------------ 4-bit weights
+
+static mla_status check_mx4(const mla_config* cfg, int K, int N) {
+  mla_status st = check_config(cfg);
+  if (st != MLA_OK) return st;
+  if (K <= 0 || N <= 0) return invalid("K and N must be positive");
+  if (K % 32) return invalid("K must be a multiple of 32 (a scale's block)");
+  if (K > (1 << 23) || N > (1 << 23)) return unsupported("K or N above 8388608");
+  return MLA_OK;
+}
+
+mla_status mla_mx4_bytes(const mla_config* cfg, int K, int N, size_t* codes_bytes, size_t* scales_bytes) {
+  mla_status st = check_mx4(cfg, K, N);
+  if (st != MLA_OK) return st;
+  if (!codes_bytes || !scales_bytes) return invalid("codes_bytes or scales_bytes is NULL");
+  *codes_bytes = (size_t)N * (K / 2);
+  *scales_bytes = (size_t)((N + 127) / 128) * ((K + 127) / 128) * 512;
+  return MLA_OK;
+}
+
+mla_status mla_mx4_quantize(const mla_config* cfg, const void* W, int K, int N, void* codes, void* scales,
+                            void* stream) {
+  mla_status st = check_mx4(cfg, K, N);
+  if (st != MLA_OK) return st;
+  if (!W || !codes || !scales) return invalid("null pointer");
+  if (!aligned16(codes, scales)) return invalid("codes and scales must be 16-byte aligned");
+  cudaError_t e = launch_mx4_quantize(cfg->act_dtype, W, K, N, codes, scales, (cudaStream_t)stream);
+  return e == cudaSuccess ? MLA_OK : cuda_fail(e, "mla_mx4_quantize");
+}
+
+mla_status mla_mx4_dequantize(const mla_config* cfg, const void* codes, const void* scales, int K, int N, void* W,
+                              void* stream) {
+  mla_status st = check_mx4(cfg, K, N);
+  if (st != MLA_OK) return st;
+  if (!W || !codes || !scales) return invalid("null pointer");
+  if (!aligned16(codes, scales)) return invalid("codes and scales must be 16-byte aligned");
+  cudaError_t e = launch_mx4_dequantize(cfg->act_dtype, codes, scales, K, N, W, (cudaStream_t)stream);
+  return e == cudaSuccess ? MLA_OK : cuda_fail(e, "mla_mx4_dequantize");
+}
+
+mla_status mla_mx4_project_workspace_size(const mla_config* cfg, int K, int N, int rows, size_t* bytes) {
+  mla_status st = check_mx4(cfg, K, N);
+  if (st != MLA_OK) return st;
+  if (rows < 0 || !bytes) return invalid("rows must be >= 0 and bytes non-NULL");
+  *bytes = 0;
+  return MLA_OK;
+}
+
+mla_status mla_mx4_project(const mla_config* cfg, const void* x, const void* codes, const void* scales, int K,
+                           int N, int rows, void* out, void* workspace, size_t workspace_bytes, void* stream) {
+  size_t need = 0;
+  mla_status st = mla_mx4_project_workspace_size(cfg, K, N, rows, &need);
+  if (st != MLA_OK) return st;
+  if (rows == 0) return MLA_OK;
+  if (!x || !codes || !scales || !out) return invalid("null pointer");
+  if (!aligned16(codes, scales)) return invalid("codes and scales must be 16-byte aligned");
+  if (need > 0 && (!workspace || workspace_bytes < need)) {
+    g_last_error = "workspace smaller than mla_mx4_project_workspace_size";
+    return MLA_ERR_WORKSPACE;
+  }
+  if (need > 0 && ((uintptr_t)workspace & 255) != 0) return invalid("workspace must be 256-byte aligned");
+  cudaError_t e = launch_mx4_project_simt(cfg->act_dtype, x, codes, scales, K, N, rows, out, (cudaStream_t)stream);
+  return e == cudaSuccess ? MLA_OK : cuda_fail(e, "mla_mx4_project");
 }
 
 mla_status mla_read_device_status(const void* status_word, void* stream, int* code) {

@@ -74,6 +74,20 @@ __device__ __forceinline__ int last_at_most(const int* a, int n, long long x) {
   return lo;
 }
 
+// Tokens of the pages on group g's list, of `see` that the query sees: every page but the last one of
+// an ascending list is full.
+__device__ __forceinline__ int listed_tokens(const PlanParams& p, int g, int see) {
+  const int32_t* list = p.pages + (long long)g * p.budget;
+  int lo = 0, hi = p.budget;                // the first negative entry
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (list[mid] >= 0) lo = mid + 1; else hi = mid;
+  }
+  if (lo == 0) return 0;
+  const long long tail = (long long)see - (long long)list[lo - 1] * p.page_size;
+  return (lo - 1) * p.page_size + (int)max(1LL, min((long long)p.page_size, tail));
+}
+
 __device__ inline void plan_body(const PlanParams& p, int* sm, bool reset_status) {
   const int groups = p.batch * p.q_len, W = p.workers;
   int* cu = sm;                             // [groups + 1] page prefix
@@ -99,6 +113,7 @@ __device__ inline void plan_body(const PlanParams& p, int* sm, bool reset_status
         if (t == 0) flag_status(p.status, MLA_ERR_DEVICE_GUARD);
       } else {
         kv = S - p.q_len + t + 1;
+        if (p.pages) kv = listed_tokens(p, g, kv);
       }
     }
     p.group_kv[g] = kv;
