@@ -334,6 +334,11 @@ cudaError_t launch_mx4_quantize(mla_dtype act, const void* W, int K, int N, void
                                 cudaStream_t s);
 cudaError_t launch_mx4_dequantize(mla_dtype act, const void* codes, const void* scales, int K, int N, void* W,
                                   cudaStream_t s);
+// The tensor-core form: bf16, x and codes at multiples of 16 bytes.
+bool mx4_project_tc_supported(mla_dtype act);
+size_t mx4_project_tc_workspace(int K, int N, int rows);
+cudaError_t launch_mx4_project_tc(const void* x, const void* codes, const void* scales, int K, int N, int rows,
+                                  void* out, void* workspace, cudaStream_t s);
 cudaError_t launch_mx4_project_simt(mla_dtype act, const void* x, const void* codes, const void* scales, int K,
                                     int N, int rows, void* out, cudaStream_t s);
 

@@ -1165,7 +1165,7 @@ mla_status mla_mx4_project_workspace_size(const mla_config* cfg, int K, int N, i
   mla_status st = check_mx4(cfg, K, N);
   if (st != MLA_OK) return st;
   if (rows < 0 || !bytes) return invalid("rows must be >= 0 and bytes non-NULL");
-  *bytes = 0;
+  *bytes = rows > 0 && mx4_project_tc_supported(cfg->act_dtype) ? mx4_project_tc_workspace(K, N, rows) : 0;
   return MLA_OK;
 }
 
@@ -1182,7 +1182,9 @@ mla_status mla_mx4_project(const mla_config* cfg, const void* x, const void* cod
     return MLA_ERR_WORKSPACE;
   }
   if (need > 0 && ((uintptr_t)workspace & 255) != 0) return invalid("workspace must be 256-byte aligned");
-  cudaError_t e = launch_mx4_project_simt(cfg->act_dtype, x, codes, scales, K, N, rows, out, (cudaStream_t)stream);
+  cudaError_t e = need > 0 && aligned16(x)
+                      ? launch_mx4_project_tc(x, codes, scales, K, N, rows, out, workspace, (cudaStream_t)stream)
+                      : launch_mx4_project_simt(cfg->act_dtype, x, codes, scales, K, N, rows, out, (cudaStream_t)stream);
   return e == cudaSuccess ? MLA_OK : cuda_fail(e, "mla_mx4_project");
 }
 
