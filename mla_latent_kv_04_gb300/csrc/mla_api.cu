@@ -981,7 +981,9 @@ mla_status mla_page_scores(const mla_config* cfg, const void* q_lat, const void*
   p.z = (float*)workspace;
   p.lse2 = (float*)((char*)workspace + page_scores_z_bytes(cfg, p.groups, max_pages));
   p.status = dev_status;
-  cudaError_t e = launch_page_scores_simt(cfg->act_dtype, p, (cudaStream_t)stream);
+  cudaError_t e = page_scores_tc_supported(cfg, num_pages, max_pages) && aligned16(q_lat, page_keys)
+                      ? launch_page_scores_tc(p, (cudaStream_t)stream)
+                      : launch_page_scores_simt(cfg->act_dtype, p, (cudaStream_t)stream);
   return e == cudaSuccess ? MLA_OK : cuda_fail(e, "mla_page_scores");
 }
 
