@@ -1,0 +1,634 @@
+// Decode over chosen pages on the tensor cores (bf16 activations, every bf16 and fp8 cache, 64-token pages,
+// d_c 512, d_r 64, a multiple of 16 heads).
+//
+// A CTA has a block of up to 64 heads and walks its work items (page ranges of one query token's list) two
+// pages, 128 tokens, at a time, with tokens in the rows of the first product and latent dims in those of
+// the second:
+//   S^T = X q_lat^T         (M = 128 tokens, N = heads, K = 576)
+//   P   = 2^(c S - r_h)     (c = softmax scale * log2 e, r_h a running reference of the head)
+//   O^T += C^T P^T          (M = 4 x 128 latent dims, N = heads, K = 128 tokens)
+// 64 heads by 512 dims of fp32 sums are half of tensor memory, and 64 heads of the query a third of shared
+// memory: scores are whole fp32 sums of exact products, with nothing to exchange between CTAs (the decode
+// over all pages splits the latent dims of 128 heads over two CTAs and exchanges partial scores in fp16,
+// which costs the LSE its last bits). The reference r_h moves only when a score exceeds it by 2^8 (in
+// log2 units 8), which the eight softmax warps agree on once a tile; O and the sums are then rescaled.
+//
+// bf16 cache: the staged rows are both products' operands (K-major rows of S^T, dims-major columns of O^T);
+// P is rounded to bf16 and takes the place of the tile's rotary keys, which S^T has used up.
+// fp8 caches: the codes themselves are the operands (kind::f8f6f4). The query is the sum of two e4m3 terms
+// under a power of two per head (two columns of S^T, split4), and so is P (two products): 8 significant
+// bits, as bf16 has. Block-scaled rows: each block of 128 dims has a product of its own in S^T, added under
+// the token's scale in registers, and a P of its own, times that scale, in O^T.
+//
+// Bound: the load, product, softmax, product chain of a tile, whose rows fill shared memory (bf16).
+#include <math.h>
+
+#include "fp8_tiles.cuh"
+#include "internal.h"
+#include "sm100_ptx.cuh"
+#include "tc_host.h"
+#include "tc_wait.cuh"
+
+namespace mla {
+namespace pdec {
+
+enum { kBf16 = 0, kE4m3 = 1, kB128 = 2 };
+constexpr int kTok = 128;
+constexpr int kChunk = kTok * 128;             // 128 bytes of 128 rows
+constexpr int kThreads = 320;                  // producer, MMA issuer, 8 softmax warps
+constexpr float kGrow = 8.f;                   // how far scores may exceed the reference (log2)
+
+template <int kFmt> struct Fmt;
+template <> struct Fmt<kBf16> {                // latent chunks of a tile, chunk buffers, bytes of the regions
+  static constexpr int kChunks = 8, kBufs = 8, kQ = 9 * 8192, kRope = kChunk, kP = 0;
+};
+template <> struct Fmt<kE4m3> {
+  static constexpr int kChunks = 4, kBufs = 8, kQ = 4 * kChunk + 8192, kRope = 8192, kP = kChunk;
+};
+template <> struct Fmt<kB128> {
+  static constexpr int kChunks = 4, kBufs = 4, kQ = 4 * kChunk + 8192, kRope = kChunk, kP = 4 * kChunk;
+};
+
+template <int kFmt> struct Layout {
+  typedef Fmt<kFmt> F;
+  static constexpr int kRing = F::kQ;
+  static constexpr int kRope = kRing + F::kBufs * kChunk;
+  static constexpr int kP = kFmt == kBf16 ? kRope : kRope + F::kRope;      // (bf16: over the rotary keys)
+  static constexpr int kRef = kRope + F::kRope + F::kP;                    // [64] references
+  static constexpr int kAlpha = kRef + 256;                                // [64] rescaling factors
+  static constexpr int kHead = kAlpha + 256;                               // [64] factors of the fp8 query
+  static constexpr int kWarp = kHead + 256;                                // [4][64] of the four token quarters
+  static constexpr int kBar = kWarp + 1024;
+  static constexpr int kSmem = kBar + 256 + 1024;
+  static_assert(kSmem <= 232448, "dynamic shared memory per CTA");
+};
+
+enum { B_CFULL = 0, B_CFREE = 8, B_RFULL = 16, B_RFREE, B_QFULL, B_QFREE, B_SFULL, B_SFREE = B_SFULL + 2,
+       B_PFULL = B_SFREE + 2, B_PDONE, B_OFREE, B_MEET, B_TEAR, B_COUNT };
+static_assert(B_COUNT * 8 <= 232, "barrier area");
+
+struct Maps {
+  CUtensorMap c, rope, q;
+};
+
+// kind::f8f6f4, e4m3 A and B with their majors
+constexpr uint32_t idesc_e4m3(int N, bool a_mn, bool b_mn) {
+  return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | (8u << 24);
+}
+
+// Sums (or maxima) over the warp's lanes of 32 columns: lane j is left with column j.
+template <bool kMax>
+__device__ __forceinline__ float columns_of_warp(float (&v)[32], int lane) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const bool up = (lane & o) != 0;
+#pragma unroll
+    for (int j = 0; j < o; ++j) {
+      const float give = up ? v[j] : v[j + o], keep = up ? v[j + o] : v[j];
+      const float got = __shfl_xor_sync(0xffffffffu, give, o);
+      v[j] = kMax ? fmaxf(keep, got) : keep + got;
+    }
+  }
+  return v[0];
+}
+
+template <int kFmt>
+__global__ void __launch_bounds__(kThreads, 1)
+    decode_pages_kernel(const __grid_constant__ Maps maps, const DecodeParams p, int blocks) {
+  typedef Fmt<kFmt> F;
+  typedef Layout<kFmt> L;
+  constexpr bool kFp8 = kFmt != kBf16;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = ptx::smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* basep = smem_raw + (base - raw);
+  volatile int* abort = reinterpret_cast<volatile int*>(basep + L::kBar + 232);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(basep + L::kBar + 236);
+  volatile int* grown = reinterpret_cast<volatile int*>(basep + L::kBar + 240);      // [2]
+  auto bar = [&](int i) { return base + L::kBar + 8 * i; };
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const int worker = blockIdx.x / blocks, h0 = 64 * (blockIdx.x % blocks), N = min(64, p.H - h0);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < B_COUNT; ++i)
+      ptx::mbar_init(bar(i), i == B_PFULL || i == B_OFREE || i == B_MEET || (i >= B_SFREE && i < B_PFULL) ||
+                                     (kFp8 && i == B_QFULL) ? 8 : 1);
+    *abort = 0;
+    grown[0] = grown[1] = -1;
+    ptx::fence_mbar_init();
+    ptx::prefetch_tensormap(&maps.c);
+    ptx::prefetch_tensormap(&maps.rope);
+    ptx::prefetch_tensormap(&maps.q);
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(ptx::smem_u32(tmem_slot), 512);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+  const uint32_t t_o = tmem, t_s = tmem + 256;                                       // O: 4 x 64 columns; S: 2 x 128
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();                         // the plan and the lists' pages
+  auto wait = [&](int i, uint32_t parity) { return bounded_wait(bar(i), parity, abort, p.status); };
+  auto wait_w = [&](int i, uint32_t parity) { return __all_sync(0xffffffffu, wait(i, parity)) != 0; };
+  const int it0 = p.worker_off[worker], it1 = p.worker_off[worker + 1];
+
+  if (warp == 0) {
+    if (lane == 0) {
+      const uint64_t pol = ptx::l2_policy_evict_first();
+      const uint8_t* cache = reinterpret_cast<const uint8_t*>(p.cache);
+      const uint32_t page_bytes = (uint32_t)(64 * p.row_bytes);
+      uint32_t c_seq = 0, tile = 0, q_seq = 0;
+      bool ok = true;
+      for (int it = it0; ok && it < it1; ++it, ++q_seq) {
+        const WorkItem item = p.items[it];
+        const int32_t* bt = p.block_table + (long long)item.group * p.max_pages;
+        auto page_of = [&](int pg) {
+          if (pg >= item.page_end) return -1;
+          const int page = bt[pg];
+          if (page >= 0 && page < p.num_pages) return page;
+          flag_status(p.status, MLA_ERR_DEVICE_GUARD);
+          return 0;
+        };
+        if constexpr (!kFp8) {
+          if (!(ok = wait(B_QFREE, (q_seq & 1) ^ 1))) break;
+          const int rows = min(64, p.H);       // (rows behind the last head read as zero)
+          ptx::mbar_arrive_expect_tx(bar(B_QFULL), 9 * rows * 128);
+          for (int c = 0; c < 9; ++c) ptx::tma_load_3d(base + 8192 * c, &maps.q, 64 * c, h0, item.group, bar(B_QFULL));
+        }
+        int a = page_of(item.page_begin), b = page_of(item.page_begin + 1);
+        for (int pg = item.page_begin; ok && pg < item.page_end; pg += 2, ++tile) {
+          const int na = page_of(pg + 2), nb = page_of(pg + 3);
+          if (h0 == 0) {                       // the next tile's pages into L2
+            if (na >= 0) ptx::bulk_prefetch_l2_hint(cache + (long long)na * page_bytes, page_bytes, pol);
+            if (nb >= 0) ptx::bulk_prefetch_l2_hint(cache + (long long)nb * page_bytes, page_bytes, pol);
+          }
+          auto load = [&](uint32_t dst, const CUtensorMap* map, int x, uint32_t half, uint32_t full) {
+            ptx::mbar_arrive_expect_tx(full, b >= 0 ? 2 * half : half);
+            ptx::tma_load_3d(dst, map, x, a * 64, 0, full);
+            if (b >= 0) ptx::tma_load_3d(dst + half, map, x, b * 64, 0, full);
+          };
+          for (int c = 0; c < F::kChunks; ++c, ++c_seq) {
+            const uint32_t st = c_seq % F::kBufs;
+            if (!(ok = wait(B_CFREE + st, ((c_seq / F::kBufs) & 1) ^ 1))) break;
+            load(base + L::kRing + st * kChunk, &maps.c, (kFp8 ? 128 : 64) * c, kChunk / 2, bar(B_CFULL + st));
+          }
+          if (!ok || !(ok = wait(B_RFREE, (tile & 1) ^ 1))) break;
+          load(base + L::kRope, &maps.rope, kFmt == kB128 ? 528 : 512, kFmt == kE4m3 ? 4096 : kChunk / 2, bar(B_RFULL));
+          a = na;
+          b = nb;
+        }
+      }
+      if (*abort) {                            // the last copies into each buffer have landed
+        for (uint32_t i = c_seq > (uint32_t)F::kBufs ? c_seq - F::kBufs : 0; i < c_seq; ++i)
+          drain_wait(bar(B_CFULL + i % F::kBufs), (i / F::kBufs) & 1);
+        if (tile) drain_wait(bar(B_RFULL), (tile - 1) & 1);
+        if (!kFp8 && q_seq) drain_wait(bar(B_QFULL), (q_seq - 1) & 1);
+        if (!kFp8) drain_wait(bar(B_QFULL), q_seq & 1);
+      }
+    }
+  } else if (warp == 1) {
+    // In one place tiles follow each other as S(0), [S(i + 1),] O(i), .. where the ring holds two tiles, and
+    // S(i), O(i) where it holds one.
+    constexpr bool kAhead = F::kBufs >= 2 * F::kChunks;
+    constexpr uint32_t kQStep = kFp8 ? kChunk : 8192;      // bytes of a chunk's query rows
+    const uint32_t id_s = kFp8 ? idesc_e4m3(2 * N, false, false) : ptx::idesc_bf16_f32(128, N, false, false);
+    const uint32_t id_r = kFmt == kB128 ? ptx::idesc_bf16_f32(128, N, false, false) : id_s;
+    const uint32_t id_o = kFp8 ? idesc_e4m3(N, true, true) : ptx::idesc_bf16_f32(128, N, true, true);
+    const uint64_t q_d = ptx::smem_desc(base, 16, 1024, ptx::kSwizzle128);
+    const uint64_t x_d = ptx::smem_desc(base + L::kRing, 16, 1024, ptx::kSwizzle128);
+    constexpr uint32_t kRopeSw = kFmt == kE4m3 ? (uint32_t)ptx::kSwizzle64 : (uint32_t)ptx::kSwizzle128;
+    constexpr uint32_t kRopeSbo = kFmt == kE4m3 ? 512 : 1024;
+    const uint64_t qr_d = ptx::smem_desc(base + (kFp8 ? 4 * kChunk : 8 * 8192), 16, kRopeSbo, kRopeSw);
+    const uint64_t xr_d = ptx::smem_desc(base + L::kRope, 16, kRopeSbo, kRopeSw);
+    // dims-major: two chunks of 64 dims (bf16) or one of 128; P by heads
+    const uint64_t c_d = ptx::smem_desc(base + L::kRing, kChunk, 1024, ptx::kSwizzle128);
+    const uint64_t p_d = kFp8 ? ptx::smem_desc(base + L::kP, 16, 512, ptx::kSwizzle64)
+                              : ptx::smem_desc(base + L::kP, 16, 1024, ptx::kSwizzle128);
+    uint32_t c_seq = 0, o_seq = 0, s_tile = 0, s_seq = 0, o_tile = 0, q_seq = 0;
+    bool ok = true;
+    auto product_s = [&](bool last) {
+      for (int c = 0; ok && c < F::kChunks; ++c, ++c_seq) {
+        const uint32_t st = c_seq % F::kBufs, sb = s_seq & 1;
+        if (c == 0 || kFmt == kB128) ok = wait_w(B_SFREE + sb, ((s_seq >> 1) & 1) ^ 1);
+        if (!ok || !(ok = wait_w(B_CFULL + st, (c_seq / F::kBufs) & 1))) return;
+        ptx::tc_fence_after();
+        if (ptx::elect_one()) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint64_t a = x_d + (st * (kChunk >> 4) + 2 * k), b = q_d + (c * (kQStep >> 4) + 2 * k);
+            const uint32_t acc = k || (c && kFmt != kB128) ? 1u : 0u;
+            if (kFp8) ptx::mma_e4m3_ss(t_s + 128 * sb, a, b, id_s, acc);
+            else ptx::mma_bf16_ss(t_s + 128 * sb, a, b, id_s, acc);
+          }
+          if (kFmt == kB128) ptx::mma_commit(bar(B_SFULL + sb));
+        }
+        __syncwarp();
+        if (kFmt == kB128) ++s_seq;
+      }
+      const uint32_t sb = s_seq & 1;
+      if (kFmt == kB128) ok = wait_w(B_SFREE + sb, ((s_seq >> 1) & 1) ^ 1);
+      if (!ok || !(ok = wait_w(B_RFULL, s_tile & 1))) return;
+      ptx::tc_fence_after();
+      if (ptx::elect_one()) {
+#pragma unroll
+        for (int k = 0; k < (kFmt == kE4m3 ? 2 : 4); ++k) {
+          const uint32_t acc = k || kFmt != kB128 ? 1u : 0u;
+          if (kFmt == kE4m3) ptx::mma_e4m3_ss(t_s + 128 * sb, xr_d + 2 * k, qr_d + 2 * k, id_r, acc);
+          else ptx::mma_bf16_ss(t_s + 128 * sb, xr_d + 2 * k, qr_d + 2 * k, id_r, acc);
+        }
+        ptx::mma_commit(bar(B_SFULL + sb));
+        if (kFp8) ptx::mma_commit(bar(B_RFREE));
+        if (!kFp8 && last) ptx::mma_commit(bar(B_QFREE));
+      }
+      __syncwarp();
+      ++s_seq;
+      ++s_tile;
+    };
+    for (int it = it0; ok && it < it1; ++it, ++q_seq) {
+      const WorkItem item = p.items[it];
+      const int tiles = (item.page_end - item.page_begin + 1) / 2;
+      if (!(ok = wait_w(B_QFULL, q_seq & 1))) break;
+      if (kAhead) product_s(tiles == 1);
+      for (int i = 0; ok && i < tiles; ++i, ++o_tile) {
+        if (!kAhead) product_s(i == tiles - 1);
+        else if (i + 1 < tiles) product_s(i + 2 == tiles);
+        if (!ok || !(ok = wait_w(B_PFULL, o_tile & 1))) break;
+        if (i == 0 && !(ok = wait_w(B_OFREE, (q_seq & 1) ^ 1))) break;
+        ptx::tc_fence_after();
+        if (ptx::elect_one()) {
+          const uint32_t acc0 = i ? 1u : 0u;
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            const uint32_t st = o_seq % F::kBufs;
+            const uint64_t a = c_d + st * (kChunk >> 4);
+            if (!kFp8) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                ptx::mma_bf16_ss(t_o + 64 * m, a + 128 * k, p_d + 128 * k, id_o, k ? 1u : acc0);
+              ptx::mma_commit(bar(B_CFREE + st));
+              ptx::mma_commit(bar(B_CFREE + st + 1));
+              o_seq += 2;
+            } else {
+              const uint64_t pm = p_d + (kFmt == kB128 ? m * (kChunk >> 4) : 0);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                ptx::mma_e4m3_ss(t_o + 64 * m, a + 256 * k, pm + 128 * k, id_o, k ? 1u : acc0);
+                ptx::mma_e4m3_ss(t_o + 64 * m, a + 256 * k, pm + (8192 >> 4) + 128 * k, id_o, 1u);
+              }
+              ptx::mma_commit(bar(B_CFREE + st));
+              o_seq += 1;
+            }
+          }
+          if (!kFp8) ptx::mma_commit(bar(B_RFREE));
+          ptx::mma_commit(bar(B_PDONE));
+        }
+        o_seq = __shfl_sync(0xffffffffu, (uint32_t)((o_tile + 1) * F::kChunks), 0);
+      }
+    }
+    if (*abort) {
+      if (ptx::elect_one()) ptx::mma_commit(bar(B_TEAR));
+      __syncwarp();
+      drain_wait(bar(B_TEAR), 0);
+    }
+  } else {
+    // two threads a token: heads hh half .. of the block
+    const int quad = warp & 3, half = warp >= 6 ? 1 : 0, tok = 32 * quad + lane, hh = N / 2;
+    const uint32_t lane_off = (uint32_t)(32 * quad) << 16;
+    float* ref = reinterpret_cast<float*>(basep + L::kRef) + hh * half;
+    float* alpha = reinterpret_cast<float*>(basep + L::kAlpha);
+    float* head = reinterpret_cast<float*>(basep + L::kHead);
+    float* quarter = reinterpret_cast<float*>(basep + L::kWarp);         // [4][64]
+    uint32_t s_seq = 0, tile = 0, meets = 0, c_seq = 0;
+    bool ok = true;
+    auto meet = [&]() {                        // the eight warps (bounded, unlike a named barrier)
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bar(B_MEET));
+      return wait_w(B_MEET, meets++ & 1);
+    };
+    for (int it = it0; ok && it < it1; ++it) {
+      const WorkItem item = p.items[it];
+      const long long g = item.group;
+      if constexpr (kFp8) {
+        // the query of these heads as two e4m3 terms (the scores of the item before have all been read, so
+        // its products are done): a warp takes heads in turn, 16 latent elements and 2 rotary ones a lane
+        for (int h = warp - 2; h < N; h += 8) {
+          const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const bf16*>(p.q_lat) + (g * p.H + h0 + h) * 576);
+          const uint4 x = src[2 * lane], y = src[2 * lane + 1];
+          const uint32_t pe = reinterpret_cast<const uint32_t*>(src + 64)[lane];
+          const uint32_t v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+          uint32_t m2 = kFmt == kB128 ? 0u : pe & 0x7FFF7FFFu;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) m2 = __vmaxu2(m2, v[k] & 0x7FFF7FFFu);
+          const float m = __uint_as_float(__reduce_max_sync(0xffffffffu, max(m2 & 0xFFFFu, m2 >> 16)) << 16);
+          // 2^e m in [128, 256) (exponents clamped: an all-zero or tiny head stays finite)
+          const int ex = max(-110, min(120, (int)((__float_as_uint(m) >> 23) & 255) - 127));
+          const float s = __uint_as_float((uint32_t)(-1 - ex + 127) << 23);
+          const float inv = __uint_as_float((uint32_t)(ex - 7 + 127) << 23);
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) split4(v[2 * k], v[2 * k + 1], s, &hi[k], &lo[k]);
+          uint8_t* q = basep + (lane >> 3) * kChunk;
+          const int unit = lane & 7, r1 = h + N;
+          *reinterpret_cast<uint4*>(q + h * 128 + ((unit ^ (h & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4*>(q + r1 * 128 + ((unit ^ (r1 & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          uint8_t* qp = basep + 4 * kChunk;
+          if (kFmt == kB128) {
+            *reinterpret_cast<uint32_t*>(qp + h * 128 + (((lane >> 2) ^ (h & 7)) << 4) + 4 * (lane & 3)) = pe;
+          } else {
+            uint32_t pe_hi, pe_lo;
+            split4(pe, 0u, s, &pe_hi, &pe_lo);
+            *reinterpret_cast<uint16_t*>(qp + h * 64 + (((lane >> 3) ^ ((h >> 1) & 3)) << 4) + 2 * (lane & 7)) = (uint16_t)pe_hi;
+            *reinterpret_cast<uint16_t*>(qp + r1 * 64 + (((lane >> 3) ^ ((r1 >> 1) & 3)) << 4) + 2 * (lane & 7)) = (uint16_t)pe_lo;
+          }
+          // infinities and NaN in the query make its scores NaN
+          if (lane == 0) head[h] = inv + (m < INFINITY ? 0.f : m - m);
+        }
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(B_QFULL));
+      }
+      if (quad == 0 && lane < hh) ref[lane] = -INFINITY;
+      if (!(ok = meet())) break;
+      float sum[32];
+#pragma unroll
+      for (int j = 0; j < 32; ++j) sum[j] = 0.f;
+      for (int pg = item.page_begin; ok && pg < item.page_end; pg += 2, ++tile, c_seq += F::kChunks) {
+        const int left = min(min(kTok, (item.page_end - pg) * 64), item.kv - pg * 64);   // tokens of this tile
+        const bool live = tok < left;
+        float4 sc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float top_scale = 0.f;                 // log2 of the token's largest scale
+        if constexpr (kFmt == kB128) {
+          if (live) {
+            int page = p.block_table[g * p.max_pages + pg + (tok >> 6)];
+            if (page < 0 || page >= p.num_pages) page = 0;               // (flagged by the producer)
+            sc = *reinterpret_cast<const float4*>(reinterpret_cast<const uint8_t*>(p.cache) +
+                                                  ((long long)page * 64 + (tok & 63)) * p.row_bytes + 512);
+          }
+          top_scale = log2f(fmaxf(fmaxf(fmaxf(sc.x, sc.y), fmaxf(sc.z, sc.w)), 1e-30f));
+        }
+        // scores of this thread's heads, in log2 units
+        float s[32];
+        if constexpr (kFmt == kBf16) {
+          const uint32_t sb = s_seq & 1;
+          if (!(ok = wait_w(B_SFULL + sb, (s_seq >> 1) & 1))) break;
+          ptx::tc_fence_after();
+#pragma unroll
+          for (int j = 0; j < 32; j += 8) {
+            if (j >= hh) break;
+            uint32_t v[8];
+            ptx::tmem_ld8(t_s + lane_off + 128 * sb + hh * half + j, v);
+            ptx::tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 8; ++k) s[j + k] = __uint_as_float(v[k]) * p.scale_log2;
+          }
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(bar(B_SFREE + sb));
+          ++s_seq;
+        } else {
+#pragma unroll
+          for (int c = 0; c < (kFmt == kB128 ? 5 : 1); ++c) {
+            const uint32_t sb = s_seq & 1;
+            if (ok) ok = wait_w(B_SFULL + sb, (s_seq >> 1) & 1);
+            if (ok) {
+              ptx::tc_fence_after();
+              const float f = kFmt == kE4m3 ? 1.f : (c == 0 ? sc.x : (c == 1 ? sc.y : (c == 2 ? sc.z : sc.w)));
+#pragma unroll
+              for (int j = 0; j < 32; j += 8) {
+                if (j >= hh) break;
+                const uint32_t at = t_s + lane_off + 128 * sb + hh * half + j;
+                uint32_t hi[8], lo[8];
+                ptx::tmem_ld8(at, hi);
+                if (c < 4) ptx::tmem_ld8(at + N, lo);
+                ptx::tmem_wait_ld();
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  const float x = __uint_as_float(hi[k]);
+                  if (c == 4) {
+                    s[j + k] = fmaf(s[j + k], head[hh * half + j + k], x) * p.scale_log2;
+                  } else {
+                    const float v = fmaf(__uint_as_float(lo[k]), 0.0625f, x);
+                    if (kFmt == kE4m3) s[j + k] = v * (head[hh * half + j + k] * p.scale_log2);
+                    else s[j + k] = c ? fmaf(f, v, s[j + k]) : f * v;
+                  }
+                }
+              }
+              ptx::tc_fence_before();
+              __syncwarp();
+              if (lane == 0) ptx::mbar_arrive(bar(B_SFREE + sb));
+              ++s_seq;
+            }
+          }
+          if (!ok) break;
+        }
+        // does a score exceed its reference by too much?
+        bool over = false;
+#pragma unroll
+        for (int j = 0; j < 32; j += 8) {
+          if (j >= hh) break;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) over = over || s[j + k] + top_scale - ref[j + k] > kGrow;
+        }
+        if (__any_sync(0xffffffffu, over && live) && lane == 0) grown[tile & 1] = (int)(tile & 0x7FFFFFFFu);
+        if (!(ok = meet())) break;
+        if (grown[tile & 1] == (int)(tile & 0x7FFFFFFFu)) {
+          // new references: the largest so far (fp8: 2^4 below, so that P keeps its bits), then rescale
+          float m[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) m[j] = j < hh && live ? s[j < hh ? j : 0] + top_scale : -INFINITY;
+          const float most = columns_of_warp<true>(m, lane);
+          if (lane < hh) quarter[64 * quad + hh * half + lane] = most;
+          if (!(ok = meet())) break;
+          float a = 0.f, now = 0.f;
+          if (lane < hh) {
+            const float* q = quarter + hh * half + lane;
+            const float old = ref[lane], top = fmaxf(fmaxf(q[0], q[64]), fmaxf(q[128], q[192])) - (kFp8 ? 4.f : 0.f);
+            now = fmaxf(old, top);
+            a = old == -INFINITY ? 0.f : ptx::ex2(old - now);
+          }
+          if (!(ok = meet())) break;
+          if (quad == 0 && lane < hh) {
+            ref[lane] = now;
+            alpha[hh * half + lane] = a;
+          }
+#pragma unroll
+          for (int j = 0; j < 32; ++j) sum[j] *= __shfl_sync(0xffffffffu, a, j);
+          if (!(ok = meet())) break;
+          if (pg > item.page_begin) {
+            if (!(ok = wait_w(B_PDONE, (tile - 1) & 1))) break;
+            ptx::tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < 2 * N; c += 16) {          // this warp's dims tiles, 2 half and 2 half + 1
+              const int m_ = 2 * half + (c >= N), h = c >= N ? c - N : c;
+              uint32_t v[16];
+              const uint32_t at = t_o + lane_off + 64 * m_ + h;
+              ptx::tmem_ld16(at, v);
+              ptx::tmem_wait_ld();
+#pragma unroll
+              for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * alpha[h + k]);
+              ptx::tmem_st16(at, v);
+            }
+            ptx::tmem_wait_st();
+          }
+        }
+        // P: rows of tokens, heads contiguous. bf16: over the rotary keys (their product is done); fp8: the
+        // products with the tile before's have to be
+        if (kFp8 && tile > 0 && !(ok = wait_w(B_PDONE, (tile - 1) & 1))) break;
+        uint8_t* prow = basep + L::kP;
+#pragma unroll
+        for (int j = 0; j < 32; j += 8) {
+          if (j >= hh) break;
+          float e[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            e[k] = live ? ptx::ex2(s[j + k] - ref[j + k]) : 0.f;
+            sum[j + k] += e[k];
+          }
+          const int hb = hh * half + j;        // first head of the eight
+          if constexpr (kFmt == kBf16) {
+            uint4 o;
+            o.x = pack_bf16(e[0], e[1]);
+            o.y = pack_bf16(e[2], e[3]);
+            o.z = pack_bf16(e[4], e[5]);
+            o.w = pack_bf16(e[6], e[7]);
+            *reinterpret_cast<uint4*>(prow + tok * 128 + (((hb >> 3) ^ (tok & 7)) << 4)) = o;
+          } else {
+            const uint32_t at = tok * 64 + (((hb >> 4) ^ ((tok >> 1) & 3)) << 4) + (hb & 8);
+#pragma unroll
+            for (int m = 0; m < (kFmt == kB128 ? 4 : 1); ++m) {
+              const float f = kFmt == kE4m3 ? 1.f : (m == 0 ? sc.x : (m == 1 ? sc.y : (m == 2 ? sc.z : sc.w)));
+              uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const float2 y = make_float2(f * e[2 * k], f * e[2 * k + 1]);
+                const uint32_t c = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
+                const float2 b = e4m3x2_to_f32(c);
+                const uint32_t d = __nv_cvt_float2_to_fp8x2(make_float2(y.x - b.x, y.y - b.y), __NV_SATFINITE, __NV_E4M3);
+                hi[k >> 1] |= c << (16 * (k & 1));
+                lo[k >> 1] |= d << (16 * (k & 1));
+              }
+              *reinterpret_cast<uint2*>(prow + m * kChunk + at) = make_uint2(hi[0], hi[1]);
+              *reinterpret_cast<uint2*>(prow + m * kChunk + 8192 + at) = make_uint2(lo[0], lo[1]);
+            }
+          }
+        }
+        if (!live) {                           // rows that may hold anything: their P is 0, 0 times NaN is not
+          const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+          for (int c = half; c < F::kChunks; c += 2) {
+            uint4* row = reinterpret_cast<uint4*>(basep + L::kRing + (c_seq + c) % F::kBufs * kChunk + tok * 128);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) row[k] = zero;
+          }
+        }
+        ptx::tc_fence_before();                // (a rescaled O)
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(B_PFULL));
+      }
+      if (!ok) break;
+      // the item's sums, LSE and output
+      const float mine = columns_of_warp<false>(sum, lane);
+      if (lane < hh) quarter[64 * quad + hh * half + lane] = mine;
+      if (!(ok = meet() && wait_w(B_PDONE, (tile - 1) & 1))) break;
+      ptx::tc_fence_after();
+      if (lane < hh && quad == 0) {
+        const float* q = quarter + hh * half + lane;
+        const float total = (q[0] + q[64]) + (q[128] + q[192]);
+        alpha[hh * half + lane] = p.out_scale / total;
+        const float lse = (ref[lane] + log2f(total)) * kLn2;
+        const int h = h0 + hh * half + lane;
+        if (item.single) p.lse[g * p.H + h] = lse;
+        else p.part_lse[(long long)it * p.H + h] = lse;
+      }
+      if (!(ok = meet())) break;
+#pragma unroll 1
+      for (int c = 0; c < 2 * N; c += 16) {
+        const int m = 2 * half + (c >= N), h = c >= N ? c - N : c;
+        uint32_t v[16];
+        ptx::tmem_ld16(t_o + lane_off + 64 * m + h, v);
+        ptx::tmem_wait_ld();
+        const long long at = (long long)(h0 + h) * 512 + 128 * m + 32 * quad + lane;
+        if (item.single) {
+          bf16* o = reinterpret_cast<bf16*>(p.out_latent) + g * p.H * 512 + at;
+#pragma unroll
+          for (int k = 0; k < 16; ++k) o[512 * k] = __float2bfloat16_rn(__uint_as_float(v[k]) * alpha[h + k]);
+        } else {
+          float* o = p.part_o + (long long)it * p.H * 512 + at;
+#pragma unroll
+          for (int k = 0; k < 16; ++k) o[512 * k] = __uint_as_float(v[k]) * alpha[h + k];
+        }
+        __syncwarp();                          // the next load is warp-wide
+      }
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bar(B_OFREE));
+    }
+  }
+  __syncwarp();
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int kFmt>
+static cudaError_t run(const Maps& maps, const DecodeParams& p, int blocks, cudaStream_t s) {
+  auto kern = decode_pages_kernel<kFmt>;
+  constexpr int smem = Layout<kFmt>::kSmem;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(p.workers * blocks), 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kern, maps, p, blocks);
+  if (e == cudaSuccess) note_launch();
+  return e;
+}
+
+}  // namespace pdec
+
+using namespace pdec;
+
+bool decode_pages_tc_supported(const mla_config* c, long long num_pages) {
+  return c->act_dtype == MLA_BF16 && c->page_size == 64 && c->d_latent == 512 && c->d_rope == 64 &&
+         c->num_heads % 16 == 0 && c->num_heads <= 1024 && num_pages * 64 <= 0x7FFFFF00LL;
+}
+
+int decode_pages_tc_workers(int H) {
+  const int blocks = (H + 63) / 64, n = device_sms() / blocks;
+  return n > 0 ? n : 1;
+}
+
+cudaError_t launch_decode_pages_tc(mla_dtype cache, const DecodeParams& p, cudaStream_t s) {
+  const int blocks = (p.H + 63) / 64;
+  const uint64_t rows = (uint64_t)p.num_pages * 64, rb = (uint64_t)p.row_bytes;
+  Maps m;
+  if (!tensor_map_bf16(&m.q, p.q_lat, 576, (uint64_t)p.H, (uint64_t)p.batch, 1152, (uint64_t)p.H * 1152, 64,
+                       (uint32_t)(p.H < 64 ? p.H : 64)))
+    return cudaErrorInvalidValue;
+  if (cache == MLA_BF16) {
+    if (!tensor_map_bf16(&m.c, p.cache, 576, rows, 1, rb, rows * rb, 64, 64)) return cudaErrorInvalidValue;
+    m.rope = m.c;
+    return run<kBf16>(m, p, blocks, s);
+  }
+  const bool b128 = cache == MLA_FP8_E4M3_B128;
+  if (!tensor_map_3d(&m.c, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_128B, p.cache, 512, rows, 1, rb,
+                     rows * rb, 128, 64) ||
+      !tensor_map_3d(&m.rope, CU_TENSOR_MAP_DATA_TYPE_UINT8, b128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                     p.cache, rb, rows, 1, rb, rows * rb, b128 ? 128 : 64, 64))
+    return cudaErrorInvalidValue;
+  return b128 ? run<kB128>(m, p, blocks, s) : run<kE4m3>(m, p, blocks, s);
+}
+
+}  // namespace mla

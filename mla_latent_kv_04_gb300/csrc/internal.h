@@ -331,6 +331,12 @@ constexpr int kPagesMaxGroups = 8192;
 // [groups][budget] (-1 for an entry out of order or out of sight).
 cudaError_t launch_pages_prep(const PlanParams& pp, const int32_t* block_table, int32_t* table, cudaStream_t s);
 
+// The decode over such a plan on the tensor cores: bf16 activations, 64-token pages, d_c 512, d_r 64, a
+// multiple of 16 heads; q_lat and cache at multiples of 16 bytes. dp.part_o is fp32 [items][H][512].
+bool decode_pages_tc_supported(const mla_config* c, long long num_pages);
+int decode_pages_tc_workers(int H);
+cudaError_t launch_decode_pages_tc(mla_dtype cache, const DecodeParams& p, cudaStream_t s);
+
 // ---- 4-bit weights -------------------------------------------------------------------------
 // codes [N][K / 2], scales in tiles of 128 columns x 4 blocks (mla.h).
 cudaError_t launch_mx4_quantize(mla_dtype act, const void* W, int K, int N, void* codes, void* scales,

@@ -1065,6 +1065,8 @@ mla_status mla_decode_pages(const mla_config* cfg, const void* q_lat, const void
   DecodeWorkspace w;
   size_t table;
   pages_layout(cfg, batch, q_len, budget, &w, &table);
+  const bool tc = decode_pages_tc_supported(cfg, num_pages) && aligned16(q_lat, cache);
+  if (tc) w.workers = std::min(w.workers, decode_pages_tc_workers(cfg->num_heads));
   cudaStream_t s = (cudaStream_t)stream;
   char* ws = (char*)workspace;
   const float code_scale = code_scale_of(cfg);
@@ -1117,7 +1119,8 @@ mla_status mla_decode_pages(const mla_config* cfg, const void* q_lat, const void
   dp.part_planar = 0;
   dp.wait_limit_ns = 2000000000ull;
   dp.withhold_page = 0;
-  e = launch_decode_simt(cfg->act_dtype, cfg->cache_dtype, dp, s);
+  e = tc ? launch_decode_pages_tc(cfg->cache_dtype, dp, s)
+         : launch_decode_simt(cfg->act_dtype, cfg->cache_dtype, dp, s);
   if (e != cudaSuccess) return cuda_fail(e, "mla_decode_pages (attention)");
   e = launch_combine(cfg->act_dtype, dp, w.groups, s);
   return e == cudaSuccess ? MLA_OK : cuda_fail(e, "mla_decode_pages (combine)");
