@@ -351,9 +351,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (quad == 0 && lane < hh) ref[lane] = -INFINITY;
       if (!(ok = meet())) break;
-      float sum[32];
+      float sum[32], r[32];                    // sums and references of this thread's heads
 #pragma unroll
-      for (int j = 0; j < 32; ++j) sum[j] = 0.f;
+      for (int j = 0; j < 32; ++j) {
+        sum[j] = 0.f;
+        r[j] = -INFINITY;
+      }
       for (int pg = item.page_begin; ok && pg < item.page_end; pg += 2, ++tile, c_seq += F::kChunks) {
         const int left = min(min(kTok, (item.page_end - pg) * 64), item.kv - pg * 64);   // tokens of this tile
         const bool live = tok < left;
@@ -374,15 +377,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t sb = s_seq & 1;
           if (!(ok = wait_w(B_SFULL + sb, (s_seq >> 1) & 1))) break;
           ptx::tc_fence_after();
+          uint32_t v[4][8];
 #pragma unroll
-          for (int j = 0; j < 32; j += 8) {
-            if (j >= hh) break;
-            uint32_t v[8];
-            ptx::tmem_ld8(t_s + lane_off + 128 * sb + hh * half + j, v);
-            ptx::tmem_wait_ld();
+          for (int j = 0; j < 4; ++j)
+            if (8 * j < hh) ptx::tmem_ld8(t_s + lane_off + 128 * sb + hh * half + 8 * j, v[j]);
+          ptx::tmem_wait_ld();
 #pragma unroll
-            for (int k = 0; k < 8; ++k) s[j + k] = __uint_as_float(v[k]) * p.scale_log2;
-          }
+          for (int j = 0; j < 32; ++j) s[j] = __uint_as_float(v[j / 8][j % 8]) * p.scale_log2;
           ptx::tc_fence_before();
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(bar(B_SFREE + sb));
@@ -423,38 +424,81 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (!ok) break;
         }
-        // does a score exceed its reference by too much?
-        bool over = false;
+        // P: rows of tokens, heads contiguous, and whether a score exceeds its reference by too much.
+        // bf16: over the rotary keys (their product is done); fp8: the products with the tile before's have to be
+        if (kFp8 && tile > 0 && !(ok = wait_w(B_PDONE, (tile - 1) & 1))) break;
+        float now[32] = {};                    // the sums with this tile
+        auto weights = [&]() {
+          float most = -INFINITY;
+          uint8_t* prow = basep + L::kP;
 #pragma unroll
-        for (int j = 0; j < 32; j += 8) {
-          if (j >= hh) break;
+          for (int j = 0; j < 32; j += 8) {
+            if (j >= hh) break;
+            float e[8];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) over = over || s[j + k] + top_scale - ref[j + k] > kGrow;
-        }
-        if (__any_sync(0xffffffffu, over && live) && lane == 0) grown[tile & 1] = (int)(tile & 0x7FFFFFFFu);
+            for (int k = 0; k < 8; ++k) {
+              const float d = s[j + k] - r[j + k];
+              most = fmaxf(most, d);
+              e[k] = live ? ptx::ex2(d) : 0.f;
+              now[j + k] = sum[j + k] + e[k];
+            }
+            const int hb = hh * half + j;      // first head of the eight
+            if constexpr (kFmt == kBf16) {
+              uint4 o;
+              o.x = pack_bf16(e[0], e[1]);
+              o.y = pack_bf16(e[2], e[3]);
+              o.z = pack_bf16(e[4], e[5]);
+              o.w = pack_bf16(e[6], e[7]);
+              *reinterpret_cast<uint4*>(prow + tok * 128 + (((hb >> 3) ^ (tok & 7)) << 4)) = o;
+            } else {
+              const uint32_t at = tok * 64 + (((hb >> 4) ^ ((tok >> 1) & 3)) << 4) + (hb & 8);
+#pragma unroll
+              for (int m = 0; m < (kFmt == kB128 ? 4 : 1); ++m) {
+                const float f = kFmt == kE4m3 ? 1.f : (m == 0 ? sc.x : (m == 1 ? sc.y : (m == 2 ? sc.z : sc.w)));
+                uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const float2 y = make_float2(f * e[2 * k], f * e[2 * k + 1]);
+                  const uint32_t c = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
+                  const float2 b = e4m3x2_to_f32(c);
+                  const uint32_t d = __nv_cvt_float2_to_fp8x2(make_float2(y.x - b.x, y.y - b.y), __NV_SATFINITE, __NV_E4M3);
+                  hi[k >> 1] |= c << (16 * (k & 1));
+                  lo[k >> 1] |= d << (16 * (k & 1));
+                }
+                *reinterpret_cast<uint2*>(prow + m * kChunk + at) = make_uint2(hi[0], hi[1]);
+                *reinterpret_cast<uint2*>(prow + m * kChunk + 8192 + at) = make_uint2(lo[0], lo[1]);
+              }
+            }
+          }
+          return live && most + top_scale > kGrow;
+        };
+        if (__any_sync(0xffffffffu, weights()) && lane == 0) grown[tile & 1] = (int)(tile & 0x7FFFFFFFu);
         if (!(ok = meet())) break;
         if (grown[tile & 1] == (int)(tile & 0x7FFFFFFFu)) {
           // new references: the largest so far (fp8: 2^4 below, so that P keeps its bits), then rescale
           float m[32];
 #pragma unroll
-          for (int j = 0; j < 32; ++j) m[j] = j < hh && live ? s[j < hh ? j : 0] + top_scale : -INFINITY;
+          for (int j = 0; j < 32; ++j) m[j] = j < hh && live ? s[j] + top_scale : -INFINITY;
           const float most = columns_of_warp<true>(m, lane);
           if (lane < hh) quarter[64 * quad + hh * half + lane] = most;
           if (!(ok = meet())) break;
-          float a = 0.f, now = 0.f;
+          float a = 0.f, next = 0.f;
           if (lane < hh) {
             const float* q = quarter + hh * half + lane;
             const float old = ref[lane], top = fmaxf(fmaxf(q[0], q[64]), fmaxf(q[128], q[192])) - (kFp8 ? 4.f : 0.f);
-            now = fmaxf(old, top);
-            a = old == -INFINITY ? 0.f : ptx::ex2(old - now);
+            next = fmaxf(old, top);
+            a = old == -INFINITY ? 0.f : ptx::ex2(old - next);
           }
           if (!(ok = meet())) break;
           if (quad == 0 && lane < hh) {
-            ref[lane] = now;
+            ref[lane] = next;
             alpha[hh * half + lane] = a;
           }
 #pragma unroll
-          for (int j = 0; j < 32; ++j) sum[j] *= __shfl_sync(0xffffffffu, a, j);
+          for (int j = 0; j < 32; ++j) {
+            sum[j] *= __shfl_sync(0xffffffffu, a, j);
+            r[j] = __shfl_sync(0xffffffffu, next, j);
+          }
           if (!(ok = meet())) break;
           if (pg > item.page_begin) {
             if (!(ok = wait_w(B_PDONE, (tile - 1) & 1))) break;
@@ -472,48 +516,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             ptx::tmem_wait_st();
           }
+          weights();
         }
-        // P: rows of tokens, heads contiguous. bf16: over the rotary keys (their product is done); fp8: the
-        // products with the tile before's have to be
-        if (kFp8 && tile > 0 && !(ok = wait_w(B_PDONE, (tile - 1) & 1))) break;
-        uint8_t* prow = basep + L::kP;
 #pragma unroll
-        for (int j = 0; j < 32; j += 8) {
-          if (j >= hh) break;
-          float e[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            e[k] = live ? ptx::ex2(s[j + k] - ref[j + k]) : 0.f;
-            sum[j + k] += e[k];
-          }
-          const int hb = hh * half + j;        // first head of the eight
-          if constexpr (kFmt == kBf16) {
-            uint4 o;
-            o.x = pack_bf16(e[0], e[1]);
-            o.y = pack_bf16(e[2], e[3]);
-            o.z = pack_bf16(e[4], e[5]);
-            o.w = pack_bf16(e[6], e[7]);
-            *reinterpret_cast<uint4*>(prow + tok * 128 + (((hb >> 3) ^ (tok & 7)) << 4)) = o;
-          } else {
-            const uint32_t at = tok * 64 + (((hb >> 4) ^ ((tok >> 1) & 3)) << 4) + (hb & 8);
-#pragma unroll
-            for (int m = 0; m < (kFmt == kB128 ? 4 : 1); ++m) {
-              const float f = kFmt == kE4m3 ? 1.f : (m == 0 ? sc.x : (m == 1 ? sc.y : (m == 2 ? sc.z : sc.w)));
-              uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const float2 y = make_float2(f * e[2 * k], f * e[2 * k + 1]);
-                const uint32_t c = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
-                const float2 b = e4m3x2_to_f32(c);
-                const uint32_t d = __nv_cvt_float2_to_fp8x2(make_float2(y.x - b.x, y.y - b.y), __NV_SATFINITE, __NV_E4M3);
-                hi[k >> 1] |= c << (16 * (k & 1));
-                lo[k >> 1] |= d << (16 * (k & 1));
-              }
-              *reinterpret_cast<uint2*>(prow + m * kChunk + at) = make_uint2(hi[0], hi[1]);
-              *reinterpret_cast<uint2*>(prow + m * kChunk + 8192 + at) = make_uint2(lo[0], lo[1]);
-            }
-          }
-        }
+        for (int j = 0; j < 32; ++j) sum[j] = now[j];
         if (!live) {                           // rows that may hold anything: their P is 0, 0 times NaN is not
           const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
           for (int c = half; c < F::kChunks; c += 2) {
