@@ -10,8 +10,9 @@
 // 64 heads by 512 dims of fp32 sums are half of tensor memory, and 64 heads of the query a third of shared
 // memory: scores are whole fp32 sums of exact products, with nothing to exchange between CTAs (the decode
 // over all pages splits the latent dims of 128 heads over two CTAs and exchanges partial scores in fp16,
-// which costs the LSE its last bits). The reference r_h moves only when a score exceeds it by 2^8 (in
-// log2 units 8), which the eight softmax warps agree on once a tile; O and the sums are then rescaled.
+// which costs the LSE its last bits). The reference r_h moves only when a score exceeds it by 8 (log2
+// units); P is formed under the old one meanwhile, and the barrier that hands P over tells all warps
+// whether it holds. If not, references, O and sums are rescaled and P is formed again.
 //
 // bf16 cache: the staged rows are both products' operands (K-major rows of S^T, dims-major columns of O^T);
 // P is rounded to bf16 and takes the place of the tile's rotary keys, which S^T has used up.
@@ -35,7 +36,7 @@ namespace pdec {
 enum { kBf16 = 0, kE4m3 = 1, kB128 = 2 };
 constexpr int kTok = 128;
 constexpr int kChunk = kTok * 128;             // 128 bytes of 128 rows
-constexpr int kThreads = 320;                  // producer, MMA issuer, 8 softmax warps
+constexpr int kThreads = 576;                  // producer, MMA issuer, 16 softmax warps
 constexpr float kGrow = 8.f;                   // how far scores may exceed the reference (log2)
 
 template <int kFmt> struct Fmt;
@@ -64,8 +65,8 @@ template <int kFmt> struct Layout {
 };
 
 enum { B_CFULL = 0, B_CFREE = 8, B_RFULL = 16, B_RFREE, B_QFULL, B_QFREE, B_SFULL, B_SFREE = B_SFULL + 2,
-       B_PFULL = B_SFREE + 2, B_PDONE, B_OFREE, B_MEET, B_TEAR, B_COUNT };
-static_assert(B_COUNT * 8 <= 232, "barrier area");
+       B_PFULL = B_SFREE + 2, B_PAGAIN, B_OFREE, B_MEET, B_PDONE, B_TEAR, B_COUNT };
+static_assert(B_COUNT * 8 <= 240, "barrier area");
 
 struct Maps {
   CUtensorMap c, rope, q;
@@ -76,11 +77,16 @@ constexpr uint32_t idesc_e4m3(int N, bool a_mn, bool b_mn) {
   return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | (8u << 24);
 }
 
-// Sums (or maxima) over the warp's lanes of 32 columns: lane j is left with column j.
+// Sums (or maxima) over the warp's lanes of 16 columns: lanes j and j + 16 are left with column j.
 template <bool kMax>
-__device__ __forceinline__ float columns_of_warp(float (&v)[32], int lane) {
+__device__ __forceinline__ float columns_of_warp(float (&v)[16], int lane) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
+  for (int j = 0; j < 16; ++j) {
+    const float got = __shfl_xor_sync(0xffffffffu, v[j], 16);
+    v[j] = kMax ? fmaxf(v[j], got) : v[j] + got;
+  }
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) {
     const bool up = (lane & o) != 0;
 #pragma unroll
     for (int j = 0; j < o; ++j) {
@@ -102,16 +108,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t raw = ptx::smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* basep = smem_raw + (base - raw);
-  volatile int* abort = reinterpret_cast<volatile int*>(basep + L::kBar + 232);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(basep + L::kBar + 236);
-  volatile int* grown = reinterpret_cast<volatile int*>(basep + L::kBar + 240);      // [2]
+  volatile int* abort = reinterpret_cast<volatile int*>(basep + L::kBar + 240);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(basep + L::kBar + 244);
+  volatile int* grown = reinterpret_cast<volatile int*>(basep + L::kBar + 248);      // [2]
   auto bar = [&](int i) { return base + L::kBar + 8 * i; };
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int worker = blockIdx.x / blocks, h0 = 64 * (blockIdx.x % blocks), N = min(64, p.H - h0);
   if (threadIdx.x == 0) {
     for (int i = 0; i < B_COUNT; ++i)
-      ptx::mbar_init(bar(i), i == B_PFULL || i == B_OFREE || i == B_MEET || (i >= B_SFREE && i < B_PFULL) ||
-                                     (kFp8 && i == B_QFULL) ? 8 : 1);
+      ptx::mbar_init(bar(i), (i >= B_SFREE && i <= B_MEET) || (kFp8 && i == B_QFULL) ? 16 : 1);
     *abort = 0;
     grown[0] = grown[1] = -1;
     ptx::fence_mbar_init();
@@ -206,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t c_d = ptx::smem_desc(base + L::kRing, kChunk, 1024, ptx::kSwizzle128);
     const uint64_t p_d = kFp8 ? ptx::smem_desc(base + L::kP, 16, 512, ptx::kSwizzle64)
                               : ptx::smem_desc(base + L::kP, 16, 1024, ptx::kSwizzle128);
-    uint32_t c_seq = 0, o_seq = 0, s_tile = 0, s_seq = 0, o_tile = 0, q_seq = 0;
+    uint32_t c_seq = 0, o_seq = 0, s_tile = 0, s_seq = 0, o_tile = 0, q_seq = 0, again = 0;
     bool ok = true;
     auto product_s = [&](bool last) {
       for (int c = 0; ok && c < F::kChunks; ++c, ++c_seq) {
@@ -255,6 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!kAhead) product_s(i == tiles - 1);
         else if (i + 1 < tiles) product_s(i + 2 == tiles);
         if (!ok || !(ok = wait_w(B_PFULL, o_tile & 1))) break;
+        if (grown[o_tile & 1] == (int)o_tile && !(ok = wait_w(B_PAGAIN, again++ & 1))) break;
         if (i == 0 && !(ok = wait_w(B_OFREE, (q_seq & 1) ^ 1))) break;
         ptx::tc_fence_after();
         if (ptx::elect_one()) {
@@ -293,16 +299,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       drain_wait(bar(B_TEAR), 0);
     }
   } else {
-    // two threads a token: heads hh half .. of the block
-    const int quad = warp & 3, half = warp >= 6 ? 1 : 0, tok = 32 * quad + lane, hh = N / 2;
+    // four threads a token: heads 16 part .. of the block (parts behind the last head have none, but their
+    // share of O, the dims tile 128 part)
+    const int quad = warp & 3, part = (warp - 2) >> 2, tok = 32 * quad + lane, hp = 16 * part, l16 = lane & 15;
+    const bool heads = hp < N;
     const uint32_t lane_off = (uint32_t)(32 * quad) << 16;
-    float* ref = reinterpret_cast<float*>(basep + L::kRef) + hh * half;
+    float* ref = reinterpret_cast<float*>(basep + L::kRef);
     float* alpha = reinterpret_cast<float*>(basep + L::kAlpha);
     float* head = reinterpret_cast<float*>(basep + L::kHead);
     float* quarter = reinterpret_cast<float*>(basep + L::kWarp);         // [4][64]
     uint32_t s_seq = 0, tile = 0, meets = 0, c_seq = 0;
     bool ok = true;
-    auto meet = [&]() {                        // the eight warps (bounded, unlike a named barrier)
+    auto meet = [&]() {                        // the sixteen warps (bounded, unlike a named barrier)
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(bar(B_MEET));
       return wait_w(B_MEET, meets++ & 1);
@@ -313,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if constexpr (kFp8) {
         // the query of these heads as two e4m3 terms (the scores of the item before have all been read, so
         // its products are done): a warp takes heads in turn, 16 latent elements and 2 rotary ones a lane
-        for (int h = warp - 2; h < N; h += 8) {
+        for (int h = warp - 2; h < N; h += 16) {
           const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const bf16*>(p.q_lat) + (g * p.H + h0 + h) * 576);
           const uint4 x = src[2 * lane], y = src[2 * lane + 1];
           const uint32_t pe = reinterpret_cast<const uint32_t*>(src + 64)[lane];
@@ -349,11 +357,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(bar(B_QFULL));
       }
-      if (quad == 0 && lane < hh) ref[lane] = -INFINITY;
-      if (!(ok = meet())) break;
-      float sum[32], r[32];                    // sums and references of this thread's heads
+      if (quad == 0 && heads && lane < 16) ref[hp + lane] = -INFINITY;
+      float fac[16];                           // and of a score of the fp8 query
+      if (kFp8) {
+        if (!(ok = wait_w(B_QFULL, (uint32_t)(it - it0) & 1))) break;
 #pragma unroll
-      for (int j = 0; j < 32; ++j) {
+        for (int j = 0; j < 16; ++j) fac[j] = heads ? head[hp + j] * (kFmt == kE4m3 ? p.scale_log2 : 1.f) : 0.f;
+      }
+      float sum[16], r[16];                    // sums and references of this thread's heads
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
         sum[j] = 0.f;
         r[j] = -INFINITY;
       }
@@ -372,68 +385,49 @@ __global__ void __launch_bounds__(kThreads, 1)
           top_scale = log2f(fmaxf(fmaxf(fmaxf(sc.x, sc.y), fmaxf(sc.z, sc.w)), 1e-30f));
         }
         // scores of this thread's heads, in log2 units
-        float s[32];
-        if constexpr (kFmt == kBf16) {
-          const uint32_t sb = s_seq & 1;
-          if (!(ok = wait_w(B_SFULL + sb, (s_seq >> 1) & 1))) break;
-          ptx::tc_fence_after();
-          uint32_t v[4][8];
+        float s[16];
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (8 * j < hh) ptx::tmem_ld8(t_s + lane_off + 128 * sb + hh * half + 8 * j, v[j]);
-          ptx::tmem_wait_ld();
-#pragma unroll
-          for (int j = 0; j < 32; ++j) s[j] = __uint_as_float(v[j / 8][j % 8]) * p.scale_log2;
-          ptx::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(bar(B_SFREE + sb));
-          ++s_seq;
-        } else {
-#pragma unroll
-          for (int c = 0; c < (kFmt == kB128 ? 5 : 1); ++c) {
-            const uint32_t sb = s_seq & 1;
-            if (ok) ok = wait_w(B_SFULL + sb, (s_seq >> 1) & 1);
-            if (ok) {
-              ptx::tc_fence_after();
-              const float f = kFmt == kE4m3 ? 1.f : (c == 0 ? sc.x : (c == 1 ? sc.y : (c == 2 ? sc.z : sc.w)));
-#pragma unroll
-              for (int j = 0; j < 32; j += 8) {
-                if (j >= hh) break;
-                const uint32_t at = t_s + lane_off + 128 * sb + hh * half + j;
-                uint32_t hi[8], lo[8];
-                ptx::tmem_ld8(at, hi);
-                if (c < 4) ptx::tmem_ld8(at + N, lo);
-                ptx::tmem_wait_ld();
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                  const float x = __uint_as_float(hi[k]);
-                  if (c == 4) {
-                    s[j + k] = fmaf(s[j + k], head[hh * half + j + k], x) * p.scale_log2;
-                  } else {
-                    const float v = fmaf(__uint_as_float(lo[k]), 0.0625f, x);
-                    if (kFmt == kE4m3) s[j + k] = v * (head[hh * half + j + k] * p.scale_log2);
-                    else s[j + k] = c ? fmaf(f, v, s[j + k]) : f * v;
-                  }
-                }
-              }
-              ptx::tc_fence_before();
-              __syncwarp();
-              if (lane == 0) ptx::mbar_arrive(bar(B_SFREE + sb));
-              ++s_seq;
+        for (int c = 0; c < (kFmt == kB128 ? 5 : 1); ++c) {
+          const uint32_t sb = s_seq & 1, at = t_s + lane_off + 128 * sb + hp;
+          if (ok) ok = wait_w(B_SFULL + sb, (s_seq >> 1) & 1);
+          if (ok) {
+            ptx::tc_fence_after();
+            uint32_t hi[16], lo[16];
+            if (heads) {
+              ptx::tmem_ld16(at, hi);
+              if (kFp8 && c < 4) ptx::tmem_ld16(at + N, lo);
+              ptx::tmem_wait_ld();
             }
+            const float f = c == 0 ? sc.x : (c == 1 ? sc.y : (c == 2 ? sc.z : sc.w));
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const float x = heads ? __uint_as_float(hi[k]) : 0.f;
+              if (kFmt == kBf16) {
+                s[k] = x * p.scale_log2;
+              } else if (c == 4) {
+                s[k] = fmaf(s[k], fac[k], x) * p.scale_log2;
+              } else {
+                const float v = fmaf(heads ? __uint_as_float(lo[k]) : 0.f, 0.0625f, x);
+                if (kFmt == kE4m3) s[k] = v * fac[k];
+                else s[k] = c ? fmaf(f, v, s[k]) : f * v;
+              }
+            }
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(bar(B_SFREE + sb));
+            ++s_seq;
           }
-          if (!ok) break;
         }
+        if (!ok) break;
         // P: rows of tokens, heads contiguous, and whether a score exceeds its reference by too much.
         // bf16: over the rotary keys (their product is done); fp8: the products with the tile before's have to be
         if (kFp8 && tile > 0 && !(ok = wait_w(B_PDONE, (tile - 1) & 1))) break;
-        float now[32] = {};                    // the sums with this tile
+        float now[16];                         // the sums with this tile
         auto weights = [&]() {
           float most = -INFINITY;
           uint8_t* prow = basep + L::kP;
 #pragma unroll
-          for (int j = 0; j < 32; j += 8) {
-            if (j >= hh) break;
+          for (int j = 0; j < 16; j += 8) {
             float e[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
@@ -442,7 +436,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               e[k] = live ? ptx::ex2(d) : 0.f;
               now[j + k] = sum[j + k] + e[k];
             }
-            const int hb = hh * half + j;      // first head of the eight
+            const int hb = hp + j;             // first head of the eight
+            if (!heads) break;
             if constexpr (kFmt == kBf16) {
               uint4 o;
               o.x = pack_bf16(e[0], e[1]);
@@ -470,32 +465,46 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
-          return live && most + top_scale > kGrow;
+          return heads && live && most + top_scale > kGrow;
         };
-        if (__any_sync(0xffffffffu, weights()) && lane == 0) grown[tile & 1] = (int)(tile & 0x7FFFFFFFu);
-        if (!(ok = meet())) break;
-        if (grown[tile & 1] == (int)(tile & 0x7FFFFFFFu)) {
-          // new references: the largest so far (fp8: 2^4 below, so that P keeps its bits), then rescale
-          float m[32];
+        auto hand_over = [&](int b) {
+          ptx::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(bar(b));
+        };
+        if (__any_sync(0xffffffffu, weights()) && lane == 0) grown[tile & 1] = (int)tile;
+        if (!live) {                           // rows that may hold anything: their P is 0, 0 times NaN is not
+          const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+          for (int c = part; c < F::kChunks; c += 4) {
+            uint4* row = reinterpret_cast<uint4*>(basep + L::kRing + (c_seq + c) % F::kBufs * kChunk + tok * 128);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) m[j] = j < hh && live ? s[j] + top_scale : -INFINITY;
+            for (int k = 0; k < 8; ++k) row[k] = zero;
+          }
+        }
+        hand_over(B_PFULL);
+        if (!(ok = wait_w(B_PFULL, tile & 1))) break;
+        if (grown[tile & 1] == (int)tile) {
+          // new references: the largest so far (fp8: 2^4 below, so that P keeps its bits), then rescale
+          float m[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) m[j] = live ? s[j] + top_scale : -INFINITY;
           const float most = columns_of_warp<true>(m, lane);
-          if (lane < hh) quarter[64 * quad + hh * half + lane] = most;
+          if (heads && lane < 16) quarter[64 * quad + hp + lane] = most;
           if (!(ok = meet())) break;
           float a = 0.f, next = 0.f;
-          if (lane < hh) {
-            const float* q = quarter + hh * half + lane;
-            const float old = ref[lane], top = fmaxf(fmaxf(q[0], q[64]), fmaxf(q[128], q[192])) - (kFp8 ? 4.f : 0.f);
+          if (heads) {
+            const float* q = quarter + hp + l16;
+            const float old = ref[hp + l16], top = fmaxf(fmaxf(q[0], q[64]), fmaxf(q[128], q[192])) - (kFp8 ? 4.f : 0.f);
             next = fmaxf(old, top);
             a = old == -INFINITY ? 0.f : ptx::ex2(old - next);
           }
           if (!(ok = meet())) break;
-          if (quad == 0 && lane < hh) {
-            ref[lane] = next;
-            alpha[hh * half + lane] = a;
+          if (quad == 0 && heads && lane < 16) {
+            ref[hp + lane] = next;
+            alpha[hp + lane] = a;
           }
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
+          for (int j = 0; j < 16; ++j) {
             sum[j] *= __shfl_sync(0xffffffffu, a, j);
             r[j] = __shfl_sync(0xffffffffu, next, j);
           }
@@ -504,10 +513,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!(ok = wait_w(B_PDONE, (tile - 1) & 1))) break;
             ptx::tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < 2 * N; c += 16) {          // this warp's dims tiles, 2 half and 2 half + 1
-              const int m_ = 2 * half + (c >= N), h = c >= N ? c - N : c;
+            for (int h = 0; h < N; h += 16) {              // this warp's dims tile
               uint32_t v[16];
-              const uint32_t at = t_o + lane_off + 64 * m_ + h;
+              const uint32_t at = t_o + lane_off + 64 * part + h;
               ptx::tmem_ld16(at, v);
               ptx::tmem_wait_ld();
 #pragma unroll
@@ -515,47 +523,36 @@ __global__ void __launch_bounds__(kThreads, 1)
               ptx::tmem_st16(at, v);
             }
             ptx::tmem_wait_st();
+            ptx::tc_fence_before();
           }
           weights();
+          hand_over(B_PAGAIN);
         }
 #pragma unroll
-        for (int j = 0; j < 32; ++j) sum[j] = now[j];
-        if (!live) {                           // rows that may hold anything: their P is 0, 0 times NaN is not
-          const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-          for (int c = half; c < F::kChunks; c += 2) {
-            uint4* row = reinterpret_cast<uint4*>(basep + L::kRing + (c_seq + c) % F::kBufs * kChunk + tok * 128);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) row[k] = zero;
-          }
-        }
-        ptx::tc_fence_before();                // (a rescaled O)
-        ptx::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(bar(B_PFULL));
+        for (int j = 0; j < 16; ++j) sum[j] = now[j];
       }
       if (!ok) break;
       // the item's sums, LSE and output
       const float mine = columns_of_warp<false>(sum, lane);
-      if (lane < hh) quarter[64 * quad + hh * half + lane] = mine;
+      if (heads && lane < 16) quarter[64 * quad + hp + lane] = mine;
       if (!(ok = meet() && wait_w(B_PDONE, (tile - 1) & 1))) break;
       ptx::tc_fence_after();
-      if (lane < hh && quad == 0) {
-        const float* q = quarter + hh * half + lane;
+      if (heads && lane < 16 && quad == 0) {
+        const float* q = quarter + hp + lane;
         const float total = (q[0] + q[64]) + (q[128] + q[192]);
-        alpha[hh * half + lane] = p.out_scale / total;
-        const float lse = (ref[lane] + log2f(total)) * kLn2;
-        const int h = h0 + hh * half + lane;
+        alpha[hp + lane] = p.out_scale / total;
+        const float lse = (ref[hp + lane] + log2f(total)) * kLn2;
+        const int h = h0 + hp + lane;
         if (item.single) p.lse[g * p.H + h] = lse;
         else p.part_lse[(long long)it * p.H + h] = lse;
       }
       if (!(ok = meet())) break;
 #pragma unroll 1
-      for (int c = 0; c < 2 * N; c += 16) {
-        const int m = 2 * half + (c >= N), h = c >= N ? c - N : c;
+      for (int h = 0; h < N; h += 16) {
         uint32_t v[16];
-        ptx::tmem_ld16(t_o + lane_off + 64 * m + h, v);
+        ptx::tmem_ld16(t_o + lane_off + 64 * part + h, v);
         ptx::tmem_wait_ld();
-        const long long at = (long long)(h0 + h) * 512 + 128 * m + 32 * quad + lane;
+        const long long at = (long long)(h0 + h) * 512 + 128 * part + 32 * quad + lane;
         if (item.single) {
           bf16* o = reinterpret_cast<bf16*>(p.out_latent) + g * p.H * 512 + at;
 #pragma unroll
@@ -581,6 +578,43 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// A query's pieces under the weights of their LSEs: block (query, 4 heads), 64 threads a head, eight dims each.
+// Pieces of one item are final and stay; a query without tokens gets 0 and -inf.
+__global__ void __launch_bounds__(256) merge_pages_kernel(const DecodeParams p) {
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  const int g = blockIdx.x, h = 4 * blockIdx.y + threadIdx.x / 64, d = 4 * (threadIdx.x % 64);
+  const int first = p.group_first[g], last = p.group_last[g];
+  const int n = first >= 0 && last >= first ? last - first + 1 : 0;
+  if (n == 1) return;
+  const float* lse = p.part_lse + (long long)first * p.H + h;
+  float m = -INFINITY;
+  for (int i = 0; i < n; ++i) m = fmaxf(m, lse[(long long)i * p.H]);
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+  float total = 0.f;
+  const float* src = p.part_o + ((long long)first * p.H + h) * 512 + d;
+#pragma unroll 4
+  for (int i = 0; i < n; ++i) {
+    const float4 x = *reinterpret_cast<const float4*>(src + (long long)i * p.H * 512);
+    const float4 y = *reinterpret_cast<const float4*>(src + (long long)i * p.H * 512 + 256);
+    const float w = expf(lse[(long long)i * p.H] - m);
+    total += w;
+    a = make_float4(fmaf(w, x.x, a.x), fmaf(w, x.y, a.y), fmaf(w, x.z, a.z), fmaf(w, x.w, a.w));
+    b = make_float4(fmaf(w, y.x, b.x), fmaf(w, y.y, b.y), fmaf(w, y.z, b.z), fmaf(w, y.w, b.w));
+  }
+  const float inv = n ? 1.f / total : 0.f;
+  bf16* out = reinterpret_cast<bf16*>(p.out_latent) + ((long long)g * p.H + h) * 512 + d;
+  if ((reinterpret_cast<uintptr_t>(p.out_latent) & 7) == 0) {
+    *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
+    *reinterpret_cast<uint2*>(out + 256) = make_uint2(pack_bf16(b.x * inv, b.y * inv), pack_bf16(b.z * inv, b.w * inv));
+  } else {
+    const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) out[(i >> 2) * 256 + (i & 3)] = __float2bfloat16_rn(v[i] * inv);
+  }
+  if (threadIdx.x % 64 == 0) p.lse[(long long)g * p.H + h] = n ? m + logf(total) : -INFINITY;
+}
+
 template <int kFmt>
 static cudaError_t run(const Maps& maps, const DecodeParams& p, int blocks, cudaStream_t s) {
   auto kern = decode_pages_kernel<kFmt>;
@@ -598,6 +632,12 @@ static cudaError_t run(const Maps& maps, const DecodeParams& p, int blocks, cuda
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, kern, maps, p, blocks);
+  if (e != cudaSuccess) return e;
+  note_launch();
+  cfg.gridDim = dim3((unsigned)p.batch, (unsigned)(p.H / 4), 1);
+  cfg.blockDim = dim3(256, 1, 1);
+  cfg.dynamicSmemBytes = 0;
+  e = cudaLaunchKernelEx(&cfg, merge_pages_kernel, p);
   if (e == cudaSuccess) note_launch();
   return e;
 }

@@ -1119,11 +1119,13 @@ mla_status mla_decode_pages(const mla_config* cfg, const void* q_lat, const void
   dp.part_planar = 0;
   dp.wait_limit_ns = 2000000000ull;
   dp.withhold_page = 0;
-  e = tc ? launch_decode_pages_tc(cfg->cache_dtype, dp, s)
-         : launch_decode_simt(cfg->act_dtype, cfg->cache_dtype, dp, s);
-  if (e != cudaSuccess) return cuda_fail(e, "mla_decode_pages (attention)");
-  e = launch_combine(cfg->act_dtype, dp, w.groups, s);
-  return e == cudaSuccess ? MLA_OK : cuda_fail(e, "mla_decode_pages (combine)");
+  if (tc) {
+    e = launch_decode_pages_tc(cfg->cache_dtype, dp, s);
+  } else {
+    e = launch_decode_simt(cfg->act_dtype, cfg->cache_dtype, dp, s);
+    if (e == cudaSuccess) e = launch_combine(cfg->act_dtype, dp, w.groups, s);
+  }
+  return e == cudaSuccess ? MLA_OK : cuda_fail(e, "mla_decode_pages (attention)");
 }
 
 // ------------------------------------------------------------------ 4-bit weights

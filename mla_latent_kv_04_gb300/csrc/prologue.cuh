@@ -78,10 +78,18 @@ __device__ __forceinline__ int last_at_most(const int* a, int n, long long x) {
 // an ascending list is full.
 __device__ __forceinline__ int listed_tokens(const PlanParams& p, int g, int see) {
   const int32_t* list = p.pages + (long long)g * p.budget;
-  int lo = 0, hi = p.budget;                // the first negative entry
+  // the first negative entry: seven probes at a time, whose loads are in flight together
+  int lo = 0, hi = p.budget;
   while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (list[mid] >= 0) lo = mid + 1; else hi = mid;
+    const int step = (hi - lo + 7) / 8;
+    int full = 0;
+#pragma unroll
+    for (int i = 1; i < 8; ++i) {
+      const int at = lo + i * step - 1;
+      full += at < hi && list[at] >= 0 ? 1 : 0;
+    }
+    lo += full * step;
+    hi = min(hi, lo + (full == 7 ? step : step - 1));
   }
   if (lo == 0) return 0;
   const long long tail = (long long)see - (long long)list[lo - 1] * p.page_size;
