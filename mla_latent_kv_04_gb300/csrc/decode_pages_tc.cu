@@ -1,8 +1,8 @@
 // Decode over chosen pages on the tensor cores (bf16 activations, every bf16 and fp8 cache, 64-token pages,
 // d_c 512, d_r 64, a multiple of 16 heads).
 //
-// A CTA has a block of up to 64 heads and walks its work items (page ranges of one query token's list) two
-// pages, 128 tokens, at a time, with tokens in the rows of the first product and latent dims in those of
+// A CTA has a block of up to 64 heads and walks its work items (ranges of one query token's list) two pages,
+// 128 tokens, at a time, with tokens in the rows of the first product and latent dims in those of
 // the second:
 //   S^T = X q_lat^T         (M = 128 tokens, N = heads, K = 576)
 //   P   = 2^(c S - r_h)     (c = softmax scale * log2 e, r_h a running reference of the head)
@@ -37,7 +37,7 @@ enum { kBf16 = 0, kE4m3 = 1, kB128 = 2 };
 constexpr int kTok = 128;
 constexpr int kChunk = kTok * 128;             // 128 bytes of 128 rows
 constexpr int kThreads = 576;                  // producer, MMA issuer, 16 softmax warps
-constexpr float kGrow = 8.f;                   // how far scores may exceed the reference (log2)
+constexpr float kGrow = 8.75f;                 // how far scores may exceed the reference (log2; e4m3 ends at 448)
 
 template <int kFmt> struct Fmt;
 template <> struct Fmt<kBf16> {                // latent chunks of a tile, chunk buffers, bytes of the regions
@@ -55,8 +55,7 @@ template <int kFmt> struct Layout {
   static constexpr int kRing = F::kQ;
   static constexpr int kRope = kRing + F::kBufs * kChunk;
   static constexpr int kP = kFmt == kBf16 ? kRope : kRope + F::kRope;      // (bf16: over the rotary keys)
-  static constexpr int kRef = kRope + F::kRope + F::kP;                    // [64] references
-  static constexpr int kAlpha = kRef + 256;                                // [64] rescaling factors
+  static constexpr int kAlpha = kRope + F::kRope + F::kP;                  // [64] rescaling factors
   static constexpr int kHead = kAlpha + 256;                               // [64] factors of the fp8 query
   static constexpr int kWarp = kHead + 256;                                // [4][64] of the four token quarters
   static constexpr int kBar = kWarp + 1024;
@@ -149,8 +148,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int it = it0; ok && it < it1; ++it, ++q_seq) {
         const WorkItem item = p.items[it];
         const int32_t* bt = p.block_table + (long long)item.group * p.max_pages;
+        const int pg0 = 2 * item.page_begin, pg1 = min(2 * item.page_end, (item.kv + 63) / 64);
         auto page_of = [&](int pg) {
-          if (pg >= item.page_end) return -1;
+          if (pg >= pg1) return -1;
           const int page = bt[pg];
           if (page >= 0 && page < p.num_pages) return page;
           flag_status(p.status, MLA_ERR_DEVICE_GUARD);
@@ -162,8 +162,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           ptx::mbar_arrive_expect_tx(bar(B_QFULL), 9 * rows * 128);
           for (int c = 0; c < 9; ++c) ptx::tma_load_3d(base + 8192 * c, &maps.q, 64 * c, h0, item.group, bar(B_QFULL));
         }
-        int a = page_of(item.page_begin), b = page_of(item.page_begin + 1);
-        for (int pg = item.page_begin; ok && pg < item.page_end; pg += 2, ++tile) {
+        if (it + 1 < it1)                      // the next item's query into L2
+          ptx::bulk_prefetch_l2(reinterpret_cast<const bf16*>(p.q_lat) + ((long long)p.items[it + 1].group * p.H + h0) * 576,
+                                (uint32_t)(N * 1152));
+        int a = page_of(pg0), b = page_of(pg0 + 1);
+        for (int pg = pg0; ok && pg < pg1; pg += 2, ++tile) {
           const int na = page_of(pg + 2), nb = page_of(pg + 3);
           if (h0 == 0) {                       // the next tile's pages into L2
             if (na >= 0) ptx::bulk_prefetch_l2_hint(cache + (long long)na * page_bytes, page_bytes, pol);
@@ -253,14 +256,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     for (int it = it0; ok && it < it1; ++it, ++q_seq) {
       const WorkItem item = p.items[it];
-      const int tiles = (item.page_end - item.page_begin + 1) / 2;
+      const int tiles = item.page_end - item.page_begin;
       if (!(ok = wait_w(B_QFULL, q_seq & 1))) break;
       if (kAhead) product_s(tiles == 1);
       for (int i = 0; ok && i < tiles; ++i, ++o_tile) {
         if (!kAhead) product_s(i == tiles - 1);
         else if (i + 1 < tiles) product_s(i + 2 == tiles);
         if (!ok || !(ok = wait_w(B_PFULL, o_tile & 1))) break;
-        if (grown[o_tile & 1] == (int)o_tile && !(ok = wait_w(B_PAGAIN, again++ & 1))) break;
+        if (i > 0 && grown[o_tile & 1] == (int)o_tile && !(ok = wait_w(B_PAGAIN, again++ & 1))) break;
         if (i == 0 && !(ok = wait_w(B_OFREE, (q_seq & 1) ^ 1))) break;
         ptx::tc_fence_after();
         if (ptx::elect_one()) {
@@ -301,10 +304,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // four threads a token: heads 16 part .. of the block (parts behind the last head have none, but their
     // share of O, the dims tile 128 part)
-    const int quad = warp & 3, part = (warp - 2) >> 2, tok = 32 * quad + lane, hp = 16 * part, l16 = lane & 15;
+    const int quad = warp & 3, part = (warp - 2) >> 2, tok = 32 * quad + lane, hp = 16 * part;
     const bool heads = hp < N;
     const uint32_t lane_off = (uint32_t)(32 * quad) << 16;
-    float* ref = reinterpret_cast<float*>(basep + L::kRef);
     float* alpha = reinterpret_cast<float*>(basep + L::kAlpha);
     float* head = reinterpret_cast<float*>(basep + L::kHead);
     float* quarter = reinterpret_cast<float*>(basep + L::kWarp);         // [4][64]
@@ -351,27 +353,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             *reinterpret_cast<uint16_t*>(qp + r1 * 64 + (((lane >> 3) ^ ((r1 >> 1) & 3)) << 4) + 2 * (lane & 7)) = (uint16_t)pe_lo;
           }
           // infinities and NaN in the query make its scores NaN
-          if (lane == 0) head[h] = inv + (m < INFINITY ? 0.f : m - m);
+          if (lane == 0) head[h] = (kFmt == kE4m3 ? inv * p.scale_log2 : inv) + (m < INFINITY ? 0.f : m - m);
         }
         ptx::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(bar(B_QFULL));
       }
-      if (quad == 0 && heads && lane < 16) ref[hp + lane] = -INFINITY;
-      float fac[16];                           // and of a score of the fp8 query
-      if (kFp8) {
-        if (!(ok = wait_w(B_QFULL, (uint32_t)(it - it0) & 1))) break;
-#pragma unroll
-        for (int j = 0; j < 16; ++j) fac[j] = heads ? head[hp + j] * (kFmt == kE4m3 ? p.scale_log2 : 1.f) : 0.f;
-      }
+      if (kFp8 && !(ok = wait_w(B_QFULL, (uint32_t)(it - it0) & 1))) break;
       float sum[16], r[16];                    // sums and references of this thread's heads
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
         sum[j] = 0.f;
         r[j] = -INFINITY;
       }
-      for (int pg = item.page_begin; ok && pg < item.page_end; pg += 2, ++tile, c_seq += F::kChunks) {
-        const int left = min(min(kTok, (item.page_end - pg) * 64), item.kv - pg * 64);   // tokens of this tile
+      for (int pg = 2 * item.page_begin; ok && pg < 2 * item.page_end; pg += 2, ++tile, c_seq += F::kChunks) {
+        const int left = min(kTok, item.kv - pg * 64);                   // tokens of this tile
+        const bool first = pg == 2 * item.page_begin;
         const bool live = tok < left;
         float4 sc = make_float4(0.f, 0.f, 0.f, 0.f);
         float top_scale = 0.f;                 // log2 of the token's largest scale
@@ -400,16 +397,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const float f = c == 0 ? sc.x : (c == 1 ? sc.y : (c == 2 ? sc.z : sc.w));
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              const float x = heads ? __uint_as_float(hi[k]) : 0.f;
-              if (kFmt == kBf16) {
-                s[k] = x * p.scale_log2;
-              } else if (c == 4) {
-                s[k] = fmaf(s[k], fac[k], x) * p.scale_log2;
-              } else {
-                const float v = fmaf(heads ? __uint_as_float(lo[k]) : 0.f, 0.0625f, x);
-                if (kFmt == kE4m3) s[k] = v * fac[k];
-                else s[k] = c ? fmaf(f, v, s[k]) : f * v;
+            for (int k = 0; k < 16; k += 4) {
+              float4 fac4 = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (kFmt == kE4m3 || c == 4) fac4 = *reinterpret_cast<const float4*>(head + hp + k);
+              const float fac[4] = {fac4.x, fac4.y, fac4.z, fac4.w};
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float x = heads ? __uint_as_float(hi[k + i]) : 0.f;
+                if (kFmt == kBf16) {
+                  s[k + i] = x * p.scale_log2;
+                } else if (c == 4) {
+                  s[k + i] = fmaf(s[k + i], fac[i], x) * p.scale_log2;
+                } else {
+                  const float v = fmaf(heads ? __uint_as_float(lo[k + i]) : 0.f, 0.0625f, x);
+                  if (kFmt == kE4m3) s[k + i] = v * fac[i];
+                  else s[k + i] = c ? fmaf(f, v, s[k + i]) : f * v;
+                }
               }
             }
             ptx::tc_fence_before();
@@ -467,12 +470,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           return heads && live && most + top_scale > kGrow;
         };
-        auto hand_over = [&](int b) {
-          ptx::fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(bar(b));
-        };
-        if (__any_sync(0xffffffffu, weights()) && lane == 0) grown[tile & 1] = (int)tile;
         if (!live) {                           // rows that may hold anything: their P is 0, 0 times NaN is not
           const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
           for (int c = part; c < F::kChunks; c += 4) {
@@ -481,59 +478,71 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = 0; k < 8; ++k) row[k] = zero;
           }
         }
-        hand_over(B_PFULL);
-        if (!(ok = wait_w(B_PFULL, tile & 1))) break;
-        if (grown[tile & 1] == (int)tile) {
-          // new references: the largest so far (fp8: 2^4 below, so that P keeps its bits), then rescale
-          float m[16];
-#pragma unroll
-          for (int j = 0; j < 16; ++j) m[j] = live ? s[j] + top_scale : -INFINITY;
-          const float most = columns_of_warp<true>(m, lane);
-          if (heads && lane < 16) quarter[64 * quad + hp + lane] = most;
-          if (!(ok = meet())) break;
-          float a = 0.f, next = 0.f;
-          if (heads) {
-            const float* q = quarter + hp + l16;
-            const float old = ref[hp + l16], top = fmaxf(fmaxf(q[0], q[64]), fmaxf(q[128], q[192])) - (kFp8 ? 4.f : 0.f);
-            next = fmaxf(old, top);
-            a = old == -INFINITY ? 0.f : ptx::ex2(old - next);
-          }
-          if (!(ok = meet())) break;
-          if (quad == 0 && heads && lane < 16) {
-            ref[hp + lane] = next;
-            alpha[hp + lane] = a;
-          }
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            sum[j] *= __shfl_sync(0xffffffffu, a, j);
-            r[j] = __shfl_sync(0xffffffffu, next, j);
-          }
-          if (!(ok = meet())) break;
-          if (pg > item.page_begin) {
-            if (!(ok = wait_w(B_PDONE, (tile - 1) & 1))) break;
-            ptx::tc_fence_after();
+        // An item's first tile has no reference to try. (One place for the code of both passes: registers.)
+        bool renew = first;
 #pragma unroll 1
-            for (int h = 0; h < N; h += 16) {              // this warp's dims tile
-              uint32_t v[16];
-              const uint32_t at = t_o + lane_off + 64 * part + h;
-              ptx::tmem_ld16(at, v);
-              ptx::tmem_wait_ld();
+        while (true) {
+          if (renew) {
+            // new references: the largest score so far (fp8: 4 below, so that P, then up to 16, keeps its bits:
+            // two e4m3 terms are off by up to 2^-9 of P, or 2^-10 where that is more)
+            float m[16];
 #pragma unroll
-              for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * alpha[h + k]);
-              ptx::tmem_st16(at, v);
+            for (int j = 0; j < 16; ++j) m[j] = live ? s[j] + top_scale : -INFINITY;
+            const float most = columns_of_warp<true>(m, lane);
+            if (heads && lane < 16) quarter[64 * quad + hp + lane] = most;
+            if (!(ok = meet())) break;
+            const float less = kFp8 ? 4.f : 0.f;
+#pragma unroll
+            for (int j = 0; j < 16; j += 4) {
+              const float4 x = *reinterpret_cast<const float4*>(quarter + hp + j);
+              const float4 y = *reinterpret_cast<const float4*>(quarter + 64 + hp + j);
+              const float4 z = *reinterpret_cast<const float4*>(quarter + 128 + hp + j);
+              const float4 w = *reinterpret_cast<const float4*>(quarter + 192 + hp + j);
+              const float top[4] = {fmaxf(fmaxf(x.x, y.x), fmaxf(z.x, w.x)), fmaxf(fmaxf(x.y, y.y), fmaxf(z.y, w.y)),
+                                    fmaxf(fmaxf(x.z, y.z), fmaxf(z.z, w.z)), fmaxf(fmaxf(x.w, y.w), fmaxf(z.w, w.w))};
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const float next = fmaxf(r[j + k], top[k] - less);
+                const float a = r[j + k] == -INFINITY ? 0.f : ptx::ex2(r[j + k] - next);
+                r[j + k] = next;
+                sum[j + k] *= a;
+                if (!first && heads && lane == 0 && quad == 0) alpha[hp + j + k] = a;
+              }
             }
-            ptx::tmem_wait_st();
-            ptx::tc_fence_before();
+            if (!first) {                        // O of the tiles before
+              if (!(ok = meet() && wait_w(B_PDONE, (tile - 1) & 1))) break;
+              ptx::tc_fence_after();
+#pragma unroll 1
+              for (int h = 0; h < N; h += 16) {              // this warp's dims tile
+                uint32_t v[16];
+                const uint32_t at = t_o + lane_off + 64 * part + h;
+                ptx::tmem_ld16(at, v);
+                ptx::tmem_wait_ld();
+#pragma unroll
+                for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * alpha[h + k]);
+                ptx::tmem_st16(at, v);
+              }
+              ptx::tmem_wait_st();
+              ptx::tc_fence_before();
+            }
           }
-          weights();
-          hand_over(B_PAGAIN);
+          const bool over = weights();
+          if (!renew && __any_sync(0xffffffffu, over) && lane == 0) grown[tile & 1] = (int)tile;
+          ptx::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(bar(renew && !first ? B_PAGAIN : B_PFULL));
+          if (renew) break;
+          if (!(ok = wait_w(B_PFULL, tile & 1)) || grown[tile & 1] != (int)tile) break;
+          renew = true;
         }
+        if (!ok) break;
 #pragma unroll
         for (int j = 0; j < 16; ++j) sum[j] = now[j];
       }
       if (!ok) break;
       // the item's sums, LSE and output
       const float mine = columns_of_warp<false>(sum, lane);
+      if (!(ok = meet())) break;               // (the maxima of a first tile have been read)
       if (heads && lane < 16) quarter[64 * quad + hp + lane] = mine;
       if (!(ok = meet() && wait_w(B_PDONE, (tile - 1) & 1))) break;
       ptx::tc_fence_after();
@@ -541,7 +550,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float* q = quarter + hp + lane;
         const float total = (q[0] + q[64]) + (q[128] + q[192]);
         alpha[hp + lane] = p.out_scale / total;
-        const float lse = (ref[hp + lane] + log2f(total)) * kLn2;
+        float own = r[0];                      // this lane's head's reference
+#pragma unroll
+        for (int j = 1; j < 16; ++j) own = lane == j ? r[j] : own;
+        const float lse = (own + log2f(total)) * kLn2;
         const int h = h0 + hp + lane;
         if (item.single) p.lse[g * p.H + h] = lse;
         else p.part_lse[(long long)it * p.H + h] = lse;

@@ -1085,6 +1085,10 @@ mla_status mla_decode_pages(const mla_config* cfg, const void* q_lat, const void
   pp.status = (int32_t*)(ws + w.status);
   pp.pages = pages;
   pp.budget = budget;
+  if (tc) {
+    pp.unit = kPagesTile;
+    pp.item_cost = kPagesItemCost;
+  }
   int32_t* listed = (int32_t*)(ws + table);
   cudaError_t e = launch_pages_prep(pp, block_table, listed, s);
   if (e != cudaSuccess) return cuda_fail(e, "mla_decode_pages (prologue)");

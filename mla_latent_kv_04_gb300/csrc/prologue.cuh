@@ -98,6 +98,7 @@ __device__ __forceinline__ int listed_tokens(const PlanParams& p, int g, int see
 
 __device__ inline void plan_body(const PlanParams& p, int* sm, bool reset_status) {
   const int groups = p.batch * p.q_len, W = p.workers;
+  const int unit = p.unit ? p.unit : p.page_size, item_cost = p.item_cost ? p.item_cost : kItemCost;
   int* cu = sm;                             // [groups + 1] page prefix
   int* vcu = cu + groups + 1;               // [groups + 1] cost prefix
   int* nz = vcu + groups + 1;               // [groups + 1] non-empty group prefix
@@ -128,9 +129,9 @@ __device__ inline void plan_body(const PlanParams& p, int* sm, bool reset_status
     kvs[g] = kv;
     p.group_first[g] = -1;
     p.group_last[g] = -2;
-    const int pages = (kv + p.page_size - 1) / p.page_size;
+    const int pages = (kv + unit - 1) / unit;
     cu[g + 1] = pages;
-    vcu[g + 1] = pages > 0 ? pages + kItemCost : 0;
+    vcu[g + 1] = pages > 0 ? pages + item_cost : 0;
     nz[g + 1] = pages > 0 ? 1 : 0;
   }
   if (tid == 0) {
@@ -154,7 +155,7 @@ __device__ inline void plan_body(const PlanParams& p, int* sm, bool reset_status
     }
     const long long c = V * k / W;
     const int g = last_at_most(vcu, groups, c);
-    const long long o = c - vcu[g] - kItemCost;
+    const long long o = c - vcu[g] - item_cost;
     cutp[k] = cu[g] + (int)(o < 0 ? 0 : o);
     cutg[k] = g;
   }

@@ -300,7 +300,22 @@ def check_attend(c, q_lat, pages, got, lse, skip=()):
             assert_within(lse[b, t], wl, dz + 2.0 ** -20 * (4 + np.abs(wl)) + tok * 2.0 ** -24, f"lse {b} {t}")
             # the softmax's weights in 16 bits (bf16; fp8: two e4m3 terms, at most that), then sums of fp32
             soft = (2.0 ** -8 if act == "bf16" else 0.0) + 2 * dz + 2.0 ** -19 * (4 + np.abs(wl).max()) + 2 * tok * 2.0 ** -24
-            assert_within(got[b, t], want, D.EPS[act] * np.abs(want) * 1.01 + soft * wmag, f"output {b} {t}")
+            assert_within(got[b, t], want, D.EPS[act] * np.abs(want) * 1.01 + soft * wmag + low_weights(c, b, pages[b, t], see),
+                          f"output {b} {t}")
+
+
+def low_weights(c, b, pages, see):
+    """Of an fp8 cache the weights P are two e4m3 terms, off by up to 2^-10 where that exceeds 2^-9 P, and
+    the largest P is at least 16: 2^-14 of the sum's total for each token (block scales: P times the scale,
+    at least 16 for the largest scale)."""
+    if not c.kind.startswith("fp8"):
+        return 0.0
+    at = np.concatenate([np.arange(p * P, min(see, p * P + P)) for p in pages if p >= 0])
+    x = np.abs(c.values[b][at][:, : c.d.d_latent])
+    if c.kind == "fp8_e4m3_b128":
+        s = x.reshape(len(at), -1, 128).max(2)
+        x = x * np.repeat(np.where(s > 0, s.max() / np.where(s > 0, s, 1.0), 0.0), 128, 1)
+    return 2.0 ** -14 * x.sum(0)
 
 
 @pytest.mark.parametrize("kind,shape,H", FORMATS)
