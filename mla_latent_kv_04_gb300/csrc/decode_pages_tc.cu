@@ -76,25 +76,26 @@ constexpr uint32_t idesc_e4m3(int N, bool a_mn, bool b_mn) {
   return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | (8u << 24);
 }
 
-// Sums (or maxima) over the warp's lanes of 16 columns: lanes j and j + 16 are left with column j.
-template <bool kMax>
-__device__ __forceinline__ float columns_of_warp(float (&v)[16], int lane) {
+// Sums over the warp's lanes of 16 columns: lanes j and j + 16 are left with column j.
+__device__ __forceinline__ float column_sums(float (&v)[16], int lane) {
 #pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    const float got = __shfl_xor_sync(0xffffffffu, v[j], 16);
-    v[j] = kMax ? fmaxf(v[j], got) : v[j] + got;
-  }
+  for (int j = 0; j < 16; ++j) v[j] += __shfl_xor_sync(0xffffffffu, v[j], 16);
 #pragma unroll
   for (int o = 8; o > 0; o >>= 1) {
     const bool up = (lane & o) != 0;
 #pragma unroll
     for (int j = 0; j < o; ++j) {
       const float give = up ? v[j] : v[j + o], keep = up ? v[j + o] : v[j];
-      const float got = __shfl_xor_sync(0xffffffffu, give, o);
-      v[j] = kMax ? fmaxf(keep, got) : keep + got;
+      v[j] = keep + __shfl_xor_sync(0xffffffffu, give, o);
     }
   }
   return v[0];
+}
+// The largest value of the warp's lanes (NaN only if all are).
+__device__ __forceinline__ float warp_most(float v) {
+  float m;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+  return m;
 }
 
 template <int kFmt>
@@ -478,62 +479,85 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = 0; k < 8; ++k) row[k] = zero;
           }
         }
-        // An item's first tile has no reference to try. (One place for the code of both passes: registers.)
-        bool renew = first;
-#pragma unroll 1
-        while (true) {
-          if (renew) {
-            // new references: the largest score so far (fp8: 4 below, so that P, then up to 16, keeps its bits:
-            // two e4m3 terms are off by up to 2^-9 of P, or 2^-10 where that is more)
-            float m[16];
+        auto renew = [&]() {
+          // new references: the largest score so far (fp8: 4 below, so that P, then up to 16, keeps its bits:
+          // two e4m3 terms are off by up to 2^-9 of P, or 2^-10 where that is more)
 #pragma unroll
-            for (int j = 0; j < 16; ++j) m[j] = live ? s[j] + top_scale : -INFINITY;
-            const float most = columns_of_warp<true>(m, lane);
-            if (heads && lane < 16) quarter[64 * quad + hp + lane] = most;
-            if (!(ok = meet())) break;
-            const float less = kFp8 ? 4.f : 0.f;
+          for (int j = 0; j < 16; j += 4) {
+            float m[4];
 #pragma unroll
-            for (int j = 0; j < 16; j += 4) {
-              const float4 x = *reinterpret_cast<const float4*>(quarter + hp + j);
-              const float4 y = *reinterpret_cast<const float4*>(quarter + 64 + hp + j);
-              const float4 z = *reinterpret_cast<const float4*>(quarter + 128 + hp + j);
-              const float4 w = *reinterpret_cast<const float4*>(quarter + 192 + hp + j);
-              const float top[4] = {fmaxf(fmaxf(x.x, y.x), fmaxf(z.x, w.x)), fmaxf(fmaxf(x.y, y.y), fmaxf(z.y, w.y)),
-                                    fmaxf(fmaxf(x.z, y.z), fmaxf(z.z, w.z)), fmaxf(fmaxf(x.w, y.w), fmaxf(z.w, w.w))};
+            for (int k = 0; k < 4; ++k) m[k] = warp_most(live ? s[j + k] + top_scale : -INFINITY);
+            if (heads && lane == 0)
+              *reinterpret_cast<float4*>(quarter + 64 * quad + hp + j) = make_float4(m[0], m[1], m[2], m[3]);
+          }
+          if (!(ok = meet())) return;
+          const float less = kFp8 ? 4.f : 0.f;
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const float next = fmaxf(r[j + k], top[k] - less);
-                const float a = r[j + k] == -INFINITY ? 0.f : ptx::ex2(r[j + k] - next);
-                r[j + k] = next;
-                sum[j + k] *= a;
-                if (!first && heads && lane == 0 && quad == 0) alpha[hp + j + k] = a;
-              }
-            }
-            if (!first) {                        // O of the tiles before
-              if (!(ok = meet() && wait_w(B_PDONE, (tile - 1) & 1))) break;
-              ptx::tc_fence_after();
-#pragma unroll 1
-              for (int h = 0; h < N; h += 16) {              // this warp's dims tile
-                uint32_t v[16];
-                const uint32_t at = t_o + lane_off + 64 * part + h;
-                ptx::tmem_ld16(at, v);
-                ptx::tmem_wait_ld();
+          for (int j = 0; j < 16; j += 4) {
+            const float4 x = *reinterpret_cast<const float4*>(quarter + hp + j);
+            const float4 y = *reinterpret_cast<const float4*>(quarter + 64 + hp + j);
+            const float4 z = *reinterpret_cast<const float4*>(quarter + 128 + hp + j);
+            const float4 w = *reinterpret_cast<const float4*>(quarter + 192 + hp + j);
+            const float top[4] = {fmaxf(fmaxf(x.x, y.x), fmaxf(z.x, w.x)), fmaxf(fmaxf(x.y, y.y), fmaxf(z.y, w.y)),
+                                  fmaxf(fmaxf(x.z, y.z), fmaxf(z.z, w.z)), fmaxf(fmaxf(x.w, y.w), fmaxf(z.w, w.w))};
 #pragma unroll
-                for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * alpha[h + k]);
-                ptx::tmem_st16(at, v);
-              }
-              ptx::tmem_wait_st();
-              ptx::tc_fence_before();
+            for (int k = 0; k < 4; ++k) {
+              const float next = fmaxf(r[j + k], top[k] - less);
+              const float a = r[j + k] == -INFINITY ? 0.f : ptx::ex2(r[j + k] - next);
+              r[j + k] = next;
+              sum[j + k] *= a;
+              if (!first && heads && lane == 0 && quad == 0) alpha[hp + j + k] = a;
             }
           }
-          const bool over = weights();
-          if (!renew && __any_sync(0xffffffffu, over) && lane == 0) grown[tile & 1] = (int)tile;
+          if (!first) {                        // O of the tiles before
+            if (!(ok = meet() && wait_w(B_PDONE, (tile - 1) & 1))) return;
+            ptx::tc_fence_after();
+#pragma unroll 1
+            for (int h = 0; h < N; h += 16) {              // this warp's dims tile
+              uint32_t v[16];
+              const uint32_t at = t_o + lane_off + 64 * part + h;
+              ptx::tmem_ld16(at, v);
+              ptx::tmem_wait_ld();
+#pragma unroll
+              for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * alpha[h + k]);
+              ptx::tmem_st16(at, v);
+            }
+            ptx::tmem_wait_st();
+            ptx::tc_fence_before();
+          }
+        };
+        auto hand_over = [&](int b) {
           ptx::fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(bar(renew && !first ? B_PAGAIN : B_PFULL));
-          if (renew) break;
-          if (!(ok = wait_w(B_PFULL, tile & 1)) || grown[tile & 1] != (int)tile) break;
-          renew = true;
+          if (lane == 0) ptx::mbar_arrive(bar(b));
+        };
+        // An item's first tile has no reference to try. fp8: one place for the code of both passes (its
+        // registers: 226 -> 205 us at 64 x 2 queries of 96 pages; bf16, where they suffice, 73 -> 77).
+        if constexpr (kFp8) {
+          bool again = first;
+#pragma unroll 1
+          while (true) {
+            if (again) renew();
+            if (!ok) break;
+            const bool over = weights();
+            if (!again && __any_sync(0xffffffffu, over) && lane == 0) grown[tile & 1] = (int)tile;
+            hand_over(again && !first ? B_PAGAIN : B_PFULL);
+            if (again) break;
+            if (!(ok = wait_w(B_PFULL, tile & 1)) || grown[tile & 1] != (int)tile) break;
+            again = true;
+          }
+        } else {
+          if (!first) {
+            if (__any_sync(0xffffffffu, weights()) && lane == 0) grown[tile & 1] = (int)tile;
+            hand_over(B_PFULL);
+            if (!(ok = wait_w(B_PFULL, tile & 1))) break;
+          }
+          if (first || grown[tile & 1] == (int)tile) {
+            renew();
+            if (!ok) break;
+            weights();
+            hand_over(first ? B_PFULL : B_PAGAIN);
+          }
         }
         if (!ok) break;
 #pragma unroll
@@ -541,7 +565,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       // the item's sums, LSE and output
-      const float mine = columns_of_warp<false>(sum, lane);
+      const float mine = column_sums(sum, lane);
       if (!(ok = meet())) break;               // (the maxima of a first tile have been read)
       if (heads && lane < 16) quarter[64 * quad + hp + lane] = mine;
       if (!(ok = meet() && wait_w(B_PDONE, (tile - 1) & 1))) break;
@@ -662,6 +686,10 @@ bool decode_pages_tc_supported(const mla_config* c, long long num_pages) {
   return c->act_dtype == MLA_BF16 && c->page_size == 64 && c->d_latent == 512 && c->d_rope == 64 &&
          c->num_heads % 16 == 0 && c->num_heads <= 1024 && num_pages * 64 <= 0x7FFFFF00LL;
 }
+
+// Tiles that an item's first loads, first reference and epilogue are worth (measured, 1 to 6 tried: bf16 73 us
+// at 1, 77 at 4; e4m3 205 at 1, 198 at 4; block-scaled 99 at 1 and 2, 108 at 4).
+int decode_pages_item_cost(mla_dtype cache) { return cache == MLA_BF16 ? 1 : (cache == MLA_FP8_E4M3 ? 4 : 2); }
 
 int decode_pages_tc_workers(int H) {
   const int blocks = (H + 63) / 64, n = device_sms() / blocks;

@@ -337,7 +337,7 @@ cudaError_t launch_pages_prep(const PlanParams& pp, const int32_t* block_table, 
 // The decode over such a plan on the tensor cores: bf16 activations, 64-token pages, d_c 512, d_r 64, a
 // multiple of 16 heads; q_lat and cache at multiples of 16 bytes. dp.part_o is fp32 [items][H][512].
 constexpr int kPagesTile = 128;       // tokens of the kernel's tiles, in which its items are planned
-constexpr int kPagesItemCost = 2;
+int decode_pages_item_cost(mla_dtype cache);
 bool decode_pages_tc_supported(const mla_config* c, long long num_pages);
 int decode_pages_tc_workers(int H);
 cudaError_t launch_decode_pages_tc(mla_dtype cache, const DecodeParams& p, cudaStream_t s);

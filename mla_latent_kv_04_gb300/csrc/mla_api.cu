@@ -1087,7 +1087,7 @@ mla_status mla_decode_pages(const mla_config* cfg, const void* q_lat, const void
   pp.budget = budget;
   if (tc) {
     pp.unit = kPagesTile;
-    pp.item_cost = kPagesItemCost;
+    pp.item_cost = decode_pages_item_cost(cfg->cache_dtype);
   }
   int32_t* listed = (int32_t*)(ws + table);
   cudaError_t e = launch_pages_prep(pp, block_table, listed, s);
