@@ -481,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         auto renew = [&]() {
           // new references: the largest score so far (fp8: 4 below, so that P, then up to 16, keeps its bits:
-          // two e4m3 terms are off by up to 2^-9 of P, or 2^-10 where that is more)
+          // two e4m3 terms are off by up to 2^-8 of P, or 2^-10 where that is more)
 #pragma unroll
           for (int j = 0; j < 16; j += 4) {
             float m[4];

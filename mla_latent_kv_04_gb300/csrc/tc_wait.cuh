@@ -20,7 +20,9 @@ __device__ __forceinline__ bool bounded_wait(uint32_t bar, uint32_t parity, vola
   if (probe()) return true;
   const uint64_t t0 = ptx::globaltimer();
   while (true) {
-    if (probe()) return true;
+#pragma unroll 1
+    for (int i = 0; i < 16; ++i)               // (the clock is slow to read)
+      if (probe()) return true;
     if (*abort) return false;
     if (ptx::globaltimer() - t0 > kWaitLimitNs) {
       *abort = 1;

@@ -305,7 +305,7 @@ def check_attend(c, q_lat, pages, got, lse, skip=()):
 
 
 def low_weights(c, b, pages, see):
-    """Of an fp8 cache the weights P are two e4m3 terms, off by up to 2^-10 where that exceeds 2^-9 P, and
+    """Of an fp8 cache the weights P are two e4m3 terms, off by up to 2^-10 where that exceeds 2^-8 P, and
     the largest P is at least 16: 2^-14 of the sum's total for each token (block scales: P times the scale,
     at least 16 for the largest scale)."""
     if not c.kind.startswith("fp8"):
