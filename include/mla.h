@@ -485,7 +485,9 @@ mla_status mla_page_scores_workspace_size(const mla_config* cfg, int batch, int 
  * they share out H. Entries behind them are left as they are.
  *   q_lat [batch][q_len][H][d_c + d_r] (act dtype; mla_absorb_query); page_keys from mla_page_keys;
  *   block_table, seq_lens as in mla_decode; scores [batch][q_len][max_pages] fp32.
- * fp32 sums and softmax. A page with an id out of range scores 0, a request with seq_lens[b] < q_len or
+ * fp32 sums and softmax. The tensor-core kernel takes bf16 at d_c 512, d_r 64, 64-token pages, up to 128
+ * heads and max_pages up to 4096, for q_lat and page_keys that start at multiples of 16 bytes; anything else
+ * takes SIMT kernels, many times slower at large sizes. A page with an id out of range scores 0, a request with seq_lens[b] < q_len or
  * above max_pages * P is left out, both with the guard; seq_lens[b] == 0 is left out. workspace: 256-byte
  * aligned device buffer of mla_page_scores_workspace_size bytes (NULL if that is 0), any contents; calls
  * that share one must be ordered on the GPU. */
@@ -522,8 +524,11 @@ mla_status mla_decode_pages_workspace_size(const mla_config* cfg, int batch, int
  * P is skipped like an empty request, with the guard; a list that is not ascending or names a page that
  * the query does not see sets the guard and leaves that query's result undefined. workspace: as in
  * mla_decode (its first int32 is the call's status word, cleared by each call). MLA_ERR_UNSUPPORTED:
- * d_latent above 512, batch * q_len above 8192. A cache that does not start at a multiple of 4 bytes is
- * refused. */
+ * d_latent above 512, batch * q_len above 8192. The tensor-core kernel takes bf16 activations at d_c 512, d_r
+ * 64, 64-token pages, any cache format and a multiple of 16 heads up to 1024, for a q_lat and cache that start
+ * at multiples of 16 bytes; anything else takes the SIMT kernel, and a cache that does not start at a multiple
+ * of 4 bytes is refused. Scores and LSE are fp32 results; the softmax's weights are rounded to bf16 (fp8 caches:
+ * to two e4m3 terms, 8 significant bits) for the product with the latents. */
 mla_status mla_decode_pages(const mla_config* cfg, const void* q_lat, const void* cache, int num_pages,
                             const int32_t* block_table, int max_pages, const int32_t* seq_lens, int batch,
                             int q_len, const int32_t* pages, int budget, void* out_latent, float* lse,
@@ -560,7 +565,11 @@ mla_status mla_mx4_project_workspace_size(const mla_config* cfg, int K, int N, i
 /* out = x W for a 4-bit W: x [rows][K], out [rows][N] (act dtype), fp32 sums. With W = W_comb and x =
  * out_latent this is mla_output_proj with a quarter of its bytes to read.
  *   workspace: 256-byte aligned device buffer of mla_mx4_project_workspace_size bytes (NULL if that is 0),
- *   any contents; calls that share one must be ordered on the GPU. rows == 0 is a no-op. */
+ *   any contents; calls that share one must be ordered on the GPU. rows == 0 is a no-op.
+ * bf16 activations run on the tensor cores (an x that does not start at a multiple of 16 bytes on the SIMT
+ * kernel): x enters as exact sums of 4-bit or e4m3 values under a power of two per 32 elements, off by at most
+ * 2^-17 of the largest of the 32, and a row that holds an infinity or NaN gives NaN in all its outputs. A
+ * column with a NaN scale gives NaN. Should a bounded wait of the kernel run out, its outputs are not written. */
 mla_status mla_mx4_project(const mla_config* cfg, const void* x, const void* codes, const void* scales, int K,
                            int N, int rows, void* out, void* workspace, size_t workspace_bytes, void* stream);
 

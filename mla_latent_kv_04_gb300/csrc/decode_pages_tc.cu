@@ -657,24 +657,9 @@ static cudaError_t run(const Maps& maps, const DecodeParams& p, int blocks, cuda
   constexpr int smem = Layout<kFmt>::kSmem;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(p.workers * blocks), 1, 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kern, maps, p, blocks);
-  if (e != cudaSuccess) return e;
-  note_launch();
-  cfg.gridDim = dim3((unsigned)p.batch, (unsigned)(p.H / 4), 1);
-  cfg.blockDim = dim3(256, 1, 1);
-  cfg.dynamicSmemBytes = 0;
-  e = cudaLaunchKernelEx(&cfg, merge_pages_kernel, p);
-  if (e == cudaSuccess) note_launch();
+  e = launch_pdl(kern, dim3((unsigned)(p.workers * blocks), 1, 1), kThreads, smem, s, maps, p, blocks);
+  if (e == cudaSuccess)
+    e = launch_pdl(merge_pages_kernel, dim3((unsigned)p.batch, (unsigned)(p.H / 4), 1), 256, 0, s, p);
   return e;
 }
 

@@ -308,8 +308,7 @@ struct PageScoreParams {
   int max_pages, num_pages, groups, q_len, H, D, P;
   float scale_log2;           // softmax scale * log2(e)
   float* scores;              // [groups][max_pages]
-  float* z;                   // workspace of the SIMT form: [groups][H][max_pages]
-  float* lse2;                // and [groups][H]
+  float* lse2;                // workspace of the SIMT form: [groups][H]
   int32_t* status;
 };
 cudaError_t launch_page_scores_simt(mla_dtype act, const PageScoreParams& p, cudaStream_t s);

@@ -935,18 +935,14 @@ mla_status mla_page_keys(const mla_config* cfg, const void* cache, int num_pages
   return e == cudaSuccess ? MLA_OK : cuda_fail(e, "mla_page_keys");
 }
 
-// Scores of every head and page, and every head's sum (of the SIMT form).
-static size_t page_scores_z_bytes(const mla_config* c, int groups, int max_pages) {
-  return align256((size_t)groups * c->num_heads * max_pages * 4);
-}
-
 mla_status mla_page_scores_workspace_size(const mla_config* cfg, int batch, int q_len, int max_pages,
                                           size_t* bytes) {
   mla_status st = check_decode_shape(cfg, batch, q_len);
   if (st == MLA_OK) st = check_pages(cfg, 1, max_pages);
   if (st != MLA_OK) return st;
   if (!bytes) return invalid("bytes is NULL");
-  *bytes = page_scores_z_bytes(cfg, batch * q_len, max_pages) + align256((size_t)batch * q_len * cfg->num_heads * 4);
+  if (cfg->num_heads > 65535) return unsupported("num_heads above 65535");
+  *bytes = align256((size_t)batch * q_len * cfg->num_heads * 4);     // every head's sum (the SIMT form)
   return MLA_OK;
 }
 
@@ -978,8 +974,7 @@ mla_status mla_page_scores(const mla_config* cfg, const void* q_lat, const void*
   p.P = cfg->page_size;
   p.scale_log2 = softmax_scale_of(cfg) * kLog2e;
   p.scores = scores;
-  p.z = (float*)workspace;
-  p.lse2 = (float*)((char*)workspace + page_scores_z_bytes(cfg, p.groups, max_pages));
+  p.lse2 = (float*)workspace;
   p.status = dev_status;
   cudaError_t e = page_scores_tc_supported(cfg, num_pages, max_pages) && aligned16(q_lat, page_keys)
                       ? launch_page_scores_tc(p, (cudaStream_t)stream)
@@ -1039,7 +1034,7 @@ mla_status mla_decode_pages_workspace_size(const mla_config* cfg, int batch, int
   mla_status st = check_config(cfg);
   if (st != MLA_OK) return st;
   DecodeWorkspace w;
-  size_t table;
+  size_t table = 0;
   st = pages_layout(cfg, batch, q_len, budget, &w, &table);
   if (st != MLA_OK) return st;
   if (!bytes) return invalid("bytes is NULL");
@@ -1063,7 +1058,7 @@ mla_status mla_decode_pages(const mla_config* cfg, const void* q_lat, const void
   if (((uintptr_t)workspace & 255) != 0) return invalid("workspace must be 256-byte aligned");
   if (((uintptr_t)cache & 3) != 0) return invalid("cache must be 4-byte aligned");
   DecodeWorkspace w;
-  size_t table;
+  size_t table = 0;
   pages_layout(cfg, batch, q_len, budget, &w, &table);
   const bool tc = decode_pages_tc_supported(cfg, num_pages) && aligned16(q_lat, cache);
   if (tc) w.workers = std::min(w.workers, decode_pages_tc_workers(cfg->num_heads));

@@ -78,12 +78,8 @@ struct Work {
 // block). Four lanes a block of 32, eight elements each. Columns of rows behind the last one are not
 // written (nor read from the product).
 template <bool kForm8>
-__global__ void __launch_bounds__(256) split_kernel(const bf16* __restrict__ x, int rows, int K, TileShape t,
-                                                    uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
-  const int k = (blockIdx.x * 256 + threadIdx.x) * 8, r = blockIdx.y;
-  ptx::griddep_launch_dependents();
-  ptx::griddep_wait();
-  if (k >= (K + 127) / 128 * 128) return;      // (sixteen lanes together)
+__device__ __forceinline__ void split_row(const bf16* __restrict__ x, int r, int k, int K, const TileShape& t,
+                                          uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
   uint4 v4 = make_uint4(0u, 0u, 0u, 0u);
   if (k < K) v4 = *reinterpret_cast<const uint4*>(x + (long long)r * K + k);
   const uint32_t v[4] = {v4.x, v4.y, v4.z, v4.w};
@@ -152,6 +148,17 @@ __global__ void __launch_bounds__(256) split_kernel(const bf16* __restrict__ x, 
     uint8_t* sc = scales + (((long long)tile * groups + k / 128) * t.atoms + at / 128) * 512;
     *reinterpret_cast<uint32_t*>(sc + (at % 32) * 16 + (at % 128) / 32 * 4) = w;
   }
+}
+
+template <bool kForm8>
+__global__ void __launch_bounds__(256) split_kernel(const bf16* __restrict__ x, int rows, int K, TileShape t,
+                                                    uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
+  const int k = (blockIdx.x * 256 + threadIdx.x) * 8;
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  if (k >= (K + 127) / 128 * 128) return;      // (sixteen lanes together)
+  for (int r = blockIdx.y; r < rows; r += gridDim.y)
+    split_row<kForm8>(x, r, k, K, t, codes, scales);
 }
 
 // ======================================================================== product
@@ -440,23 +447,6 @@ ProjectLayout project_layout(int K, const TileShape& t, int grid) {
   return l;
 }
 
-template <typename K, typename... A>
-cudaError_t launch_pdl(K kern, dim3 grid, int threads, size_t smem, cudaStream_t s, A... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3((unsigned)threads, 1, 1);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
-  if (e == cudaSuccess) note_launch();
-  return e;
-}
-
 template <bool kForm8>
 size_t project_workspace(int K, int N, int rows) {
   const TileShape t = tile_shape<kForm8>(rows);
@@ -492,7 +482,7 @@ cudaError_t project(const void* x, const void* codes, const void* scales, int K,
   auto kern = t.atoms == 2 ? project_tc_kernel<kForm8, 2> : project_tc_kernel<kForm8, 1>;
   cudaError_t e = allow_smem(kern, smem);
   if (e == cudaSuccess)
-    e = launch_pdl(split_kernel<kForm8>, dim3((unsigned)((K + 2047) / 2048), (unsigned)rows, 1), 256, 0, s, (const bf16*)x,
+    e = launch_pdl(split_kernel<kForm8>, dim3((unsigned)((K + 2047) / 2048), (unsigned)(rows < 32768 ? rows : 32768), 1), 256, 0, s, (const bf16*)x,
                    rows, K, t, ws + l.codes, ws + l.scales);
   if (e == cudaSuccess) e = launch_pdl(kern, dim3((unsigned)p.work.grid, 1, 1), kThreads, smem, s, tw, tx, p);
   if (e == cudaSuccess)

@@ -11,23 +11,6 @@
 namespace mla {
 namespace {
 
-template <typename K, typename... A>
-cudaError_t launch_pdl(K kern, dim3 grid, int threads, size_t smem, cudaStream_t s, A... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3((unsigned)threads, 1, 1);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
-  if (e == cudaSuccess) note_launch();
-  return e;
-}
-
 // ======================================================================== page keys
 // key_p = mean of the cached rows of page p, in fp32, rounded once. A block takes one page: its
 // threads are (row group, VB-byte column) pairs that sum every G-th row, then the groups' sums are
@@ -134,54 +117,64 @@ __device__ __forceinline__ int tokens_seen(const PageScoreParams& p, int g) {
   return S - p.q_len + t + 1;
 }
 
-// z[g][h][pg] = softmax scale * q_lat . key; a warp per page, over all heads.
+// softmax scale * log2 e * q . key of one head and page; every lane of the warp gets it.
 template <typename AT>
-__global__ void __launch_bounds__(256) page_z_kernel(PageScoreParams p) {
+__device__ __forceinline__ float page_z(const PageScoreParams& p, const AT* q, int page, int lane) {
+  const AT* key = reinterpret_cast<const AT*>(p.page_keys) + (long long)page * p.D;
+  float acc = 0.f;
+  for (int d = lane; d < p.D; d += 32) acc = fmaf(to_f32(q[d]), to_f32(key[d]), acc);
+  return warp_sum(acc) * p.scale_log2;
+}
+
+// lse2[g][h] = log2 sum_pg m_pg 2^z (+inf without a page); a block per head, its warps take the pages in turn.
+template <typename AT>
+__global__ void __launch_bounds__(256) page_lse_kernel(PageScoreParams p) {
+  __shared__ float2 part[8];
+  const int g = blockIdx.x, h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int see = tokens_seen(p, g);
+  if (see == 0) {
+    if (threadIdx.x == 0 && h == 0 && g % p.q_len == 0 && p.seq_lens[g / p.q_len] != 0)
+      flag_status(p.status, MLA_ERR_DEVICE_GUARD);
+    return;
+  }
+  const int32_t* bt = p.block_table + (long long)(g / p.q_len) * p.max_pages;
+  const AT* q = reinterpret_cast<const AT*>(p.q_lat) + ((long long)g * p.H + h) * p.D;
+  float m = -INFINITY, l = 0.f;
+  for (int pg = warp; (long long)pg * p.P < see; pg += 8) {
+    const int page = bt[pg];
+    if (page < 0 || page >= p.num_pages) {
+      if (lane == 0) flag_status(p.status, MLA_ERR_DEVICE_GUARD);
+      continue;
+    }
+    const float z = page_z(p, q, page, lane), top = fmaxf(m, z);
+    l = (l > 0.f ? l * exp2f(m - top) : l) + exp2f(z - top) * (float)min(p.P, see - pg * p.P);
+    m = top;
+  }
+  if (lane == 0) part[warp] = make_float2(m, l);
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 0; w < 8; ++w) m = fmaxf(m, part[w].x);
+    l = 0.f;
+    for (int w = 0; w < 8; ++w)
+      if (part[w].y != 0.f) l = fmaf(part[w].y, exp2f(part[w].x - m), l);
+    p.lse2[(long long)g * p.H + h] = l == 0.f ? INFINITY : m + log2f(l);
+  }
+}
+
+// scores[g][pg] = m_pg sum_h 2^(z - lse2); a warp per page, over all heads.
+template <typename AT>
+__global__ void __launch_bounds__(256) page_mass_kernel(PageScoreParams p) {
   const int g = blockIdx.y, pg = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int see = tokens_seen(p, g);
-  if (see == 0 && blockIdx.x == 0 && threadIdx.x == 0 && g % p.q_len == 0 && p.seq_lens[g / p.q_len] != 0)
-    flag_status(p.status, MLA_ERR_DEVICE_GUARD);
   if ((long long)pg * p.P >= see) return;
   const int page = p.block_table[(long long)(g / p.q_len) * p.max_pages + pg];
-  const bool ok = page >= 0 && page < p.num_pages;
-  if (!ok && lane == 0) flag_status(p.status, MLA_ERR_DEVICE_GUARD);
-  const AT* key = reinterpret_cast<const AT*>(p.page_keys) + (long long)(ok ? page : 0) * p.D;
-  for (int h = 0; h < p.H; ++h) {
-    const AT* q = reinterpret_cast<const AT*>(p.q_lat) + ((long long)g * p.H + h) * p.D;
-    float acc = 0.f;
-    for (int d = lane; d < p.D; d += 32) acc = fmaf(to_f32(q[d]), to_f32(key[d]), acc);
-    acc = warp_sum(acc);
-    if (lane == 0) p.z[((long long)g * p.H + h) * p.max_pages + pg] = ok ? acc * p.scale_log2 : -INFINITY;
-  }
-}
-
-// lse2[g][h] = log2 sum_pg m_pg 2^z; a warp per head.
-__global__ void __launch_bounds__(256) page_lse_kernel(PageScoreParams p) {
-  const long long gh = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (gh >= (long long)p.groups * p.H) return;
-  const int see = tokens_seen(p, (int)(gh / p.H)), lane = threadIdx.x & 31;
-  const int pages = (see + p.P - 1) / p.P;
-  const float* z = p.z + gh * p.max_pages;
-  float m = -INFINITY;
-  for (int i = lane; i < pages; i += 32) m = fmaxf(m, z[i]);
-  m = warp_max(m);
-  float l = 0.f;
-  for (int i = lane; i < pages; i += 32) l += exp2f(z[i] - m) * (float)min(p.P, see - i * p.P);
-  l = warp_sum(l);
-  if (lane == 0) p.lse2[gh] = m == -INFINITY ? INFINITY : m + log2f(l);
-}
-
-// scores[g][pg] = m_pg sum_h 2^(z - lse2)
-__global__ void __launch_bounds__(128) page_mass_kernel(PageScoreParams p) {
-  const int g = blockIdx.y, pg = blockIdx.x * 128 + threadIdx.x;
-  const int see = tokens_seen(p, g);
-  if ((long long)pg * p.P >= see) return;
   float s = 0.f;
-  for (int h = 0; h < p.H; ++h) {
-    const long long gh = (long long)g * p.H + h;
-    s += exp2f(p.z[gh * p.max_pages + pg] - p.lse2[gh]);
+  if (page >= 0 && page < p.num_pages) {
+    const AT* q = reinterpret_cast<const AT*>(p.q_lat) + (long long)g * p.H * p.D;
+    for (int h = 0; h < p.H; ++h)
+      s += exp2f(page_z(p, q + (long long)h * p.D, page, lane) - p.lse2[(long long)g * p.H + h]);
   }
-  p.scores[(long long)g * p.max_pages + pg] = s * (float)min(p.P, see - pg * p.P);
+  if (lane == 0) p.scores[(long long)g * p.max_pages + pg] = s * (float)min(p.P, see - pg * p.P);
 }
 
 // ======================================================================== page selection
@@ -336,14 +329,15 @@ cudaError_t launch_page_keys(mla_dtype act, mla_dtype cache, const PageKeysParam
   return v16 && p.d_c % 512 == 0 ? page_keys_t<3, 16, bf16>(p, s) : page_keys_t<3, 4, bf16>(p, s);
 }
 
-cudaError_t launch_page_scores_simt(mla_dtype act, const PageScoreParams& p, cudaStream_t s) {
-  const dim3 zg((unsigned)((p.max_pages + 7) / 8), (unsigned)p.groups, 1);
-  if (act == MLA_F32) page_z_kernel<float><<<zg, 256, 0, s>>>(p);
-  else page_z_kernel<bf16><<<zg, 256, 0, s>>>(p);
-  page_lse_kernel<<<(unsigned)(((long long)p.groups * p.H + 7) / 8), 256, 0, s>>>(p);
-  page_mass_kernel<<<dim3((unsigned)((p.max_pages + 127) / 128), (unsigned)p.groups, 1), 128, 0, s>>>(p);
-  note_launch(3);
+template <typename AT>
+static cudaError_t page_scores_t(const PageScoreParams& p, cudaStream_t s) {
+  page_lse_kernel<AT><<<dim3((unsigned)p.groups, (unsigned)p.H, 1), 256, 0, s>>>(p);
+  page_mass_kernel<AT><<<dim3((unsigned)((p.max_pages + 7) / 8), (unsigned)p.groups, 1), 256, 0, s>>>(p);
+  note_launch(2);
   return cudaGetLastError();
+}
+cudaError_t launch_page_scores_simt(mla_dtype act, const PageScoreParams& p, cudaStream_t s) {
+  return act == MLA_F32 ? page_scores_t<float>(p, s) : page_scores_t<bf16>(p, s);
 }
 
 cudaError_t launch_select_pages(const SelectParams& p, int groups, cudaStream_t s) {

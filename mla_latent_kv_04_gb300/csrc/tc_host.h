@@ -1,4 +1,4 @@
-// Host-side helpers of the tensor-core kernels: tensor maps and the SM count.
+// Host-side helpers of the kernels: tensor maps, the SM count, launches.
 #pragma once
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -63,6 +63,26 @@ template <typename K>
 inline cudaError_t allow_smem(K kern, size_t dynamic, size_t fixed = 0) {
   if (dynamic + fixed <= 48 * 1024) return cudaSuccess;
   return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(kSmemPerCta - fixed));
+}
+
+// A launch with programmatic serialization: it may start while the kernel before it in the stream ends, and
+// waits for that one (griddepcontrol.wait) before it reads or writes.
+void note_launch(int n);
+template <typename K, typename... A>
+inline cudaError_t launch_pdl(K kern, dim3 grid, int threads, size_t smem, cudaStream_t s, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+  if (e == cudaSuccess) note_launch(1);
+  return e;
 }
 
 }  // namespace mla
