@@ -162,9 +162,15 @@ def make_config(dims, act: str = "bf16", cache: str = "bf16", cache_scale: float
 
 # ----------------------------------------------------------------------------- marshalling
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _act_dtype(cfg):
@@ -206,7 +212,7 @@ def _ptr(x, name, dtypes=None, numel=None, allow_none=False, peer=False):
             return None
         raise ValueError(f"{name} is required")
     device = x.get_device()
-    if device != _current_device():
+    if device != (_device_query or _current_device)():
         if not x.is_cuda:
             raise ValueError(f"{name} must be a CUDA tensor")
         if not peer:
@@ -258,8 +264,14 @@ def mla_absorb_weights(cfg, W_UK, W_UV, W_O, W_UK_abs, W_comb, stream=None):
         _peer_ptr(W_comb, "W_comb", a, H * d_c * d), _stream(stream)), "mla_absorb_weights")
 
 
+_i32_types = None
+
+
 def _i32(t):
-    return (_torch().int32,)
+    global _i32_types
+    if _i32_types is None:
+        _i32_types = (_torch().int32,)
+    return _i32_types
 
 
 def mla_append_cache_workspace_size(cfg, T) -> int:
@@ -649,9 +661,10 @@ def mla_mx4_bytes(cfg, K, N):
 
 
 def _mx4(cfg, K, N, codes, scales):
-    t = _torch()
-    c, s = mla_mx4_bytes(cfg, K, N)
-    return _ptr(codes, "codes", (t.uint8,), c), _ptr(scales, "scales", (t.uint8,), s)
+    # (the sizes of mla_mx4_bytes, without a call; K and N are checked by the call that follows)
+    u8 = (_torch().uint8,)
+    return (_ptr(codes, "codes", u8, N * (K // 2)),
+            _ptr(scales, "scales", u8, -(-N // 128) * -(-K // 128) * 512))
 
 
 def mla_mx4_quantize(cfg, W, codes, scales, stream=None):
