@@ -486,7 +486,7 @@ mla_status mla_page_scores_workspace_size(const mla_config* cfg, int batch, int 
  *   q_lat [batch][q_len][H][d_c + d_r] (act dtype; mla_absorb_query); page_keys from mla_page_keys;
  *   block_table, seq_lens as in mla_decode; scores [batch][q_len][max_pages] fp32.
  * fp32 sums and softmax. The tensor-core kernel takes bf16 at d_c 512, d_r 64, 64-token pages, up to 128
- * heads and max_pages up to 4096, for q_lat and page_keys that start at multiples of 16 bytes; anything else
+ * heads and max_pages up to 8192, for q_lat and page_keys that start at multiples of 16 bytes; anything else
  * takes SIMT kernels, many times slower at large sizes. A page with an id out of range scores 0, a request with seq_lens[b] < q_len or
  * above max_pages * P is left out, both with the guard; seq_lens[b] == 0 is left out. workspace: 256-byte
  * aligned device buffer of mla_page_scores_workspace_size bytes (NULL if that is 0), any contents; calls

@@ -312,7 +312,8 @@ struct PageScoreParams {
   int32_t* status;
 };
 cudaError_t launch_page_scores_simt(mla_dtype act, const PageScoreParams& p, cudaStream_t s);
-// The tensor-core form: bf16, 64-token pages, d_c 512, d_r 64, up to 128 heads and 4096 pages a request.
+// The tensor-core form: bf16, 64-token pages, d_c 512, d_r 64, up to 128 heads and 8192 pages a request (4096
+// where the GPU places no clusters of 16).
 bool page_scores_tc_supported(const mla_config* c, int num_pages, int max_pages);
 cudaError_t launch_page_scores_tc(const PageScoreParams& p, cudaStream_t s);
 

@@ -2,7 +2,7 @@
 //
 //   Z = q_lat K^T (M = heads, N = 128 pages, K = 576),  score_p = m_p sum_h 2^(c Z_hp) / L_h,
 //   L_h = sum_p m_p 2^(c Z_hp),   c = softmax scale * log2 e, m_p the tokens of page p that the query sees.
-// A cluster of up to 8 CTAs takes one query token; each CTA computes up to four tiles of 128 pages and
+// A cluster of up to 16 CTAs takes one query token; each CTA computes up to four tiles of 128 pages and
 // keeps them in tensor memory (512 columns), so that nothing but the heads' maxima and sums, which the
 // CTAs exchange through distributed shared memory, stands between the product and the scores. A head is
 // a lane of tensor memory: its maximum and sum are a thread's own; the sum over heads is a butterfly of
@@ -23,7 +23,7 @@ namespace pscore {
 
 constexpr int kD = 576, kChunks = 9, kTile = 128;
 constexpr int kTiles = 4;                      // of a CTA
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16;                // above 8: where the GPU places such a cluster
 constexpr int kChunk = 128 * 64 * 2;
 constexpr int kStages = 4;
 constexpr int kOffRing = kChunks * kChunk;     // the query first
@@ -293,9 +293,38 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 using namespace pscore;
 
+// The largest cluster that this GPU places, 8 or 16 CTAs (a GPC has to have room for one CTA an SM).
+static int largest_cluster() {
+  static int cached[64] = {0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 8;
+  if (!cached[dev]) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kMaxCluster, 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = kSmem;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = kMaxCluster;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    const bool ok =
+        cudaFuncSetAttribute(page_scores_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) == cudaSuccess &&
+        cudaFuncSetAttribute(page_scores_tc_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+        cudaOccupancyMaxActiveClusters(&n, page_scores_tc_kernel, &cfg) == cudaSuccess && n > 0;
+    if (!ok) (void)cudaGetLastError();
+    cached[dev] = ok ? kMaxCluster : 8;
+  }
+  return cached[dev];
+}
+
 bool page_scores_tc_supported(const mla_config* c, int num_pages, int max_pages) {
+  const int tiles = (max_pages + kTile - 1) / kTile;
   return c->act_dtype == MLA_BF16 && c->page_size == 64 && c->d_latent == 512 && c->d_rope == 64 &&
-         c->num_heads <= 128 && (max_pages + kTile - 1) / kTile <= kTiles * kMaxCluster && num_pages > 0;
+         c->num_heads <= 128 && num_pages > 0 &&
+         (tiles <= kTiles * 8 || (tiles <= kTiles * kMaxCluster && largest_cluster() == kMaxCluster));
 }
 
 cudaError_t launch_page_scores_tc(const PageScoreParams& p, cudaStream_t s) {
@@ -305,10 +334,16 @@ cudaError_t launch_page_scores_tc(const PageScoreParams& p, cudaStream_t s) {
     return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(page_scores_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  // as many CTAs a query as its tiles need, or as the GPU has room for
+  // as many CTAs a query as its tiles need, or as the GPU has room for; above 8 only for the need (4 requests of 32K
+  // to 128K tokens, 2 query tokens each: 15.1 us with clusters of 8, two tiles a CTA, 24.3 with 16)
   const int tiles = (p.max_pages + kTile - 1) / kTile;
   int C = 1;
-  while (C < kMaxCluster && C < tiles && (C * kTiles < tiles || (long long)p.groups * C * 2 <= device_sms())) C *= 2;
+  while (C < 8 && C < tiles && (C * kTiles < tiles || (long long)p.groups * C * 2 <= device_sms())) C *= 2;
+  if (C * kTiles < tiles) {
+    C = kMaxCluster;
+    e = cudaFuncSetAttribute(page_scores_tc_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(p.groups * C), 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);

@@ -123,10 +123,13 @@ def test_pools_past_2_31_bytes(kind):
         assert_within(keys[at.tolist()].double().cpu().numpy(), want, 2.0 ** -8 * np.abs(want) * 1.01 + 70 * 2.0 ** -24 * mag, "keys")
 
 
-def test_scores_of_the_longest_requests_that_the_tensor_cores_take():
-    """4096 pages (a cluster of eight, four tiles each), and lengths that leave CTAs without a tile."""
+@pytest.mark.parametrize("pages", [4096, 8192])
+def test_scores_of_the_longest_requests_that_the_tensor_cores_take(pages):
+    """8192 and 4096 pages (clusters of sixteen or eight, four tiles a CTA), and lengths that leave CTAs without a
+    tile."""
     rng = np.random.default_rng(4)
-    c = pg.Tables(rng, "bf16", D.dims("v2", 128), (4096 * P, 4095 * P + 1, 128 * P, 129 * P + 7, 0, 1), 4096)
+    most = pages
+    c = pg.Tables(rng, "bf16", D.dims("v2", 128), (most * P, (most - 1) * P + 1, 128 * P, 129 * P + 7, 0, 1), most)
     q_lat, keys = pg.draw_query(rng, c, 1, 1.0), pg.draw_keys(rng, c)
     got = pg.score(c, q_lat, keys)
     pg.check_scores(c, q_lat, keys, got)
