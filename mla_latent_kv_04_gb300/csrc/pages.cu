@@ -3,6 +3,7 @@
 // prologue of the decode over chosen pages.
 #include <math.h>
 
+#include "fp8_tiles.cuh"
 #include "internal.h"
 #include "prologue.cuh"
 #include "sm100_ptx.cuh"
@@ -14,20 +15,24 @@ namespace {
 // ======================================================================== page keys
 // key_p = mean of the cached rows of page p, in fp32, rounded once. A block takes one page: its
 // threads are (row group, VB-byte column) pairs that sum every G-th row, then the groups' sums are
-// added in order. Bound by memory: each row is read once.
+// added in order. Bound by memory, which reads each row once: 32 x 4096 tokens of bf16 (151 MB) in 29 us among
+// calls, 5.3 TB/s; e4m3 21 us and block scales 29, where conversions and the groups' sums add to it.
 // Kind: 0 fp32, 1 bf16, 2 e4m3, 3 block-scaled e4m3 (codes, fp32 scales, bf16 rotary part).
-constexpr int kKeyThreads = 288;               // 4 groups of a bf16 row's 72 columns, 8 of e4m3's 36
-constexpr int kKeyLoads = 8;                   // rows in flight per thread
+constexpr int kKeyThreads = 288;               // 4 groups of a bf16 row's 72 columns, 8 of e4m3's 36, 7 of 41
+// rows in flight per thread (block scales hold a scale for each as well: 4 of them take 38 us, 8 take 40, 16 65;
+// the others at 8 as fast as at 4 or 16)
+template <int kKind> constexpr int key_loads() { return kKind == 3 ? 4 : 8; }
 
 template <int VB> struct KeyVec;
 template <> struct KeyVec<16> { typedef uint4 type; };
 template <> struct KeyVec<4> { typedef uint32_t type; };
 
 template <int kKind, int VB, typename AT>
-__global__ void __launch_bounds__(kKeyThreads) page_keys_kernel(PageKeysParams p, int G) {
+__global__ void __launch_bounds__(kKeyThreads) page_keys_kernel(PageKeysParams p, int G, int stride) {
   typedef typename KeyVec<VB>::type V;
   constexpr int kWords = VB / 4, kPer = kKind == 0 ? 1 : (kKind == 1 ? 2 : 4);   // elements of a word
-  extern __shared__ float sums[];                                             // [G][D]
+  constexpr int kElems = kWords * kPer, kKeyLoads = key_loads<kKind>();
+  extern __shared__ __align__(16) float sums[];                               // [G][D], or [G][cols][stride]
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const int b = blockIdx.y, S = p.seq_lens[b], D = p.d_c + p.d_r;
@@ -50,9 +55,9 @@ __global__ void __launch_bounds__(kKeyThreads) page_keys_kernel(PageKeysParams p
   for (int c = threadIdx.x % cols; c < cols && grp < G; c += kKeyThreads) {
     const int w0 = c * kWords;
     const bool code = kKind == 2 || (kKind == 3 && w0 < code_words);
-    float acc[kWords * kPer];
+    float acc[kElems];
 #pragma unroll
-    for (int i = 0; i < kWords * kPer; ++i) acc[i] = 0.f;
+    for (int i = 0; i < kElems; ++i) acc[i] = 0.f;
     for (int r0 = grp; r0 < n; r0 += kKeyLoads * G) {
       V v[kKeyLoads];
       float sc[kKeyLoads];
@@ -77,8 +82,11 @@ __global__ void __launch_bounds__(kKeyThreads) page_keys_kernel(PageKeysParams p
             acc[2 * j] += __uint_as_float(x << 16);
             acc[2 * j + 1] += __uint_as_float(x & 0xFFFF0000u);
           } else if (code) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[4 * j + i] = fmaf(fp8_to_f32((uint8_t)(x >> (8 * i))), sc[u], acc[4 * j + i]);
+            const float2 a = e4m3x2_to_f32(x & 0xFFFFu), b = e4m3x2_to_f32(x >> 16);
+            acc[4 * j] = fmaf(a.x, sc[u], acc[4 * j]);
+            acc[4 * j + 1] = fmaf(a.y, sc[u], acc[4 * j + 1]);
+            acc[4 * j + 2] = fmaf(b.x, sc[u], acc[4 * j + 2]);
+            acc[4 * j + 3] = fmaf(b.y, sc[u], acc[4 * j + 3]);
           } else {
             acc[4 * j] += __uint_as_float(x << 16);
             acc[4 * j + 1] += __uint_as_float(x & 0xFFFF0000u);
@@ -86,25 +94,43 @@ __global__ void __launch_bounds__(kKeyThreads) page_keys_kernel(PageKeysParams p
         }
       }
     }
-    float* mine = sums + (long long)grp * D;
+    const int w = w0 - code_words - scale_words;                              // (kind 3: a rotary column's first word)
+    if (stride > 0) {
+      float* mine = sums + ((long long)grp * cols + c) * stride;
+      if constexpr (kElems >= 4) {
+        if (kKind < 3 || code) {
 #pragma unroll
-    for (int j = 0; j < kWords; ++j) {
-      const int w = w0 + j;
-      if (kKind < 3 || code) {
+          for (int i = 0; i < kElems; i += 4)
+            *reinterpret_cast<float4*>(mine + i) = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
+        } else {
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) mine[w * kPer + i] = acc[j * kPer + i];
-      } else if (w >= code_words + scale_words) {
-        const int e = p.d_c + 2 * (w - code_words - scale_words);
-        mine[e] = acc[4 * j];
-        mine[e + 1] = acc[4 * j + 1];
+          for (int j = 0; j < kWords; ++j) *reinterpret_cast<float2*>(mine + 2 * j) = make_float2(acc[4 * j], acc[4 * j + 1]);
+        }
+      }
+    } else if (kKind < 3 || code) {
+#pragma unroll
+      for (int i = 0; i < kElems; ++i) sums[(long long)grp * D + w0 * kPer + i] = acc[i];
+    } else if (w >= 0) {
+#pragma unroll
+      for (int j = 0; j < kWords; ++j) {
+        float* mine = sums + (long long)grp * D + p.d_c + 2 * (w + j);
+        mine[0] = acc[4 * j];
+        mine[1] = acc[4 * j + 1];
       }
     }
   }
   __syncthreads();
   AT* out = reinterpret_cast<AT*>(p.page_keys) + (long long)page * D;
   for (int d = threadIdx.x; d < D; d += kKeyThreads) {
+    int at = d, step = D;
+    if (stride > 0) {
+      const int half = kElems / 2 > 0 ? kElems / 2 : 1;
+      if (kKind < 3 || d < p.d_c) at = d / kElems * stride + d % kElems;
+      else at = ((code_words + scale_words) / kWords + (d - p.d_c) / half) * stride + (d - p.d_c) % half;
+      step = cols * stride;
+    }
     float s = 0.f;
-    for (int g = 0; g < G; ++g) s += sums[g * D + d];
+    for (int g = 0; g < G; ++g) s += sums[g * step + at];
     out[d] = from_f32<AT>(s * p.cache_scale / (float)n);
   }
 }
@@ -309,13 +335,17 @@ template <int kKind, int VB, typename AT>
 static cudaError_t page_keys_t(const PageKeysParams& p, cudaStream_t s) {
   const long long cols = p.row_bytes / VB;
   const int G = cols < kKeyThreads ? (int)(kKeyThreads / cols) : 1;
-  const size_t smem = (size_t)G * (p.d_c + p.d_r) * sizeof(float);
+  constexpr int kElems = kKind == 0 ? VB / 4 : (kKind == 1 ? VB / 2 : VB);
+  // Columns of 8 or 16 sums lie 4 words apart, so that a warp's 16-byte stores meet no bank twice (32 x 4096
+  // tokens with a cold L2, element by element instead: e4m3 40 us against 30, block scales 60 against 40)
+  const int stride = G > 1 && kElems >= 4 ? kElems + (kElems > 4 ? 4 : 0) : 0;
+  const size_t smem = (size_t)G * (stride > 0 ? (size_t)cols * stride : p.d_c + p.d_r) * sizeof(float);
   auto kern = page_keys_kernel<kKind, VB, AT>;
   cudaError_t e = allow_smem(kern, smem);
   if (e != cudaSuccess) return e;
   const long long touched = ((long long)p.new_tokens - 1) / p.P + 2;
   const unsigned gx = (unsigned)(touched < p.max_pages ? touched : p.max_pages);
-  return launch_pdl(kern, dim3(gx, (unsigned)p.batch, 1), kKeyThreads, smem, s, p, G);
+  return launch_pdl(kern, dim3(gx, (unsigned)p.batch, 1), kKeyThreads, smem, s, p, G, stride);
 }
 
 bool page_keys_fits(int d_c, int d_r) { return (size_t)(d_c + d_r) * 4 <= kSmemPerCta; }
