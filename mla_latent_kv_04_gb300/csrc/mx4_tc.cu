@@ -13,9 +13,13 @@
 //     exactly for elements down to 2^-13 of the largest, off by at most 2^(E - 21). Two columns a row.
 // The form of six columns reads the codes as they lie in memory. For an 8-bit MMA they are spread to 8
 // bytes in 16 of shared memory, which the TMA does at 3.5 TB/s in all; with many rows the MMAs count, and
-// six columns of 4 bits take 1.5 times two of 8. 65536 x 5120 weights, form 4 against form 8: 1 row 44
-// against 58 us, 32 rows 57 against 71, 64 rows 75 against 74, 128 rows 122 against 91, 512 rows 431 against
-// 280.
+// six columns of 4 bits take 1.5 times two of 8. 65536 x 5120 weights with a cold L2, form 4 against form 8: 1
+// row 44 against 56 us, 32 rows 50 against 61, 64 rows 74 against 67, 128 rows 124 against 83, 512 rows 519
+// against 267 (the bf16 product with the same weights: 115 to 320).
+//
+// Bound: up to 40 rows HBM (32 rows: 182 MB in 41 us among calls, the product alone 35, 5.2 TB/s), with the
+// split in front and the sum of pieces behind (6 and 4 us); many rows the MMAs, whose pipe is busy 56 percent of the
+// cycles at 512 rows x 16384 x 5120 (65 of 79 us; columns of two terms double the products).
 //
 // Work is the sequence of (128 columns, row tile, 256 or 128 of K) steps, cut into one equal range per CTA; a
 // CTA that does not have all of a tile's steps writes its fp32 sums to a piece, and a second kernel adds a
@@ -385,7 +389,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Adds a tile's pieces in the order of its steps. Block (tile, 8 rows): thread = column and four rows.
+// Adds a tile's pieces in the order of its steps. Block (tile, 8 rows): thread = column and four rows. Bound by
+// L2: pieces of 152 CTAs, 4.7 us for 32 rows x 5120 columns, 9 for 512.
 __global__ void __launch_bounds__(256) merge_kernel(const Work work, const float* __restrict__ pieces, int rows, int N,
                                                     int T, bf16* __restrict__ out) {
   const int tile = blockIdx.x, mt = tile / work.row_tiles, rt = tile % work.row_tiles;

@@ -1,4 +1,4 @@
-// Bounded mbarrier waits shared by the tensor-core kernels of the prefix and key-weight calls.
+// Bounded mbarrier waits shared by the tensor-core kernels of the prefix, key-weight, page and 4-bit calls.
 #pragma once
 #include "common.cuh"
 #include "sm100_ptx.cuh"
