@@ -22,8 +22,9 @@
 // the token's scale in registers, and a P of its own, times that scale, in O^T.
 //
 // Bound: the load, product, softmax, product chain of a tile, whose rows fill shared memory (bf16: 2.9 us a
-// tile); e4m3: the MMAs, N = 64 columns of which take as long as 128 would. 32 queries of 64 pages, 128 heads, a
-// cold L2: bf16 75 us (151 MB; this kernel 55), e4m3 61, block scales 99. 64 x 2 queries of 96 pages, e4m3: 188.
+// tile); e4m3: 3550 cycles a tile, of which its MMAs take 3000 (64 columns as long as 128 would) and the way from
+// scores to P as long. 32 queries of 64 pages, 128 heads, a cold L2: bf16 75 us (151 MB; this kernel 55), e4m3 60,
+// block scales 99. 64 x 2 queries of 96 pages, e4m3: 185.
 #include <math.h>
 
 #include "fp8_tiles.cuh"
@@ -427,11 +428,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         // P: rows of tokens, heads contiguous, and whether a score exceeds its reference by too much.
         // bf16: over the rotary keys (their product is done); fp8: the products with the tile before's have to be
-        if (kFp8 && tile > 0 && !(ok = wait_w(B_PDONE, (tile - 1) & 1))) break;
+        // (e4m3: once the terms are formed, 173 -> 169 us at 64 x 2 queries of 96 pages)
+        if (kFmt == kB128 && tile > 0 && !(ok = wait_w(B_PDONE, (tile - 1) & 1))) break;
         float now[16];                         // the sums with this tile
         auto weights = [&]() {
           float most = -INFINITY;
           uint8_t* prow = basep + L::kP;
+          uint32_t terms[2][4];                // e4m3: both terms of P
 #pragma unroll
           for (int j = 0; j < 16; j += 8) {
             float e[8];
@@ -443,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               now[j + k] = sum[j + k] + e[k];
             }
             const int hb = hp + j;             // first head of the eight
-            if (!heads) break;
+            if (kFmt != kE4m3 && !heads) break;
             if constexpr (kFmt == kBf16) {
               uint4 o;
               o.x = pack_bf16(e[0], e[1]);
@@ -466,9 +469,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                   hi[k >> 1] |= c << (16 * (k & 1));
                   lo[k >> 1] |= d << (16 * (k & 1));
                 }
-                *reinterpret_cast<uint2*>(prow + m * kChunk + at) = make_uint2(hi[0], hi[1]);
-                *reinterpret_cast<uint2*>(prow + m * kChunk + 8192 + at) = make_uint2(lo[0], lo[1]);
+                if (kFmt == kB128) {
+                  *reinterpret_cast<uint2*>(prow + m * kChunk + at) = make_uint2(hi[0], hi[1]);
+                  *reinterpret_cast<uint2*>(prow + m * kChunk + 8192 + at) = make_uint2(lo[0], lo[1]);
+                } else {
+#pragma unroll
+                  for (int k = 0; k < 2; ++k) {
+                    terms[0][j / 4 + k] = hi[k];
+                    terms[1][j / 4 + k] = lo[k];
+                  }
+                }
               }
+            }
+          }
+          if constexpr (kFmt == kE4m3) {
+            if (tile > 0) ok = wait_w(B_PDONE, (tile - 1) & 1);
+            if (ok && heads) {
+              uint8_t* at = prow + tok * 64 + (((hp >> 4) ^ ((tok >> 1) & 3)) << 4);
+              *reinterpret_cast<uint4*>(at) = make_uint4(terms[0][0], terms[0][1], terms[0][2], terms[0][3]);
+              *reinterpret_cast<uint4*>(at + 8192) = make_uint4(terms[1][0], terms[1][1], terms[1][2], terms[1][3]);
             }
           }
           return heads && live && most + top_scale > kGrow;
@@ -542,6 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (again) renew();
             if (!ok) break;
             const bool over = weights();
+            if (!ok) break;
             if (!again && __any_sync(0xffffffffu, over) && lane == 0) grown[tile & 1] = (int)tile;
             hand_over(again && !first ? B_PAGAIN : B_PFULL);
             if (again) break;
