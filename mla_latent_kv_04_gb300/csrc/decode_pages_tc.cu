@@ -21,10 +21,10 @@
 // bits, as bf16 has. Block-scaled rows: each block of 128 dims has a product of its own in S^T, added under
 // the token's scale in registers, and a P of its own, times that scale, in O^T.
 //
-// Bound: the load, product, softmax, product chain of a tile, whose rows fill shared memory (bf16: 2.9 us a
+// Bound: the load, product, softmax, product chain of a tile, whose rows fill shared memory (bf16: 2.6 us a
 // tile); e4m3: 3550 cycles a tile, of which its MMAs take 3000 (64 columns as long as 128 would) and the way from
-// scores to P as long. 32 queries of 64 pages, 128 heads, a cold L2: bf16 75 us (151 MB; this kernel 55), e4m3 60,
-// block scales 99. 64 x 2 queries of 96 pages, e4m3: 185.
+// scores to P as long. 32 queries of 64 pages, 128 heads, X
+// block scales 95. 64 x 2 queries of 96 pages, e4m3: 184.
 #include <math.h>
 
 #include "fp8_tiles.cuh"
@@ -61,7 +61,8 @@ template <int kFmt> struct Layout {
   static constexpr int kAlpha = kRope + F::kRope + F::kP;                  // [64] rescaling factors
   static constexpr int kHead = kAlpha + 256;                               // [64] factors of the fp8 query
   static constexpr int kWarp = kHead + 256;                                // [4][64] of the four token quarters
-  static constexpr int kBar = kWarp + 1024;
+  static constexpr int kRef = kWarp + 1024;                                // [64] references
+  static constexpr int kBar = kRef + 256;
   static constexpr int kSmem = kBar + 256 + 1024;
   static_assert(kSmem <= 232448, "dynamic shared memory per CTA");
 };
@@ -314,6 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* alpha = reinterpret_cast<float*>(basep + L::kAlpha);
     float* head = reinterpret_cast<float*>(basep + L::kHead);
     float* quarter = reinterpret_cast<float*>(basep + L::kWarp);         // [4][64]
+    float* ref = reinterpret_cast<float*>(basep + L::kRef);              // [64] (from registers, which spilled, bf16 took 75 us, not 71)
     uint32_t s_seq = 0, tile = 0, meets = 0, c_seq = 0;
     bool ok = true;
     auto meet = [&]() {                        // the sixteen warps (bounded, unlike a named barrier)
@@ -364,12 +366,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) ptx::mbar_arrive(bar(B_QFULL));
       }
       if (kFp8 && !(ok = wait_w(B_QFULL, (uint32_t)(it - it0) & 1))) break;
-      float sum[16], r[16];                    // sums and references of this thread's heads
+      float sum[16];                           // of this thread's heads
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        sum[j] = 0.f;
-        r[j] = -INFINITY;
-      }
+      for (int j = 0; j < 16; ++j) sum[j] = 0.f;
       for (int pg = 2 * item.page_begin; ok && pg < 2 * item.page_end; pg += 2, ++tile, c_seq += F::kChunks) {
         const int left = min(kTok, item.kv - pg * 64);                   // tokens of this tile
         const bool first = pg == 2 * item.page_begin;
@@ -438,9 +437,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int j = 0; j < 16; j += 8) {
             float e[8];
+            const float4 r0 = *reinterpret_cast<const float4*>(ref + hp + j);
+            const float4 r1 = *reinterpret_cast<const float4*>(ref + hp + j + 4);
+            const float r[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-              const float d = s[j + k] - r[j + k];
+              const float d = s[j + k] - r[k];
               most = fmaxf(most, d);
               e[k] = live ? ptx::ex2(d) : 0.f;
               now[j + k] = sum[j + k] + e[k];
@@ -521,17 +523,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float4 w = *reinterpret_cast<const float4*>(quarter + 192 + hp + j);
             const float top[4] = {fmaxf(fmaxf(x.x, y.x), fmaxf(z.x, w.x)), fmaxf(fmaxf(x.y, y.y), fmaxf(z.y, w.y)),
                                   fmaxf(fmaxf(x.z, y.z), fmaxf(z.z, w.z)), fmaxf(fmaxf(x.w, y.w), fmaxf(z.w, w.w))};
+            float4 next = make_float4(top[0] - less, top[1] - less, top[2] - less, top[3] - less);
+            if (!first) {
+              const float4 r = *reinterpret_cast<const float4*>(ref + hp + j);
+              next = make_float4(fmaxf(r.x, next.x), fmaxf(r.y, next.y), fmaxf(r.z, next.z), fmaxf(r.w, next.w));
+              const float a[4] = {ptx::ex2(r.x - next.x), ptx::ex2(r.y - next.y), ptx::ex2(r.z - next.z),
+                                  ptx::ex2(r.w - next.w)};
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float next = fmaxf(r[j + k], top[k] - less);
-              const float a = r[j + k] == -INFINITY ? 0.f : ptx::ex2(r[j + k] - next);
-              r[j + k] = next;
-              sum[j + k] *= a;
-              if (!first && heads && lane == 0 && quad == 0) alpha[hp + j + k] = a;
+              for (int k = 0; k < 4; ++k) sum[j + k] *= a[k];
+              if (heads && lane == 0 && quad == 0)
+                *reinterpret_cast<float4*>(alpha + hp + j) = make_float4(a[0], a[1], a[2], a[3]);
+            } else if (heads && lane == 0) {   // (the four warps of these heads write the same)
+              *reinterpret_cast<float4*>(ref + hp + j) = next;
             }
           }
+          __syncwarp();
           if (!first) {                        // O of the tiles before
-            if (!(ok = meet() && wait_w(B_PDONE, (tile - 1) & 1))) return;
+            if (!(ok = meet())) return;
+            if (heads && lane < 16) {          // (all have read the old ones; the same from each of the four warps)
+              const float* x = quarter + hp + lane;
+              ref[hp + lane] = fmaxf(ref[hp + lane], fmaxf(fmaxf(x[0], x[64]), fmaxf(x[128], x[192])) - less);
+            }
+            __syncwarp();
+            if (!(ok = wait_w(B_PDONE, (tile - 1) & 1))) return;
             ptx::tc_fence_after();
 #pragma unroll 1
             for (int h = 0; h < N; h += 16) {              // this warp's dims tile
@@ -552,9 +566,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(bar(b));
         };
-        // An item's first tile has no reference to try. fp8: one place for the code of both passes (its
-        // registers: 226 -> 205 us at 64 x 2 queries of 96 pages; bf16, where they suffice, 73 -> 77).
-        if constexpr (kFp8) {
+        // An item's first tile has no reference to try. e4m3: one place for the code of both passes (as fast as two,
+        // in half the code; bf16 71 us from two places, 73 from one, block scales 95 and 101: 32 queries of 64 pages).
+        if constexpr (kFmt == kE4m3) {
           bool again = first;
 #pragma unroll 1
           while (true) {
@@ -596,10 +610,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float* q = quarter + hp + lane;
         const float total = (q[0] + q[64]) + (q[128] + q[192]);
         alpha[hp + lane] = p.out_scale / total;
-        float own = r[0];                      // this lane's head's reference
-#pragma unroll
-        for (int j = 1; j < 16; ++j) own = lane == j ? r[j] : own;
-        const float lse = (own + log2f(total)) * kLn2;
+        const float lse = (ref[hp + lane] + log2f(total)) * kLn2;
         const int h = h0 + hp + lane;
         if (item.single) p.lse[g * p.H + h] = lse;
         else p.part_lse[(long long)it * p.H + h] = lse;
