@@ -23,8 +23,8 @@
 //
 // Bound: the load, product, softmax, product chain of a tile, whose rows fill shared memory (bf16: 2.6 us a
 // tile); e4m3: 3550 cycles a tile, of which its MMAs take 3000 (64 columns as long as 128 would) and the way from
-// scores to P as long. 32 queries of 64 pages, 128 heads, X
-// block scales 95. 64 x 2 queries of 96 pages, e4m3: 184.
+// scores to P as long. 32 queries of 64 pages, 128 heads, a cold L2: bf16 71 us (151 MB), e4m3 60, block scales 95.
+// 64 x 2 queries of 96 pages, e4m3: 184.
 #include <math.h>
 
 #include "fp8_tiles.cuh"
