@@ -75,11 +75,24 @@ __device__ __forceinline__ int last_at_most(const int* a, int n, long long x) {
 }
 
 // Tokens of the pages on group g's list, of `see` that the query sees: every page but the last one of
-// an ascending list is full.
-__device__ __forceinline__ int listed_tokens(const PlanParams& p, int g, int see) {
+// an ascending list is full. `last` is the list's last entry, loaded along with the length.
+__device__ __forceinline__ int listed_tokens(const PlanParams& p, int g, int see, int last) {
   const int32_t* list = p.pages + (long long)g * p.budget;
-  // the first negative entry: seven probes at a time, whose loads are in flight together
   int lo = 0, hi = p.budget;
+  if (last >= 0) {
+    lo = hi;
+  } else {
+    // a list of all that the query sees, or the first negative entry: seven probes at a time, whose loads are
+    // in flight together
+    const int seen = min(p.budget - 1, (see - 1) / p.page_size + 1);
+    if (seen > 0) {
+      const int a = list[seen - 1], b = list[seen];
+      if (a >= 0 && b < 0) {
+        last = a;
+        lo = hi = seen;
+      }
+    }
+  }
   while (lo < hi) {
     const int step = (hi - lo + 7) / 8;
     int full = 0;
@@ -92,7 +105,8 @@ __device__ __forceinline__ int listed_tokens(const PlanParams& p, int g, int see
     hi = min(hi, lo + (full == 7 ? step : step - 1));
   }
   if (lo == 0) return 0;
-  const long long tail = (long long)see - (long long)list[lo - 1] * p.page_size;
+  if (last < 0) last = list[lo - 1];
+  const long long tail = (long long)see - (long long)last * p.page_size;
   return (lo - 1) * p.page_size + (int)max(1LL, min((long long)p.page_size, tail));
 }
 
@@ -116,13 +130,14 @@ __device__ inline void plan_body(const PlanParams& p, int* sm, bool reset_status
   for (int g = tid; g < groups; g += nt) {
     const int b = g / p.q_len, t = g % p.q_len;
     const int S = p.seq_lens[b];
+    const int last = p.pages ? p.pages[(long long)g * p.budget + p.budget - 1] : 0;
     int kv = 0;
     if (S != 0) {
       if (S < p.q_len || (long long)S > (long long)p.max_pages * p.page_size) {
         if (t == 0) flag_status(p.status, MLA_ERR_DEVICE_GUARD);
       } else {
         kv = S - p.q_len + t + 1;
-        if (p.pages) kv = listed_tokens(p, g, kv);
+        if (p.pages) kv = listed_tokens(p, g, kv, last);
       }
     }
     p.group_kv[g] = kv;
