@@ -519,15 +519,6 @@ __device__ void softmax_epilogue(const Shared& sh, const DecodeParams& p, uint32
         xa[4 * c] = a.x; xa[4 * c + 1] = a.y; xa[4 * c + 2] = a.z; xa[4 * c + 3] = a.w;
         xb[4 * c] = b.x; xb[4 * c + 1] = b.y; xb[4 * c + 2] = b.z; xb[4 * c + 3] = b.w;
       }
-      // every lane's buffer reads have returned before the buffers are released
-      uint32_t dep = 0;
-#pragma unroll
-      for (int i = 0; i < 16; i += 4) dep ^= xa[i] ^ xb[i];
-      const uint32_t all = __ballot_sync(0xffffffffu, dep != 0x7fc00001u);
-      if (lane == 0) {
-        ptx::mbar_arrive_remote_relaxed(peer_xempty0 + 8 * xj, all);
-        ptx::mbar_arrive(sh.bar(B_STGFREE0 + xj));
-      }
     }
     // Columns past the last token: both partials arrive as 0; make the peer's -inf so the
     // column gets P = 0. Their c_kv rows may hold anything, NaN included, and 0 * NaN would
@@ -574,7 +565,15 @@ __device__ void softmax_epilogue(const Shared& sh, const DecodeParams& p, uint32
       mine = fmaxf(f.x, f.y);
       slot[half * 128 + row] = mine;
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(sh.bar(B_RED0 + 2 * quarter + j));
+      // The buffers are released here because the store above needs the maximum, and that needs every word read
+      // from them (whose column has a token): a relaxed arrive by itself may overtake the reads. It did, when
+      // it only carried a value made of them that nothing used: with 2100 requests of 1 to 4 pages, a warp that was held
+      // up between the two read rows of the page after next, in 1 call of 130.
+      if (lane == 0) {
+        ptx::mbar_arrive(sh.bar(B_RED0 + 2 * quarter + j));
+        ptx::mbar_arrive_remote_relaxed(peer_xempty0 + 8 * xj);
+        ptx::mbar_arrive(sh.bar(B_STGFREE0 + xj));
+      }
     }
     // P and its row sum against reference value m_ref
     uint32_t packed[16];

@@ -260,7 +260,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ptx::tmem_wait_ld();
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive_remote_relaxed(free0 + 8 * (z & 1), 0u);   // (only tensor memory was read)
+        if (lane == 0) ptx::mbar_arrive_remote_relaxed(free0 + 8 * (z & 1));   // (only tensor memory was read)
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           if (lane == 0) ptx::bulk_wait_read_le1();    // this buffer's last store has read it
@@ -338,7 +338,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       ptx::tmem_wait_st();
       ptx::tc_fence_before();
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive_remote_relaxed(full, 0u);      // (only tensor memory was written)
+      if (lane == 0) ptx::mbar_arrive_remote_relaxed(full);      // (only tensor memory was written)
       ++n;
     }
   }

@@ -333,7 +333,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads2, 1)
           if (i == kTiles - 1 && q == 3) {
             ptx::tc_fence_before();
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive_remote_relaxed(free0 + 8 * b, 0u);
+            if (lane == 0) ptx::mbar_arrive_remote_relaxed(free0 + 8 * b);
           }
           if (r >= w.rows) continue;
           if (!full) {

@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // the pair's need no release: one at cluster scope waits out the thread's memory traffic
     // first (it cost 1.1 us of every block).
     auto arrive = [&](uint32_t b) {
-      if (kPair) ptx::mbar_arrive_remote_relaxed(b, 0u);
+      if (kPair) ptx::mbar_arrive_remote_relaxed(b);
       else ptx::mbar_arrive(b);
     };
     uint32_t g = 0, x = 0, s = 0;                  // blocks, exchanges and segments so far

@@ -26,14 +26,11 @@ __device__ __forceinline__ void mbar_arrive_expect_tx(uint32_t bar, uint32_t byt
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
                : "memory");
 }
-// Relaxed arrive on another CTA's mbarrier. `dep` must be computed from every value whose
-// read has to complete first: the instruction reads it, so in-order issue cannot send the
-// arrive before those reads returned.
-__device__ __forceinline__ void mbar_arrive_remote_relaxed(uint32_t remote_bar, uint32_t dep) {
-  asm volatile(
-      "{\n\t.reg .b32 d;\n\tmov.b32 d, %1;\n\t"
-      "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n\t}"
-      ::"r"(remote_bar), "r"(dep) : "memory");
+// Relaxed arrive on another CTA's mbarrier: it orders nothing. Reads of shared memory that have to
+// be complete first must decide whether it is executed (a branch on their values); tensor-memory loads
+// and stores are waited for.
+__device__ __forceinline__ void mbar_arrive_remote_relaxed(uint32_t remote_bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote_bar) : "memory");
 }
 __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
   uint32_t ok;
