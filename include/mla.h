@@ -527,8 +527,11 @@ mla_status mla_decode_pages_workspace_size(const mla_config* cfg, int batch, int
  * d_latent above 512, batch * q_len above 8192. The tensor-core kernel takes bf16 activations at d_c 512, d_r
  * 64, 64-token pages, any cache format and a multiple of 16 heads up to 1024, for a q_lat and cache that start
  * at multiples of 16 bytes; anything else takes the SIMT kernel, and a cache that does not start at a multiple
- * of 4 bytes is refused. Scores and LSE are fp32 results; the softmax's weights are rounded to bf16 (fp8 caches:
- * to two e4m3 terms, 8 significant bits) for the product with the latents. */
+ * of 4 bytes is refused. Scores and LSE are fp32 results; the softmax's weights are rounded to bf16 for the
+ * product with the latents. On the tensor cores an fp8 cache's are two e4m3 terms under a power of two per head and
+ * 32 tokens of a page (block scales: the weights times the tokens' scales, per 128 dims): off by 2^-9 of
+ * themselves, or by 2^-21 of the largest of the 32 (of the largest weight times the largest scale) where that is
+ * more. */
 mla_status mla_decode_pages(const mla_config* cfg, const void* q_lat, const void* cache, int num_pages,
                             const int32_t* block_table, int max_pages, const int32_t* seq_lens, int batch,
                             int q_len, const int32_t* pages, int budget, void* out_latent, float* lse,

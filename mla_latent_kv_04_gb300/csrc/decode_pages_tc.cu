@@ -17,14 +17,19 @@
 // bf16 cache: the staged rows are both products' operands (K-major rows of S^T, dims-major columns of O^T);
 // P is rounded to bf16 and takes the place of the tile's rotary keys, which S^T has used up.
 // fp8 caches: the codes themselves are the operands (kind::f8f6f4). The query is the sum of two e4m3 terms
-// under a power of two per head (two columns of S^T, split4), and so is P (two products): 8 significant
-// bits, as bf16 has. Block-scaled rows: each block of 128 dims has a product of its own in S^T, added under
-// the token's scale in registers, and a P of its own, times that scale, in O^T.
+// under a power of two per head (two columns of S^T, split4). So is P, under a power of two per head and 32
+// tokens (kind::mxf8f6f4, which applies it): y = hi + lo / 16, the largest y of the 32 between 2^7 and 2^8.5, so a
+// weight is off by 2^-9 of itself or 2^-21 of the largest of the 32, whatever came before it. Under one power of two for the
+// whole list, what lay 2^-14 below the largest weight was lost: a heavy first token in front of 6000 others had them
+// as 0. Such a P has no reference to try either: the sums' and scales' own moves when one exceeds it by 2^64.
+// Block-scaled rows: each block of 128 dims has a product of its own in S^T, added under the token's scale in
+// registers, and a P of its own, times that scale, in O^T; the 32 tokens' power of two covers the largest weight and
+// the largest scale.
 //
 // Bound: the load, product, softmax, product chain of a tile, whose rows fill shared memory (bf16: 2.6 us a
-// tile); e4m3: 3550 cycles a tile, of which its MMAs take 3000 (64 columns as long as 128 would) and the way from
-// scores to P as long. 32 queries of 64 pages, 128 heads, a cold L2: bf16 71 us (151 MB), e4m3 60, block scales 95.
-// 64 x 2 queries of 96 pages, e4m3: 184.
+// tile); e4m3: the MMAs (64 columns as long as 128 would) and, as long again, the way from scores to P. 32
+// queries of 64 pages, 128 heads, a cold L2: bf16 71 us (151 MB), e4m3 63, block scales 105. 64 x 2 queries of 96
+// pages, e4m3: 194. (Under one power of two for the list, without the maxima of every 32 tokens: 59, 93 and 181.)
 #include <math.h>
 
 #include "fp8_tiles.cuh"
@@ -40,17 +45,18 @@ enum { kBf16 = 0, kE4m3 = 1, kB128 = 2 };
 constexpr int kTok = 128;
 constexpr int kChunk = kTok * 128;             // 128 bytes of 128 rows
 constexpr int kThreads = 576;                  // producer, MMA issuer, 16 softmax warps
-constexpr float kGrow = 8.75f;                 // how far scores may exceed the reference (log2; e4m3 ends at 448)
+constexpr float kGrow = 8.75f;                 // how far scores may exceed the reference (log2)
+constexpr float kGrow8 = 64.f;                 // fp8: and scales of P, which fp32 sums hold by themselves
 
 template <int kFmt> struct Fmt;
-template <> struct Fmt<kBf16> {                // latent chunks of a tile, chunk buffers, bytes of the regions
-  static constexpr int kChunks = 8, kBufs = 8, kQ = 9 * 8192, kRope = kChunk, kP = 0;
+template <> struct Fmt<kBf16> {                // latent chunks of a tile, chunk buffers, bytes of the regions, score buffers
+  static constexpr int kChunks = 8, kBufs = 8, kQ = 9 * 8192, kRope = kChunk, kP = 0, kAtoms = 0, kSBufs = 2;
 };
 template <> struct Fmt<kE4m3> {
-  static constexpr int kChunks = 4, kBufs = 8, kQ = 4 * kChunk + 8192, kRope = 8192, kP = kChunk;
+  static constexpr int kChunks = 4, kBufs = 8, kQ = 4 * kChunk + 8192, kRope = 8192, kP = kChunk, kAtoms = 1, kSBufs = 1;
 };
 template <> struct Fmt<kB128> {
-  static constexpr int kChunks = 4, kBufs = 4, kQ = 4 * kChunk + 8192, kRope = kChunk, kP = 4 * kChunk;
+  static constexpr int kChunks = 4, kBufs = 4, kQ = 4 * kChunk + 8192, kRope = kChunk, kP = 4 * kChunk, kAtoms = 6, kSBufs = 2;
 };
 
 template <int kFmt> struct Layout {
@@ -63,8 +69,11 @@ template <int kFmt> struct Layout {
   static constexpr int kWarp = kHead + 256;                                // [4][64] of the four token quarters
   static constexpr int kRef = kWarp + 1024;                                // [64] references
   static constexpr int kBar = kRef + 256;
-  static constexpr int kSmem = kBar + 256 + 1024;
-  static_assert(kSmem <= 232448, "dynamic shared memory per CTA");
+  static constexpr int kSf = kBar + 256;                                   // scale atoms of P (fp8), then constant ones
+  static constexpr int kUsed = kSf + F::kAtoms * 512;
+  // what rounding the base up to 1024 may take; e4m3 has no room for it (a base off that is refused)
+  static constexpr int kSmem = kUsed + 1024 <= 232448 ? kUsed + 1024 : 232448;
+  static_assert(kUsed <= kSmem, "dynamic shared memory per CTA");
 };
 
 enum { B_CFULL = 0, B_CFREE = 8, B_RFULL = 16, B_RFREE, B_QFULL, B_QFREE, B_SFULL, B_SFREE = B_SFULL + 2,
@@ -79,6 +88,20 @@ struct Maps {
 constexpr uint32_t idesc_e4m3(int N, bool a_mn, bool b_mn) {
   return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | (8u << 24);
 }
+
+// kind::mxf8f6f4, e4m3 A and B in the order of their MN dimensions, scales as powers of two; the scale byte of
+// a step of 32 tokens is its own (kIdescByte further).
+constexpr uint32_t idesc_mx_e4m3(int N) {
+  return (1u << 15) | (1u << 16) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | (1u << 27);
+}
+constexpr uint32_t kIdescByte = (1u << 4) | (1u << 29);
+
+// 2^x of a whole x, 0 below 2^-126.
+__device__ __forceinline__ float pow2(float x) {
+  return __uint_as_float((uint32_t)((int)fminf(fmaxf(x, -127.f), 127.f) + 127) << 23);
+}
+// The byte of a scale 2^x, at the ends of its range the end.
+__device__ __forceinline__ uint8_t scale_byte(float x) { return (uint8_t)((int)fminf(fmaxf(x, -127.f), 127.f) + 127); }
 
 // Sums over the warp's lanes of 16 columns: lanes j and j + 16 are left with column j.
 __device__ __forceinline__ float column_sums(float (&v)[16], int lane) {
@@ -108,9 +131,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   typedef Fmt<kFmt> F;
   typedef Layout<kFmt> L;
   constexpr bool kFp8 = kFmt != kBf16;
-  extern __shared__ uint8_t smem_raw[];
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t raw = ptx::smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
+  if (base - raw + L::kUsed > L::kSmem) {
+    ptx::griddep_wait();
+    if (threadIdx.x == 0) flag_status(p.status, MLA_ERR_CUDA);
+    return;
+  }
   uint8_t* basep = smem_raw + (base - raw);
   volatile int* abort = reinterpret_cast<volatile int*>(basep + L::kBar + 240);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(basep + L::kBar + 244);
@@ -132,11 +160,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::tmem_alloc(ptx::smem_u32(tmem_slot), 512);
     ptx::tmem_relinquish();
   }
+  if constexpr (kFmt == kB128) {               // scales of 1 and of 1 / 16
+    if (threadIdx.x < 256)
+      reinterpret_cast<uint32_t*>(basep + L::kSf + 4 * 512)[threadIdx.x] = threadIdx.x < 128 ? 0x7F7F7F7Fu : 0x7B7B7B7Bu;
+    ptx::fence_proxy_async_smem();
+  }
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
-  const uint32_t t_o = tmem, t_s = tmem + 256;                                       // O: 4 x 64 columns; S: 2 x 128
+  // O: 4 x 64 columns; S: 2 x 128. P's scales (of A, for the terms' 1 and 1 / 16, then of B): e4m3, which has one S
+  // buffer, behind it; block scales in an S buffer, between a tile's scores and the next tile's
+  const uint32_t t_o = tmem, t_s = tmem + 256, t_sf = tmem + 384;
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();                         // the plan and the lists' pages
   auto wait = [&](int i, uint32_t parity) { return bounded_wait(bar(i), parity, abort, p.status); };
@@ -208,7 +243,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t kQStep = kFp8 ? kChunk : 8192;      // bytes of a chunk's query rows
     const uint32_t id_s = kFp8 ? idesc_e4m3(2 * N, false, false) : ptx::idesc_bf16_f32(128, N, false, false);
     const uint32_t id_r = kFmt == kB128 ? ptx::idesc_bf16_f32(128, N, false, false) : id_s;
-    const uint32_t id_o = kFp8 ? idesc_e4m3(N, true, true) : ptx::idesc_bf16_f32(128, N, true, true);
+    const uint32_t id_o = kFp8 ? idesc_mx_e4m3(N) : ptx::idesc_bf16_f32(128, N, true, true);
+    const uint64_t sf_d = ptx::smem_desc(base + L::kSf, 0, 128, ptx::kSwizzleNone);
     const uint64_t q_d = ptx::smem_desc(base, 16, 1024, ptx::kSwizzle128);
     const uint64_t x_d = ptx::smem_desc(base + L::kRing, 16, 1024, ptx::kSwizzle128);
     constexpr uint32_t kRopeSw = kFmt == kE4m3 ? (uint32_t)ptx::kSwizzle64 : (uint32_t)ptx::kSwizzle128;
@@ -223,8 +259,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     auto product_s = [&](bool last) {
       for (int c = 0; ok && c < F::kChunks; ++c, ++c_seq) {
-        const uint32_t st = c_seq % F::kBufs, sb = s_seq & 1;
-        if (c == 0 || kFmt == kB128) ok = wait_w(B_SFREE + sb, ((s_seq >> 1) & 1) ^ 1);
+        const uint32_t st = c_seq % F::kBufs, sb = s_seq % F::kSBufs;
+        if (c == 0 || kFmt == kB128) ok = wait_w(B_SFREE + sb, ((s_seq / F::kSBufs) & 1) ^ 1);
+        // (the buffer that held the scales of the tile before)
+        if (ok && kFmt == kB128 && c == 1 && o_tile > 0) ok = wait_w(B_PDONE, (o_tile - 1) & 1);
         if (!ok || !(ok = wait_w(B_CFULL + st, (c_seq / F::kBufs) & 1))) return;
         ptx::tc_fence_after();
         if (ptx::elect_one()) {
@@ -240,8 +278,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (kFmt == kB128) ++s_seq;
       }
-      const uint32_t sb = s_seq & 1;
-      if (kFmt == kB128) ok = wait_w(B_SFREE + sb, ((s_seq >> 1) & 1) ^ 1);
+      const uint32_t sb = s_seq % F::kSBufs;
+      if (kFmt == kB128) ok = wait_w(B_SFREE + sb, ((s_seq / F::kSBufs) & 1) ^ 1);
       if (!ok || !(ok = wait_w(B_RFULL, s_tile & 1))) return;
       ptx::tc_fence_after();
       if (ptx::elect_one()) {
@@ -271,8 +309,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (i > 0 && grown[o_tile & 1] == (int)o_tile && !(ok = wait_w(B_PAGAIN, again++ & 1))) break;
         if (i == 0 && !(ok = wait_w(B_OFREE, (q_seq & 1) ^ 1))) break;
         ptx::tc_fence_after();
+        const uint32_t sf = kFmt == kB128 ? t_s + 128 * ((s_seq + 1) & 1) : t_sf;
         if (ptx::elect_one()) {
           const uint32_t acc0 = i ? 1u : 0u;
+          if constexpr (kFmt == kE4m3) {
+            ptx::tmem_cp_scales(sf + 8, sf_d);
+          } else if constexpr (kFmt == kB128) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) ptx::tmem_cp_scales(sf + 4 * k, sf_d + 32 * (4 + k));
+#pragma unroll
+            for (int m = 0; m < 4; ++m) ptx::tmem_cp_scales(sf + 8 + 4 * m, sf_d + 32 * m);
+          }
 #pragma unroll
           for (int m = 0; m < 4; ++m) {
             const uint32_t st = o_seq % F::kBufs;
@@ -286,10 +333,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               o_seq += 2;
             } else {
               const uint64_t pm = p_d + (kFmt == kB128 ? m * (kChunk >> 4) : 0);
+              const uint32_t sfb = sf + 8 + (kFmt == kB128 ? 4 * m : 0);
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
-                ptx::mma_e4m3_ss(t_o + 64 * m, a + 256 * k, pm + 128 * k, id_o, k ? 1u : acc0);
-                ptx::mma_e4m3_ss(t_o + 64 * m, a + 256 * k, pm + (8192 >> 4) + 128 * k, id_o, 1u);
+                ptx::mma_mx8_ss(t_o + 64 * m, a + 256 * k, pm + 128 * k, id_o + k * kIdescByte, sf, sfb, k ? 1u : acc0);
+                ptx::mma_mx8_ss(t_o + 64 * m, a + 256 * k, pm + (8192 >> 4) + 128 * k, id_o + k * kIdescByte, sf + 4, sfb, 1u);
               }
               ptx::mma_commit(bar(B_CFREE + st));
               o_seq += 1;
@@ -318,6 +366,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* ref = reinterpret_cast<float*>(basep + L::kRef);              // [64] (from registers, which spilled, bf16 took 75 us, not 71)
     uint32_t s_seq = 0, tile = 0, meets = 0, c_seq = 0;
     bool ok = true;
+    uint8_t* scale = basep + L::kSf + ((hp + lane) & 31) * 16 + ((hp + lane) >> 5) * 4 + quad;   // (lanes 0 .. 15)
+    if constexpr (kFmt == kE4m3) {             // P's terms count 1 and 1 / 16 (four words of each; the rest is not read)
+      if (part == 0) {
+        uint32_t v[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) v[k] = k < 4 ? 0x7F7F7F7Fu : 0x7B7B7B7Bu;
+        ptx::tmem_st16(t_sf + lane_off, v);
+        ptx::tmem_wait_st();
+        ptx::tc_fence_before();
+        __syncwarp();
+      }
+    }
     auto meet = [&]() {                        // the sixteen warps (bounded, unlike a named barrier)
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(bar(B_MEET));
@@ -374,7 +434,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool first = pg == 2 * item.page_begin;
         const bool live = tok < left;
         float4 sc = make_float4(0.f, 0.f, 0.f, 0.f);
-        float top_scale = 0.f;                 // log2 of the token's largest scale
         if constexpr (kFmt == kB128) {
           if (live) {
             int page = p.block_table[g * p.max_pages + pg + (tok >> 6)];
@@ -382,14 +441,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             sc = *reinterpret_cast<const float4*>(reinterpret_cast<const uint8_t*>(p.cache) +
                                                   ((long long)page * 64 + (tok & 63)) * p.row_bytes + 512);
           }
-          top_scale = log2f(fmaxf(fmaxf(fmaxf(sc.x, sc.y), fmaxf(sc.z, sc.w)), 1e-30f));
         }
         // scores of this thread's heads, in log2 units
         float s[16];
 #pragma unroll
         for (int c = 0; c < (kFmt == kB128 ? 5 : 1); ++c) {
-          const uint32_t sb = s_seq & 1, at = t_s + lane_off + 128 * sb + hp;
-          if (ok) ok = wait_w(B_SFULL + sb, (s_seq >> 1) & 1);
+          const uint32_t sb = s_seq % F::kSBufs, at = t_s + lane_off + 128 * sb + hp;
+          if (ok) ok = wait_w(B_SFULL + sb, (s_seq / F::kSBufs) & 1);
           if (ok) {
             ptx::tc_fence_after();
             uint32_t hi[16], lo[16];
@@ -425,38 +483,89 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (!ok) break;
-        // P: rows of tokens, heads contiguous, and whether a score exceeds its reference by too much.
-        // bf16: over the rotary keys (their product is done); fp8: the products with the tile before's have to be
-        // (e4m3: once the terms are formed, 173 -> 169 us at 64 x 2 queries of 96 pages)
-        if (kFmt == kB128 && tile > 0 && !(ok = wait_w(B_PDONE, (tile - 1) & 1))) break;
-        float now[16];                         // the sums with this tile
-        auto weights = [&]() {
-          float most = -INFINITY;
-          uint8_t* prow = basep + L::kP;
-          uint32_t terms[2][4];                // e4m3: both terms of P
+        if (!live) {                           // rows that may hold anything: their P is 0, 0 times NaN is not
+          const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+          for (int c = part; c < F::kChunks; c += 4) {
+            uint4* row = reinterpret_cast<uint4*>(basep + L::kRing + (c_seq + c) % F::kBufs * kChunk + tok * 128);
 #pragma unroll
-          for (int j = 0; j < 16; j += 8) {
-            float e[8];
-            const float4 r0 = *reinterpret_cast<const float4*>(ref + hp + j);
-            const float4 r1 = *reinterpret_cast<const float4*>(ref + hp + j + 4);
-            const float r[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
+            for (int k = 0; k < 8; ++k) row[k] = zero;
+          }
+        }
+        auto hand_over = [&](int b) {
+          ptx::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(bar(b));
+        };
+        // O of the tiles before, times the heads' alpha
+        auto rescale = [&]() {
+          ptx::tc_fence_after();
+#pragma unroll 1
+          for (int h = 0; h < N; h += 16) {                // this warp's dims tile
+            uint32_t v[16];
+            const uint32_t at = t_o + lane_off + 64 * part + h;
+            ptx::tmem_ld16(at, v);
+            ptx::tmem_wait_ld();
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const float d = s[j + k] - r[k];
-              most = fmaxf(most, d);
-              e[k] = live ? ptx::ex2(d) : 0.f;
-              now[j + k] = sum[j + k] + e[k];
+            for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * alpha[h + k]);
+            ptx::tmem_st16(at, v);
+          }
+          ptx::tmem_wait_st();
+          ptx::tc_fence_before();
+        };
+        uint8_t* prow = basep + L::kP;
+        if constexpr (kFp8) {
+          // A head's weights of the warp's 32 tokens, which are the K of one MMA, have a power of two of their own: the
+          // largest is 2^7 to 2^8.5 of it (block scales: with the largest scale of each 128 dims in it as well).
+          // Lane j keeps head j's.
+          float k8 = 0.f, far = 0.f;
+          {
+            float m[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              m[j] = warp_most(live ? s[j] : -INFINITY);
+              far = fmaxf(far, fabsf(m[j]));
             }
-            const int hb = hp + j;             // first head of the eight
-            if (kFmt != kE4m3 && !heads) break;
-            if constexpr (kFmt == kBf16) {
-              uint4 o;
-              o.x = pack_bf16(e[0], e[1]);
-              o.y = pack_bf16(e[2], e[3]);
-              o.z = pack_bf16(e[4], e[5]);
-              o.w = pack_bf16(e[6], e[7]);
-              *reinterpret_cast<uint4*>(prow + tok * 128 + (((hb >> 3) ^ (tok & 7)) << 4)) = o;
-            } else {
+            if (far < 4194304.f) {             // to the nearest whole number
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                const float k = (m[j] + 12582912.f) - 12582920.f;
+                s[j] -= k;
+                if (lane == j) k8 = k;
+              }
+            } else {                           // no token, or scores that have no fractions
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                const float k = ceilf(fmaxf(m[j], -3.0e38f)) - 8.f;
+                s[j] -= k;
+                if (lane == j) k8 = k;
+              }
+            }
+          }
+          int fe[4] = {0, 0, 0, 0};
+          if constexpr (kFmt == kB128) {
+            float* f[4] = {&sc.x, &sc.y, &sc.z, &sc.w};
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+              const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(*f[m]) & 0x7FFFFFFFu);
+              fe[m] = min(126, (int)(top >> 23) - 126);
+              *f[m] *= __uint_as_float((uint32_t)(127 - fe[m]) << 23);
+            }
+          }
+          const float top = k8 + (float)max(max(fe[0], fe[1]), max(fe[2], fe[3]));
+          if (first) {                         // the item's reference: the largest of the four warps
+            if (heads && lane < 16) quarter[64 * quad + hp + lane] = top;
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(bar(B_MEET));
+          }
+          // (the products with the tile before's P have to be done; e4m3: once the terms are formed)
+          if (kFmt == kB128 && tile > 0 && !(ok = wait_w(B_PDONE, (tile - 1) & 1))) break;
+          uint32_t terms[2][4];                // e4m3: both terms of P
+          if (heads) {
+#pragma unroll
+            for (int j = 0; j < 16; j += 8) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k) s[j + k] = live ? ptx::ex2(s[j + k]) : 0.f;
+              const int hb = hp + j;           // first head of the eight
               const uint32_t at = tok * 64 + (((hb >> 4) ^ ((tok >> 1) & 3)) << 4) + (hb & 8);
 #pragma unroll
               for (int m = 0; m < (kFmt == kB128 ? 4 : 1); ++m) {
@@ -464,10 +573,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                  const float2 y = make_float2(f * e[2 * k], f * e[2 * k + 1]);
+                  const float2 y = make_float2(f * s[j + 2 * k], f * s[j + 2 * k + 1]);
                   const uint32_t c = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
                   const float2 b = e4m3x2_to_f32(c);
-                  const uint32_t d = __nv_cvt_float2_to_fp8x2(make_float2(y.x - b.x, y.y - b.y), __NV_SATFINITE, __NV_E4M3);
+                  const uint32_t d = __nv_cvt_float2_to_fp8x2(make_float2((y.x - b.x) * 16.f, (y.y - b.y) * 16.f),
+                                                              __NV_SATFINITE, __NV_E4M3);
                   hi[k >> 1] |= c << (16 * (k & 1));
                   lo[k >> 1] |= d << (16 * (k & 1));
                 }
@@ -485,104 +595,140 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           if constexpr (kFmt == kE4m3) {
-            if (tile > 0) ok = wait_w(B_PDONE, (tile - 1) & 1);
-            if (ok && heads) {
+            if (tile > 0 && !(ok = wait_w(B_PDONE, (tile - 1) & 1))) break;
+            if (heads) {
               uint8_t* at = prow + tok * 64 + (((hp >> 4) ^ ((tok >> 1) & 3)) << 4);
               *reinterpret_cast<uint4*>(at) = make_uint4(terms[0][0], terms[0][1], terms[0][2], terms[0][3]);
               *reinterpret_cast<uint4*>(at + 8192) = make_uint4(terms[1][0], terms[1][1], terms[1][2], terms[1][3]);
             }
           }
-          return heads && live && most + top_scale > kGrow;
-        };
-        if (!live) {                           // rows that may hold anything: their P is 0, 0 times NaN is not
-          const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-          for (int c = part; c < F::kChunks; c += 4) {
-            uint4* row = reinterpret_cast<uint4*>(basep + L::kRing + (c_seq + c) % F::kBufs * kChunk + tok * 128);
+          if (first && !(ok = wait_w(B_MEET, meets++ & 1))) break;
+          // The scales and sums count from the head's reference, which moves only when one exceeds it by 2^64.
+          auto four = [&]() {
+            const float* x = quarter + hp + lane;
+            return fmaxf(fmaxf(x[0], x[64]), fmaxf(x[128], x[192]));
+          };
+          auto put = [&](float r) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) row[k] = zero;
+            for (int m = 0; m < (kFmt == kB128 ? 4 : 1); ++m) scale[512 * m] = scale_byte(k8 - r + (float)fe[m]);
+          };
+          float r = 0.f, w = 0.f;
+          bool over = false;
+          if (heads && lane < 16) {
+            if (first) ref[hp + lane] = r = four();        // (the four warps of these heads write the same)
+            else over = top - (r = ref[hp + lane]) > kGrow8;
+            put(r);
+            w = over ? 0.f : pow2(k8 - r);
           }
-        }
-        auto renew = [&]() {
-          // new references: the largest score so far (fp8: 4 below, so that P, then up to 16, keeps its bits:
-          // two e4m3 terms are off by up to 2^-8 of P, or 2^-10 where that is more)
+          over = __any_sync(0xffffffffu, over);
+          if (over && lane == 0) grown[tile & 1] = (int)tile;
+          hand_over(B_PFULL);
+          if (heads) {
 #pragma unroll
-          for (int j = 0; j < 16; j += 4) {
-            float m[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) m[k] = warp_most(live ? s[j + k] + top_scale : -INFINITY);
-            if (heads && lane == 0)
-              *reinterpret_cast<float4*>(quarter + 64 * quad + hp + j) = make_float4(m[0], m[1], m[2], m[3]);
+            for (int j = 0; j < 16; ++j) sum[j] = fmaf(s[j], __shfl_sync(0xffffffffu, w, j), sum[j]);
           }
-          if (!(ok = meet())) return;
-          const float less = kFp8 ? 4.f : 0.f;
+          if (!first) {
+            if (!(ok = wait_w(B_PFULL, tile & 1))) break;
+            if (grown[tile & 1] == (int)tile) {
+              if (heads && lane < 16) quarter[64 * quad + hp + lane] = top;
+              if (!(ok = meet())) break;
+              float next = 0.f, a = 0.f;
+              w = 0.f;
+              if (heads && lane < 16) {
+                next = fmaxf(r, four());
+                a = pow2(r - next);
+                if (top - r > kGrow8) w = pow2(k8 - next);               // (was left out of the sum)
+                if (quad == 0) alpha[hp + lane] = a;
+                put(next);
+              }
+              if (heads) {
 #pragma unroll
-          for (int j = 0; j < 16; j += 4) {
-            const float4 x = *reinterpret_cast<const float4*>(quarter + hp + j);
-            const float4 y = *reinterpret_cast<const float4*>(quarter + 64 + hp + j);
-            const float4 z = *reinterpret_cast<const float4*>(quarter + 128 + hp + j);
-            const float4 w = *reinterpret_cast<const float4*>(quarter + 192 + hp + j);
-            const float top[4] = {fmaxf(fmaxf(x.x, y.x), fmaxf(z.x, w.x)), fmaxf(fmaxf(x.y, y.y), fmaxf(z.y, w.y)),
-                                  fmaxf(fmaxf(x.z, y.z), fmaxf(z.z, w.z)), fmaxf(fmaxf(x.w, y.w), fmaxf(z.w, w.w))};
-            float4 next = make_float4(top[0] - less, top[1] - less, top[2] - less, top[3] - less);
-            if (!first) {
-              const float4 r = *reinterpret_cast<const float4*>(ref + hp + j);
-              next = make_float4(fmaxf(r.x, next.x), fmaxf(r.y, next.y), fmaxf(r.z, next.z), fmaxf(r.w, next.w));
-              const float a[4] = {ptx::ex2(r.x - next.x), ptx::ex2(r.y - next.y), ptx::ex2(r.z - next.z),
-                                  ptx::ex2(r.w - next.w)};
-#pragma unroll
-              for (int k = 0; k < 4; ++k) sum[j + k] *= a[k];
-              if (heads && lane == 0 && quad == 0)
-                *reinterpret_cast<float4*>(alpha + hp + j) = make_float4(a[0], a[1], a[2], a[3]);
-            } else if (heads && lane == 0) {   // (the four warps of these heads write the same)
-              *reinterpret_cast<float4*>(ref + hp + j) = next;
+                for (int j = 0; j < 16; ++j)
+                  sum[j] = fmaf(s[j], __shfl_sync(0xffffffffu, w, j), sum[j] * __shfl_sync(0xffffffffu, a, j));
+              }
+              if (!(ok = meet())) break;       // (all have read the old references)
+              if (heads && lane < 16) ref[hp + lane] = next;
+              __syncwarp();
+              rescale();
+              hand_over(B_PAGAIN);
             }
-          }
-          __syncwarp();
-          if (!first) {                        // O of the tiles before
-            if (!(ok = meet())) return;
-            if (heads && lane < 16) {          // (all have read the old ones; the same from each of the four warps)
-              const float* x = quarter + hp + lane;
-              ref[hp + lane] = fmaxf(ref[hp + lane], fmaxf(fmaxf(x[0], x[64]), fmaxf(x[128], x[192])) - less);
-            }
-            __syncwarp();
-            if (!(ok = wait_w(B_PDONE, (tile - 1) & 1))) return;
-            ptx::tc_fence_after();
-#pragma unroll 1
-            for (int h = 0; h < N; h += 16) {              // this warp's dims tile
-              uint32_t v[16];
-              const uint32_t at = t_o + lane_off + 64 * part + h;
-              ptx::tmem_ld16(at, v);
-              ptx::tmem_wait_ld();
-#pragma unroll
-              for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * alpha[h + k]);
-              ptx::tmem_st16(at, v);
-            }
-            ptx::tmem_wait_st();
-            ptx::tc_fence_before();
-          }
-        };
-        auto hand_over = [&](int b) {
-          ptx::fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(bar(b));
-        };
-        // An item's first tile has no reference to try. e4m3: one place for the code of both passes (as fast as two,
-        // in half the code; bf16 71 us from two places, 73 from one, block scales 95 and 101: 32 queries of 64 pages).
-        if constexpr (kFmt == kE4m3) {
-          bool again = first;
-#pragma unroll 1
-          while (true) {
-            if (again) renew();
-            if (!ok) break;
-            const bool over = weights();
-            if (!ok) break;
-            if (!again && __any_sync(0xffffffffu, over) && lane == 0) grown[tile & 1] = (int)tile;
-            hand_over(again && !first ? B_PAGAIN : B_PFULL);
-            if (again) break;
-            if (!(ok = wait_w(B_PFULL, tile & 1)) || grown[tile & 1] != (int)tile) break;
-            again = true;
           }
         } else {
+          // P: rows of tokens, heads contiguous, over the rotary keys (their product is done), and whether a score
+          // exceeds its reference by too much
+          float now[16];                       // the sums with this tile
+          auto weights = [&]() {
+            float most = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < 16; j += 8) {
+              float e[8];
+              const float4 r0 = *reinterpret_cast<const float4*>(ref + hp + j);
+              const float4 r1 = *reinterpret_cast<const float4*>(ref + hp + j + 4);
+              const float r[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const float d = s[j + k] - r[k];
+                most = fmaxf(most, d);
+                e[k] = live ? ptx::ex2(d) : 0.f;
+                now[j + k] = sum[j + k] + e[k];
+              }
+              const int hb = hp + j;           // first head of the eight
+              if (!heads) break;
+              uint4 o;
+              o.x = pack_bf16(e[0], e[1]);
+              o.y = pack_bf16(e[2], e[3]);
+              o.z = pack_bf16(e[4], e[5]);
+              o.w = pack_bf16(e[6], e[7]);
+              *reinterpret_cast<uint4*>(prow + tok * 128 + (((hb >> 3) ^ (tok & 7)) << 4)) = o;
+            }
+            return heads && live && most > kGrow;
+          };
+          auto renew = [&]() {
+            // new references: the largest score so far
+#pragma unroll
+            for (int j = 0; j < 16; j += 4) {
+              float m[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) m[k] = warp_most(live ? s[j + k] : -INFINITY);
+              if (heads && lane == 0)
+                *reinterpret_cast<float4*>(quarter + 64 * quad + hp + j) = make_float4(m[0], m[1], m[2], m[3]);
+            }
+            if (!(ok = meet())) return;
+#pragma unroll
+            for (int j = 0; j < 16; j += 4) {
+              const float4 x = *reinterpret_cast<const float4*>(quarter + hp + j);
+              const float4 y = *reinterpret_cast<const float4*>(quarter + 64 + hp + j);
+              const float4 z = *reinterpret_cast<const float4*>(quarter + 128 + hp + j);
+              const float4 w = *reinterpret_cast<const float4*>(quarter + 192 + hp + j);
+              float4 next = make_float4(fmaxf(fmaxf(x.x, y.x), fmaxf(z.x, w.x)), fmaxf(fmaxf(x.y, y.y), fmaxf(z.y, w.y)),
+                                        fmaxf(fmaxf(x.z, y.z), fmaxf(z.z, w.z)), fmaxf(fmaxf(x.w, y.w), fmaxf(z.w, w.w)));
+              if (!first) {
+                const float4 r = *reinterpret_cast<const float4*>(ref + hp + j);
+                next = make_float4(fmaxf(r.x, next.x), fmaxf(r.y, next.y), fmaxf(r.z, next.z), fmaxf(r.w, next.w));
+                const float a[4] = {ptx::ex2(r.x - next.x), ptx::ex2(r.y - next.y), ptx::ex2(r.z - next.z),
+                                    ptx::ex2(r.w - next.w)};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) sum[j + k] *= a[k];
+                if (heads && lane == 0 && quad == 0)
+                  *reinterpret_cast<float4*>(alpha + hp + j) = make_float4(a[0], a[1], a[2], a[3]);
+              } else if (heads && lane == 0) { // (the four warps of these heads write the same)
+                *reinterpret_cast<float4*>(ref + hp + j) = next;
+              }
+            }
+            __syncwarp();
+            if (!first) {
+              if (!(ok = meet())) return;
+              if (heads && lane < 16) {        // (all have read the old ones; the same from each of the four warps)
+                const float* x = quarter + hp + lane;
+                ref[hp + lane] = fmaxf(ref[hp + lane], fmaxf(fmaxf(x[0], x[64]), fmaxf(x[128], x[192])));
+              }
+              __syncwarp();
+              if (!(ok = wait_w(B_PDONE, (tile - 1) & 1))) return;
+              rescale();
+            }
+          };
+          // An item's first tile has no reference to try. (The code of both passes twice: 71 us at 32 queries of 64
+          // pages, from one place 73.)
           if (!first) {
             if (__any_sync(0xffffffffu, weights()) && lane == 0) grown[tile & 1] = (int)tile;
             hand_over(B_PFULL);
@@ -594,10 +740,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             weights();
             hand_over(first ? B_PFULL : B_PAGAIN);
           }
-        }
-        if (!ok) break;
 #pragma unroll
-        for (int j = 0; j < 16; ++j) sum[j] = now[j];
+          for (int j = 0; j < 16; ++j) sum[j] = now[j];
+        }
       }
       if (!ok) break;
       // the item's sums, LSE and output

@@ -172,21 +172,13 @@ template <bool kForm8>
 __device__ __forceinline__ void mma_mx_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
                                           uint32_t sfb, uint32_t accumulate) {
   if constexpr (kForm8)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
-        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate) : "memory");
+    ptx::mma_mx8_ss(d, a, b, idesc, sfa, sfb, accumulate);
   else
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %6, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
         ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate) : "memory");
-}
-// 32 rows x 16 bytes of shared memory to four columns of tensor memory, in each quarter of the lanes.
-__device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint64_t desc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
 // Untiled copy of `bytes` (a multiple of 16) into shared memory, counted on a barrier.
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
@@ -315,10 +307,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < F::kGroups; ++i) {
             if (i == 1 && half) break;
-            tmem_cp_scales(sf + 4 * i, s + 32 * i);
+            ptx::tmem_cp_scales(sf + 4 * i, s + 32 * i);
 #pragma unroll
             for (int at = 0; at < kAtoms; ++at)
-              tmem_cp_scales(sf + 4 * (F::kGroups + kAtoms * i + at), s + 32 * (F::kGroups + kAtoms * i + at));
+              ptx::tmem_cp_scales(sf + 4 * (F::kGroups + kAtoms * i + at), s + 32 * (F::kGroups + kAtoms * i + at));
           }
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
