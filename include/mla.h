@@ -568,11 +568,13 @@ mla_status mla_mx4_project_workspace_size(const mla_config* cfg, int K, int N, i
 /* out = x W for a 4-bit W: x [rows][K], out [rows][N] (act dtype), fp32 sums. With W = W_comb and x =
  * out_latent this is mla_output_proj with a quarter of its bytes to read.
  *   workspace: 256-byte aligned device buffer of mla_mx4_project_workspace_size bytes (NULL if that is 0),
- *   any contents; calls that share one must be ordered on the GPU. rows == 0 is a no-op.
+ *   any contents; calls that share one must be ordered on the GPU. Its first int32 is the call's status word,
+ *   cleared by each call (mla_read_device_status). rows == 0 is a no-op.
  * bf16 activations run on the tensor cores (an x that does not start at a multiple of 16 bytes on the SIMT
  * kernel): x enters as exact sums of 4-bit or e4m3 values under a power of two per 32 elements, off by at most
  * 2^-17 of the largest of the 32, and a row that holds an infinity or NaN gives NaN in all its outputs. A
- * column with a NaN scale gives NaN. Should a bounded wait of the kernel run out, its outputs are not written. */
+ * column with a NaN scale gives NaN. Should a bounded wait of the kernel run out, the status word gets
+ * MLA_ERR_TIMEOUT and outputs that need the missing sums are not written. */
 mla_status mla_mx4_project(const mla_config* cfg, const void* x, const void* codes, const void* scales, int K,
                            int N, int rows, void* out, void* workspace, size_t workspace_bytes, void* stream);
 
@@ -589,8 +591,13 @@ const char* mla_last_error(void);
 
 /* Library ABI version (major * 100 + minor). 1.02: mla_append_cache needs no workspace
  * (its size is 0). 1.03: the shared-prefix and eviction calls. 1.04: page-sparse decoding and 4-bit
- * weights. */
+ * weights. 1.05: the workspace of mla_mx4_project starts with its status word. */
 int mla_version(void);
+
+/* Testing hook of the failure paths of mla_mx4_project's tensor-core kernel, for this host thread's calls until it is
+ * set again: wait_limit_us (0: the default, 2 s) is how long a barrier wait may last; the first CTA never loads the
+ * copy of index withhold - 1 (0: none withheld), so that the wait for it runs out. */
+void mla_testing_waits(int wait_limit_us, int withhold);
 
 /* Number of CUDA kernels the library has launched in this process so far (all
  * threads, all devices); lets a caller count the kernels of a timed region. */

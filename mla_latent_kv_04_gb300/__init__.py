@@ -108,6 +108,7 @@ _SIGNATURES = {
     "mla_status_string": (ctypes.c_char_p, [_I]),
     "mla_last_error": (ctypes.c_char_p, []),
     "mla_version": (_I, []),
+    "mla_testing_waits": (None, [_I, _I]),
     "mla_kernel_launches": (ctypes.c_uint64, []),
 }
 
@@ -145,6 +146,11 @@ def mla_last_error() -> str:
 
 def mla_version() -> int:
     return lib().mla_version()
+
+
+def mla_testing_waits(wait_limit_us: int = 0, withhold: int = 0):
+    """Testing hook of failure paths, for this thread's calls until it is set again (0, 0: off)."""
+    lib().mla_testing_waits(int(wait_limit_us), int(withhold))
 
 
 def _check(status: int, where: str):
@@ -692,7 +698,7 @@ def mla_mx4_project_workspace_size(cfg, K, N, rows) -> int:
 
 def mla_mx4_project(cfg, x, codes, scales, out, workspace=None, stream=None):
     """out [rows][N] = x [rows][K] times the 4-bit weight. workspace: uint8 device tensor of
-    mla_mx4_project_workspace_size bytes (None if 0)."""
+    mla_mx4_project_workspace_size bytes (None if 0); its first int32 is the call's status word."""
     a = (_act_dtype(cfg),)
     rows, K = x.shape
     N = out.shape[1]

@@ -285,6 +285,12 @@ struct EvictParams {
 constexpr long long kEvictMaxKeys = 8LL * 48 * 1024;
 cudaError_t launch_evict(mla_dtype cache, const EvictParams& p, cudaStream_t s);
 
+// Of a call's tensor-core kernel: how long its waits may last, and (from 1 on; tests only) the copy that it leaves out.
+struct TestWaits {
+  unsigned long long limit_ns = 2000000000ull;
+  int withhold = 0;
+};
+
 // ---- page-sparse decoding ------------------------------------------------------------------
 struct PageKeysParams {
   const void* cache;
@@ -352,7 +358,7 @@ cudaError_t launch_mx4_dequantize(mla_dtype act, const void* codes, const void* 
 bool mx4_project_tc_supported(mla_dtype act);
 size_t mx4_project_tc_workspace(int K, int N, int rows);
 cudaError_t launch_mx4_project_tc(const void* x, const void* codes, const void* scales, int K, int N, int rows,
-                                  void* out, void* workspace, cudaStream_t s);
+                                  void* out, void* workspace, const TestWaits& test, cudaStream_t s);
 cudaError_t launch_mx4_project_simt(mla_dtype act, const void* x, const void* codes, const void* scales, int K,
                                     int N, int rows, void* out, cudaStream_t s);
 

@@ -23,6 +23,7 @@ void note_launch(int n) { g_launches.fetch_add((unsigned long long)n, std::memor
 namespace {
 
 thread_local std::string g_last_error;
+thread_local TestWaits g_test_waits;           // (mla_testing_waits)
 
 mla_status cuda_fail(cudaError_t e, const char* where) {
   g_last_error = std::string(where) + ": " + cudaGetErrorString(e);
@@ -177,7 +178,13 @@ void set_last_error(const std::string& what) { g_last_error = what; }
 
 extern "C" {
 
-int mla_version(void) { return 104; }
+int mla_version(void) { return 105; }
+
+void mla_testing_waits(int wait_limit_us, int withhold) {
+  g_test_waits = TestWaits();
+  if (wait_limit_us > 0) g_test_waits.limit_ns = 1000ull * (unsigned long long)wait_limit_us;
+  if (withhold > 0) g_test_waits.withhold = withhold;
+}
 
 uint64_t mla_kernel_launches(void) { return (uint64_t)mla::g_launches.load(); }
 
@@ -1188,9 +1195,14 @@ mla_status mla_mx4_project(const mla_config* cfg, const void* x, const void* cod
     return MLA_ERR_WORKSPACE;
   }
   if (need > 0 && ((uintptr_t)workspace & 255) != 0) return invalid("workspace must be 256-byte aligned");
-  cudaError_t e = need > 0 && aligned16(x)
-                      ? launch_mx4_project_tc(x, codes, scales, K, N, rows, out, workspace, (cudaStream_t)stream)
-                      : launch_mx4_project_simt(cfg->act_dtype, x, codes, scales, K, N, rows, out, (cudaStream_t)stream);
+  cudaStream_t s = (cudaStream_t)stream;
+  cudaError_t e;
+  if (need > 0 && aligned16(x)) {
+    e = launch_mx4_project_tc(x, codes, scales, K, N, rows, out, workspace, g_test_waits, s);
+  } else {
+    e = need > 0 ? cudaMemsetAsync(workspace, 0, 4, s) : cudaSuccess;      // the status word
+    if (e == cudaSuccess) e = launch_mx4_project_simt(cfg->act_dtype, x, codes, scales, K, N, rows, out, s);
+  }
   return e == cudaSuccess ? MLA_OK : cuda_fail(e, "mla_mx4_project");
 }
 

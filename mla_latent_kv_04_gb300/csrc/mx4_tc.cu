@@ -156,10 +156,12 @@ __device__ __forceinline__ void split_row(const bf16* __restrict__ x, int r, int
 
 template <bool kForm8>
 __global__ void __launch_bounds__(256) split_kernel(const bf16* __restrict__ x, int rows, int K, TileShape t,
-                                                    uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
+                                                    uint8_t* __restrict__ codes, uint8_t* __restrict__ scales,
+                                                    int32_t* status) {
   const int k = (blockIdx.x * 256 + threadIdx.x) * 8;
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
+  if (k == 0 && blockIdx.y == 0) *status = 0;
   if (k >= (K + 127) / 128 * 128) return;      // (sixteen lanes together)
   for (int r = blockIdx.y; r < rows; r += gridDim.y)
     split_row<kForm8>(x, r, k, K, t, codes, scales);
@@ -204,7 +206,8 @@ struct ProjectParams {
   int rows, N, groups;
   bf16* out;
   float* pieces;               // [2 grid][T][128]
-  int32_t* status;
+  int32_t* status;             // the call's, cleared by the split
+  TestWaits test;
 };
 
 enum { B_FULL = 0, B_EMPTY = kMaxStages, B_DFULL = 2 * kMaxStages, B_DFREE, B_TEAR, B_COUNT };
@@ -242,7 +245,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   ptx::tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   ptx::griddep_launch_dependents();
-  auto wait = [&](int i, uint32_t parity) { return bounded_wait(bar(i), parity, abort, p.status); };
+  const uint64_t limit = p.test.limit_ns;
+  auto wait = [&](int i, uint32_t parity) { return bounded_wait(bar(i), parity, abort, p.status, limit); };
   auto wait_w = [&](int i, uint32_t parity) { return __all_sync(0xffffffffu, wait(i, parity)) != 0; };
   if (warp == 0) {
     if (lane == 0) {
@@ -259,13 +263,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t dst = base + st * p.shape.stage, full = bar(B_FULL + st);
         if (!wait(B_EMPTY + st, phase)) break;
         const uint32_t n = (uint32_t)min(F::kGroups, p.groups - F::kGroups * k);   // groups of 128 of this step
-        ptx::mbar_arrive_expect_tx(full, F::kTx + p.shape.cols * 128 + n * 512 * (1 + kAtoms));
-        if (p.work.row_tiles == 1) ptx::tma_load_3d_hint(dst, &tm_w, kX * k, 128 * mt, 0, full, pol);
-        else ptx::tma_load_3d(dst, &tm_w, kX * k, 128 * mt, 0, full);
-        ptx::tma_load_3d(dst + off_x, &tm_x, 128 * k, 0, rt, full);
-        bulk_load(dst + off_sfw, p.w_scales + ((long long)mt * p.groups + F::kGroups * k) * 512, n * 512, full);
-        bulk_load(dst + off_sfx, p.x_scales + ((long long)rt * p.groups + F::kGroups * k) * (kAtoms * 512),
-                  n * (kAtoms * 512), full);
+        if (blockIdx.x != 0 || (int)g != p.test.withhold - 1) {
+          ptx::mbar_arrive_expect_tx(full, F::kTx + p.shape.cols * 128 + n * 512 * (1 + kAtoms));
+          if (p.work.row_tiles == 1) ptx::tma_load_3d_hint(dst, &tm_w, kX * k, 128 * mt, 0, full, pol);
+          else ptx::tma_load_3d(dst, &tm_w, kX * k, 128 * mt, 0, full);
+          ptx::tma_load_3d(dst + off_x, &tm_x, 128 * k, 0, rt, full);
+          bulk_load(dst + off_sfw, p.w_scales + ((long long)mt * p.groups + F::kGroups * k) * 512, n * 512, full);
+          bulk_load(dst + off_sfx, p.x_scales + ((long long)rt * p.groups + F::kGroups * k) * (kAtoms * 512),
+                    n * (kAtoms * 512), full);
+        }
         if (++st == (uint32_t)stages) {
           st = 0;
           phase ^= 1;
@@ -280,9 +286,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (*abort)
         for (uint32_t i = g > (uint32_t)stages ? g - stages : 0; i < g; ++i)
-          drain_wait(bar(B_FULL + i % stages), (i / stages) & 1);
+          drain_wait(bar(B_FULL + i % stages), (i / stages) & 1, limit);
     }
   } else if (warp == 1) {
+    ptx::griddep_wait();                                       // (from here on the waits have an end)
     uint32_t st = 0, phase = 0, seg = 0;
     bool ok = true;
     // in units of 16 bytes, as descriptors count
@@ -333,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (*abort) {
       if (ptx::elect_one()) ptx::mma_commit(bar(B_TEAR));
       __syncwarp();
-      drain_wait(bar(B_TEAR), 0);
+      drain_wait(bar(B_TEAR), 0, limit);
     }
   } else {
     const int quad = warp & 3, col = 32 * quad + lane;         // column of the tile
@@ -381,10 +388,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Adds a tile's pieces in the order of its steps. Block (tile, 8 rows): thread = column and four rows. Bound by
+// Adds a tile's pieces in the order of its steps; nothing where a CTA gave up before it wrote its own. Block (tile, 8 rows): thread = column and four rows. Bound by
 // L2: pieces of 152 CTAs, 4.7 us for 32 rows x 5120 columns, 9 for 512.
 __global__ void __launch_bounds__(256) merge_kernel(const Work work, const float* __restrict__ pieces, int rows, int N,
-                                                    int T, bf16* __restrict__ out) {
+                                                    int T, bf16* __restrict__ out, const int32_t* status) {
   const int tile = blockIdx.x, mt = tile / work.row_tiles, rt = tile % work.row_tiles;
   const int col = threadIdx.x % 128, n = 128 * mt + col;
   const long long s0 = (long long)tile * work.steps;
@@ -392,6 +399,7 @@ __global__ void __launch_bounds__(256) merge_kernel(const Work work, const float
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   if (c0 == c1) return;                        // written by its only CTA
+  const int32_t gave_up = *status;             // (looked at last: its load is in flight with the pieces')
   const int r0 = 8 * blockIdx.y + 4 * (threadIdx.x / 128), m = min(4, min(T, rows - rt * T) - r0);
   // a CTA that began before this tile (the first one, if any) has it as its second piece
   const float* src = pieces + ((long long)2 * c0 * T + r0) * 128 + col;
@@ -404,7 +412,7 @@ __global__ void __launch_bounds__(256) merge_kernel(const Work work, const float
     for (int i = 0; i < 4; ++i)
       if (i < m) v[i] += piece[i * 128];
   }
-  if (n >= N) return;
+  if (n >= N || gave_up != 0) return;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     if (i < m) out[(long long)(rt * T + r0 + i) * N + n] = __float2bfloat16_rn(v[i]);
@@ -431,14 +439,14 @@ Work make_work(int K, int N, const TileShape& t) {
 
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-struct ProjectLayout {
+struct ProjectLayout {                         // (behind the status word)
   size_t codes, scales, pieces, total;
 };
 template <bool kForm8>
 ProjectLayout project_layout(int K, const TileShape& t, int grid) {
   ProjectLayout l;
-  l.codes = 0;
-  l.scales = up256((size_t)t.tiles * t.cols * (kForm8 ? K : K / 2));
+  l.codes = 256;
+  l.scales = up256(l.codes + (size_t)t.tiles * t.cols * (kForm8 ? K : K / 2));
   l.pieces = up256(l.scales + (size_t)t.tiles * ((K + 127) / 128) * t.atoms * 512);
   l.total = up256(l.pieces + (size_t)2 * grid * t.T * 128 * 4);
   return l;
@@ -452,7 +460,7 @@ size_t project_workspace(int K, int N, int rows) {
 
 template <bool kForm8>
 cudaError_t project(const void* x, const void* codes, const void* scales, int K, int N, int rows, void* out,
-                    void* workspace, cudaStream_t s) {
+                    void* workspace, const TestWaits& test, cudaStream_t s) {
   const TileShape t = tile_shape<kForm8>(rows);
   ProjectParams p;
   p.work = make_work<kForm8>(K, N, t);
@@ -466,7 +474,8 @@ cudaError_t project(const void* x, const void* codes, const void* scales, int K,
   p.groups = (K + 127) / 128;
   p.out = (bf16*)out;
   p.pieces = (float*)(ws + l.pieces);
-  p.status = nullptr;
+  p.status = (int32_t*)workspace;
+  p.test = test;
   CUtensorMap tw, tx;
   const uint64_t row = (uint64_t)K / 2, x_row = kForm8 ? K : K / 2;
   if (!tensor_map_3d(&tw, kForm8 ? CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B : CU_TENSOR_MAP_DATA_TYPE_UINT8,
@@ -480,11 +489,11 @@ cudaError_t project(const void* x, const void* codes, const void* scales, int K,
   cudaError_t e = allow_smem(kern, smem);
   if (e == cudaSuccess)
     e = launch_pdl(split_kernel<kForm8>, dim3((unsigned)((K + 2047) / 2048), (unsigned)(rows < 32768 ? rows : 32768), 1), 256, 0, s, (const bf16*)x,
-                   rows, K, t, ws + l.codes, ws + l.scales);
+                   rows, K, t, ws + l.codes, ws + l.scales, p.status);
   if (e == cudaSuccess) e = launch_pdl(kern, dim3((unsigned)p.work.grid, 1, 1), kThreads, smem, s, tw, tx, p);
   if (e == cudaSuccess)
     e = launch_pdl(merge_kernel, dim3((unsigned)p.work.tiles, (unsigned)((t.T + 7) / 8), 1), 256, 0, s, p.work,
-                   (const float*)p.pieces, rows, N, t.T, (bf16*)out);
+                   (const float*)p.pieces, rows, N, t.T, (bf16*)out, (const int32_t*)p.status);
   return e;
 }
 
@@ -504,10 +513,10 @@ size_t mx4_project_tc_workspace(int K, int N, int rows) {
 }
 
 cudaError_t launch_mx4_project_tc(const void* x, const void* codes, const void* scales, int K, int N, int rows,
-                                  void* out, void* workspace, cudaStream_t s) {
+                                  void* out, void* workspace, const TestWaits& test, cudaStream_t s) {
   if (form8_fits(K, rows) && ((uintptr_t)codes & 31) == 0)
-    return project<true>(x, codes, scales, K, N, rows, out, workspace, s);
-  return project<false>(x, codes, scales, K, N, rows, out, workspace, s);
+    return project<true>(x, codes, scales, K, N, rows, out, workspace, test, s);
+  return project<false>(x, codes, scales, K, N, rows, out, workspace, test, s);
 }
 
 }  // namespace mla
