@@ -488,7 +488,9 @@ mla_status mla_page_scores_workspace_size(const mla_config* cfg, int batch, int 
  * fp32 sums and softmax. The tensor-core kernel takes bf16 at d_c 512, d_r 64, 64-token pages, up to 128
  * heads and max_pages up to 8192, for q_lat and page_keys that start at multiples of 16 bytes; anything else
  * takes SIMT kernels, many times slower at large sizes. A page with an id out of range scores 0, a request with seq_lens[b] < q_len or
- * above max_pages * P is left out, both with the guard; seq_lens[b] == 0 is left out. workspace: 256-byte
+ * above max_pages * P is left out, both with the guard; seq_lens[b] == 0 is left out. Should a bounded wait of the
+ * tensor-core kernel run out, MLA_ERR_TIMEOUT is OR-ed into *dev_status and that query's scores are not written.
+ * workspace: 256-byte
  * aligned device buffer of mla_page_scores_workspace_size bytes (NULL if that is 0), any contents; calls
  * that share one must be ordered on the GPU. */
 mla_status mla_page_scores(const mla_config* cfg, const void* q_lat, const void* page_keys, int num_pages,
@@ -594,9 +596,10 @@ const char* mla_last_error(void);
  * weights. 1.05: the workspace of mla_mx4_project starts with its status word. */
 int mla_version(void);
 
-/* Testing hook of the failure paths of mla_mx4_project's tensor-core kernel, for this host thread's calls until it is
- * set again: wait_limit_us (0: the default, 2 s) is how long a barrier wait may last; the first CTA never loads the
- * copy of index withhold - 1 (0: none withheld), so that the wait for it runs out. */
+/* Testing hook of the failure paths of the tensor-core kernels of mla_mx4_project and mla_page_scores, for this host
+ * thread's calls until it is set again: wait_limit_us (0: the default, 2 s) is how long a barrier wait may last; the
+ * first CTA never loads (or hands over) the copy of index withhold - 1 (0: all are), so that the wait for it runs
+ * out. */
 void mla_testing_waits(int wait_limit_us, int withhold);
 
 /* Number of CUDA kernels the library has launched in this process so far (all

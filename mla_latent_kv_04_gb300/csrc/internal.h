@@ -316,6 +316,7 @@ struct PageScoreParams {
   float* scores;              // [groups][max_pages]
   float* lse2;                // workspace of the SIMT form: [groups][H]
   int32_t* status;
+  TestWaits test;
 };
 cudaError_t launch_page_scores_simt(mla_dtype act, const PageScoreParams& p, cudaStream_t s);
 // The tensor-core form: bf16, 64-token pages, d_c 512, d_r 64, up to 128 heads and 8192 pages a request (4096

@@ -983,6 +983,7 @@ mla_status mla_page_scores(const mla_config* cfg, const void* q_lat, const void*
   p.scores = scores;
   p.lse2 = (float*)workspace;
   p.status = dev_status;
+  p.test = g_test_waits;
   cudaError_t e = page_scores_tc_supported(cfg, num_pages, max_pages) && aligned16(q_lat, page_keys)
                       ? launch_page_scores_tc(p, (cudaStream_t)stream)
                       : launch_page_scores_simt(cfg->act_dtype, p, (cudaStream_t)stream);

@@ -92,7 +92,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
-  auto wait = [&](int i, uint32_t parity) { return bounded_wait(bar(i), parity, abort, p.status); };
+  const uint64_t limit = p.test.limit_ns;
+  auto wait = [&](int i, uint32_t parity) { return bounded_wait(bar(i), parity, abort, p.status, limit); };
   auto wait_w = [&](int i, uint32_t parity) { return __all_sync(0xffffffffu, wait(i, parity)) != 0; };
   float2* head = reinterpret_cast<float2*>(basep + kOffHead);
   float* part = reinterpret_cast<float*>(basep + kOffRing);                // [4][kTiles][128], after the products
@@ -138,8 +139,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (*abort) {
         if (ptx::elect_one()) ptx::mma_commit(bar(B_TEAR));
         __syncwarp();
-        drain_wait(bar(B_TEAR), 0);
-        drain_wait(bar(B_QFULL), 0);
+        drain_wait(bar(B_TEAR), 0, limit);
+        drain_wait(bar(B_QFULL), 0, limit);
       }
     }
   } else {
@@ -172,7 +173,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         cp_async_wait<kStages - 1>();
         ptx::fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(bar(B_FULL + (n - kStages + 1) % kStages));
+        if (lane == 0 && (blockIdx.x != 0 || n - kStages + 1 != p.test.withhold - 1))
+          ptx::mbar_arrive(bar(B_FULL + (n - kStages + 1) % kStages));
       }
     }
     cp_async_wait<0>();
@@ -221,6 +223,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncwarp();
   if (C > 1) ptx::cluster_sync();
   else __syncthreads();
+  if (warp == 0 && C > 1) {                    // a CTA that gave up has no sums to share: nobody writes
+    const uint32_t at = ptx::map_to_rank(ptx::smem_u32(const_cast<int*>(abort)), (uint32_t)(lane < C ? lane : 0));
+    if (__any_sync(0xffffffffu, ptx::ld_dsmem_u32(at) != 0) && lane == 0) *abort = 1;
+    __syncwarp();
+  }
   if (warp >= 2) {
     // the head's over the cluster, in order of ranks
     float top = -INFINITY, sum = 0.f;
