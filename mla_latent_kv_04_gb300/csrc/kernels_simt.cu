@@ -372,8 +372,8 @@ __global__ void __launch_bounds__(256) decode_simt_kernel(DecodeParams p) {
       m = m_new;
     }
     if (head_ok) {
-      const float inv_l = (l > 0.f) ? p.out_scale / l : 0.f;
-      const float lse_v = (l > 0.f) ? (m + log2f(l)) * kLn2 : -INFINITY;
+      const float inv_l = l == 0.f ? 0.f : p.out_scale / l;                 // (NaN stays NaN)
+      const float lse_v = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
       if (item.single) {
         QT* out = reinterpret_cast<QT*>(p.out_latent) + ((long long)g * p.H + h) * p.d_c;
 #pragma unroll
@@ -411,8 +411,13 @@ __global__ void __launch_bounds__(256) combine_kernel(DecodeParams p, int groups
   QT* out = reinterpret_cast<QT*>(p.out_latent) + gh * p.d_c;
   if (n == 1) return;                          // written directly by the attention kernel
   float m = -INFINITY;
-  for (int s = 0; s < n; ++s) m = fmaxf(m, p.part_lse[(long long)(first + s) * p.H + h]);
-  if (n == 0 || m == -INFINITY) {
+  bool nan = false;
+  for (int s = 0; s < n; ++s) {
+    const float l = p.part_lse[(long long)(first + s) * p.H + h];
+    m = fmaxf(m, l);
+    nan |= l != l;
+  }
+  if (n == 0 || (m == -INFINITY && !nan)) {
     for (int k = lane; k < p.d_c; k += 32) out[k] = from_f32<QT>(0.f);
     if (lane == 0) p.lse[gh] = -INFINITY;
     return;
