@@ -684,12 +684,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             return heads && live && most > kGrow;
           };
           auto renew = [&]() {
-            // new references: the largest score so far
+            // new references: the largest score so far (finite, so that scores of -infinity weigh 0)
 #pragma unroll
             for (int j = 0; j < 16; j += 4) {
               float m[4];
 #pragma unroll
-              for (int k = 0; k < 4; ++k) m[k] = warp_most(live ? s[j + k] : -INFINITY);
+              for (int k = 0; k < 4; ++k) m[k] = fmaxf(warp_most(live ? s[j + k] : -INFINITY), -3.0e38f);
               if (heads && lane == 0)
                 *reinterpret_cast<float4*>(quarter + 64 * quad + hp + j) = make_float4(m[0], m[1], m[2], m[3]);
             }
@@ -754,7 +754,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (heads && lane < 16 && quad == 0) {
         const float* q = quarter + hp + lane;
         const float total = (q[0] + q[64]) + (q[128] + q[192]);
-        alpha[hp + lane] = p.out_scale / total;
+        alpha[hp + lane] = total == 0.f ? 0.f : p.out_scale / total;       // (every score -infinity)
         const float lse = (ref[hp + lane] + log2f(total)) * kLn2;
         const int h = h0 + hp + lane;
         if (item.single) p.lse[g * p.H + h] = lse;
@@ -793,7 +793,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // A query's pieces under the weights of their LSEs: block (query, 4 heads), 64 threads a head, eight dims each.
-// Pieces of one item are final and stay; a query without tokens gets 0 and -inf. Bound by L2, 10.5 us alone (32
+// Pieces of one item are final and stay; a query without tokens (or with scores of -inf alone) gets 0 and -inf. Bound by L2, 10.5 us alone (32
 // queries of 64 pages), most of its start-up hidden under the attention's end.
 __global__ void __launch_bounds__(256) merge_pages_kernel(const DecodeParams p) {
   ptx::griddep_launch_dependents();
@@ -812,12 +812,12 @@ __global__ void __launch_bounds__(256) merge_pages_kernel(const DecodeParams p) 
   for (int i = 0; i < n; ++i) {
     const float4 x = *reinterpret_cast<const float4*>(src + (long long)i * p.H * 512);
     const float4 y = *reinterpret_cast<const float4*>(src + (long long)i * p.H * 512 + 256);
-    const float w = expf(lse[(long long)i * p.H] - m);
+    const float l = lse[(long long)i * p.H], w = l == -INFINITY ? 0.f : expf(l - m);
     total += w;
     a = make_float4(fmaf(w, x.x, a.x), fmaf(w, x.y, a.y), fmaf(w, x.z, a.z), fmaf(w, x.w, a.w));
     b = make_float4(fmaf(w, y.x, b.x), fmaf(w, y.y, b.y), fmaf(w, y.z, b.z), fmaf(w, y.w, b.w));
   }
-  const float inv = n ? 1.f / total : 0.f;
+  const float inv = total == 0.f ? 0.f : 1.f / total;
   bf16* out = reinterpret_cast<bf16*>(p.out_latent) + ((long long)g * p.H + h) * 512 + d;
   if ((reinterpret_cast<uintptr_t>(p.out_latent) & 7) == 0) {
     *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
@@ -827,7 +827,7 @@ __global__ void __launch_bounds__(256) merge_pages_kernel(const DecodeParams p) 
 #pragma unroll
     for (int i = 0; i < 8; ++i) out[(i >> 2) * 256 + (i & 3)] = __float2bfloat16_rn(v[i] * inv);
   }
-  if (threadIdx.x % 64 == 0) p.lse[(long long)g * p.H + h] = n ? m + logf(total) : -INFINITY;
+  if (threadIdx.x % 64 == 0) p.lse[(long long)g * p.H + h] = total == 0.f ? -INFINITY : m + logf(total);
 }
 
 template <int kFmt>

@@ -355,8 +355,9 @@ __global__ void __launch_bounds__(256) decode_simt_kernel(DecodeParams p) {
       if (lane < ntok) s0 = PageElem<CT>::dot(page_s + lane * stride, qh, D, p.d_c) * p.scale_log2;
       if (lane + 32 < ntok) s1 = PageElem<CT>::dot(page_s + (lane + 32) * stride, qh, D, p.d_c) * p.scale_log2;
       const float m_new = fmaxf(m, warp_max(fmaxf(s0, s1)));
-      const float alpha = exp2f(m - m_new);
-      const float p0 = exp2f(s0 - m_new), p1 = exp2f(s1 - m_new);
+      const float ref = fmaxf(m_new, -3.0e38f);            // (finite: scores of -infinity weigh 0)
+      const float alpha = exp2f(m - ref);
+      const float p0 = exp2f(s0 - ref), p1 = exp2f(s1 - ref);
       l = l * alpha + warp_sum(p0 + p1);
 #pragma unroll
       for (int i = 0; i < VPL; ++i) o[i] *= alpha;

@@ -93,6 +93,38 @@ def test_a_nan_in_a_row(kind, shape, H, b, j):
     assert np.array_equal(got[rest], good[0][rest]) and np.array_equal(lse[rest], good[1][rest])
 
 
+@pytest.mark.parametrize("kind,shape,H", [x for x in CASES if x[0] != "fp8_e4m3"])
+@pytest.mark.parametrize("pages_out", [1, 2, 5])
+def test_rotary_keys_of_minus_infinity_weigh_nothing(kind, shape, H, pages_out):
+    """The first pages' scores are -infinity for every head (half a tile, a tile, and more): the result is that of
+    the other pages."""
+    c, q_lat, pages = inputs(kind, shape, H, (900, 3000))
+    k = c.d.d_latent + 1
+    q_lat[..., k] = 0.5
+    for b in range(2):
+        pages[b, 0, : min(40, -(-c.lens[b] // P))] = np.arange(-(-c.lens[b] // P))[:40]
+        for j in range(pages_out * P):
+            put(c, b, j, k, -np.inf)
+    got, lse, st = pg.attend(c, q_lat, pages)
+    assert st == M.MLA_OK
+    pg.check_attend(c, q_lat, np.where(pages < pages_out, -1, pages), got, lse)
+
+
+def test_nothing_but_minus_infinity():
+    """Scores that are all -infinity: no weight at all, so the result of an empty list or NaN, never a number."""
+    for kind, shape, H in (("bf16", "v2", 128), ("fp8_e4m3_b128", "v2", 128), ("f32", "tiny", 16)):
+        c, q_lat, pages = inputs(kind, shape, H, (100, 900))
+        dc = c.d.d_latent
+        q_lat[..., dc + 1] = 1.0
+        pages[0, 0, :2] = (0, 1)
+        for j in range(100):
+            put(c, 0, j, dc + 1, -np.inf)
+        got, lse, st = pg.attend(c, q_lat, pages)
+        assert st == M.MLA_OK
+        assert (np.isnan(got[0]) | (got[0] == 0)).all() and (np.isnan(lse[0]) | np.isneginf(lse[0])).all()
+        assert np.isfinite(got[1]).all()
+
+
 # ----------------------------------------------------------------------------- 4-bit product, many rows
 
 FORM8 = [(70, 256, 256), (41, 1024, 160), (300, 128, 70)]
