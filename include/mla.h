@@ -523,8 +523,8 @@ mla_status mla_decode_pages_workspace_size(const mla_config* cfg, int batch, int
  *   mla_select_pages, or any other choice); the rest as in mla_decode. A list of all pages gives
  *   mla_decode's result up to rounding.
  * An empty list or seq_lens[b] == 0: out_latent = 0, lse = -inf. A length below q_len or above max_pages *
- * P is skipped like an empty request, with the guard; a list that is not ascending or names a page that
- * the query does not see sets the guard and leaves that query's result undefined. workspace: as in
+ * P is skipped like an empty request, with the guard; a list that is not ascending, has a page behind a -1 or names
+ * one that the query does not see sets the guard and leaves that query's result undefined. workspace: as in
  * mla_decode (its first int32 is the call's status word, cleared by each call). MLA_ERR_UNSUPPORTED:
  * d_latent above 512, batch * q_len above 8192. The tensor-core kernel takes bf16 activations at d_c 512, d_r
  * 64, 64-token pages, any cache format and a multiple of 16 heads up to 1024, for a q_lat and cache that start

@@ -801,6 +801,7 @@ __global__ void __launch_bounds__(256) merge_pages_kernel(const DecodeParams p) 
   const int g = blockIdx.x, h = 4 * blockIdx.y + threadIdx.x / 64, d = 4 * (threadIdx.x % 64);
   const int first = p.group_first[g], last = p.group_last[g];
   const int n = first >= 0 && last >= first ? last - first + 1 : 0;
+  if (blockIdx.y == 0 && threadIdx.x == 0 && p.bad_lists[g]) flag_status(p.status, MLA_ERR_DEVICE_GUARD);
   if (n == 1) return;
   const float* lse = p.part_lse + (long long)first * p.H + h;
   float m = -INFINITY;

@@ -81,6 +81,8 @@ struct DecodeParams {
   // 0: part_o is fp32 [items][H][d_c]; 1: bf16 [items][d_c / 8][H][8] (eight latent dims of
   // every head contiguous, so a warp of consecutive heads writes one 512-byte run)
   int part_planar;
+  // decode over chosen pages: [groups], whether the query's list has an entry that it must not have
+  const int32_t* bad_lists = nullptr;
 };
 
 // Counts kernels launched through the library (read by mla_kernel_launches).
@@ -338,8 +340,9 @@ cudaError_t launch_select_pages(const SelectParams& p, int groups, cudaStream_t 
 // Groups whose plan fits the shared memory of one block.
 constexpr int kPagesMaxGroups = 8192;
 // Plans the decode over the lists of pp.pages, and writes their physical pages to table
-// [groups][budget] (-1 for an entry out of order or out of sight).
-cudaError_t launch_pages_prep(const PlanParams& pp, const int32_t* block_table, int32_t* table, cudaStream_t s);
+// [groups][budget] (-1 for an entry out of order or out of sight) and whether a list has such an entry to bad [groups].
+cudaError_t launch_pages_prep(const PlanParams& pp, const int32_t* block_table, int32_t* table, int32_t* bad,
+                              cudaStream_t s);
 
 // The decode over such a plan on the tensor cores: bf16 activations, 64-token pages, d_c 512, d_r 64, a
 // multiple of 16 heads; q_lat and cache at multiples of 16 bytes. dp.part_o is fp32 [items][H][512].

@@ -410,6 +410,7 @@ __global__ void __launch_bounds__(256) combine_kernel(DecodeParams p, int groups
   const int first = p.group_first[g], last = p.group_last[g];
   const int n = (first >= 0 && last >= first) ? last - first + 1 : 0;
   QT* out = reinterpret_cast<QT*>(p.out_latent) + gh * p.d_c;
+  if (p.bad_lists && h == 0 && lane == 0 && p.bad_lists[g]) flag_status(p.status, MLA_ERR_DEVICE_GUARD);
   if (n == 1) return;                          // written directly by the attention kernel
   float m = -INFINITY;
   bool nan = false;

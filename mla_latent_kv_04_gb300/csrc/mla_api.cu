@@ -1022,7 +1022,8 @@ mla_status mla_select_pages(const mla_config* cfg, const float* scores, int max_
   return e == cudaSuccess ? MLA_OK : cuda_fail(e, "mla_select_pages");
 }
 
-// the decode's workspace without its query (which is given), then the physical pages of every list
+// the decode's workspace without its query (which is given), then the physical pages of every list and whether each
+// list has entries that it must not have
 static mla_status pages_layout(const mla_config* cfg, int batch, int q_len, int budget, DecodeWorkspace* w,
                                size_t* table) {
   mla_status st = check_decode(cfg, batch, q_len);
@@ -1034,7 +1035,7 @@ static mla_status pages_layout(const mla_config* cfg, int batch, int q_len, int 
   w->part_o -= query;
   w->part_lse -= query;
   *table = w->total - query;
-  w->total = align256(*table + (size_t)batch * q_len * budget * 4);
+  w->total = align256(*table + (size_t)batch * q_len * ((size_t)budget + 1) * 4);
   return MLA_OK;
 }
 
@@ -1093,13 +1094,15 @@ mla_status mla_decode_pages(const mla_config* cfg, const void* q_lat, const void
     pp.item_cost = decode_pages_item_cost(cfg->cache_dtype);
   }
   int32_t* listed = (int32_t*)(ws + table);
-  cudaError_t e = launch_pages_prep(pp, block_table, listed, s);
+  int32_t* bad = listed + (long long)w.groups * budget;
+  cudaError_t e = launch_pages_prep(pp, block_table, listed, bad, s);
   if (e != cudaSuccess) return cuda_fail(e, "mla_decode_pages (prologue)");
   // every query is a request of its own, with its list as its pages
   DecodeParams dp;
   dp.q_lat = q_lat;
   dp.cache = cache;
   dp.block_table = listed;
+  dp.bad_lists = bad;
   dp.max_pages = budget;
   dp.num_pages = num_pages;
   dp.batch = w.groups;

@@ -312,10 +312,10 @@ __global__ void __launch_bounds__(kSelThreads) select_pages_kernel(SelectParams 
 
 // ======================================================================== decode over chosen pages
 // Block 0 plans; block 1 + g writes the physical pages of query g's list. An entry that is out of
-// order, or a page that the query does not see, becomes -1, which the attention flags. 6 us, the plan's
-// chain of dependent steps.
+// order, behind a -1, or a page that the query does not see, becomes -1 and sets bad[g], which the merge of the pieces
+// flags (block 0 clears the status word meanwhile). 6 us, the plan's chain of dependent steps.
 __global__ void __launch_bounds__(256) pages_prep_kernel(PlanParams pp, const int32_t* __restrict__ block_table,
-                                                         int32_t* __restrict__ table) {
+                                                         int32_t* __restrict__ table, int32_t* __restrict__ bad) {
   extern __shared__ int sm[];
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
@@ -327,11 +327,15 @@ __global__ void __launch_bounds__(256) pages_prep_kernel(PlanParams pp, const in
   const int seen = S < pp.q_len || S <= 0 || S > (long long)pp.max_pages * pp.page_size
                        ? 0 : (S - pp.q_len + g % pp.q_len) / pp.page_size + 1;
   const int32_t* list = pp.pages + (long long)g * pp.budget;
+  int wrong = 0;
   for (int k = threadIdx.x; k < pp.budget; k += 256) {
     const int pg = list[k], before = k > 0 ? list[k - 1] : -1;
     const bool ok = pg > before && pg < seen && (k == 0 || before >= 0);
     table[(long long)g * pp.budget + k] = ok ? block_table[(long long)b * pp.max_pages + pg] : -1;
+    wrong |= pg >= 0 && !ok;
   }
+  wrong = __syncthreads_or(wrong);
+  if (threadIdx.x == 0) bad[g] = wrong && seen > 0;
 }
 
 }  // namespace
@@ -383,12 +387,13 @@ cudaError_t launch_select_pages(const SelectParams& p, int groups, cudaStream_t 
   return launch_pdl(select_pages_kernel, dim3((unsigned)groups, 1, 1), kSelThreads, smem, s, p);
 }
 
-cudaError_t launch_pages_prep(const PlanParams& pp, const int32_t* block_table, int32_t* table, cudaStream_t s) {
+cudaError_t launch_pages_prep(const PlanParams& pp, const int32_t* block_table, int32_t* table, int32_t* bad,
+                              cudaStream_t s) {
   const int groups = pp.batch * pp.q_len;
   const size_t smem = plan_smem_bytes(groups, pp.workers);
   cudaError_t e = allow_smem(pages_prep_kernel, smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(pages_prep_kernel, dim3((unsigned)(1 + groups), 1, 1), 256, smem, s, pp, block_table, table);
+  return launch_pdl(pages_prep_kernel, dim3((unsigned)(1 + groups), 1, 1), 256, smem, s, pp, block_table, table, bad);
 }
 
 }  // namespace mla
