@@ -26,8 +26,10 @@ __device__ __forceinline__ void mbar_arrive_expect_tx(uint32_t bar, uint32_t byt
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
                : "memory");
 }
-// Relaxed arrive on another CTA's mbarrier: it orders nothing. Reads of shared memory that have to
-// be complete first must decide whether it is executed (a branch on their values); tensor-memory loads
+// Relaxed arrive on another CTA's mbarrier: it orders nothing by itself. Where reads of shared memory have to be
+// complete first, a volatile store of a value that needs every word read stands in front of it in program order (and a
+// __syncwarp between, for other lanes' reads): a warp issues in order, and the store cannot be issued, nor moved or
+// left out by the compiler, before the words are there. An operand that nothing uses does not do. Tensor-memory loads
 // and stores are waited for.
 __device__ __forceinline__ void mbar_arrive_remote_relaxed(uint32_t remote_bar) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote_bar) : "memory");
