@@ -37,3 +37,19 @@ def test_lists_with_an_entry_out_of_place(kind, shape, H):
     got, lse, st = pg.attend(c, q_lat, p, lens=(300, 0, 150))
     assert st == M.MLA_OK and (got[1] == 0).all() and np.isneginf(lse[1]).all()
     pg.check_attend(c, q_lat, pages, got, lse, skip=(1,))
+
+
+@pytest.mark.parametrize("kind,shape,H", [("f32", "tiny", 16), ("bf16", "v2", 128), ("fp8_e4m3", "v2", 16)])
+@pytest.mark.parametrize("bad", [{32: 5}, {9: 5, 10: 6}, {0: -1, 1: -1, 20: 3}, {63: 7}, {0: -1, 1: -1, 41: 0}])
+def test_long_lists_with_an_entry_far_behind_their_end(kind, shape, H, bad):
+    rng = np.random.default_rng(2)
+    c = D.Cache(rng, kind, D.dims(shape, H), (3000, 900, 700))
+    q_lat, pages = pg.draw_query(rng, c, 1), pg.lists(rng, c, 1, 64, "short")
+    p = pages.copy()
+    p[1, 0, 2:] = -1
+    p[1, 0, :2] = (0, 1)
+    for k, page in bad.items():
+        p[1, 0, k] = page
+    got, lse, st = pg.attend(c, q_lat, p)
+    assert st == M.MLA_ERR_DEVICE_GUARD
+    pg.check_attend(c, q_lat, pages, got, lse, skip=(1,))
