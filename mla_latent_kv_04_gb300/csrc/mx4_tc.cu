@@ -259,19 +259,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::tma_prefetch_3d_hint(&tm_w, kX * i, 128 * mt, 0, pol);
       ptx::griddep_wait();
       uint32_t g = 0, st = 0, phase = 1;
-      for (long long u = u0; u < u1; ++u, ++g) {
+      // (the testing hook: no step from a withheld one on, those before it are awaited by their products)
+      const long long stop = p.test.withhold > 0 && blockIdx.x == 0 ? min(u1, u0 + p.test.withhold - 1) : u1;
+      for (long long u = u0; u < stop; ++u, ++g) {
         const uint32_t dst = base + st * p.shape.stage, full = bar(B_FULL + st);
         if (!wait(B_EMPTY + st, phase)) break;
         const uint32_t n = (uint32_t)min(F::kGroups, p.groups - F::kGroups * k);   // groups of 128 of this step
-        if (blockIdx.x != 0 || (int)g != p.test.withhold - 1) {
-          ptx::mbar_arrive_expect_tx(full, F::kTx + p.shape.cols * 128 + n * 512 * (1 + kAtoms));
-          if (p.work.row_tiles == 1) ptx::tma_load_3d_hint(dst, &tm_w, kX * k, 128 * mt, 0, full, pol);
-          else ptx::tma_load_3d(dst, &tm_w, kX * k, 128 * mt, 0, full);
-          ptx::tma_load_3d(dst + off_x, &tm_x, 128 * k, 0, rt, full);
-          bulk_load(dst + off_sfw, p.w_scales + ((long long)mt * p.groups + F::kGroups * k) * 512, n * 512, full);
-          bulk_load(dst + off_sfx, p.x_scales + ((long long)rt * p.groups + F::kGroups * k) * (kAtoms * 512),
-                    n * (kAtoms * 512), full);
-        }
+        ptx::mbar_arrive_expect_tx(full, F::kTx + p.shape.cols * 128 + n * 512 * (1 + kAtoms));
+        if (p.work.row_tiles == 1) ptx::tma_load_3d_hint(dst, &tm_w, kX * k, 128 * mt, 0, full, pol);
+        else ptx::tma_load_3d(dst, &tm_w, kX * k, 128 * mt, 0, full);
+        ptx::tma_load_3d(dst + off_x, &tm_x, 128 * k, 0, rt, full);
+        bulk_load(dst + off_sfw, p.w_scales + ((long long)mt * p.groups + F::kGroups * k) * 512, n * 512, full);
+        bulk_load(dst + off_sfx, p.x_scales + ((long long)rt * p.groups + F::kGroups * k) * (kAtoms * 512),
+                  n * (kAtoms * 512), full);
         if (++st == (uint32_t)stages) {
           st = 0;
           phase ^= 1;
