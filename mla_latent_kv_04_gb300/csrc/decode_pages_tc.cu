@@ -28,8 +28,8 @@
 //
 // Bound: the load, product, softmax, product chain of a tile, whose rows fill shared memory (bf16: 2.6 us a
 // tile); e4m3: the MMAs (64 columns as long as 128 would) and, as long again, the way from scores to P. 32
-// queries of 64 pages, 128 heads, a cold L2: bf16 71 us (151 MB), e4m3 63, block scales 105. 64 x 2 queries of 96
-// pages, e4m3: 194. (Under one power of two for the list, without the maxima of every 32 tokens: 59, 93 and 181.)
+// queries of 64 pages, 128 heads, a cold L2: bf16 71 us (151 MB), e4m3 61, block scales 102. 64 x 2 queries of 96
+// pages, e4m3: 192. (Under one power of two for the list, without the maxima of every 32 tokens: 59, 93 and 181.)
 #include <math.h>
 
 #include "fp8_tiles.cuh"
@@ -434,6 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool first = pg == 2 * item.page_begin;
         const bool live = tok < left;
         float4 sc = make_float4(0.f, 0.f, 0.f, 0.f);
+        int fe[4] = {0, 0, 0, 0};
         if constexpr (kFmt == kB128) {
           if (live) {
             int page = p.block_table[g * p.max_pages + pg + (tok >> 6)];
@@ -441,6 +442,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             sc = *reinterpret_cast<const float4*>(reinterpret_cast<const uint8_t*>(p.cache) +
                                                   ((long long)page * 64 + (tok & 63)) * p.row_bytes + 512);
           }
+          // powers of two above the 32 tokens' scales of each 128 dims (while the first scores are formed)
+          const float f[4] = {sc.x, sc.y, sc.z, sc.w};
+#pragma unroll
+          for (int m = 0; m < 4; ++m)
+            fe[m] = min(126, (int)(__reduce_max_sync(0xffffffffu, __float_as_uint(f[m]) & 0x7FFFFFFFu) >> 23) - 126);
         }
         // scores of this thread's heads, in log2 units
         float s[16];
@@ -541,15 +547,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
-          int fe[4] = {0, 0, 0, 0};
           if constexpr (kFmt == kB128) {
             float* f[4] = {&sc.x, &sc.y, &sc.z, &sc.w};
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
-              const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(*f[m]) & 0x7FFFFFFFu);
-              fe[m] = min(126, (int)(top >> 23) - 126);
-              *f[m] *= __uint_as_float((uint32_t)(127 - fe[m]) << 23);
-            }
+            for (int m = 0; m < 4; ++m) *f[m] *= __uint_as_float((uint32_t)(127 - fe[m]) << 23);
           }
           const float top = k8 + (float)max(max(fe[0], fe[1]), max(fe[2], fe[3]));
           if (first) {                         // the item's reference: the largest of the four warps
