@@ -104,6 +104,39 @@ def test_scores_of_a_wide_spread(kind, rising, monkeypatch):
     check(c, q_lat, pages, got, lse, monkeypatch)
 
 
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("how", ["rising", "jump", "falling", "far"])
+def test_scores_hundreds_of_octaves_apart(kind, how, monkeypatch):
+    """Running maxima that leave the range of a scale's 8 bits and of fp32 itself within one item: 500 log2 units
+    up over the list, 300 up at once in the middle of a tile, 300 down; and scores of 10^7, which have no fractions.
+    Keys of 0, 0.125 .. 1 are exact in every format, and so are the products."""
+    rng = np.random.default_rng(9)
+    n, H = 3000, 128
+    x = rng.standard_normal((n, 576)) * 0.5
+    x[:, :512] += 0.3
+    x[:, 512:] = 0.0
+    at = np.arange(n)
+    x[:, 512] = {"rising": at * 8 // n / 8, "jump": at >= 1500, "falling": at < 1501, "far": at * 8 // n / 8}[how]
+    c = cache_of(rng, kind, H, [x], scale=2.0 ** -7)
+    q_lat = rope_query(1, H, np.linspace(1, 1.2, H) * {"rising": 500.0, "far": 1.0e7}.get(how, 300.0), 0.0)
+    pages = every_page(c)
+    got, lse, st = pg.attend(c, q_lat, pages)
+    assert st == M.MLA_OK
+    # the weights are 0 or equal: the outputs are means of the heaviest tokens' latents, whatever the scores' size
+    top = c.values[0][:, 512] == c.values[0][:, 512].max()
+    want = c.values[0][top][:, :512].mean(0)
+    tol = D.EPS["bf16"] * np.abs(want) * 1.01 + 2.0 ** -8 * np.abs(c.values[0][top][:, :512]).mean(0)
+    if how == "far":
+        # A list's pieces (ranges of tiles of 128 tokens) are weighed by their LSEs, fp32 numbers near 8e6: rounded to a
+        # whole log2 unit (0.35 nat) and then to half a nat (0.25), so that two weights are off by up to e^1.2.
+        tiles = [(v[m], m.sum()) for k in range(0, n, 128)
+                 for v, m in [(c.values[0][k: k + 128, :512], top[k: k + 128])] if m.any()]
+        tol = tol + (np.exp(1.2) - 1) * sum(k * np.abs(v.mean(0) - want) for v, k in tiles) / top.sum()
+    D.assert_within(got[0, 0], np.broadcast_to(want, (H, 512)), np.broadcast_to(tol, (H, 512)), how)
+    z = oracle.softmax_scale(128, 64) * q_lat[0, 0, :, 512].astype(np.float64) * c.values[0][:, 512].max()
+    D.assert_within(lse[0, 0], z + np.log(top.sum()), 2.0 ** -20 * np.abs(z) + 1e-3, how)
+
+
 @pytest.mark.parametrize("scales", [(1, 1 / 64, 1, 1 / 64), (1, 2.0 ** -8, 2.0 ** -10, 2.0 ** -13), (2.0 ** -30, 1, 2.0 ** 40, 1)])
 @pytest.mark.parametrize("spread", [0.0, 2.9])
 def test_blocks_of_dims_under_scales_far_apart(scales, spread, monkeypatch):
