@@ -474,7 +474,8 @@ mla_status mla_page_keys(const mla_config* cfg, const void* cache, int num_pages
                          int max_pages, const int32_t* seq_lens, int batch, int new_tokens, void* page_keys,
                          int32_t* dev_status, void* stream);
 
-/* Bytes of workspace mla_page_scores needs for this batch on the current device (may be 0). */
+/* Bytes of workspace mla_page_scores needs for this batch on the current device: every head's sum for the SIMT
+ * kernels, asked for whichever kernel a call's addresses will choose. */
 mla_status mla_page_scores_workspace_size(const mla_config* cfg, int batch, int q_len, int max_pages,
                                           size_t* bytes);
 
@@ -491,8 +492,8 @@ mla_status mla_page_scores_workspace_size(const mla_config* cfg, int batch, int 
  * above max_pages * P is left out, both with the guard; seq_lens[b] == 0 is left out. Should a bounded wait of the
  * tensor-core kernel run out, MLA_ERR_TIMEOUT is OR-ed into *dev_status and that query's scores are not written.
  * workspace: 256-byte
- * aligned device buffer of mla_page_scores_workspace_size bytes (NULL if that is 0), any contents; calls
- * that share one must be ordered on the GPU. */
+ * aligned device buffer of mla_page_scores_workspace_size bytes, any contents; calls that share one must be
+ * ordered on the GPU. */
 mla_status mla_page_scores(const mla_config* cfg, const void* q_lat, const void* page_keys, int num_pages,
                            const int32_t* block_table, int max_pages, const int32_t* seq_lens, int batch,
                            int q_len, float* scores, void* workspace, size_t workspace_bytes,
@@ -574,7 +575,7 @@ mla_status mla_mx4_project_workspace_size(const mla_config* cfg, int K, int N, i
  *   cleared by each call (mla_read_device_status). rows == 0 is a no-op.
  * bf16 activations run on the tensor cores (an x that does not start at a multiple of 16 bytes on the SIMT
  * kernel): x enters as exact sums of 4-bit or e4m3 values under a power of two per 32 elements, off by at most
- * 2^-17 of the largest of the 32, and a row that holds an infinity or NaN gives NaN in all its outputs. A
+ * 2^-17 of the largest of the 32 (or 2^-128 where that is more), and a row that holds an infinity or NaN gives NaN in all its outputs. A
  * column with a NaN scale gives NaN. Should a bounded wait of the kernel run out, the status word gets
  * MLA_ERR_TIMEOUT and outputs that need the missing sums are not written. */
 mla_status mla_mx4_project(const mla_config* cfg, const void* x, const void* codes, const void* scales, int K,

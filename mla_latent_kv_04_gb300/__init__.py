@@ -601,7 +601,7 @@ def mla_page_scores_workspace_size(cfg, batch, q_len, max_pages) -> int:
 def mla_page_scores(cfg, q_lat, page_keys, block_table, seq_lens, scores, workspace=None, dev_status=None,
                     stream=None):
     """q_lat [B][q_len][H][d_c + d_r] (mla_absorb_query) -> scores [B][q_len][max_pages] fp32. workspace:
-    uint8 device tensor of mla_page_scores_workspace_size bytes (None if 0)."""
+    uint8 device tensor of mla_page_scores_workspace_size bytes."""
     a = (_act_dtype(cfg),)
     t = _torch()
     batch, q_len = q_lat.shape[0], q_lat.shape[1]

@@ -6,7 +6,8 @@
 //   form 4 (kind::mxf4, up to 40 rows): e2m1 holds the integers -3 .. 4, digits enough for a base-8 number;
 //     with s = 2^(E - 1)
 //       |x| = s (d_0 + d_1 / 8 + ... + d_5 / 8^5),  d_0 in 0 .. 4, the others in -3 .. 4,
-//     for |x| / s rounded to a multiple of 8^-5: off by at most 2^(E - 17), and exact for elements down to
+//     for |x| / s rounded to a multiple of 8^-5: off by at most 2^(E - 17) (E not below -111, where the last
+//     digit's scale ends), and exact for elements down to
 //     2^-9 of the largest (bf16 has 8 significant bits). Six columns a row, digit i under s / 8^i.
 //   form 8 (kind::mxf8f6f4, more rows): an e4m3 value has 4 significant bits; with s = 2^(E - 7)
 //       x = s (hi + lo / 16),  hi = e4m3(x / s), lo = e4m3(16 (x / s - hi)),
