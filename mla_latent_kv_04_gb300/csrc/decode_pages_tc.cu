@@ -15,7 +15,8 @@
 // whether it holds. If not, references, O and sums are rescaled and P is formed again.
 //
 // bf16 cache: the staged rows are both products' operands (K-major rows of S^T, dims-major columns of O^T);
-// P is rounded to bf16 and takes the place of the tile's rotary keys, which S^T has used up.
+// P is rounded to bf16 (the type of the rows, which both operands of an MMA share; the sums count the unrounded
+// weights) and takes the place of the tile's rotary keys, which S^T has used up.
 // fp8 caches: the codes themselves are the operands (kind::f8f6f4). The query is the sum of two e4m3 terms
 // under a power of two per head (two columns of S^T, split4). So is P, under a power of two per head and 32
 // tokens (kind::mxf8f6f4, which applies it): y = hi + lo / 16, the largest y of the 32 between 2^7 and 2^8.5, so a
