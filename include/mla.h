@@ -577,7 +577,7 @@ mla_status mla_mx4_project_workspace_size(const mla_config* cfg, int K, int N, i
  * kernel): x enters as exact sums of 4-bit or e4m3 values under a power of two per 32 elements, off by at most
  * 2^-17 of the largest of the 32 (or 2^-128 where that is more), and a row that holds an infinity or NaN gives NaN in all its outputs. A
  * column with a NaN scale gives NaN. Should a bounded wait of the kernel run out, the status word gets
- * MLA_ERR_TIMEOUT and outputs that need the missing sums are not written. */
+ * MLA_ERR_TIMEOUT and outputs may be left as they were; none gets a partial sum. */
 mla_status mla_mx4_project(const mla_config* cfg, const void* x, const void* codes, const void* scales, int K,
                            int N, int rows, void* out, void* workspace, size_t workspace_bytes, void* stream);
 
