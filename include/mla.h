@@ -598,9 +598,9 @@ const char* mla_last_error(void);
 int mla_version(void);
 
 /* Testing hook of the failure paths of the tensor-core kernels of mla_mx4_project and mla_page_scores, for this host
- * thread's calls until it is set again: wait_limit_us (0: the default, 2 s) is how long a barrier wait may last; the
- * first CTA never loads (or hands over) the copy of index withhold - 1 (0: all are), so that the wait for it runs
- * out. */
+ * thread's calls until it is set again: wait_limit_us (0: the default, 2 s) is how long a barrier wait may last. With
+ * withhold >= 1 the first CTA's copy of index withhold - 1 never arrives (mla_mx4_project: nor those behind it), so that
+ * the wait for it runs out; 0: all do. */
 void mla_testing_waits(int wait_limit_us, int withhold);
 
 /* Number of CUDA kernels the library has launched in this process so far (all
